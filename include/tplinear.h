@@ -362,6 +362,180 @@ tp_status tp_linear_row_noalloc(const void *X, int64_t ldx, const void *W, int64
                                 int64_t M, int64_t N, int64_t K, int32_t P,
                                 int32_t dtype, void *stream);
 
+/* ---- 8-bit integers ------------------------------------------------------
+ *
+ * The same layers with X and W held as int8 and one fp32 scale for each token
+ * and each output channel: x ~ x_scale[m] * X[m, k], w ~ w_scale[n] * W[n, k].
+ * The integer sums are exact; they are rounded once to fp32 and scaled.
+ */
+
+/*
+ * tp_quantize_rows -- rows to int8 with a scale for each of G equal column
+ * groups: for row m and group j (columns [j*K/G, (j+1)*K/G))
+ *   scale[m*lds + j] = max |x| / 127, rounded to fp32;
+ *   Q[m, k] = X[m, k] / scale, the exact quotient rounded to the nearest whole
+ *   number (halves to even), at most 127 in size.
+ * G = 1: the scales of a column layer's tokens, or of a weight's output
+ * channels.  G = P: a row layer's input, shard i's columns with a scale of
+ * their own (what P ranks would each find for their Shard(1) slice).
+ * A group of zeros (or whose scale rounds to 0) has scale 0 and zeros.  A group
+ * that holds an infinity or a NaN has scale NaN and zeros, so the row's
+ * products come out NaN.
+ * X [M, K] of dtype, ldx >= K; Q [M, K], ldq >= K; lds >= G.
+ * Errors: TP_ERR_NULL, TP_ERR_SHAPE (sizes, leading dims, G out of 1 ..
+ * TP_MAX_SHARDS), TP_ERR_INDIVISIBLE (K % G != 0), TP_ERR_DTYPE, TP_ERR_HIP.
+ */
+tp_status tp_quantize_rows(const void *X, int64_t ldx, int8_t *Q, int64_t ldq, float *scale,
+                           int64_t lds, int64_t M, int64_t K, int32_t G, int32_t dtype,
+                           void *stream);
+
+/*
+ * tp_linear_column_quant -- tp_linear_column_ex (one X, optional bias and gated
+ * unit) on int8 operands.
+ *
+ * x_scale: token m's at x_scale[m*ldxs], ldxs >= 1.  w_scale: [N], in the order
+ * of W's rows (Shard(0), as the bias).  Output feature n of token m before the
+ * activation: fma(float(sum_k X W) * x_scale[m], w_scale[n], bias[n] or 0).
+ * out_dtype: TP_BF16 or TP_F32, the type of Y and of the bias.
+ * K is at most 131071, so that no int32 sum overflows.
+ * Other arguments and errors as tp_linear_column_ex (no x_slices);
+ * TP_ERR_SHAPE for a longer K or ldxs < 1, TP_ERR_NULL for a missing scale.
+ */
+tp_status tp_linear_column_quant(const int8_t *X, int64_t ldx, const float *x_scale, int64_t ldxs,
+                                 const int8_t *W, int64_t ldw, const float *w_scale,
+                                 const void *bias, void *Y, int64_t ldy, int32_t y_mode,
+                                 int32_t act, int64_t M, int64_t N, int64_t K, int32_t P,
+                                 int32_t out_dtype, void *stream);
+
+/*
+ * tp_linear_row_quant -- tp_linear_row_ex on int8 operands.
+ *
+ * x_groups: scales a token has, 1 or P; that of shard i at x_scale[m*ldxs + i]
+ * (x_groups = P) or x_scale[m*ldxs] (1), ldxs >= x_groups.  w_scale: [N], the
+ * same for every shard (the channel's scale of the whole weight).
+ * With acc_i the int32 sum over shard i's columns:
+ *   x_groups = P:  S = fma(acc_i, x_scale_i, S), i ascending from
+ *                  S = acc_0 * x_scale_0;
+ *   x_groups = 1:  S = float(sum_i acc_i) * x_scale, the sum in integers;
+ *   Y[m, n] = fma(S, w_scale[n], bias[n] or 0), one rounding to out_dtype.
+ * TP_ROW_SUM and TP_ROW_FUSED are the same call here: the library folds inside
+ * the product or by way of int32 partials in the workspace, whichever is
+ * faster, with the same bits.  TP_ROW_SCATTER places the same values as token
+ * slices.  TP_ROW_PARTIAL writes float(acc_i) * x_scale_i * w_scale[n] as fp32.
+ * workspace: as tp_linear_row (tp_row_workspace_bytes).
+ * K/P (with x_groups = 1 and a sum: K) is at most 131071.
+ * Other arguments and errors as tp_linear_row_ex; TP_ERR_SHAPE for a longer
+ * K, x_groups not 1 or P, or ldxs < x_groups; TP_ERR_NULL for a missing scale.
+ */
+tp_status tp_linear_row_quant(const int8_t *X, int64_t ldx, const float *x_scale, int64_t ldxs,
+                              int32_t x_groups, const int8_t *W, int64_t ldw,
+                              const float *w_scale, const void *bias, void *Y,
+                              void *const *y_slices, int64_t ldy, int64_t y_slice_stride,
+                              int32_t mode, void *workspace, size_t ws_bytes, int64_t M,
+                              int64_t N, int64_t K, int32_t P, int32_t out_dtype, void *stream);
+
+/* ---- heads of a fused QKV layer ------------------------------------------
+ *
+ * A fused QKV column layer gives shard i its Hq/P query heads, then its Hkv/P
+ * key heads, then its Hkv/P value heads of D features each (whole heads per
+ * shard, "Tensor Parallel": the column split leaves the attention of a shard's
+ * heads to the shard).  X is that layer's output: x_mode TP_Y_CONCAT: [T, N], N
+ * = (Hq + 2 Hkv) D, shard i at columns [i*N/P, (i+1)*N/P); TP_Y_SHARDS: P blocks
+ * [T, N/P] at X + i*T*ldx.  Head j of shard i is query head i*Hq/P + j (key and
+ * value heads likewise), the order of the outputs.
+ *
+ * Rotation: the first R features of a head (R even, 0 for none) as R/2 pairs;
+ * pair j is (y[j], y[j + R/2]) for TP_ROPE_HALVES or (y[2j], y[2j+1]) for
+ * TP_ROPE_PAIRS, turned to (a cos - b sin, b cos + a sin) with the cosine and
+ * sine of row p of the tables (fp32, [n_pos, R/2] contiguous), p the token's
+ * position.
+ * Norm: y = x * rsqrt(mean(x^2) + eps) * weight over the D features of a head;
+ * weights are [D] of dtype, shared by the heads and shards (Replicate); a NULL
+ * weight means no norm for that kind of head.
+ * Arithmetic in fp32, one rounding to dtype (X, weights, outputs, caches).
+ */
+enum { TP_ROPE_HALVES = 0, TP_ROPE_PAIRS = 1 };
+
+/*
+ * tp_qk_norm_rope -- norm and rotation of queries and keys in one pass.
+ *
+ * pos: device int64 [T] (may be NULL for R = 0).  A position outside [0,
+ * n_pos) -- a padding token's -1 -- gives zero rows and, when bad_flag (device
+ * int32) is not NULL, stores 1 there (the library never clears it).
+ * Q: [T, Hq*D], ldq >= Hq*D, or NULL; K: [T, Hkv*D], ldk >= Hkv*D, or NULL; not
+ * both NULL.
+ * Errors: TP_ERR_NULL, TP_ERR_SHAPE (sizes, leading dims, D not in 1 .. 1024, R
+ * odd or above D, eps negative or NaN), TP_ERR_INDIVISIBLE (Hq or Hkv % P),
+ * TP_ERR_DTYPE, TP_ERR_MODE (x_mode, style), TP_ERR_HIP.
+ */
+tp_status tp_qk_norm_rope(const void *X, int64_t ldx, int32_t x_mode, const int64_t *pos,
+                          const float *cos_t, const float *sin_t, int64_t n_pos, int64_t R,
+                          int32_t style, const void *q_weight, const void *k_weight, float eps,
+                          void *Q, int64_t ldq, void *K, int64_t ldk, int64_t T, int64_t Hq,
+                          int64_t Hkv, int64_t D, int32_t P, int32_t dtype, int32_t *bad_flag,
+                          void *stream);
+
+/*
+ * tp_qk_norm_rope_backward -- the gradients of tp_qk_norm_rope.
+ *
+ * dQ [T, Hq*D], dK [T, Hkv*D], dV [T, Hkv*D] of dtype (NULL: that part of dX is
+ * left as it is); dX with the layout of X (row stride lddx): the gradient of
+ * X's query and key features, and a copy of dV in its value features, so that
+ * dX is whole.  Tokens whose position is outside the table have zero query and
+ * key gradients and count nowhere else (bad_flag as above).
+ * dq_weight, dk_weight: fp32 [D] or NULL; the sums over all tokens and heads,
+ * added in an order fixed by T alone.  They need a workspace of
+ * tp_qk_norm_rope_workspace_bytes(T, D), 256-byte aligned, which calls that may
+ * overlap must not share.
+ * X is read only where there is a norm (may be NULL without).
+ * Errors: as tp_qk_norm_rope; TP_ERR_NULL also for a weight's gradient without
+ * the weight, TP_ERR_WORKSPACE.
+ */
+tp_status tp_qk_norm_rope_backward(const void *X, int64_t ldx, int32_t x_mode, const int64_t *pos,
+                                   const float *cos_t, const float *sin_t, int64_t n_pos,
+                                   int64_t R, int32_t style, const void *q_weight,
+                                   const void *k_weight, float eps, const void *dQ, int64_t lddq,
+                                   const void *dK, int64_t lddk, const void *dV, int64_t lddv,
+                                   void *dX, int64_t lddx, float *dq_weight, float *dk_weight,
+                                   void *workspace, size_t ws_bytes, int64_t T, int64_t Hq,
+                                   int64_t Hkv, int64_t D, int32_t P, int32_t dtype,
+                                   int32_t *bad_flag, void *stream);
+
+/* Bytes of workspace the weight gradients need; 0 for invalid sizes. */
+size_t tp_qk_norm_rope_workspace_bytes(int64_t T, int64_t D);
+
+/*
+ * tp_kv_append -- append the keys (normed and rotated) and the values of new
+ * tokens to a paged cache; with Q, the queries too (normed and rotated), so
+ * that a decode step needs one launch.
+ *
+ * cu: device int32 [B + 1], non-decreasing; sequence s has the rows cu[s] ..
+ * cu[s+1] - 1 of X.  past: device int32 [B], the tokens sequence s already has:
+ * row t's position is past[s] + t - cu[s].  table: device int32 [B, max_pages],
+ * row stride ldt: position p lies in slot p % page_size of page
+ * table[s*ldt + p/page_size].
+ * k_cache, v_cache: dtype, row (page, slot, head) at page*page_stride +
+ * slot*slot_stride + head*head_stride, D contiguous features; the same strides
+ * for both, and no two rows may share elements.
+ * Rows no sequence owns (before cu[0], from cu[B] on) are left alone, in the
+ * caches and in Q.  A row whose position is outside [0, max_pages*page_size)
+ * or (R > 0) the tables, or whose page is outside [0, n_pages), is not appended,
+ * has a zero row in Q and sets *bad_flag.
+ * Two rows of one call must not lie in the same slot (the slot then holds parts
+ * of either).
+ * Errors: as tp_qk_norm_rope; TP_ERR_SHAPE also for strides that let rows share
+ * elements, page_size < 1, ldt < max_pages.
+ */
+tp_status tp_kv_append(const void *X, int64_t ldx, int32_t x_mode, const float *cos_t,
+                       const float *sin_t, int64_t n_pos, int64_t R, int32_t style,
+                       const void *q_weight, const void *k_weight, float eps, const int32_t *cu,
+                       const int32_t *past, int64_t B, const int32_t *table, int64_t ldt,
+                       int64_t max_pages, void *k_cache, void *v_cache, int64_t n_pages,
+                       int64_t page_size, int64_t page_stride, int64_t slot_stride,
+                       int64_t head_stride, void *Q, int64_t ldq, int64_t T, int64_t Hq,
+                       int64_t Hkv, int64_t D, int32_t P, int32_t dtype, int32_t *bad_flag,
+                       void *stream);
+
 /* Bytes of workspace tp_linear_row needs for (mode, M, N, P); 0 for
  * TP_ROW_PARTIAL, and for invalid arguments (including P*M*N*4 > 2^60,
  * which tp_linear_row rejects with TP_ERR_SHAPE). */

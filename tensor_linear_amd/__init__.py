@@ -48,12 +48,15 @@ TP_REPLICATE, TP_SHARD, TP_PARTIAL = 0, 1, 2
 TP_Y_CONCAT, TP_Y_SHARDS = 0, 1
 TP_ROW_PARTIAL, TP_ROW_SUM, TP_ROW_FUSED, TP_ROW_SCATTER = 0, 1, 2, 3
 TP_ACT_NONE, TP_ACT_SWIGLU = 0, 1
+TP_ROPE_HALVES, TP_ROPE_PAIRS = 0, 1
 TP_MAX_SHARDS = 64
 
 EXPORTS = ("tp_shard_layout", "tp_linear_column", "tp_linear_row", "tp_shard_reduce",
            "tp_linear_column_ex", "tp_linear_row_ex", "tp_shard_reduce_ex", "tp_embedding",
            "tp_row_workspace_bytes", "tp_workspace_zero", "tp_status_str", "tp_version",
-           "tp_linear_row_noalloc")
+           "tp_linear_row_noalloc", "tp_quantize_rows", "tp_linear_column_quant",
+           "tp_linear_row_quant", "tp_qk_norm_rope", "tp_qk_norm_rope_backward",
+           "tp_qk_norm_rope_workspace_bytes", "tp_kv_append")
 TP_NOALLOC_SCRATCH_BYTES = 32 << 20
 
 
@@ -68,6 +71,7 @@ class tp_view(ctypes.Structure):
 
 
 _i32, _i64, _ptr, _sz = ctypes.c_int32, ctypes.c_int64, ctypes.c_void_p, ctypes.c_size_t
+_f32 = ctypes.c_float
 
 
 def _declare(lib):
@@ -97,6 +101,30 @@ def _declare(lib):
     lib.tp_linear_row_noalloc.argtypes = [_ptr, _i64, _ptr, _i64, _ptr, _i64, _i64, _i32,
                                           _i64, _i64, _i64, _i32, _i32, _ptr]
     lib.tp_linear_row_noalloc.restype = _i32
+    lib.tp_quantize_rows.argtypes = [_ptr, _i64, _ptr, _i64, _ptr, _i64, _i64, _i64, _i32, _i32,
+                                     _ptr]
+    lib.tp_quantize_rows.restype = _i32
+    lib.tp_linear_column_quant.argtypes = [_ptr, _i64, _ptr, _i64, _ptr, _i64, _ptr, _ptr, _ptr,
+                                           _i64, _i32, _i32, _i64, _i64, _i64, _i32, _i32, _ptr]
+    lib.tp_linear_column_quant.restype = _i32
+    lib.tp_linear_row_quant.argtypes = [_ptr, _i64, _ptr, _i64, _i32, _ptr, _i64, _ptr, _ptr, _ptr,
+                                        _ptr, _i64, _i64, _i32, _ptr, _sz, _i64, _i64, _i64, _i32,
+                                        _i32, _ptr]
+    lib.tp_linear_row_quant.restype = _i32
+    # the QKV matrix, the rotation and the norms, then the tokens and heads
+    rot = [_ptr, _ptr, _i64, _i64, _i32, _ptr, _ptr, _f32]
+    heads = [_i64, _i64, _i64, _i64, _i32, _i32, _ptr, _ptr]
+    lib.tp_qk_norm_rope.argtypes = ([_ptr, _i64, _i32, _ptr] + rot + [_ptr, _i64, _ptr, _i64] +
+                                    heads)
+    lib.tp_qk_norm_rope.restype = _i32
+    lib.tp_qk_norm_rope_backward.argtypes = ([_ptr, _i64, _i32, _ptr] + rot + [_ptr, _i64] * 4 +
+                                             [_ptr, _ptr, _ptr, _sz] + heads)
+    lib.tp_qk_norm_rope_backward.restype = _i32
+    lib.tp_qk_norm_rope_workspace_bytes.argtypes = [_i64, _i64]
+    lib.tp_qk_norm_rope_workspace_bytes.restype = _sz
+    lib.tp_kv_append.argtypes = ([_ptr, _i64, _i32] + rot + [_ptr, _ptr, _i64, _ptr, _i64, _i64,
+                                 _ptr, _ptr, _i64, _i64, _i64, _i64, _i64, _ptr, _i64] + heads)
+    lib.tp_kv_append.restype = _i32
     lib.tp_row_workspace_bytes.argtypes = [_i32, _i64, _i64, _i32]
     lib.tp_row_workspace_bytes.restype = _sz
     lib.tp_workspace_zero.argtypes = [_ptr, _sz, _ptr]
@@ -544,3 +572,321 @@ def tp_embedding(ids, Y, P: int, E=None, e_shards=None, y_mode: int = TP_Y_CONCA
     _same_gpu(ids, Y, E, e_shards, bad)
     check(_get_lib().tp_embedding(ids.data_ptr(), T, ep, es, lde, V, D, yp, ldy, y_mode, P, dt,
                                   None if bad is None else bad.data_ptr(), _stream(ids, stream)))
+
+
+# ---- 8-bit integers -------------------------------------------------------
+
+def _int8_mat(t, name):
+    import torch
+    if t.dtype != torch.int8:
+        raise TypeError(f"{name} must be int8, got {t.dtype}")
+    return _mat(t, name)
+
+
+def _token_scales(t, M, groups, name):
+    """(pointer, row stride, scales a token) of fp32 scales [M] or [M, G], G
+    one of `groups`."""
+    import torch
+    if t.dtype != torch.float32:
+        raise TypeError(f"{name} must be float32, got {t.dtype}")
+    G = t.shape[1] if t.dim() == 2 else 1
+    if t.dim() not in (1, 2) or t.shape[0] != M or G not in groups:
+        raise ValueError(f"{name} must have shape [{M}] or [{M}, G] with G in {groups}, "
+                         f"got {tuple(t.shape)}")
+    if G > 1 and t.stride(1) != 1:
+        raise ValueError(f"{name} must have unit column stride")
+    ld = t.stride(0) if M > 1 else G
+    if ld < G:
+        raise ValueError(f"{name} must have a row stride of at least {G}")
+    return t.data_ptr(), ld, G
+
+
+def _channel_scales(t, N, name):
+    import torch
+    if t.dtype != torch.float32:
+        raise TypeError(f"{name} must be float32, got {t.dtype}")
+    _expect_shape(t, (N,), name)
+    if N > 1 and t.stride(0) != 1:
+        raise ValueError(f"{name} must be a contiguous 1-D tensor")
+    return t.data_ptr()
+
+
+def tp_quantize_rows(X, Q, scale, stream=None) -> None:
+    """Rows to int8.  X [M, K] bfloat16 or float32; Q int8 [M, K]; scale
+    float32 [M] or [M, G]: one scale for each row and each of G equal column
+    groups (G = P for a row layer's input)."""
+    xp, M, K, ldx = _mat(X, "X")
+    qp, _, _, ldq = _int8_mat(Q, "Q")
+    _expect_shape(Q, (M, K), "Q")
+    G = scale.shape[1] if scale.dim() == 2 else 1
+    _check_p(G)
+    sp, lds, _ = _token_scales(scale, M, (G,), "scale")
+    _same_gpu(X, Q, scale)
+    check(_get_lib().tp_quantize_rows(xp, ldx, qp, ldq, sp, lds, M, K, G, _dtype_code(X),
+                                      _stream(X, stream)))
+
+
+def tp_linear_column_quant(X, x_scale, W, w_scale, Y, P: int, y_mode: int = TP_Y_CONCAT,
+                           bias=None, act: int = TP_ACT_NONE, stream=None) -> None:
+    """Column-parallel Linear on int8 operands.  X int8 [M, K] with x_scale
+    float32 [M] or [M, 1]; W int8 [N, K] with w_scale float32 [N]; Y and bias
+    [N] as in tp_linear_column_ex, bfloat16 or float32."""
+    _check_p(P)
+    xp, M, K, ldx = _int8_mat(X, "X")
+    wp, N, Kw, ldw = _int8_mat(W, "W")
+    if Kw != K:
+        raise ValueError(f"X has K={K} but W has K={Kw}")
+    dt = _dtype_code(Y)
+    if N % P or (act == TP_ACT_SWIGLU and (N // P) % 2):
+        check(TP_ERR_INDIVISIBLE)
+    On = N // P // 2 if act == TP_ACT_SWIGLU else N // P
+    sp, lds, _ = _token_scales(x_scale, M, (1,), "x_scale")
+    wsp = _channel_scales(w_scale, N, "w_scale")
+    if bias is not None:
+        _expect_shape(bias, (N,), "bias")
+    if y_mode == TP_Y_SHARDS:
+        yp, ldy = _block_out(Y, P, M, On)
+    else:
+        yp, _, _, ldy = _mat(Y, "Y")
+        _expect_shape(Y, (M, P * On), "Y")
+    _same_gpu(X, x_scale, W, w_scale, Y, bias)
+    check(_get_lib().tp_linear_column_quant(xp, ldx, sp, lds, wp, ldw, wsp, _bias_ptr(bias, dt),
+                                            yp, ldy, y_mode, act, M, N, K, P, dt,
+                                            _stream(X, stream)))
+
+
+def tp_linear_row_quant(X, x_scale, W, w_scale, Y, P: int, mode: int = TP_ROW_SUM,
+                        workspace=None, bias=None, y_slices=None, y_slice_stride: int = 0,
+                        stream=None) -> None:
+    """Row-parallel Linear on int8 operands.  X int8 [M, K] with x_scale
+    float32 [M], [M, 1] or [M, P] (a scale for each token and shard); W int8
+    [N, K] with w_scale float32 [N]; the rest as in tp_linear_row_ex (Y or
+    y_slices bfloat16 or float32; float32 [P, M, N] for TP_ROW_PARTIAL)."""
+    _check_p(P)
+    xp, M, K, ldx = _int8_mat(X, "X")
+    wp, N, Kw, ldw = _int8_mat(W, "W")
+    if Kw != K:
+        raise ValueError(f"X has K={K} but W has K={Kw}")
+    sp, lds, G = _token_scales(x_scale, M, (1, P), "x_scale")
+    wsp = _channel_scales(w_scale, N, "w_scale")
+    if bias is not None:
+        _expect_shape(bias, (N,), "bias")
+    ys = None
+    if y_slices is not None:
+        if Y is not None:
+            raise ValueError("give Y or y_slices, not both")
+        if len(y_slices) != P:
+            raise ValueError(f"y_slices must hold P={P} tensors")
+        if M % P:
+            check(TP_ERR_INDIVISIBLE)
+        _, _, _, ldy = _mat(y_slices[0], "y_slices[0]")
+        dt = _dtype_code(y_slices[0])
+        for j, t in enumerate(y_slices):
+            _, mj, nj, lj = _mat(t, f"y_slices[{j}]")
+            if (mj, nj) != (M // P, N) or (mj > 1 and lj != ldy) or _dtype_code(t) != dt:
+                raise ValueError("y_slices must be [M/P, N] of one dtype and row stride")
+        yp, ys = None, _ptr_array(y_slices, "y_slices")
+    elif mode == TP_ROW_PARTIAL:
+        import torch
+        if Y.dtype != torch.float32:
+            raise ValueError("Y must be float32 [P, M, N] for TP_ROW_PARTIAL")
+        dt = TP_F32
+        yp, ldy = _block_out(Y, P, M, N)
+    else:
+        dt = _dtype_code(Y)
+        yp, ldy = _scatter_out(Y, M, N, P, mode == TP_ROW_SCATTER, y_slice_stride)
+    if workspace is not None:
+        wkp, wkb = workspace.data_ptr(), workspace.numel() * workspace.element_size()
+    else:
+        wkp, wkb = None, 0
+    _same_gpu(X, x_scale, W, w_scale, Y, workspace, bias, y_slices)
+    check(_get_lib().tp_linear_row_quant(xp, ldx, sp, lds, G, wp, ldw, wsp, _bias_ptr(bias, dt),
+                                         yp, ys, ldy, y_slice_stride, mode, wkp, wkb, M, N, K, P,
+                                         dt, _stream(X, stream)))
+
+
+# ---- heads of a fused QKV layer -------------------------------------------
+
+def _qkv(X, P, Hq, Hkv, x_mode, name):
+    """(pointer, row stride, T, D) of a fused QKV layer's output: [T, N] or
+    [P, T, N/P], N = (Hq + 2 Hkv) D."""
+    _check_p(P)
+    if Hq < 0 or Hkv < 0 or Hq + Hkv < 1:
+        raise ValueError(f"Hq={Hq} and Hkv={Hkv} heads: at least one head is needed")
+    if Hq % P or Hkv % P:
+        check(TP_ERR_INDIVISIBLE)
+    shards = x_mode == TP_Y_SHARDS
+    if X.dim() != (3 if shards else 2) or (shards and X.shape[0] != P):
+        raise ValueError(f"{name} must be [T, N], or [P, T, N/P] with TP_Y_SHARDS, got "
+                         f"{tuple(X.shape)}")
+    T, cols = X.shape[-2], X.shape[-1]
+    heads = (Hq + 2 * Hkv) // (P if shards else 1)
+    if cols == 0 or cols % heads:
+        raise ValueError(f"{name} has {cols} columns: not a multiple of its {heads} heads")
+    if shards:
+        xp, ld = _block_out(X, P, T, cols, name)
+    else:
+        xp, _, _, ld = _mat(X, name)
+    return xp, ld, T, cols // heads
+
+
+def _rows(t, T, cols, dt, name):
+    """(pointer, row stride) of a [T, cols] tensor of dtype code dt, or of
+    none."""
+    if t is None:
+        return None, 0
+    p, _, _, ld = _mat(t, name)
+    _expect_shape(t, (T, cols), name)
+    if _dtype_code(t) != dt:
+        raise TypeError(f"{name} must have the dtype of the QKV matrix")
+    return p, ld
+
+
+def _rotation(cos, sin, q_weight, k_weight, D, dt, eps, style):
+    """The rotation's and norms' arguments in the order of the C calls."""
+    import torch
+    if (cos is None) != (sin is None):
+        raise ValueError("give both cos and sin, or neither")
+    n_pos = R = 0
+    if cos is not None:
+        for t, name in ((cos, "cos"), (sin, "sin")):
+            if t.dtype != torch.float32 or t.dim() != 2 or not t.is_contiguous():
+                raise ValueError(f"{name} must be a contiguous float32 [n_pos, R/2] tensor")
+        _expect_shape(sin, cos.shape, "sin")
+        n_pos, R = cos.shape[0], 2 * cos.shape[1]
+    for t, name in ((q_weight, "q_weight"), (k_weight, "k_weight")):
+        if t is not None:
+            _expect_shape(t, (D,), name)
+            if D > 1 and t.stride(0) != 1:
+                raise ValueError(f"{name} must be a contiguous 1-D tensor")
+            if _dtype_code(t) != dt:
+                raise TypeError(f"{name} must have the dtype of the QKV matrix")
+    return (None if cos is None else cos.data_ptr(), None if sin is None else sin.data_ptr(),
+            n_pos, R, style, None if q_weight is None else q_weight.data_ptr(),
+            None if k_weight is None else k_weight.data_ptr(), eps)
+
+
+def _positions(pos, T, R):
+    import torch
+    if pos is None:
+        if R:
+            raise ValueError("pos is needed where heads are rotated")
+        return None
+    if pos.dtype != torch.int64 or pos.dim() != 1 or (T > 1 and pos.stride(0) != 1):
+        raise ValueError("pos must be a contiguous int64 [T] tensor")
+    _expect_shape(pos, (T,), "pos")
+    return pos.data_ptr()
+
+
+def _flag(bad):
+    import torch
+    if bad is None:
+        return None
+    if bad.dtype != torch.int32 or bad.numel() < 1:
+        raise ValueError("bad must be an int32 tensor")
+    return bad.data_ptr()
+
+
+def tp_qk_norm_rope(X, pos, cos, sin, Q, K, P: int, Hq: int, Hkv: int, q_weight=None,
+                    k_weight=None, eps: float = 1e-6, style: int = TP_ROPE_HALVES,
+                    x_mode: int = TP_Y_CONCAT, bad=None, stream=None) -> None:
+    """Norm and rotation of the query and key heads of a fused QKV layer's
+    output X ([T, N], or [P, T, N/P] with x_mode TP_Y_SHARDS).  pos int64 [T];
+    cos, sin float32 [n_pos, R/2] (None: no rotation); q_weight, k_weight [D]
+    (None: no norm); Q [T, Hq*D] and K [T, Hkv*D], either may be None.  A
+    position outside the table gives zero rows and sets bad (int32)."""
+    xp, ldx, T, D = _qkv(X, P, Hq, Hkv, x_mode, "X")
+    dt = _dtype_code(X)
+    rot = _rotation(cos, sin, q_weight, k_weight, D, dt, eps, style)
+    pp = _positions(pos, T, rot[3])
+    qp, ldq = _rows(Q, T, Hq * D, dt, "Q")
+    kp, ldk = _rows(K, T, Hkv * D, dt, "K")
+    _same_gpu(X, pos, cos, sin, Q, K, q_weight, k_weight, bad)
+    check(_get_lib().tp_qk_norm_rope(xp, ldx, x_mode, pp, *rot, qp, ldq, kp, ldk, T, Hq, Hkv, D, P,
+                                     dt, _flag(bad), _stream(X, stream)))
+
+
+def tp_qk_norm_rope_workspace_bytes(T: int, D: int) -> int:
+    return int(_get_lib().tp_qk_norm_rope_workspace_bytes(T, D))
+
+
+def tp_qk_norm_rope_backward(X, pos, cos, sin, dQ, dK, dX, P: int, Hq: int, Hkv: int, dV=None,
+                             q_weight=None, k_weight=None, dq_weight=None, dk_weight=None,
+                             workspace=None, eps: float = 1e-6, style: int = TP_ROPE_HALVES,
+                             x_mode: int = TP_Y_CONCAT, bad=None, stream=None) -> None:
+    """Gradients of tp_qk_norm_rope: dX (the layout of X) from dQ [T, Hq*D], dK
+    and dV [T, Hkv*D] (dV is copied into the value features; a part whose
+    gradient is None is left as it is), and the weights' gradients dq_weight,
+    dk_weight (float32 [D], or None), which need a workspace of
+    tp_qk_norm_rope_workspace_bytes(T, D).  X may be None without a norm."""
+    import torch
+    dxp, lddx, T, D = _qkv(dX, P, Hq, Hkv, x_mode, "dX")
+    dt = _dtype_code(dX)
+    xp, ldx = None, lddx
+    if X is not None:
+        xp, ldx, _, _ = _qkv(X, P, Hq, Hkv, x_mode, "X")
+        _expect_shape(X, dX.shape, "X")
+        if _dtype_code(X) != dt:
+            raise TypeError("X and dX must share one dtype")
+    rot = _rotation(cos, sin, q_weight, k_weight, D, dt, eps, style)
+    pp = _positions(pos, T, rot[3])
+    qp, ldq = _rows(dQ, T, Hq * D, dt, "dQ")
+    kp, ldk = _rows(dK, T, Hkv * D, dt, "dK")
+    vp, ldv = _rows(dV, T, Hkv * D, dt, "dV")
+    for t, name in ((dq_weight, "dq_weight"), (dk_weight, "dk_weight")):
+        if t is not None:
+            _expect_shape(t, (D,), name)
+            if t.dtype != torch.float32 or (D > 1 and t.stride(0) != 1):
+                raise ValueError(f"{name} must be a contiguous float32 [D] tensor")
+    if workspace is not None:
+        wkp, wkb = workspace.data_ptr(), workspace.numel() * workspace.element_size()
+    else:
+        wkp, wkb = None, 0
+    _same_gpu(X, pos, cos, sin, dQ, dK, dV, dX, q_weight, k_weight, dq_weight, dk_weight,
+              workspace, bad)
+    check(_get_lib().tp_qk_norm_rope_backward(
+        xp, ldx, x_mode, pp, *rot, qp, ldq, kp, ldk, vp, ldv, dxp, lddx,
+        None if dq_weight is None else dq_weight.data_ptr(),
+        None if dk_weight is None else dk_weight.data_ptr(), wkp, wkb, T, Hq, Hkv, D, P, dt,
+        _flag(bad), _stream(dX, stream)))
+
+
+def tp_kv_append(X, cos, sin, past, cu, table, k_cache, v_cache, P: int, Hq: int, Hkv: int,
+                 Q=None, q_weight=None, k_weight=None, eps: float = 1e-6,
+                 style: int = TP_ROPE_HALVES, x_mode: int = TP_Y_CONCAT, bad=None,
+                 stream=None) -> None:
+    """Append the keys (normed, rotated) and values of a fused QKV layer's
+    output X to a paged cache, and with Q ([T, Hq*D]) write the queries.
+    past int32 [B], cu int32 [B + 1], table int32 [B, max_pages]; k_cache and
+    v_cache [n_pages, page_size, Hkv, D] views of one set of strides with
+    contiguous features (a permuted view gives another order in memory)."""
+    import torch
+    xp, ldx, T, D = _qkv(X, P, Hq, Hkv, x_mode, "X")
+    dt = _dtype_code(X)
+    rot = _rotation(cos, sin, q_weight, k_weight, D, dt, eps, style)
+    if past.dim() != 1 or table.dim() != 2:
+        raise ValueError("past must be [B] and table [B, max_pages]")
+    B = past.shape[0]
+    for t, shape, name in ((past, (B,), "past"), (cu, (B + 1,), "cu"),
+                           (table, (B, table.shape[1]), "table")):
+        _expect_shape(t, shape, name)
+        if t.dtype != torch.int32 or (t.shape[-1] > 1 and t.stride(-1) != 1):
+            raise ValueError(f"{name} must be int32 with unit stride")
+    _, _, max_pages, ldt = _mat(table, "table")
+    if k_cache.dim() != 4:
+        raise ValueError("k_cache must be [n_pages, page_size, Hkv, D]")
+    pages, size = k_cache.shape[:2]
+    for t, name in ((k_cache, "k_cache"), (v_cache, "v_cache")):
+        _expect_shape(t, (pages, size, Hkv, D), name)
+        if _dtype_code(t) != dt:
+            raise TypeError(f"{name} must have the dtype of the QKV matrix")
+        if D > 1 and t.stride(3) != 1:
+            raise ValueError(f"{name} must have contiguous features")
+    if k_cache.stride() != v_cache.stride():
+        raise ValueError("k_cache and v_cache must have the same strides")
+    qp, ldq = _rows(Q, T, Hq * D, dt, "Q")
+    _same_gpu(X, cos, sin, past, cu, table, k_cache, v_cache, Q, q_weight, k_weight, bad)
+    check(_get_lib().tp_kv_append(
+        xp, ldx, x_mode, *rot, cu.data_ptr(), past.data_ptr(), B, table.data_ptr(), ldt, max_pages,
+        k_cache.data_ptr(), v_cache.data_ptr(), pages, size, k_cache.stride(0), k_cache.stride(1),
+        k_cache.stride(2), qp, ldq, T, Hq, Hkv, D, P, dt, _flag(bad), _stream(X, stream)))

@@ -1,0 +1,604 @@
+// Per-head steps on a fused QKV column layer's output ("模型并行", "Tensor
+// Parallel": the column split of the QKV weight gives each shard whole heads, so
+// these need no exchange): the root-mean-square norm of each query and key head
+// with the rotation of its pairs by the token's position in the same pass, the
+// append of keys and values to a paged cache, and the gradients.
+//
+//   y = x rsqrt(mean(x^2) + eps) w          (without a weight: y = x)
+//   pair j < R/2: (a, b) = (y[j], y[j + R/2]), or (y[2j], y[2j + 1]) with `pairs`
+//   out = (a cos - b sin, b cos + a sin); elements from R on pass through
+// and backwards, with g the gradient turned back by the same angle, r the
+// reciprocal root and n = x r:
+//   dw = sum over tokens and heads of g n;  h = g w;  dx = r (h - n mean(h n)).
+// All in fp32, one rounding to the output's type.
+//
+// Bound by memory: each value is read and written once, the angles come from a
+// table (cosines and sines of a far position need more than fp32 angles).  A
+// lane owns 16 values of a head as two 16- (bf16) or 32-byte runs that hold
+// both halves of its pairs, so the rotation stays in the lane; D / 16 lanes
+// (rounded up to a power of two) share a head, and the norm's sum crosses only
+// them.  A wavefront takes several heads of ONE token, so that a token's 16
+// cosines and sines are loaded once per lane and used for every head: for 72
+// heads of 128 the table's bytes would otherwise double the load instructions.
+// With few tokens the heads of a token are spread over more wavefronts.
+#include "heads.h"
+#include "kernels.h"
+
+namespace tpl {
+namespace {
+
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+
+constexpr int HT = 256;
+
+// 8 consecutive values (16-byte aligned).
+template <int ES>
+__device__ __forceinline__ void get8(const void *p, int64_t i, float *v) {
+    if (ES == 2) {
+        const u32x4 h = *(const u32x4 *)((const uint16_t *)p + i);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            v[2 * e] = __uint_as_float(h[e] << 16);
+            v[2 * e + 1] = __uint_as_float(h[e] & 0xFFFF0000u);
+        }
+    } else {
+        const u32x4 a = *(const u32x4 *)((const float *)p + i), b = *(const u32x4 *)((const float *)p + i + 4);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) { v[e] = __uint_as_float(a[e]); v[4 + e] = __uint_as_float(b[e]); }
+    }
+}
+
+template <int ES>
+__device__ __forceinline__ void put8(void *p, int64_t i, const float *v) {
+    if (ES == 2) {
+        typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
+        bf16x8 h;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) h[e] = (__bf16)v[e];
+        *(bf16x8 *)((uint16_t *)p + i) = h;
+    } else {
+        u32x4 a, b;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) { a[e] = __float_as_uint(v[e]); b[e] = __float_as_uint(v[4 + e]); }
+        *(u32x4 *)((float *)p + i) = a;
+        *(u32x4 *)((float *)p + i + 4) = b;
+    }
+}
+
+template <int ES>
+__device__ __forceinline__ float get1(const void *p, int64_t i) {
+    return ES == 2 ? (float)((const __bf16 *)p)[i] : ((const float *)p)[i];
+}
+template <int ES>
+__device__ __forceinline__ void put1(void *p, int64_t i, float v) {
+    if (ES == 2) ((__bf16 *)p)[i] = (__bf16)v;
+    else ((float *)p)[i] = v;
+}
+
+enum { HEAD_Q = 0, HEAD_K = 1, HEAD_V = 2 };
+
+// Where a token goes: its position and, for the append, the element offset of
+// its slot.  ok: the position is in the table (and the slot in the cache).
+struct Place { int64_t pos, slot; bool mine, ok; };
+
+// Token t's sequence by a 64-way search of cu, its position, page and slot.
+// mine: some sequence owns the token.  Nothing read from the caller's arrays is
+// used as an index before it is checked.
+__device__ __forceinline__ Place find_place(const HeadArgs &a, int64_t t, int lane) {
+    Place p{0, 0, false, false};
+    // the number of sequences s in [0, B) with cu[s] <= t, for non-decreasing cu
+    int64_t lo = 0, n = a.B;
+    while (n > 0) {
+        const int64_t step = (n + 63) / 64;
+        const int64_t i = lo + lane * step;
+        const bool below = lane * step < n && a.cu[i] <= t;
+        const int c = __popcll(__ballot(below));
+        if (c == 0) { n = 0; break; }
+        const int64_t base = (int64_t)(c - 1) * step;      // the last such probe
+        lo += base + 1;
+        n = (n - base < step ? n - base : step) - 1;
+    }
+    const int64_t s = lo - 1;
+    if (s < 0) return p;
+    if (t >= a.cu[s + 1]) return p;
+    p.mine = true;
+    p.pos = (int64_t)a.past[s] + (t - a.cu[s]);
+    if (p.pos < 0 || p.pos >= a.max_pages * a.page || (a.R > 0 && p.pos >= a.n_pos)) return p;
+    const int64_t pg = p.pos / a.page;
+    const int64_t id = a.table[s * a.ldt + pg];
+    if (id < 0 || id >= a.n_pages) return p;
+    p.slot = id * a.s_page + (p.pos - pg * a.page) * a.s_slot;
+    p.ok = true;
+    return p;
+}
+
+__device__ __forceinline__ Place given_place(const HeadArgs &a, int64_t t) {
+    Place p{0, 0, true, true};
+    if (a.R > 0) {
+        p.pos = a.pos[t];
+        p.ok = p.pos >= 0 && p.pos < a.n_pos;
+    }
+    return p;
+}
+
+// Lane's two runs of 8 values inside a head: the pairs' halves where it
+// rotates, 16 consecutive values else.
+struct Runs { int a, b; bool on, turn; };
+__device__ __forceinline__ Runs runs_of(int unit, int D, int R, int pairs) {
+    Runs r;
+    r.on = unit * 16 < D;
+    r.turn = unit * 16 < R;
+    r.a = r.turn && !pairs ? unit * 8 : unit * 16;
+    r.b = r.turn && !pairs ? R / 2 + unit * 8 : unit * 16 + 8;
+    return r;
+}
+
+// The rotation of a lane's pairs by +angle (back: by -angle).
+__device__ __forceinline__ void turn16(float *v, const float *c, const float *s, bool pairs, bool back) {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+        const int ia = pairs ? 2 * e : e, ib = pairs ? 2 * e + 1 : e + 8;
+        const float x = v[ia], y = v[ib], sn = back ? -s[e] : s[e];
+        v[ia] = x * c[e] - y * sn;
+        v[ib] = y * c[e] + x * sn;
+    }
+}
+
+__device__ __forceinline__ float lanes_sum(float v, int width) {
+    for (int o = width >> 1; o > 0; o >>= 1) v += __shfl_xor(v, o);
+    return v;
+}
+
+// The heads of a shard that a call handles, of its hq q, hk k and hk v heads in
+// the order of X: `per` of them from `first` on.
+struct Span { int first, per; };
+__device__ __host__ __forceinline__ Span span_of(const HeadArgs &a, bool q, bool k, bool v) {
+    const int first = q ? 0 : k ? a.hq : a.hq + a.hk;
+    return Span{first, (v ? a.hq + 2 * a.hk : k ? a.hq + a.hk : a.hq) - first};
+}
+
+// Slot s of a token's heads: shard, then the heads of the span.
+struct Head { int kind, head, shard, col; bool on; };
+__device__ __forceinline__ Head head_of(const HeadArgs &a, int slot, const Span &sp, int slots) {
+    Head h;
+    h.on = slot < slots;
+    h.shard = (h.on ? slot : 0) / sp.per;
+    const int j = (h.on ? slot : 0) - h.shard * sp.per + sp.first;
+    h.kind = j < a.hq ? HEAD_Q : j < a.hq + a.hk ? HEAD_K : HEAD_V;
+    h.head = h.kind == HEAD_Q ? h.shard * a.hq + j
+                              : h.shard * a.hk + (j - a.hq - (h.kind == HEAD_V ? a.hk : 0));
+    h.col = j * a.D;
+    return h;
+}
+
+// LH: lanes per head.  One wavefront per (token, part): part p of `parts`
+// takes the groups of 64 / LH heads p, p + parts, ...
+template <int ES, int LH, bool APPEND>
+__global__ __launch_bounds__(HT)
+void heads_vec(HeadArgs a, int parts) {
+    const int lane = threadIdx.x & 63;
+    const int64_t w = (int64_t)blockIdx.x * (HT / 64) + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    if (w >= a.T * parts) return;
+    const int64_t t = w / parts;
+    const int part = (int)(w - t * parts);
+    const Place pl = APPEND ? find_place(a, t, lane) : given_place(a, t);
+    if (!pl.ok && pl.mine && a.bad && lane == 0) *a.bad = 1;
+    if (APPEND && !pl.mine) return;
+    const int unit = lane % LH;
+    const Runs r = runs_of(unit, a.D, a.R, a.pairs);
+    float c[8], s[8], wq[16] = {}, wk[16] = {};
+    if (r.on && r.turn && pl.ok) {
+        get8<4>(a.cos, pl.pos * (a.R / 2) + unit * 8, c);
+        get8<4>(a.sin, pl.pos * (a.R / 2) + unit * 8, s);
+    }
+    if (a.wq && r.on) { get8<ES>(a.wq, r.a, wq); get8<ES>(a.wq, r.b, wq + 8); }
+    if (a.wk && r.on) { get8<ES>(a.wk, r.a, wk); get8<ES>(a.wk, r.b, wk + 8); }
+    const Span sp = span_of(a, a.Q != nullptr, APPEND || a.K, APPEND);
+    const int slots = sp.per * a.P;
+    constexpr int HW = 64 / LH;
+    for (int g = part * HW; g < slots; g += parts * HW) {
+        const Head h = head_of(a, g + lane / LH, sp, slots);
+        const bool live = h.on && r.on;
+        float v[16];
+#pragma unroll
+        for (int e = 0; e < 16; ++e) v[e] = 0.0f;
+        if (live && pl.ok) {
+            const int64_t x = h.shard * a.x_shard + t * a.ldx + h.col;
+            get8<ES>(a.X, x + r.a, v);
+            get8<ES>(a.X, x + r.b, v + 8);
+        }
+        const void *wt = h.kind == HEAD_Q ? a.wq : a.wk;
+        if (a.wq || a.wk) {
+            float sum = 0.0f;
+#pragma unroll
+            for (int e = 0; e < 16; ++e) sum = __builtin_fmaf(v[e], v[e], sum);
+            sum = lanes_sum(sum, LH);
+            if (h.kind != HEAD_V && wt && pl.ok) {   // a token without a place stays zero, whatever eps is
+                const float rr = rsqrtf(sum / (float)a.D + a.eps);
+#pragma unroll
+                for (int e = 0; e < 16; ++e) v[e] = v[e] * rr * (h.kind == HEAD_Q ? wq[e] : wk[e]);
+            }
+        }
+        if (r.turn && h.kind != HEAD_V && pl.ok) {
+            if (a.pairs) turn16(v, c, s, true, false);
+            else turn16(v, c, s, false, false);
+        }
+        if (!live) continue;
+        if (h.kind == HEAD_Q) {
+            if (a.Q) {
+                put8<ES>(a.Q, t * a.ldq + (int64_t)h.head * a.D + r.a, v);
+                put8<ES>(a.Q, t * a.ldq + (int64_t)h.head * a.D + r.b, v + 8);
+            }
+        } else if (APPEND) {
+            if (pl.ok) {
+                void *dst = h.kind == HEAD_K ? a.kc : a.vc;
+                put8<ES>(dst, pl.slot + h.head * a.s_head + r.a, v);
+                put8<ES>(dst, pl.slot + h.head * a.s_head + r.b, v + 8);
+            }
+        } else if (a.K) {
+            put8<ES>(a.K, t * a.ldk + (int64_t)h.head * a.D + r.a, v);
+            put8<ES>(a.K, t * a.ldk + (int64_t)h.head * a.D + r.b, v + 8);
+        }
+    }
+}
+
+// Position of pair j's two elements, or of the single elements from R on:
+// j counts R/2 pairs, then D - R singles (b < 0).
+__device__ __forceinline__ void pair_at(const HeadArgs &a, int j, int &x, int &y) {
+    if (j >= a.R / 2) { x = a.R + (j - a.R / 2); y = -1; return; }
+    x = a.pairs ? 2 * j : j;
+    y = a.pairs ? 2 * j + 1 : j + a.R / 2;
+}
+
+// Any D, R and alignment: a wavefront per (token, head), one element or pair a lane.
+template <int ES, bool APPEND>
+__global__ __launch_bounds__(HT)
+void heads_any(HeadArgs a) {
+    const int lane = threadIdx.x & 63;
+    const Span sp = span_of(a, a.Q != nullptr, APPEND || a.K, APPEND);
+    const int slots = sp.per * a.P;
+    const int64_t w = (int64_t)blockIdx.x * (HT / 64) + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    if (w >= a.T * slots) return;
+    const int64_t t = w / slots;
+    const Head h = head_of(a, (int)(w - t * slots), sp, slots);
+    const Place pl = APPEND ? find_place(a, t, lane) : given_place(a, t);
+    if (!pl.ok && pl.mine && a.bad && lane == 0) *a.bad = 1;
+    if (APPEND && !pl.mine) return;
+    void *dst; int64_t o;
+    if (h.kind == HEAD_Q) { dst = a.Q; o = t * a.ldq + (int64_t)h.head * a.D; }
+    else if (APPEND) { dst = pl.ok ? (h.kind == HEAD_K ? a.kc : a.vc) : nullptr; o = pl.slot + h.head * a.s_head; }
+    else { dst = a.K; o = t * a.ldk + (int64_t)h.head * a.D; }
+    if (!dst) return;
+    const int64_t x0 = h.shard * a.x_shard + t * a.ldx + h.col;
+    const void *wt = h.kind == HEAD_Q ? a.wq : h.kind == HEAD_K ? a.wk : nullptr;
+    float rr = 1.0f;
+    if (wt) {
+        float sum = 0.0f;
+        for (int d = lane; d < a.D; d += 64) { const float x = get1<ES>(a.X, x0 + d); sum = __builtin_fmaf(x, x, sum); }
+        rr = rsqrtf(lanes_sum(sum, 64) / (float)a.D + a.eps);
+    }
+    for (int j = lane; j < a.D - a.R / 2; j += 64) {
+        int ia, ib;
+        pair_at(a, j, ia, ib);
+        float x = 0.0f, y = 0.0f;
+        if (pl.ok) {
+            x = get1<ES>(a.X, x0 + ia);
+            if (ib >= 0) y = get1<ES>(a.X, x0 + ib);
+            if (wt) {
+                x = x * rr * get1<ES>(wt, ia);
+                if (ib >= 0) y = y * rr * get1<ES>(wt, ib);
+            }
+            if (ib >= 0 && h.kind != HEAD_V) {
+                const float c = a.cos[pl.pos * (a.R / 2) + j], s = a.sin[pl.pos * (a.R / 2) + j];
+                const float p = x * c - y * s, q = y * c + x * s;
+                x = p; y = q;
+            }
+        }
+        put1<ES>(dst, o + ia, x);
+        if (ib >= 0) put1<ES>(dst, o + ib, y);
+    }
+}
+
+// ---- gradients ---------------------------------------------------------------
+
+// As heads_vec; a wavefront walks the tokens w, w + waves, ..., keeping the
+// weights' gradient sums of its 16 values in registers; they are added over the
+// heads of a wavefront and the four wavefronts in a fixed order and left in
+// partials[block][kind][D], which a second kernel adds in block order: the
+// result does not depend on scheduling.
+template <int ES, int LH>
+__global__ __launch_bounds__(HT)
+void heads_backward_vec(HeadArgs a) {
+    __shared__ float red[4][2][LH * 16];
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int unit = lane % LH;
+    const Runs r = runs_of(unit, a.D, a.R, a.pairs);
+    float wq[16] = {}, wk[16] = {}, gq[16] = {}, gk[16] = {};
+    if (a.wq && r.on) { get8<ES>(a.wq, r.a, wq); get8<ES>(a.wq, r.b, wq + 8); }
+    if (a.wk && r.on) { get8<ES>(a.wk, r.a, wk); get8<ES>(a.wk, r.b, wk + 8); }
+    const Span sp = span_of(a, a.dQ != nullptr, a.dK != nullptr, a.dV != nullptr);
+    const int slots = sp.per * a.P;
+    constexpr int HW = 64 / LH;
+    for (int64_t t = (int64_t)blockIdx.x * (HT / 64) + wave; t < a.T; t += (int64_t)gridDim.x * (HT / 64)) {
+        const Place pl = given_place(a, t);
+        if (!pl.ok && a.bad && lane == 0) *a.bad = 1;
+        float c[8], s[8];
+        if (r.on && r.turn && pl.ok) {
+            get8<4>(a.cos, pl.pos * (a.R / 2) + unit * 8, c);
+            get8<4>(a.sin, pl.pos * (a.R / 2) + unit * 8, s);
+        }
+        for (int g = 0; g < slots; g += HW) {
+            const Head h = head_of(a, g + lane / LH, sp, slots);
+            const bool live = h.on && r.on;
+            const void *wt = h.kind == HEAD_Q ? a.wq : h.kind == HEAD_K ? a.wk : nullptr;
+            const void *dy = h.kind == HEAD_Q ? a.dQ : h.kind == HEAD_K ? a.dK : a.dV;
+            const int64_t ldy = h.kind == HEAD_Q ? a.lddq : h.kind == HEAD_K ? a.lddk : a.lddv;
+            float v[16], x[16];
+#pragma unroll
+            for (int e = 0; e < 16; ++e) v[e] = x[e] = 0.0f;
+            if (live && dy && (pl.ok || h.kind == HEAD_V)) {
+                const int64_t o = t * ldy + (int64_t)h.head * a.D;
+                get8<ES>(dy, o + r.a, v);
+                get8<ES>(dy, o + r.b, v + 8);
+                if (wt) {
+                    const int64_t xo = h.shard * a.x_shard + t * a.ldx + h.col;
+                    get8<ES>(a.X, xo + r.a, x);
+                    get8<ES>(a.X, xo + r.b, x + 8);
+                }
+            }
+            if (r.turn && h.kind != HEAD_V && pl.ok) {
+                if (a.pairs) turn16(v, c, s, true, true);
+                else turn16(v, c, s, false, true);
+            }
+            if (a.wq || a.wk) {
+                float sum = 0.0f, dot = 0.0f;
+#pragma unroll
+                for (int e = 0; e < 16; ++e) {
+                    sum = __builtin_fmaf(x[e], x[e], sum);
+                    dot = __builtin_fmaf(x[e], v[e] * (h.kind == HEAD_Q ? wq[e] : wk[e]), dot);
+                }
+                if (!wt) dot = 0.0f;
+                sum = lanes_sum(sum, LH);
+                dot = lanes_sum(dot, LH);
+                if (wt && live && pl.ok) {
+                    const float rr = rsqrtf(sum / (float)a.D + a.eps);
+                    const float mean = dot * rr / (float)a.D;
+#pragma unroll
+                    for (int e = 0; e < 16; ++e) {
+                        const float n = x[e] * rr;
+                        if (h.kind == HEAD_Q) gq[e] = __builtin_fmaf(v[e], n, gq[e]);
+                        else gk[e] = __builtin_fmaf(v[e], n, gk[e]);
+                        v[e] = rr * (v[e] * (h.kind == HEAD_Q ? wq[e] : wk[e]) - n * mean);
+                    }
+                }
+            }
+            if (live && dy) {
+                const int64_t o = h.shard * a.dx_shard + t * a.lddx + h.col;
+                put8<ES>(a.dX, o + r.a, v);
+                put8<ES>(a.dX, o + r.b, v + 8);
+            }
+        }
+    }
+    if (!a.partials) return;
+#pragma unroll
+    for (int e = 0; e < 16; ++e) {
+        float q = gq[e], k = gk[e];
+        for (int o = LH; o < 64; o <<= 1) { q += __shfl_xor(q, o); k += __shfl_xor(k, o); }
+        if (lane < LH) {
+            // the value's place in the head (units past D keep their own cells)
+            const int d = r.on ? (e < 8 ? r.a + e : r.b + e - 8) : unit * 16 + e;
+            red[wave][0][d] = q;
+            red[wave][1][d] = k;
+        }
+    }
+    __syncthreads();
+    for (int i = threadIdx.x; i < 2 * a.D; i += HT) {
+        const int kind = i / a.D, d = i - kind * a.D;
+        a.partials[(int64_t)blockIdx.x * 2 * a.D + i] =
+            ((red[0][kind][d] + red[1][kind][d]) + red[2][kind][d]) + red[3][kind][d];
+    }
+}
+
+// Any D, R and alignment: a wavefront per token, heads one after another; its
+// weight-gradient sums live in LDS (each lane its own elements).
+constexpr int ANY_D = 1024;   // largest head of the unaligned form
+template <int ES>
+__global__ __launch_bounds__(HT)
+void heads_backward_any(HeadArgs a) {
+    __shared__ float acc[4][2][ANY_D];
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int items = a.D - a.R / 2;
+    for (int d = lane; d < a.D; d += 64) acc[wave][0][d] = acc[wave][1][d] = 0.0f;
+    __syncthreads();
+    const Span sp = span_of(a, a.dQ != nullptr, a.dK != nullptr, a.dV != nullptr);
+    const int slots = sp.per * a.P;
+    for (int64_t t = (int64_t)blockIdx.x * (HT / 64) + wave; t < a.T; t += (int64_t)gridDim.x * (HT / 64)) {
+        const Place pl = given_place(a, t);
+        if (!pl.ok && a.bad && lane == 0) *a.bad = 1;
+        for (int g = 0; g < slots; ++g) {
+            const Head h = head_of(a, g, sp, slots);
+            const void *wt = h.kind == HEAD_Q ? a.wq : h.kind == HEAD_K ? a.wk : nullptr;
+            const void *dy = h.kind == HEAD_Q ? a.dQ : h.kind == HEAD_K ? a.dK : a.dV;
+            if (!dy) continue;
+            const int64_t ldy = h.kind == HEAD_Q ? a.lddq : h.kind == HEAD_K ? a.lddk : a.lddv;
+            const int64_t y0 = t * ldy + (int64_t)h.head * a.D, x0 = h.shard * a.x_shard + t * a.ldx + h.col;
+            const int64_t o = h.shard * a.dx_shard + t * a.lddx + h.col;
+            const bool in = pl.ok || h.kind == HEAD_V;
+            // element or pair j's gradient, turned back
+            auto grad = [&](int j, int &ia, int &ib, float &p, float &q) {
+                pair_at(a, j, ia, ib);
+                p = in ? get1<ES>(dy, y0 + ia) : 0.0f;
+                q = in && ib >= 0 ? get1<ES>(dy, y0 + ib) : 0.0f;
+                if (ib >= 0 && h.kind != HEAD_V && pl.ok) {
+                    const float c = a.cos[pl.pos * (a.R / 2) + j], s = a.sin[pl.pos * (a.R / 2) + j];
+                    const float u = p * c + q * s, v = q * c - p * s;
+                    p = u; q = v;
+                }
+            };
+            float rr = 1.0f, mean = 0.0f;
+            if (wt && in) {
+                float sum = 0.0f, dot = 0.0f;
+                for (int j = lane; j < items; j += 64) {
+                    int ia, ib;
+                    float p, q;
+                    grad(j, ia, ib, p, q);
+                    const float x = get1<ES>(a.X, x0 + ia), y = ib >= 0 ? get1<ES>(a.X, x0 + ib) : 0.0f;
+                    sum = __builtin_fmaf(x, x, __builtin_fmaf(y, y, sum));
+                    dot = __builtin_fmaf(x, p * get1<ES>(wt, ia), dot);
+                    if (ib >= 0) dot = __builtin_fmaf(y, q * get1<ES>(wt, ib), dot);
+                }
+                rr = rsqrtf(lanes_sum(sum, 64) / (float)a.D + a.eps);
+                mean = lanes_sum(dot, 64) * rr / (float)a.D;
+            }
+            for (int j = lane; j < items; j += 64) {
+                int ia, ib;
+                float p, q;
+                grad(j, ia, ib, p, q);
+                if (wt && in) {
+                    const float x = get1<ES>(a.X, x0 + ia) * rr;
+                    acc[wave][h.kind][ia] += p * x;
+                    p = rr * (p * get1<ES>(wt, ia) - x * mean);
+                    if (ib >= 0) {
+                        const float y = get1<ES>(a.X, x0 + ib) * rr;
+                        acc[wave][h.kind][ib] += q * y;
+                        q = rr * (q * get1<ES>(wt, ib) - y * mean);
+                    }
+                }
+                put1<ES>(a.dX, o + ia, p);
+                if (ib >= 0) put1<ES>(a.dX, o + ib, q);
+            }
+        }
+    }
+    if (!a.partials) return;
+    __syncthreads();
+    for (int i = threadIdx.x; i < 2 * a.D; i += HT) {
+        const int kind = i / a.D, d = i - kind * a.D;
+        a.partials[(int64_t)blockIdx.x * 2 * a.D + i] =
+            ((acc[0][kind][d] + acc[1][kind][d]) + acc[2][kind][d]) + acc[3][kind][d];
+    }
+}
+
+// dw[kind][d] = sum over blocks of partials[block][kind][d]: 16 columns by 16
+// strands of blocks a workgroup, each strand in block order, then the strands.
+__global__ __launch_bounds__(HT)
+void weight_grad_sum(const float *partials, int64_t blocks, int D, float *dwq, float *dwk) {
+    __shared__ float red[16][17];
+    const int col = blockIdx.x * 16 + (threadIdx.x & 15), strand = threadIdx.x >> 4;
+    float s = 0.0f;
+    if (col < 2 * D)
+        for (int64_t b = strand; b < blocks; b += 16) s += partials[b * 2 * D + col];
+    red[strand][threadIdx.x & 15] = s;
+    __syncthreads();
+    if (threadIdx.x < 16 && col < 2 * D) {
+        float v = red[0][threadIdx.x];
+#pragma unroll
+        for (int i = 1; i < 16; ++i) v += red[i][threadIdx.x];
+        float *dw = col < D ? dwq : dwk;
+        if (dw) dw[col < D ? col : col - D] = v;
+    }
+}
+
+inline bool al16(const void *p) { return ((uintptr_t)p & 15u) == 0; }
+
+// Whether the 16-values-a-lane form takes the call.
+template <int ES>
+bool vec_ok(const HeadArgs &a, bool append, bool backward) {
+    auto st = [](int64_t v) { return v * ES % 16 == 0; };
+    if (a.D % 16 || a.R % 16 || a.D > 512) return false;
+    if (!(al16(a.X) && st(a.ldx) && st(a.x_shard) && al16(a.cos) && al16(a.sin) && al16(a.wq) && al16(a.wk))) return false;
+    if (backward)
+        return al16(a.dQ) && al16(a.dK) && al16(a.dV) && st(a.lddq) && st(a.lddk) && st(a.lddv) &&
+               al16(a.dX) && st(a.lddx) && st(a.dx_shard);
+    if (!(al16(a.Q) && st(a.ldq))) return false;
+    if (append) return al16(a.kc) && al16(a.vc) && st(a.s_page) && st(a.s_slot) && st(a.s_head);
+    return al16(a.K) && st(a.ldk);
+}
+
+int lanes_per_head(int D) {
+    int l = 1;
+    while (l * 16 < D) l <<= 1;
+    return l;
+}
+
+template <int ES, int LH, bool APPEND>
+hipError_t launch_vec(const HeadArgs &a, hipStream_t s) {
+    const int64_t slots = (int64_t)span_of(a, a.Q != nullptr, APPEND || a.K, APPEND).per * a.P, hw = 64 / LH;
+    const int64_t groups = (slots + hw - 1) / hw;
+    // Enough wavefronts to fill the chip (32 for each of 256 CUs), else one
+    // wavefront a token, which loads its angles and weights once.
+    int64_t parts = (8192 + a.T - 1) / a.T;
+    if (parts > groups) parts = groups;
+    const int64_t blocks = (a.T * parts + HT / 64 - 1) / (HT / 64);
+    if (blocks > 0x7FFFFFFFll) return hipErrorInvalidConfiguration;
+    heads_vec<ES, LH, APPEND><<<dim3((unsigned)blocks), dim3(HT), 0, s>>>(a, (int)parts);
+    return hipGetLastError();
+}
+
+template <int ES, bool APPEND>
+hipError_t launch_fwd(const HeadArgs &a, hipStream_t s) {
+    const Span sp = span_of(a, a.Q != nullptr, APPEND || a.K, APPEND);
+    if (a.T == 0 || sp.per == 0) return hipSuccess;
+    if (!vec_ok<ES>(a, APPEND, false)) {
+        const int64_t waves = a.T * (int64_t)sp.per * a.P;
+        const int64_t blocks = (waves + HT / 64 - 1) / (HT / 64);
+        if (blocks > 0x7FFFFFFFll) return hipErrorInvalidConfiguration;
+        heads_any<ES, APPEND><<<dim3((unsigned)blocks), dim3(HT), 0, s>>>(a);
+        return hipGetLastError();
+    }
+    switch (lanes_per_head(a.D)) {
+        case 1: return launch_vec<ES, 1, APPEND>(a, s);
+        case 2: return launch_vec<ES, 2, APPEND>(a, s);
+        case 4: return launch_vec<ES, 4, APPEND>(a, s);
+        case 8: return launch_vec<ES, 8, APPEND>(a, s);
+        case 16: return launch_vec<ES, 16, APPEND>(a, s);
+        default: return launch_vec<ES, 32, APPEND>(a, s);
+    }
+}
+
+template <int ES>
+hipError_t launch_bwd(const HeadArgs &a, hipStream_t s) {
+    if (a.D > ANY_D) return hipErrorInvalidValue;
+    const int64_t blocks = qk_backward_blocks(a.T);
+    const bool any = a.T > 0 && span_of(a, a.dQ != nullptr, a.dK != nullptr, a.dV != nullptr).per > 0;
+    if (any) {
+        const dim3 grid((unsigned)blocks), block(HT);
+        if (!vec_ok<ES>(a, false, true)) heads_backward_any<ES><<<grid, block, 0, s>>>(a);
+        else switch (lanes_per_head(a.D)) {
+            case 1: heads_backward_vec<ES, 1><<<grid, block, 0, s>>>(a); break;
+            case 2: heads_backward_vec<ES, 2><<<grid, block, 0, s>>>(a); break;
+            case 4: heads_backward_vec<ES, 4><<<grid, block, 0, s>>>(a); break;
+            case 8: heads_backward_vec<ES, 8><<<grid, block, 0, s>>>(a); break;
+            case 16: heads_backward_vec<ES, 16><<<grid, block, 0, s>>>(a); break;
+            default: heads_backward_vec<ES, 32><<<grid, block, 0, s>>>(a); break;
+        }
+        const hipError_t e = hipGetLastError();
+        if (e != hipSuccess) return e;
+    }
+    if (a.dwq || a.dwk) {
+        const int64_t n = any ? blocks : 0;   // no tokens: zero gradients
+        weight_grad_sum<<<dim3((unsigned)((2 * a.D + 15) / 16)), dim3(HT), 0, s>>>(a.partials, n, a.D, a.dwq, a.dwk);
+    }
+    return hipGetLastError();
+}
+
+}  // namespace
+
+// One wavefront a token up to 512 workgroups, then more tokens each.
+int64_t qk_backward_blocks(int64_t T) {
+    const int64_t b = (T + HT / 64 - 1) / (HT / 64);
+    return b < 1 ? 1 : b > 512 ? 512 : b;
+}
+
+hipError_t launch_qk_norm_rope(const HeadArgs &a, int es, hipStream_t s) {
+    return es == 2 ? launch_fwd<2, false>(a, s) : launch_fwd<4, false>(a, s);
+}
+
+hipError_t launch_kv_append(const HeadArgs &a, int es, hipStream_t s) {
+    return es == 2 ? launch_fwd<2, true>(a, s) : launch_fwd<4, true>(a, s);
+}
+
+hipError_t launch_qk_norm_rope_backward(const HeadArgs &a, int es, hipStream_t s) {
+    return es == 2 ? launch_bwd<2>(a, s) : launch_bwd<4>(a, s);
+}
+
+}  // namespace tpl

@@ -1,0 +1,50 @@
+// Launch interface of the 8-bit integer Linear: the quantizer, the int8 shard
+// GEMMs and the fold of their int32 partials.  Internal, as kernels.h.
+#pragma once
+
+#include "kernels.h"
+
+namespace tpl {
+
+// Output of an int8 GEMM besides OUT_F32 / OUT_BF16: the int32 sums as they
+// are (a row layer's partials; no scales, bias or activation).
+constexpr int OUT_I32 = 2;
+
+// The scales of an int8 product.  Token m of shard i: x_scale[m * x_ld + i *
+// x_shard]; W row n of shard i: w_scale[i * w_shard + n].
+struct QuantArgs {
+    const float *x_scale; int64_t x_ld; int64_t x_shard;
+    const float *w_scale; int64_t w_shard;
+};
+
+// One output of an int8 product: the exact int32 sum, rounded once to fp32,
+// times the token's scale, then one fused multiply-add with the channel's
+// scale and the bias (0 without one).  Every kernel uses this, so results do
+// not depend on which kernel a shape takes.
+__device__ __forceinline__ float quant_value(int32_t acc, float sx, float sw, float bias) {
+    return __builtin_fmaf((float)acc * sx, sw, bias);
+}
+
+// Any shape, stride or alignment; every output type, bias and the gated unit.
+// GemmArgs counts elements (bytes of A and B); ex as for the bf16 kernels
+// (x_rows is not taken).
+hipError_t launch_quant_generic(const GemmArgs &g, int out_type, const GemmExtra &ex,
+                                const QuantArgs &q, hipStream_t s);
+
+// Rows of X to int8: scale[m * lds + j] for column group j of G.
+struct QuantizeArgs {
+    const void *X; int64_t ldx;
+    int8_t *Q; int64_t ldq;
+    float *scale; int64_t lds;
+    int64_t M, Kg; int32_t G;
+};
+hipError_t launch_quantize_rows(const QuantizeArgs &a, int in_type, hipStream_t s);
+
+// Fold of P int32 partials (r.partials, as int32) into the scaled output:
+// per_shard: S = fma chain of float(p_i) * x_scale[m * x_ld + i], ascending;
+// else S = float(sum of the p_i) * x_scale[m * x_ld].  Y = fma(S, w_scale[n],
+// bias[n] or 0), placed as launch_shard_fold places it.
+hipError_t launch_quant_fold(const ReduceArgs &r, const QuantArgs &q, bool per_shard, int out_type,
+                             hipStream_t s);
+
+}  // namespace tpl
