@@ -31,6 +31,13 @@ __device__ __forceinline__ float quant_value(int32_t acc, float sx, float sw, fl
 hipError_t launch_quant_generic(const GemmArgs &g, int out_type, const GemmExtra &ex,
                                 const QuantArgs &q, hipStream_t s);
 
+// Whether the DMA-fed int8 kernels can load g's operands with tiles of `rows`
+// rows: K, leading dims and shard offsets multiples of 16, 16-byte aligned.
+bool quant_dma_supported(const GemmArgs &g, const GemmExtra &ex, int rows);
+// 256 x 256 tiles; as launch_quant_generic otherwise.
+hipError_t launch_quant_tile(const GemmArgs &g, int out_type, const GemmExtra &ex,
+                             const QuantArgs &q, hipStream_t s);
+
 // Rows of X to int8: scale[m * lds + j] for column group j of G.
 struct QuantizeArgs {
     const void *X; int64_t ldx;

@@ -21,6 +21,7 @@ constexpr int64_t MAX_QUANT_K = 131071;
 
 hipError_t run_quant(const GemmArgs &g, int out, const GemmExtra &ex, const QuantArgs &q,
                      hipStream_t s) {
+    if (quant_dma_supported(g, ex, 256) && g.M > 128) return launch_quant_tile(g, out, ex, q, s);
     return launch_quant_generic(g, out, ex, q, s);
 }
 
