@@ -38,6 +38,17 @@ bool quant_dma_supported(const GemmArgs &g, const GemmExtra &ex, int rows);
 hipError_t launch_quant_tile(const GemmArgs &g, int out_type, const GemmExtra &ex,
                              const QuantArgs &q, hipStream_t s);
 
+// 256 x 128, 128 x 128 or 128 x 64 tiles, by their number.
+hipError_t launch_quant_narrow(const GemmArgs &g, int out_type, const GemmExtra &ex,
+                               const QuantArgs &q, hipStream_t s);
+
+// 256 x 128 tiles with the fold of the P shards in registers, a scale for each
+// token and shard (q.x_shard = 1); r places the output as in
+// launch_gemm_rowfold.
+bool quant_rowfold_supported(const GemmArgs &g, const ReduceArgs &r, const QuantArgs &q);
+hipError_t launch_quant_rowfold(const GemmArgs &g, const ReduceArgs &r, const QuantArgs &q,
+                                int out_type, hipStream_t s);
+
 // Rows of X to int8: scale[m * lds + j] for column group j of G.
 struct QuantizeArgs {
     const void *X; int64_t ldx;

@@ -1,0 +1,64 @@
+// Launch of the narrow tiles (gemm_narrow_impl.h) on int8 operands.
+#include "gemm_narrow_impl.h"
+
+namespace tpl {
+namespace {
+
+inline bool aligned16(const void *p) { return ((uintptr_t)p & 15u) == 0; }
+
+template <int OUT, int FM, int TN, bool SW>
+void launch_t(const GemmArgs &g, const NarrowSched &ts, int vec, const GemmExtra &ex, const QuantArgs &q,
+              int grid, hipStream_t s) {
+    if (g.K % 128)
+        gemm_narrow_kernel<OUT, FM, TN, SW, OpI8, true><<<dim3(grid), dim3(FM * 2), 0, s>>>(g, ts, ex.bias, ex.bias_shard, vec, ex.up_off, q);
+    else
+        gemm_narrow_kernel<OUT, FM, TN, SW, OpI8, false><<<dim3(grid), dim3(FM * 2), 0, s>>>(g, ts, ex.bias, ex.bias_shard, vec, ex.up_off, q);
+}
+
+template <int FM, int TN>
+void launch_out(int out_type, bool sw, const GemmArgs &g, const NarrowSched &ts, int vec, const GemmExtra &ex,
+                const QuantArgs &q, int grid, hipStream_t s) {
+    if constexpr (TN == 128) {
+        if (sw) {
+            if (out_type == OUT_BF16) launch_t<OUT_BF16, FM, 128, true>(g, ts, vec, ex, q, grid, s);
+            else launch_t<OUT_F32, FM, 128, true>(g, ts, vec, ex, q, grid, s);
+            return;
+        }
+    }
+    if (out_type == OUT_I32) launch_t<OUT_I32, FM, TN, false>(g, ts, vec, ex, q, grid, s);
+    else if (out_type == OUT_BF16) launch_t<OUT_BF16, FM, TN, false>(g, ts, vec, ex, q, grid, s);
+    else launch_t<OUT_F32, FM, TN, false>(g, ts, vec, ex, q, grid, s);
+}
+
+}  // namespace
+
+hipError_t launch_quant_narrow(const GemmArgs &g, int out_type, const GemmExtra &ex,
+                               const QuantArgs &q, hipStream_t s) {
+    if (g.M == 0 || g.N == 0 || g.P == 0) return hipSuccess;
+    const bool sw = ex.act == ACT_SWIGLU;
+    // The tile shape by the bf16 form's rule: the pipeline is the same.
+    const int cus = device_cu_count();
+    const int64_t tn128 = sw ? (g.N + 63) / 64 : (g.N + 127) / 128;   // tiles of 128 W rows
+    const int FM = ((g.M + 127) / 128) * tn128 * g.P <= cus ? 128 : 256;
+    const int64_t tm = (g.M + FM - 1) / FM;
+    const int TN = (!sw && FM == 128 && 2 * tm * tn128 * g.P <= cus) ? 64 : 128;
+    const int64_t tn = sw ? tn128 : (g.N + TN - 1) / TN;
+    const int64_t T = tm * tn * g.P;
+    if (tm > 0x7FFFFFFFll || tn > 0x7FFFFFFFll || tm * tn > 0x7FFFFFFFll || T > 0x7FFFFFFFll)
+        return hipErrorInvalidConfiguration;
+    NarrowSched ts;
+    ts.tiles_m = (int)tm;
+    ts.tiles_n = (int)tn;
+    ts.T = (int)T;
+    const int grid = (int)(T < cus ? T : cus);
+    ts.xcd_split = (grid == cus && cus % 8 == 0 && T >= cus) ? 1 : 0;
+    ts.per_xcd = grid / 8;
+    const int vw = out_type == OUT_BF16 ? 8 : 4;
+    const int vec = g.ldc % vw == 0 && g.c_shard % vw == 0 && aligned16(g.C);
+    if (FM == 256) launch_out<256, 128>(out_type, sw, g, ts, vec, ex, q, grid, s);
+    else if (TN == 128) launch_out<128, 128>(out_type, sw, g, ts, vec, ex, q, grid, s);
+    else launch_out<128, 64>(out_type, sw, g, ts, vec, ex, q, grid, s);
+    return hipGetLastError();
+}
+
+}  // namespace tpl

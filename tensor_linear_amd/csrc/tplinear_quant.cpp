@@ -21,7 +21,12 @@ constexpr int64_t MAX_QUANT_K = 131071;
 
 hipError_t run_quant(const GemmArgs &g, int out, const GemmExtra &ex, const QuantArgs &q,
                      hipStream_t s) {
-    if (quant_dma_supported(g, ex, 256) && g.M > 128) return launch_quant_tile(g, out, ex, q, s);
+    if (quant_dma_supported(g, ex, 256) && g.M > 32) {
+        const bool sw = ex.act == ACT_SWIGLU;
+        const int64_t t256 = ((g.M + 255) / 256) * ((g.N + (sw ? 127 : 255)) / (sw ? 128 : 256)) * g.P;
+        if (2 * t256 <= device_cu_count()) return launch_quant_narrow(g, out, ex, q, s);
+        return launch_quant_tile(g, out, ex, q, s);
+    }
     return launch_quant_generic(g, out, ex, q, s);
 }
 
@@ -147,6 +152,10 @@ tp_status tp_linear_row_quant(const int8_t *X, int64_t ldx, const float *x_scale
     set_out_slices(r, y_slices, P);
     r.slice_rows = mode == TP_ROW_SCATTER ? M / P : M;
     r.slice_stride = mode == TP_ROW_SCATTER ? (y_slice_stride ? y_slice_stride : s_stride) : 0;
+    if (per_shard && M > 64 && quant_rowfold_supported(g, r, q)) {
+        const int64_t tiles = ((M + 255) / 256) * ((N + 127) / 128);
+        if (tiles >= device_cu_count()) return hip_status(launch_quant_rowfold(g, r, q, out, s));
+    }
     const hipError_t e = run_quant(g, OUT_I32, ex, q, s);
     if (e != hipSuccess) return TP_ERR_HIP;
     return hip_status(launch_quant_fold(r, q, per_shard, out, s));
