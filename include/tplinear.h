@@ -420,7 +420,8 @@ tp_status tp_linear_column_quant(const int8_t *X, int64_t ldx, const float *x_sc
  *   Y[m, n] = fma(S, w_scale[n], bias[n] or 0), one rounding to out_dtype.
  * TP_ROW_SUM and TP_ROW_FUSED are the same call here: the library folds inside
  * the product or by way of int32 partials in the workspace, whichever is
- * faster, with the same bits.  TP_ROW_SCATTER places the same values as token
+ * faster, with the same bits (TPLINEAR_ROW_FOLD=gemm as in tp_linear_row).
+ * TP_ROW_SCATTER places the same values as token
  * slices.  TP_ROW_PARTIAL writes float(acc_i) * x_scale_i * w_scale[n] as fp32.
  * workspace: as tp_linear_row (tp_row_workspace_bytes).
  * K/P (with x_groups = 1 and a sum: K) is at most 131071.

@@ -26,6 +26,7 @@ SOURCES = ["tplinear.cpp", "device.cpp", "gemm_tile.hip", "gemm_skinny.hip", "ge
            "shard_fold.hip", "embedding.hip", "gemm_rowfold.hip", "gemm_narrow.hip",
            "noalloc.hip", "tplinear_quant.cpp", "quantize.hip", "quant_generic.hip",
            "quant_tile.hip", "quant_narrow.hip", "quant_rowfold.hip",
+           "quant_skinny.hip",
            "quant_fold.hip", "tplinear_heads.cpp", "heads.hip"]
 
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")

@@ -150,6 +150,9 @@ tp_status plan_row(const void *X, int64_t ldx, const void *W, int64_t ldw, const
                    void *Y, void *const *y_slices, int64_t ldy, int64_t y_slice_stride,
                    int32_t mode, int64_t M, int64_t N, int64_t K, int32_t P, int32_t dtype,
                    size_t ws_cap, RowPlan &plan);
+// Whether TPLINEAR_ROW_FOLD=gemm asks for the fold inside the GEMM wherever a
+// kernel takes the call.
+bool row_fold_in_gemm_forced();
 // Queue the plan's kernels; `workspace` is read only by PARTIALS_AND_FOLD
 // (TP_ERR_WORKSPACE if it is null there).
 tp_status run_row(RowPlan &plan, float *workspace, hipStream_t s);

@@ -49,6 +49,12 @@ bool quant_rowfold_supported(const GemmArgs &g, const ReduceArgs &r, const Quant
 hipError_t launch_quant_rowfold(const GemmArgs &g, const ReduceArgs &r, const QuantArgs &q,
                                 int out_type, hipStream_t s);
 
+// Up to 48 tokens, streaming W; fold != NULL: the P shard products folded with a
+// scale for each token and shard into fold->Y (C unused).
+bool quant_skinny_supported(const GemmArgs &g, const GemmExtra &ex);
+hipError_t launch_quant_skinny(const GemmArgs &g, int out_type, const FoldArgs *fold,
+                               const GemmExtra &ex, const QuantArgs &q, hipStream_t s);
+
 // Rows of X to int8: scale[m * lds + j] for column group j of G.
 struct QuantizeArgs {
     const void *X; int64_t ldx;

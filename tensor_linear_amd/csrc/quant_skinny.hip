@@ -1,0 +1,71 @@
+// Launch of the skinny kernel (gemm_skinny_impl.h) on int8 operands: decode
+// shapes, bound by streaming W.
+#include "gemm_skinny_impl.h"
+
+namespace tpl {
+namespace {
+
+template <int NB, int MB, int KB, int NST>
+hipError_t launch_t(const GemmArgs &g, int out_type, const FoldArgs *fold, const GemmExtra &ex,
+                    const QuantArgs &q, hipStream_t s) {
+    constexpr int BN = 16 * NB;
+    const bool sw = ex.act == ACT_SWIGLU;
+    const int64_t tn = (g.N + (sw ? 16 : BN) - 1) / (sw ? 16 : BN);
+    const int64_t blocks = fold ? tn : tn * g.P;
+    if (tn > 0x7FFFFFFFll || blocks > 0x7FFFFFFFll) return hipErrorInvalidConfiguration;
+    const dim3 grid((unsigned)blocks), block(SK_THREADS);
+    const FoldArgs f = fold ? *fold : FoldArgs{nullptr, 0, 0};
+    if (sw) {
+        if constexpr (NB == 2) {
+            if (out_type == OUT_BF16) gemm_skinny_kernel<NB, MB, KB, NST, OUT_BF16, false, true, OpI8><<<grid, block, 0, s>>>(g, f, ex, q);
+            else gemm_skinny_kernel<NB, MB, KB, NST, OUT_F32, false, true, OpI8><<<grid, block, 0, s>>>(g, f, ex, q);
+        } else {
+            return hipErrorInvalidValue;
+        }
+    } else if (fold) {
+        if (out_type == OUT_BF16) gemm_skinny_kernel<NB, MB, KB, NST, OUT_BF16, true, false, OpI8><<<grid, block, 0, s>>>(g, f, ex, q);
+        else gemm_skinny_kernel<NB, MB, KB, NST, OUT_F32, true, false, OpI8><<<grid, block, 0, s>>>(g, f, ex, q);
+    } else if (out_type == OUT_I32) {
+        gemm_skinny_kernel<NB, MB, KB, NST, OUT_I32, false, false, OpI8><<<grid, block, 0, s>>>(g, f, ex, q);
+    } else if (out_type == OUT_BF16) {
+        gemm_skinny_kernel<NB, MB, KB, NST, OUT_BF16, false, false, OpI8><<<grid, block, 0, s>>>(g, f, ex, q);
+    } else {
+        gemm_skinny_kernel<NB, MB, KB, NST, OUT_F32, false, false, OpI8><<<grid, block, 0, s>>>(g, f, ex, q);
+    }
+    return hipGetLastError();
+}
+
+inline bool aligned16(const void *p) { return ((uintptr_t)p & 15u) == 0; }
+
+}  // namespace
+
+bool quant_skinny_supported(const GemmArgs &g, const GemmExtra &ex) {
+    return ex.x_rows == 0 && g.M >= 1 && g.M <= SKINNY_MAX_M && g.K > 0 && g.K % 16 == 0 &&
+           g.lda % 16 == 0 && g.ldb % 16 == 0 && g.a_shard % 16 == 0 && g.b_shard % 16 == 0 &&
+           aligned16(g.A) && aligned16(g.B);
+}
+
+hipError_t launch_quant_skinny(const GemmArgs &g, int out_type, const FoldArgs *fold,
+                               const GemmExtra &ex, const QuantArgs &q, hipStream_t s) {
+    if (g.M == 0 || g.N == 0 || g.P == 0) return hipSuccess;
+    if (ex.act == ACT_SWIGLU) {
+        if (fold || out_type == OUT_I32) return hipErrorInvalidValue;
+        if (g.M <= 16) return launch_t<2, 1, 256, 3>(g, out_type, fold, ex, q, s);
+        if (g.M <= 32) return launch_t<2, 2, 256, 2>(g, out_type, fold, ex, q, s);
+        return launch_t<2, 4, 256, 2>(g, out_type, fold, ex, q, s);
+    }
+    if (g.M <= 16) {
+        if (fold && g.N >= 32 * (int64_t)device_cu_count())
+            return launch_t<2, 1, 256, 4>(g, out_type, fold, ex, q, s);
+        if (fold) return launch_t<1, 1, 256, 4>(g, out_type, fold, ex, q, s);
+        return launch_t<1, 1, 256, 3>(g, out_type, fold, ex, q, s);
+    }
+    if (g.M <= 32) {
+        if (fold) return launch_t<4, 2, 256, 2>(g, out_type, fold, ex, q, s);
+        return launch_t<2, 2, 256, 2>(g, out_type, fold, ex, q, s);
+    }
+    if (fold) return launch_t<2, 4, 128, 3>(g, out_type, fold, ex, q, s);
+    return launch_t<4, 3, 256, 2>(g, out_type, fold, ex, q, s);
+}
+
+}  // namespace tpl

@@ -19,15 +19,73 @@ using namespace tpl;
 // this many terms stays below 2^31.
 constexpr int64_t MAX_QUANT_K = 131071;
 
+// The kernel for an int8 shard GEMM.  All give the same bits, so the choice is
+// by speed; same box, 8 shards, us after a read-only 1 GiB flush / warm:
+//  - skinny (streams W) up to 32 tokens, and up to 48 where the 128-row tiles of
+//    all shards would fill at most half of the CUs: 16 tokens skinny vs narrow
+//    4096 -> 28672 28.1 / 20.9 vs 28.6 / 20.7, 8192 -> 28672 45.9 / 37.7 vs 52.1 /
+//    36.3, 8192 -> 10240 22.3 / 17.7 vs 36.6 / 25.4; 40 tokens 4096 -> 28672 44.9 /
+//    35.4 vs 34.8 / 21.6, 8192 -> 10240 35.0 / 28.1 vs 37.6 / 26.0;
+//  - narrow tiles where the 256 x 256 ones would fill at most half of the CUs:
+//    narrow vs tile 4096 -> 28672, 256 tokens (112 tiles) 40.2 / 32.2 vs 53.1 /
+//    47.6, 512 tokens (224) 68.2 / 60.9 vs 61.1 / 53.9; 8192 -> 10240, 768 tokens
+//    (120) 64.8 / 61.3 vs 90.1 / 82.8, 1024 tokens (160) 114.2 / 102.1 vs 91.1 / 81.1;
+//  - generic where K, a stride or an address is not a multiple of 16 (2000 ->
+//    3336, 16 tokens: skinny 8.0 / 4.7, generic 20.7 / 12.5; 128 tokens: narrow
+//    19.8 / 12.2, generic 24.2 / 16.4).
 hipError_t run_quant(const GemmArgs &g, int out, const GemmExtra &ex, const QuantArgs &q,
                      hipStream_t s) {
-    if (quant_dma_supported(g, ex, 256) && g.M > 32) {
-        const bool sw = ex.act == ACT_SWIGLU;
+    const bool sw = ex.act == ACT_SWIGLU;
+    const int64_t cus = device_cu_count();
+    if (quant_skinny_supported(g, ex)) {
+        const int64_t cols = sw ? 64 : 128;   // outputs per 128 W rows
+        const int64_t t128 = (g.N * g.P + cols - 1) / cols;
+        if (g.M <= 32 || 2 * t128 <= cus) return launch_quant_skinny(g, out, nullptr, ex, q, s);
+    }
+    if (quant_dma_supported(g, ex, 256)) {
         const int64_t t256 = ((g.M + 255) / 256) * ((g.N + (sw ? 127 : 255)) / (sw ? 128 : 256)) * g.P;
-        if (2 * t256 <= device_cu_count()) return launch_quant_narrow(g, out, ex, q, s);
+        if (2 * t256 <= cus) return launch_quant_narrow(g, out, ex, q, s);
         return launch_quant_tile(g, out, ex, q, s);
     }
     return launch_quant_generic(g, out, ex, q, s);
+}
+
+// One scale a token: one product over all of K, or P int32 partials and their
+// fold (the same integer sums).  The product has P times fewer workgroups to
+// hide its longer loop; the partials cost 8 P M N bytes.  Same box, 8 shards, us
+// after a flush, product vs partials: 16 tokens 14336 -> 4096 19.7 vs 24.6, 8192 ->
+// 8192 18.7 vs 27.0, 28672 -> 8192 48.3 vs 55.5, but 28672 -> 2048 31.1 vs 22.8; 32
+// tokens 8192 -> 8192 26.3 vs 28.4, 14336 -> 4096 35.1 vs 24.9; above, with r = P M N
+// / K: 4096 -> 2048 at 200 tokens (r = 800) 21.8 vs 17.0, at 600 (2400) 22.7 vs 30.3;
+// 14336 -> 4096 at 512 (1170) 60.4 vs 51.5, at 768 (1755) 75.3 vs 79.6; 8192 -> 8192 at
+// 128 (1024) 38.8 vs 34.8, at 256 (2048) 39.8 vs 46.9; the second launch itself is
+// about 1.2e6 of P M N (1024 -> 1024 at 64 tokens 11.0 vs 13.3).
+bool one_product_faster(int64_t M, int64_t N, int64_t K, int32_t P) {
+    if (P == 1) return true;
+    if (M <= 16 && N >= 16 * (int64_t)device_cu_count()) return true;
+    if (M <= 32) return K <= 8192;
+    return (double)P * M * N + 1.2e6 >= 1500.0 * K;
+}
+
+// A scale for each token and shard: the fold inside the product, or int32
+// partials and their fold (the same bits).  Same box, 8 shards, us after a flush,
+// fold inside vs partials.  Up to 16 tokens (skinny): 14336 -> 4096 23.2 vs 24.5,
+// 28672 -> 8192 52.4 vs 55.4, 4096 -> 2048 11.8 vs 13.9, 1024 -> 1024 11.2 vs 12.3, but
+// 28672 -> 2048 32.1 vs 23.5 and 14080 -> 2000 22.0 vs 18.7 (fewer workgroups than
+// CUs and a long K); 32 tokens 14336 -> 4096 53.2 vs 25.1.
+bool skinny_fold_faster(int64_t M, int64_t N, int64_t K) {
+    return M <= 16 && (N >= 16 * (int64_t)device_cu_count() || K <= 4096);
+}
+
+// 256 x 128 tiles with the fold in registers walk the shards of a tile in turn,
+// so they need enough tiles, the more the longer the shard's K: K/P = 512 at 64
+// tiles 43.6 vs 37.2, at 96 44.5 vs 54.9; 1024 at 64 68.5 vs 45.6, at 128 68.3 vs 79.4;
+// 1792 at 128 107.6 vs 94.4, at 192 110.3 vs 132.0; 3584 at 192 209.8 vs 200.7, at 256
+// 212.7 vs 272.0; 4096 tokens 14336 -> 4096 220.0 vs 332.4, 28672 -> 8192 757.6 vs 1021.5.
+bool rowfold_faster(int64_t M, int64_t N, int64_t Ks) {
+    if (M <= 64) return false;   // its 256-row tile would be three-quarters empty
+    const int64_t tiles = ((M + 255) / 256) * ((N + 127) / 128), cus = device_cu_count();
+    return tiles >= cus || tiles * 6400 >= cus * (1536 + Ks);
 }
 
 }  // namespace
@@ -152,10 +210,31 @@ tp_status tp_linear_row_quant(const int8_t *X, int64_t ldx, const float *x_scale
     set_out_slices(r, y_slices, P);
     r.slice_rows = mode == TP_ROW_SCATTER ? M / P : M;
     r.slice_stride = mode == TP_ROW_SCATTER ? (y_slice_stride ? y_slice_stride : s_stride) : 0;
-    if (per_shard && M > 64 && quant_rowfold_supported(g, r, q)) {
-        const int64_t tiles = ((M + 255) / 256) * ((N + 127) / 128);
-        if (tiles >= device_cu_count()) return hip_status(launch_quant_rowfold(g, r, q, out, s));
+    // Inside the product where that is faster, or with TPLINEAR_ROW_FOLD=gemm
+    // wherever a kernel takes the call.
+    const bool forced = row_fold_in_gemm_forced();
+    ex.bias = bias;
+    if (!per_shard) {
+        if (!y_slices && (forced || one_product_faster(M, N, K, P))) {
+            GemmArgs d = g;
+            d.K = K; d.P = 1; d.a_shard = d.b_shard = 0;
+            d.C = Y; d.ldc = ldy; d.c_shard = 0;
+            if (mode == TP_ROW_SCATTER) {
+                // the token slices as shards in M: row block j of X into slice j
+                d.M = M / P; d.P = P;
+                d.a_shard = (M / P) * ldx; d.c_shard = r.slice_stride;
+                q.x_shard = (M / P) * ldxs;
+            }
+            return hip_status(run_quant(d, out, ex, q, s));
+        }
+    } else if (mode != TP_ROW_SCATTER && quant_skinny_supported(g, ex) &&
+               (forced || skinny_fold_faster(M, N, K))) {
+        const FoldArgs f{Y, ldy, out};
+        return hip_status(launch_quant_skinny(g, out, &f, ex, q, s));
+    } else if (quant_rowfold_supported(g, r, q) && (forced || rowfold_faster(M, N, K / P))) {
+        return hip_status(launch_quant_rowfold(g, r, q, out, s));
     }
+    ex.bias = nullptr;
     const hipError_t e = run_quant(g, OUT_I32, ex, q, s);
     if (e != hipSuccess) return TP_ERR_HIP;
     return hip_status(launch_quant_fold(r, q, per_shard, out, s));

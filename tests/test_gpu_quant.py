@@ -14,7 +14,7 @@ import pytest
 import torch
 
 import tensor_linear_amd as tl
-from gpu_util import DEV, workspace
+from gpu_util import DEV, FOLD_POLICIES, row_fold, workspace
 
 pytestmark = pytest.mark.gpu
 
@@ -226,7 +226,7 @@ def test_nan_scale_marks_its_row():
 
 ROW = [  # M, K/P, N, P
     (1, 16, 1, 1), (3, 128, 20, 3), (16, 1024, 64, 8), (16, 512, 8200, 2), (17, 144, 33, 8), (6, 100, 24, 2), (33, 2048, 96, 2),
-    (64, 256, 136, 4), (128, 1376, 264, 2), (520, 256, 1160, 8), (300, 384, 520, 3), (260, 33, 72, 2), (1024, 128, 8200, 4),
+    (64, 256, 136, 4), (128, 1376, 264, 2), (512, 256, 264, 2), (768, 144, 200, 3), (2048, 48, 136, 8), (48, 1040, 520, 2), (300, 1376, 2056, 3), (520, 256, 1160, 8), (300, 384, 520, 3), (260, 33, 72, 2), (1024, 128, 8200, 4),
     (12, 0, 24, 2)]
 
 
@@ -261,6 +261,11 @@ def test_row_quant(M, Ks, N, P, per_shard, t):
             buf = torch.full((M, N + 3), -7.0, dtype=t, device=DEV)
             tl.tp_linear_row_quant(xd, sxd, wd, swd, buf[:, :N], P, mode, workspace(mode, M, N, P), bias=bd)
             got = buf[:, :N].cpu()
+            for policy in FOLD_POLICIES[1:]:          # the other kernels that take the shape
+                other = torch.full((M, N + 3), -7.0, dtype=t, device=DEV)
+                with row_fold(policy):
+                    tl.tp_linear_row_quant(xd, sxd, wd, swd, other[:, :N], P, mode, workspace(mode, M, N, P), bias=bd)
+                assert torch.equal(other[:, :N].cpu(), got) and torch.all(other[:, N:] == -7.0)
             bad = (got.double() - want).abs() - 1.01 * (err + half_step(t) * want.abs() + 2.0 ** -133)
             assert float(bad.max()) <= 0, (mode, bias, float(bad.max()))
             assert torch.all(buf[:, N:] == -7.0)
@@ -269,6 +274,10 @@ def test_row_quant(M, Ks, N, P, per_shard, t):
             ys = [torch.full((M // P, N), -7.0, dtype=t, device=DEV) for _ in range(P)]
             tl.tp_linear_row_quant(xd, sxd, wd, swd, None, P, tl.TP_ROW_SCATTER, workspace(tl.TP_ROW_SCATTER, M, N, P), bias=bd, y_slices=ys)
             assert torch.equal(torch.cat(ys).cpu(), outs[bias])
+            with row_fold("gemm"):
+                ys = [torch.full((M // P, N), -7.0, dtype=t, device=DEV) for _ in range(P)]
+                tl.tp_linear_row_quant(xd, sxd, wd, swd, None, P, tl.TP_ROW_SCATTER, workspace(tl.TP_ROW_SCATTER, M, N, P), bias=bd, y_slices=ys)
+                assert torch.equal(torch.cat(ys).cpu(), outs[bias])
             gap = torch.full((P * (M // P * N + 40),), -7.0, dtype=t, device=DEV)
             tl.tp_linear_row_quant(xd, sxd, wd, swd, gap[:M // P * N].view(M // P, N), P, tl.TP_ROW_SCATTER,
                                    workspace(tl.TP_ROW_SCATTER, M, N, P), bias=bd, y_slice_stride=M // P * N + 40)
