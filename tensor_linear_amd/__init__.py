@@ -166,44 +166,71 @@ def tp_version() -> int:
 
 # ---- marshalling helpers --------------------------------------------------
 
+# torch is imported at the first call that is given a tensor (the C library and
+# this module's constants need none).  A call's checks cost the host more than a
+# small kernel runs, so they read each tensor's shape, strides and device once.
+
+def _torch():
+    global _torch_module, _DTYPES
+    if _torch_module is None:
+        import torch
+        _torch_module = torch
+        _DTYPES = {torch.bfloat16: TP_BF16, torch.float32: TP_F32}
+    return _torch_module
+
+
+_torch_module = None
+_DTYPES = {}
+
+
 def _dtype_code(t) -> int:
-    import torch
-    if t.dtype == torch.bfloat16:
-        return TP_BF16
-    if t.dtype == torch.float32:
-        return TP_F32
-    raise TypeError(f"unsupported dtype {t.dtype}: bfloat16 or float32")
+    c = _DTYPES.get(t.dtype)
+    if c is None:
+        _torch()
+        c = _DTYPES.get(t.dtype)
+        if c is None:
+            raise TypeError(f"unsupported dtype {t.dtype}: bfloat16 or float32")
+    return c
 
 
 def _mat(t, name):
     """(data pointer, rows, cols, leading dim) of a 2-D unit-column-stride view."""
-    if t.dim() != 2:
-        raise ValueError(f"{name} must be 2-D, got shape {tuple(t.shape)}")
-    if t.shape[1] > 1 and t.stride(1) != 1:
+    shape = t.shape
+    if len(shape) != 2:
+        raise ValueError(f"{name} must be 2-D, got shape {tuple(shape)}")
+    rows, cols = shape
+    ld, unit = t.stride()
+    if cols > 1 and unit != 1:
         raise ValueError(f"{name} must have unit column stride")
     # A one-row view keeps the row stride of the buffer it was cut from when
     # that stride is a valid leading dim (it places the blocks of a [P, 1, N]
     # output); otherwise its leading dim is its width.
-    ld = t.stride(0) if t.shape[0] > 1 or t.stride(0) >= t.shape[1] else t.shape[1]
-    return t.data_ptr(), t.shape[0], t.shape[1], max(ld, t.shape[1], 1)
+    if ld < cols:
+        ld = cols
+    return t.data_ptr(), rows, cols, ld or 1
 
 
 def _same_gpu(*items):
     """Every tensor given (lists of tensors included, None skipped) must live
     on one GPU: the kernels dereference the data pointers on that device, so
     a host tensor or a second device is rejected here, before any launch."""
-    dev = None
+    dev = first = None
     for it in items:
+        if it is None:
+            continue
         for t in (it if isinstance(it, (list, tuple)) else (it,)):
             if t is None:
+                continue
+            d = t.get_device()
+            if d == dev:
                 continue
             if not t.is_cuda:
                 raise ValueError("every tensor must be a GPU tensor (got one on "
                                  f"{t.device})")
             if dev is None:
-                dev = t.device
-            elif t.device != dev:
-                raise ValueError(f"tensors on {dev} and {t.device}: all must share one GPU")
+                dev, first = d, t
+            else:
+                raise ValueError(f"tensors on {first.device} and {t.device}: all must share one GPU")
 
 
 def _ptr_array(ts, name):
@@ -221,7 +248,7 @@ def _check_p(P):
 def _expect_shape(t, shape, name):
     """The library writes exactly `shape`; a smaller or differently shaped
     output would be written out of bounds, so it is refused here."""
-    if tuple(t.shape) != tuple(shape):
+    if t.shape != shape and tuple(t.shape) != tuple(shape):
         raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
 
 
@@ -254,8 +281,11 @@ def _block_out(Y, P, rows, cols, name="Y"):
     """Pointer and row stride of a [P, rows, cols] output whose blocks are
     rows*ldy elements apart."""
     _expect_shape(Y, (P, rows, cols), name)
-    _, _, _, ldy = _mat(Y[0], f"{name}[0]")
-    if P > 1 and Y.stride(0) != rows * ldy:
+    block, ldy, unit = Y.stride()
+    if cols > 1 and unit != 1:
+        raise ValueError(f"{name}[0] must have unit column stride")
+    ldy = max(ldy, cols, 1)
+    if P > 1 and block != rows * ldy:
         raise ValueError(f"{name} blocks must be rows*ldy elements apart")
     return Y.data_ptr(), ldy
 
@@ -271,12 +301,13 @@ def _bias_ptr(bias, dt):
 
 
 def _stream(t, stream):
+    """The stream handle of a call: the one given, or the current one of t's
+    device."""
     if stream is not None:
-        return ctypes.c_void_p(int(stream))
-    import torch
+        return int(stream)
     if t.is_cuda:
-        return ctypes.c_void_p(torch.cuda.current_stream(t.device).cuda_stream)
-    return ctypes.c_void_p(0)
+        return _torch()._C._cuda_getCurrentRawStream(t.get_device())
+    return 0
 
 
 # ---- entry points ---------------------------------------------------------
@@ -577,7 +608,7 @@ def tp_embedding(ids, Y, P: int, E=None, e_shards=None, y_mode: int = TP_Y_CONCA
 # ---- 8-bit integers -------------------------------------------------------
 
 def _int8_mat(t, name):
-    import torch
+    torch = _torch()
     if t.dtype != torch.int8:
         raise TypeError(f"{name} must be int8, got {t.dtype}")
     return _mat(t, name)
@@ -586,23 +617,24 @@ def _int8_mat(t, name):
 def _token_scales(t, M, groups, name):
     """(pointer, row stride, scales a token) of fp32 scales [M] or [M, G], G
     one of `groups`."""
-    import torch
+    torch = _torch()
     if t.dtype != torch.float32:
         raise TypeError(f"{name} must be float32, got {t.dtype}")
-    G = t.shape[1] if t.dim() == 2 else 1
-    if t.dim() not in (1, 2) or t.shape[0] != M or G not in groups:
+    shape, strides = t.shape, t.stride()
+    G = shape[1] if len(shape) == 2 else 1
+    if len(shape) not in (1, 2) or shape[0] != M or G not in groups:
         raise ValueError(f"{name} must have shape [{M}] or [{M}, G] with G in {groups}, "
-                         f"got {tuple(t.shape)}")
-    if G > 1 and t.stride(1) != 1:
+                         f"got {tuple(shape)}")
+    if G > 1 and strides[1] != 1:
         raise ValueError(f"{name} must have unit column stride")
-    ld = t.stride(0) if M > 1 else G
+    ld = strides[0] if M > 1 else G
     if ld < G:
         raise ValueError(f"{name} must have a row stride of at least {G}")
     return t.data_ptr(), ld, G
 
 
 def _channel_scales(t, N, name):
-    import torch
+    torch = _torch()
     if t.dtype != torch.float32:
         raise TypeError(f"{name} must be float32, got {t.dtype}")
     _expect_shape(t, (N,), name)
@@ -687,7 +719,7 @@ def tp_linear_row_quant(X, x_scale, W, w_scale, Y, P: int, mode: int = TP_ROW_SU
                 raise ValueError("y_slices must be [M/P, N] of one dtype and row stride")
         yp, ys = None, _ptr_array(y_slices, "y_slices")
     elif mode == TP_ROW_PARTIAL:
-        import torch
+        torch = _torch()
         if Y.dtype != torch.float32:
             raise ValueError("Y must be float32 [P, M, N] for TP_ROW_PARTIAL")
         dt = TP_F32
@@ -716,10 +748,11 @@ def _qkv(X, P, Hq, Hkv, x_mode, name):
     if Hq % P or Hkv % P:
         check(TP_ERR_INDIVISIBLE)
     shards = x_mode == TP_Y_SHARDS
-    if X.dim() != (3 if shards else 2) or (shards and X.shape[0] != P):
+    shape = X.shape
+    if len(shape) != (3 if shards else 2) or (shards and shape[0] != P):
         raise ValueError(f"{name} must be [T, N], or [P, T, N/P] with TP_Y_SHARDS, got "
-                         f"{tuple(X.shape)}")
-    T, cols = X.shape[-2], X.shape[-1]
+                         f"{tuple(shape)}")
+    T, cols = shape[-2], shape[-1]
     heads = (Hq + 2 * Hkv) // (P if shards else 1)
     if cols == 0 or cols % heads:
         raise ValueError(f"{name} has {cols} columns: not a multiple of its {heads} heads")
@@ -744,16 +777,18 @@ def _rows(t, T, cols, dt, name):
 
 def _rotation(cos, sin, q_weight, k_weight, D, dt, eps, style):
     """The rotation's and norms' arguments in the order of the C calls."""
-    import torch
+    torch = _torch()
     if (cos is None) != (sin is None):
         raise ValueError("give both cos and sin, or neither")
     n_pos = R = 0
     if cos is not None:
+        f32 = torch.float32
         for t, name in ((cos, "cos"), (sin, "sin")):
-            if t.dtype != torch.float32 or t.dim() != 2 or not t.is_contiguous():
+            if t.dtype != f32 or t.dim() != 2 or not t.is_contiguous():
                 raise ValueError(f"{name} must be a contiguous float32 [n_pos, R/2] tensor")
-        _expect_shape(sin, cos.shape, "sin")
-        n_pos, R = cos.shape[0], 2 * cos.shape[1]
+        shape = cos.shape
+        _expect_shape(sin, shape, "sin")
+        n_pos, R = shape[0], 2 * shape[1]
     for t, name in ((q_weight, "q_weight"), (k_weight, "k_weight")):
         if t is not None:
             _expect_shape(t, (D,), name)
@@ -767,7 +802,7 @@ def _rotation(cos, sin, q_weight, k_weight, D, dt, eps, style):
 
 
 def _positions(pos, T, R):
-    import torch
+    torch = _torch()
     if pos is None:
         if R:
             raise ValueError("pos is needed where heads are rotated")
@@ -779,7 +814,7 @@ def _positions(pos, T, R):
 
 
 def _flag(bad):
-    import torch
+    torch = _torch()
     if bad is None:
         return None
     if bad.dtype != torch.int32 or bad.numel() < 1:
@@ -819,7 +854,7 @@ def tp_qk_norm_rope_backward(X, pos, cos, sin, dQ, dK, dX, P: int, Hq: int, Hkv:
     gradient is None is left as it is), and the weights' gradients dq_weight,
     dk_weight (float32 [D], or None), which need a workspace of
     tp_qk_norm_rope_workspace_bytes(T, D).  X may be None without a norm."""
-    import torch
+    torch = _torch()
     dxp, lddx, T, D = _qkv(dX, P, Hq, Hkv, x_mode, "dX")
     dt = _dtype_code(dX)
     xp, ldx = None, lddx
@@ -860,33 +895,33 @@ def tp_kv_append(X, cos, sin, past, cu, table, k_cache, v_cache, P: int, Hq: int
     past int32 [B], cu int32 [B + 1], table int32 [B, max_pages]; k_cache and
     v_cache [n_pages, page_size, Hkv, D] views of one set of strides with
     contiguous features (a permuted view gives another order in memory)."""
-    import torch
+    torch = _torch()
     xp, ldx, T, D = _qkv(X, P, Hq, Hkv, x_mode, "X")
     dt = _dtype_code(X)
     rot = _rotation(cos, sin, q_weight, k_weight, D, dt, eps, style)
-    if past.dim() != 1 or table.dim() != 2:
-        raise ValueError("past must be [B] and table [B, max_pages]")
-    B = past.shape[0]
-    for t, shape, name in ((past, (B,), "past"), (cu, (B + 1,), "cu"),
-                           (table, (B, table.shape[1]), "table")):
+    if past.dim() != 1:
+        raise ValueError("past must be [B]")
+    B, i32 = past.shape[0], torch.int32
+    for t, shape, name in ((past, (B,), "past"), (cu, (B + 1,), "cu")):
         _expect_shape(t, shape, name)
-        if t.dtype != torch.int32 or (t.shape[-1] > 1 and t.stride(-1) != 1):
+        if t.dtype != i32 or (shape[0] > 1 and t.stride(0) != 1):
             raise ValueError(f"{name} must be int32 with unit stride")
-    _, _, max_pages, ldt = _mat(table, "table")
-    if k_cache.dim() != 4:
-        raise ValueError("k_cache must be [n_pages, page_size, Hkv, D]")
-    pages, size = k_cache.shape[:2]
-    for t, name in ((k_cache, "k_cache"), (v_cache, "v_cache")):
-        _expect_shape(t, (pages, size, Hkv, D), name)
-        if _dtype_code(t) != dt:
-            raise TypeError(f"{name} must have the dtype of the QKV matrix")
-        if D > 1 and t.stride(3) != 1:
-            raise ValueError(f"{name} must have contiguous features")
-    if k_cache.stride() != v_cache.stride():
+    tp, rows, max_pages, ldt = _mat(table, "table")
+    if table.dtype != i32 or rows != B:
+        raise ValueError(f"table must be int32 [{B}, max_pages]")
+    shape, strides = k_cache.shape, k_cache.stride()
+    if len(shape) != 4 or shape[2] != Hkv or shape[3] != D:
+        raise ValueError(f"k_cache must be [n_pages, page_size, {Hkv}, {D}]")
+    _expect_shape(v_cache, shape, "v_cache")
+    if D > 1 and strides[3] != 1:
+        raise ValueError("k_cache and v_cache must have contiguous features")
+    if strides != v_cache.stride():
         raise ValueError("k_cache and v_cache must have the same strides")
+    if _dtype_code(k_cache) != dt or _dtype_code(v_cache) != dt:
+        raise TypeError("k_cache and v_cache must have the dtype of the QKV matrix")
     qp, ldq = _rows(Q, T, Hq * D, dt, "Q")
     _same_gpu(X, cos, sin, past, cu, table, k_cache, v_cache, Q, q_weight, k_weight, bad)
     check(_get_lib().tp_kv_append(
-        xp, ldx, x_mode, *rot, cu.data_ptr(), past.data_ptr(), B, table.data_ptr(), ldt, max_pages,
-        k_cache.data_ptr(), v_cache.data_ptr(), pages, size, k_cache.stride(0), k_cache.stride(1),
-        k_cache.stride(2), qp, ldq, T, Hq, Hkv, D, P, dt, _flag(bad), _stream(X, stream)))
+        xp, ldx, x_mode, *rot, cu.data_ptr(), past.data_ptr(), B, tp, ldt, max_pages,
+        k_cache.data_ptr(), v_cache.data_ptr(), shape[0], shape[1], strides[0], strides[1],
+        strides[2], qp, ldq, T, Hq, Hkv, D, P, dt, _flag(bad), _stream(X, stream)))
