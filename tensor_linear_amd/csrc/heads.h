@@ -40,7 +40,8 @@ hipError_t launch_qk_norm_rope(const HeadArgs &a, int elem_bytes, hipStream_t s)
 hipError_t launch_kv_append(const HeadArgs &a, int elem_bytes, hipStream_t s);
 hipError_t launch_qk_norm_rope_backward(const HeadArgs &a, int elem_bytes, hipStream_t s);
 
-// Workgroups that leave weight-gradient sums (2 * D floats each) in `partials`.
+// Most workgroups that leave weight-gradient sums of either kind (D floats each)
+// in `partials`.
 int64_t qk_backward_blocks(int64_t T);
 
 }  // namespace tpl

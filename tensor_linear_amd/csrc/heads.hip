@@ -75,6 +75,25 @@ __device__ __forceinline__ void put1(void *p, int64_t i, float v) {
     else ((float *)p)[i] = v;
 }
 
+// 8 consecutive values as they are, and widened.
+template <int ES>
+struct Raw8 { u32x4 w[ES / 2]; };
+template <int ES>
+__device__ __forceinline__ Raw8<ES> raw8(const void *p, int64_t i) {
+    Raw8<ES> r;
+#pragma unroll
+    for (int h = 0; h < ES / 2; ++h) r.w[h] = *(const u32x4 *)((const char *)p + i * ES + 16 * h);
+    return r;
+}
+template <int ES>
+__device__ __forceinline__ void widen8(const Raw8<ES> &r, float *v) {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+        if (ES == 2) v[e] = __uint_as_float((e & 1) ? r.w[0][e / 2] & 0xFFFF0000u : r.w[0][e / 2] << 16);
+        else v[e] = __uint_as_float(r.w[ES / 2 * e / 8][e % 4]);
+    }
+}
+
 enum { HEAD_Q = 0, HEAD_K = 1, HEAD_V = 2 };
 
 // Where a token goes: its position and, for the append, the element offset of
@@ -181,31 +200,47 @@ void heads_vec(HeadArgs a, int parts) {
     if (w >= a.T * parts) return;
     const int64_t t = w / parts;
     const int part = (int)(w - t * parts);
+    const int unit = lane % LH;
+    const Runs r = runs_of(unit, a.D, a.R, a.pairs);
+    const Span sp = span_of(a, a.Q != nullptr, APPEND || a.K, APPEND);
+    const int slots = sp.per * a.P;
+    constexpr int HW = 64 / LH;
+    // The next heads' values are loaded while the current ones are worked on, the
+    // first ones while the token's place is looked up.
+    struct Vals { Head h; Raw8<ES> x[2]; };
+    auto load = [&](int g) {
+        Vals v = {};
+        v.h = head_of(a, g + lane / LH, sp, slots);
+        if (v.h.on && r.on) {
+            const int64_t x = v.h.shard * a.x_shard + t * a.ldx + v.h.col;
+            v.x[0] = raw8<ES>(a.X, x + r.a);
+            v.x[1] = raw8<ES>(a.X, x + r.b);
+        }
+        return v;
+    };
+    Vals next = load(part * HW);
     const Place pl = APPEND ? find_place(a, t, lane) : given_place(a, t);
     if (!pl.ok && pl.mine && a.bad && lane == 0) *a.bad = 1;
     if (APPEND && !pl.mine) return;
-    const int unit = lane % LH;
-    const Runs r = runs_of(unit, a.D, a.R, a.pairs);
-    float c[8], s[8], wq[16] = {}, wk[16] = {};
+    float c[8], s[8];
+    Raw8<ES> wq[2] = {}, wk[2] = {};
     if (r.on && r.turn && pl.ok) {
         get8<4>(a.cos, pl.pos * (a.R / 2) + unit * 8, c);
         get8<4>(a.sin, pl.pos * (a.R / 2) + unit * 8, s);
     }
-    if (a.wq && r.on) { get8<ES>(a.wq, r.a, wq); get8<ES>(a.wq, r.b, wq + 8); }
-    if (a.wk && r.on) { get8<ES>(a.wk, r.a, wk); get8<ES>(a.wk, r.b, wk + 8); }
-    const Span sp = span_of(a, a.Q != nullptr, APPEND || a.K, APPEND);
-    const int slots = sp.per * a.P;
-    constexpr int HW = 64 / LH;
+    if (a.wq && r.on) { wq[0] = raw8<ES>(a.wq, r.a); wq[1] = raw8<ES>(a.wq, r.b); }
+    if (a.wk && r.on) { wk[0] = raw8<ES>(a.wk, r.a); wk[1] = raw8<ES>(a.wk, r.b); }
     for (int g = part * HW; g < slots; g += parts * HW) {
-        const Head h = head_of(a, g + lane / LH, sp, slots);
+        const Vals cur = next;
+        if (g + parts * HW < slots) next = load(g + parts * HW);
+        const Head h = cur.h;
         const bool live = h.on && r.on;
         float v[16];
+        widen8<ES>(cur.x[0], v);
+        widen8<ES>(cur.x[1], v + 8);
+        if (!pl.ok) {
 #pragma unroll
-        for (int e = 0; e < 16; ++e) v[e] = 0.0f;
-        if (live && pl.ok) {
-            const int64_t x = h.shard * a.x_shard + t * a.ldx + h.col;
-            get8<ES>(a.X, x + r.a, v);
-            get8<ES>(a.X, x + r.b, v + 8);
+            for (int e = 0; e < 16; ++e) v[e] = 0.0f;
         }
         const void *wt = h.kind == HEAD_Q ? a.wq : a.wk;
         if (a.wq || a.wk) {
@@ -215,8 +250,16 @@ void heads_vec(HeadArgs a, int parts) {
             sum = lanes_sum(sum, LH);
             if (h.kind != HEAD_V && wt && pl.ok) {   // a token without a place stays zero, whatever eps is
                 const float rr = rsqrtf(sum / (float)a.D + a.eps);
+                float w[16];
+                Raw8<ES> wr[2];
 #pragma unroll
-                for (int e = 0; e < 16; ++e) v[e] = v[e] * rr * (h.kind == HEAD_Q ? wq[e] : wk[e]);
+                for (int i = 0; i < 2; ++i)
+#pragma unroll
+                    for (int e = 0; e < ES / 2; ++e) wr[i].w[e] = h.kind == HEAD_Q ? wq[i].w[e] : wk[i].w[e];
+                widen8<ES>(wr[0], w);
+                widen8<ES>(wr[1], w + 8);
+#pragma unroll
+                for (int e = 0; e < 16; ++e) v[e] = v[e] * rr * w[e];
             }
         }
         if (r.turn && h.kind != HEAD_V && pl.ok) {
@@ -301,102 +344,146 @@ void heads_any(HeadArgs a) {
 
 // ---- gradients ---------------------------------------------------------------
 
-// As heads_vec; a wavefront walks the tokens w, w + waves, ..., keeping the
-// weights' gradient sums of its 16 values in registers; they are added over the
-// heads of a wavefront and the four wavefronts in a fixed order and left in
-// partials[block][kind][D], which a second kernel adds in block order: the
-// result does not depend on scheduling.
+// A workgroup takes the queries (the first qblocks of the grid) or the keys and
+// values, so that a wavefront's weight and sums are of one kind; a wavefront walks
+// the tokens w, w + waves, ..., 64 / LH heads at a time, the next heads' values and
+// the next token's angles loaded while the current ones are worked on (with 84
+// registers held for sums, weights and angles only three wavefronts fit a SIMD, too
+// few to hide the loads by themselves).  The weights' gradient sums of a lane's 16
+// values stay in registers; they are added over the heads of a wavefront and the
+// four wavefronts in a fixed order and left in partials[kind][block][D], which a
+// second kernel adds in an order of its own: the result does not depend on
+// scheduling.
 template <int ES, int LH>
 __global__ __launch_bounds__(HT)
-void heads_backward_vec(HeadArgs a) {
-    __shared__ float red[4][2][LH * 16];
+void heads_backward_vec(HeadArgs a, int qblocks, int64_t kind_stride) {
+    __shared__ float red[4][LH * 16];
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const bool isq = (int)blockIdx.x < qblocks;
+    const int blk = isq ? blockIdx.x : blockIdx.x - qblocks, nblk = isq ? qblocks : gridDim.x - qblocks;
     const int unit = lane % LH;
     const Runs r = runs_of(unit, a.D, a.R, a.pairs);
-    float wq[16] = {}, wk[16] = {}, gq[16] = {}, gk[16] = {};
-    if (a.wq && r.on) { get8<ES>(a.wq, r.a, wq); get8<ES>(a.wq, r.b, wq + 8); }
-    if (a.wk && r.on) { get8<ES>(a.wk, r.a, wk); get8<ES>(a.wk, r.b, wk + 8); }
-    const Span sp = span_of(a, a.dQ != nullptr, a.dK != nullptr, a.dV != nullptr);
-    const int slots = sp.per * a.P;
+    const void *wt = isq ? a.wq : a.wk, *dy = isq ? a.dQ : a.dK;
+    const int64_t ldy = isq ? a.lddq : a.lddk;
+    const int nh = isq ? a.hq : a.hk, first = isq ? 0 : a.hq;     // heads of a shard, the first one's place
+    float w[16] = {}, gw[16] = {};
+    if (wt && r.on) { get8<ES>(wt, r.a, w); get8<ES>(wt, r.b, w + 8); }
     constexpr int HW = 64 / LH;
-    for (int64_t t = (int64_t)blockIdx.x * (HT / 64) + wave; t < a.T; t += (int64_t)gridDim.x * (HT / 64)) {
-        const Place pl = given_place(a, t);
-        if (!pl.ok && a.bad && lane == 0) *a.bad = 1;
-        float c[8], s[8];
-        if (r.on && r.turn && pl.ok) {
-            get8<4>(a.cos, pl.pos * (a.R / 2) + unit * 8, c);
-            get8<4>(a.sin, pl.pos * (a.R / 2) + unit * 8, s);
+    const int heads = nh * a.P;
+    const int groups = dy ? (heads + HW - 1) / HW : 0;            // of gradients, then of value copies
+    const int all = groups + (!isq && a.dV ? (heads + HW - 1) / HW : 0);
+    const int64_t step = (int64_t)nblk * (HT / 64);
+    int64_t t = (int64_t)blk * (HT / 64) + wave;
+
+    // values of group g of token t: the outputs' gradients and (with a norm) X
+    struct Vals { Raw8<ES> y[2], x[2]; };
+    auto load = [&](int64_t t, int g) {
+        Vals v = {};
+        const bool val = g >= groups;
+        const int h = (val ? g - groups : g) * HW + lane / LH;
+        if (h < heads && r.on) {
+            const void *src = val ? a.dV : dy;
+            const int64_t o = t * (val ? a.lddv : ldy) + (int64_t)h * a.D;
+            v.y[0] = raw8<ES>(src, o + r.a);
+            v.y[1] = raw8<ES>(src, o + r.b);
+            if (wt && !val) {
+                const int i = h / nh;
+                const int64_t x = i * a.x_shard + t * a.ldx + (int64_t)(first + h - i * nh) * a.D;
+                v.x[0] = raw8<ES>(a.X, x + r.a);
+                v.x[1] = raw8<ES>(a.X, x + r.b);
+            }
         }
-        for (int g = 0; g < slots; g += HW) {
-            const Head h = head_of(a, g + lane / LH, sp, slots);
-            const bool live = h.on && r.on;
-            const void *wt = h.kind == HEAD_Q ? a.wq : h.kind == HEAD_K ? a.wk : nullptr;
-            const void *dy = h.kind == HEAD_Q ? a.dQ : h.kind == HEAD_K ? a.dK : a.dV;
-            const int64_t ldy = h.kind == HEAD_Q ? a.lddq : h.kind == HEAD_K ? a.lddk : a.lddv;
-            float v[16], x[16];
+        return v;
+    };
+    struct Turn { float c[8], s[8]; bool ok; };
+    auto angles = [&](int64_t t) {
+        Turn u = {};
+        const Place pl = given_place(a, t);
+        u.ok = pl.ok;
+        if (!pl.ok && a.bad && lane == 0) *a.bad = 1;
+        if (r.on && r.turn && pl.ok) {
+            get8<4>(a.cos, pl.pos * (a.R / 2) + unit * 8, u.c);
+            get8<4>(a.sin, pl.pos * (a.R / 2) + unit * 8, u.s);
+        }
+        return u;
+    };
+    if (t < a.T && all > 0) {
+        Turn now = angles(t);
+        Vals cur = load(t, 0);
+        int g = 0;
+        Turn then = t + step < a.T ? angles(t + step) : Turn{};
+        while (true) {
+            int64_t tn = t;
+            int gn = g + 1;
+            if (gn == all) { gn = 0; tn = t + step; }
+            Vals nxt = {};
+            if (tn < a.T) nxt = load(tn, gn);
+            const bool val = g >= groups;
+            const int h = (val ? g - groups : g) * HW + lane / LH;
+            const bool live = h < heads && r.on;
+            float v[16];
+            widen8<ES>(cur.y[0], v);
+            widen8<ES>(cur.y[1], v + 8);
+            if (!val) {
+                if (!now.ok) {
 #pragma unroll
-            for (int e = 0; e < 16; ++e) v[e] = x[e] = 0.0f;
-            if (live && dy && (pl.ok || h.kind == HEAD_V)) {
-                const int64_t o = t * ldy + (int64_t)h.head * a.D;
-                get8<ES>(dy, o + r.a, v);
-                get8<ES>(dy, o + r.b, v + 8);
-                if (wt) {
-                    const int64_t xo = h.shard * a.x_shard + t * a.ldx + h.col;
-                    get8<ES>(a.X, xo + r.a, x);
-                    get8<ES>(a.X, xo + r.b, x + 8);
-                }
-            }
-            if (r.turn && h.kind != HEAD_V && pl.ok) {
-                if (a.pairs) turn16(v, c, s, true, true);
-                else turn16(v, c, s, false, true);
-            }
-            if (a.wq || a.wk) {
-                float sum = 0.0f, dot = 0.0f;
+                    for (int e = 0; e < 16; ++e) v[e] = 0.0f;
+                } else {
+                    if (r.turn) {
+                        if (a.pairs) turn16(v, now.c, now.s, true, true);
+                        else turn16(v, now.c, now.s, false, true);
+                    }
+                    if (wt) {
+                        float x[16], sum = 0.0f, dot = 0.0f;
+                        widen8<ES>(cur.x[0], x);
+                        widen8<ES>(cur.x[1], x + 8);
 #pragma unroll
-                for (int e = 0; e < 16; ++e) {
-                    sum = __builtin_fmaf(x[e], x[e], sum);
-                    dot = __builtin_fmaf(x[e], v[e] * (h.kind == HEAD_Q ? wq[e] : wk[e]), dot);
-                }
-                if (!wt) dot = 0.0f;
-                sum = lanes_sum(sum, LH);
-                dot = lanes_sum(dot, LH);
-                if (wt && live && pl.ok) {
-                    const float rr = rsqrtf(sum / (float)a.D + a.eps);
-                    const float mean = dot * rr / (float)a.D;
+                        for (int e = 0; e < 16; ++e) {
+                            sum = __builtin_fmaf(x[e], x[e], sum);
+                            dot = __builtin_fmaf(x[e], v[e] * w[e], dot);
+                        }
+                        sum = lanes_sum(sum, LH);
+                        dot = lanes_sum(dot, LH);
+                        if (live) {
+                            const float rr = rsqrtf(sum / (float)a.D + a.eps);
+                            const float mean = dot * rr / (float)a.D;
 #pragma unroll
-                    for (int e = 0; e < 16; ++e) {
-                        const float n = x[e] * rr;
-                        if (h.kind == HEAD_Q) gq[e] = __builtin_fmaf(v[e], n, gq[e]);
-                        else gk[e] = __builtin_fmaf(v[e], n, gk[e]);
-                        v[e] = rr * (v[e] * (h.kind == HEAD_Q ? wq[e] : wk[e]) - n * mean);
+                            for (int e = 0; e < 16; ++e) {
+                                const float n = x[e] * rr;
+                                gw[e] = __builtin_fmaf(v[e], n, gw[e]);
+                                v[e] = rr * (v[e] * w[e] - n * mean);
+                            }
+                        }
                     }
                 }
             }
-            if (live && dy) {
-                const int64_t o = h.shard * a.dx_shard + t * a.lddx + h.col;
+            if (live) {
+                const int i = h / nh;
+                const int64_t o = i * a.dx_shard + t * a.lddx + (int64_t)(first + (val ? a.hk : 0) + h - i * nh) * a.D;
                 put8<ES>(a.dX, o + r.a, v);
                 put8<ES>(a.dX, o + r.b, v + 8);
             }
+            if (tn >= a.T) break;
+            if (gn == 0) {
+                now = then;
+                if (tn + step < a.T) then = angles(tn + step);
+            }
+            cur = nxt;
+            t = tn;
+            g = gn;
         }
     }
-    if (!a.partials) return;
+    if (!a.partials || !wt) return;      // uniform over the workgroup
 #pragma unroll
     for (int e = 0; e < 16; ++e) {
-        float q = gq[e], k = gk[e];
-        for (int o = LH; o < 64; o <<= 1) { q += __shfl_xor(q, o); k += __shfl_xor(k, o); }
-        if (lane < LH) {
-            // the value's place in the head (units past D keep their own cells)
-            const int d = r.on ? (e < 8 ? r.a + e : r.b + e - 8) : unit * 16 + e;
-            red[wave][0][d] = q;
-            red[wave][1][d] = k;
-        }
+        float q = gw[e];
+        for (int o = LH; o < 64; o <<= 1) q += __shfl_xor(q, o);
+        // the value's place in the head (units past D keep their own cells)
+        if (lane < LH) red[wave][r.on ? (e < 8 ? r.a + e : r.b + e - 8) : unit * 16 + e] = q;
     }
     __syncthreads();
-    for (int i = threadIdx.x; i < 2 * a.D; i += HT) {
-        const int kind = i / a.D, d = i - kind * a.D;
-        a.partials[(int64_t)blockIdx.x * 2 * a.D + i] =
-            ((red[0][kind][d] + red[1][kind][d]) + red[2][kind][d]) + red[3][kind][d];
-    }
+    for (int d = threadIdx.x; d < a.D; d += HT)
+        a.partials[(isq ? 0 : kind_stride) + (int64_t)blk * a.D + d] = ((red[0][d] + red[1][d]) + red[2][d]) + red[3][d];
 }
 
 // Any D, R and alignment: a wavefront per token, heads one after another; its
@@ -404,7 +491,7 @@ void heads_backward_vec(HeadArgs a) {
 constexpr int ANY_D = 1024;   // largest head of the unaligned form
 template <int ES>
 __global__ __launch_bounds__(HT)
-void heads_backward_any(HeadArgs a) {
+void heads_backward_any(HeadArgs a, int64_t kind_stride) {
     __shared__ float acc[4][2][ANY_D];
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int items = a.D - a.R / 2;
@@ -473,28 +560,33 @@ void heads_backward_any(HeadArgs a) {
     __syncthreads();
     for (int i = threadIdx.x; i < 2 * a.D; i += HT) {
         const int kind = i / a.D, d = i - kind * a.D;
-        a.partials[(int64_t)blockIdx.x * 2 * a.D + i] =
+        a.partials[kind * kind_stride + (int64_t)blockIdx.x * a.D + d] =
             ((acc[0][kind][d] + acc[1][kind][d]) + acc[2][kind][d]) + acc[3][kind][d];
     }
 }
 
-// dw[kind][d] = sum over blocks of partials[block][kind][d]: 16 columns by 16
-// strands of blocks a workgroup, each strand in block order, then the strands.
+// dw[kind][d] = sum over blocks of partials[kind][block][d]: four columns by 64
+// strands of blocks a workgroup, each strand in block order, then the strands in
+// a tree whose order is fixed.  Columns 0 .. D - 1 are the queries'.
 __global__ __launch_bounds__(HT)
-void weight_grad_sum(const float *partials, int64_t blocks, int D, float *dwq, float *dwk) {
-    __shared__ float red[16][17];
-    const int col = blockIdx.x * 16 + (threadIdx.x & 15), strand = threadIdx.x >> 4;
+void weight_grad_sum(const float *partials, int64_t kind_stride, int64_t qblocks, int64_t kblocks, int D,
+                     float *dwq, float *dwk) {
+    __shared__ float red[4][64];
+    const int c = threadIdx.x & 3, strand = threadIdx.x >> 2, col = blockIdx.x * 4 + c;
     float s = 0.0f;
-    if (col < 2 * D)
-        for (int64_t b = strand; b < blocks; b += 16) s += partials[b * 2 * D + col];
-    red[strand][threadIdx.x & 15] = s;
+    if (col < 2 * D) {
+        const float *p = col < D ? partials + col : partials + kind_stride + col - D;
+        const int64_t n = col < D ? qblocks : kblocks;
+#pragma unroll 8
+        for (int64_t b = strand; b < n; b += 64) s += p[b * D];
+    }
+    red[c][strand] = s;
     __syncthreads();
-    if (threadIdx.x < 16 && col < 2 * D) {
-        float v = red[0][threadIdx.x];
-#pragma unroll
-        for (int i = 1; i < 16; ++i) v += red[i][threadIdx.x];
-        float *dw = col < D ? dwq : dwk;
-        if (dw) dw[col < D ? col : col - D] = v;
+    const int lane = threadIdx.x & 63, k = threadIdx.x >> 6, at = blockIdx.x * 4 + k;   // a wavefront a column
+    const float v = lanes_sum(red[k][lane], 64);
+    if (lane == 0 && at < 2 * D) {
+        float *dw = at < D ? dwq : dwk;
+        if (dw) dw[at < D ? at : at - D] = v;
     }
 }
 
@@ -555,38 +647,55 @@ hipError_t launch_fwd(const HeadArgs &a, hipStream_t s) {
     }
 }
 
+template <int ES, int LH>
+void launch_bwd_vec(const HeadArgs &a, int64_t qb, int64_t kb, int64_t stride, hipStream_t s) {
+    heads_backward_vec<ES, LH><<<dim3((unsigned)(qb + kb)), dim3(HT), 0, s>>>(a, (int)qb, stride);
+}
+
 template <int ES>
 hipError_t launch_bwd(const HeadArgs &a, hipStream_t s) {
     if (a.D > ANY_D) return hipErrorInvalidValue;
-    const int64_t blocks = qk_backward_blocks(a.T);
-    const bool any = a.T > 0 && span_of(a, a.dQ != nullptr, a.dK != nullptr, a.dV != nullptr).per > 0;
-    if (any) {
-        const dim3 grid((unsigned)blocks), block(HT);
-        if (!vec_ok<ES>(a, false, true)) heads_backward_any<ES><<<grid, block, 0, s>>>(a);
-        else switch (lanes_per_head(a.D)) {
-            case 1: heads_backward_vec<ES, 1><<<grid, block, 0, s>>>(a); break;
-            case 2: heads_backward_vec<ES, 2><<<grid, block, 0, s>>>(a); break;
-            case 4: heads_backward_vec<ES, 4><<<grid, block, 0, s>>>(a); break;
-            case 8: heads_backward_vec<ES, 8><<<grid, block, 0, s>>>(a); break;
-            case 16: heads_backward_vec<ES, 16><<<grid, block, 0, s>>>(a); break;
-            default: heads_backward_vec<ES, 32><<<grid, block, 0, s>>>(a); break;
+    const int64_t most = qk_backward_blocks(a.T), stride = most * a.D;
+    const bool q = a.dQ && a.hq > 0, k = (a.dK || a.dV) && a.hk > 0;
+    int64_t qb = q ? most : 0, kb = k ? most : 0;   // workgroups that leave sums, of either kind
+    if (a.T == 0) qb = kb = 0;
+    if (qb + kb > 0) {
+        if (!vec_ok<ES>(a, false, true)) {
+            heads_backward_any<ES><<<dim3((unsigned)most), dim3(HT), 0, s>>>(a, stride);
+            qb = kb = most;
+        } else {
+            // workgroups in proportion to the heads (a value head moves half the bytes)
+            if (qb && kb) {
+                const int64_t kv = (a.dK ? 2 : 0) * a.hk + (a.dV ? 1 : 0) * a.hk;
+                kb = (most * kv + 2 * a.hq + kv - 1) / (2 * a.hq + kv);
+                if (kb > most) kb = most;
+                if (most > kb) qb = most - kb;
+            }
+            switch (lanes_per_head(a.D)) {
+                case 1: launch_bwd_vec<ES, 1>(a, qb, kb, stride, s); break;
+                case 2: launch_bwd_vec<ES, 2>(a, qb, kb, stride, s); break;
+                case 4: launch_bwd_vec<ES, 4>(a, qb, kb, stride, s); break;
+                case 8: launch_bwd_vec<ES, 8>(a, qb, kb, stride, s); break;
+                case 16: launch_bwd_vec<ES, 16>(a, qb, kb, stride, s); break;
+                default: launch_bwd_vec<ES, 32>(a, qb, kb, stride, s); break;
+            }
+            if (!a.dK) kb = 0;                      // value copies leave no sums
         }
         const hipError_t e = hipGetLastError();
         if (e != hipSuccess) return e;
     }
-    if (a.dwq || a.dwk) {
-        const int64_t n = any ? blocks : 0;   // no tokens: zero gradients
-        weight_grad_sum<<<dim3((unsigned)((2 * a.D + 15) / 16)), dim3(HT), 0, s>>>(a.partials, n, a.D, a.dwq, a.dwk);
-    }
+    if (a.dwq || a.dwk)   // no tokens or no gradient of a kind: zeros
+        weight_grad_sum<<<dim3((unsigned)((2 * a.D + 3) / 4)), dim3(HT), 0, s>>>(a.partials, stride, qb, kb, a.D, a.dwq, a.dwk);
     return hipGetLastError();
 }
 
 }  // namespace
 
-// One wavefront a token up to 512 workgroups, then more tokens each.
+// One wavefront a token up to 768 workgroups (three wavefronts on each SIMD of
+// 256 CUs), then more tokens each.
 int64_t qk_backward_blocks(int64_t T) {
     const int64_t b = (T + HT / 64 - 1) / (HT / 64);
-    return b < 1 ? 1 : b > 512 ? 512 : b;
+    return b < 1 ? 1 : b > 768 ? 768 : b;
 }
 
 hipError_t launch_qk_norm_rope(const HeadArgs &a, int es, hipStream_t s) {

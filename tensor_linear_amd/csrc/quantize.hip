@@ -8,9 +8,12 @@
 // with r = rint(x * (1/s)) off by at most one, e = x - r s is exact in one fused
 // multiply-add (r has 7 bits; the difference is a multiple of the smaller ulp
 // and at most about s / 2), and comparing |e| with s / 2 settles the last step.
-// That costs four instructions more than rounding x * (1/s), and keeps results
-// the same wherever the quotient is computed (bf16 inputs hit halves often: x =
-// a / 2 is 63.5).
+// That keeps results the same wherever the quotient is computed (bf16 inputs hit
+// halves often: x = a / 2 is 63.5).  Most values need none of it: a wavefront
+// first rounds 8 values a lane by adding 1.5 * 2^23 in one multiply-add (the sum's
+// low byte is the whole number), and only where some lane's distance from its
+// whole number is within 2^-15 of a half -- x * (1/s) is off by less than 2^-16 --
+// does it go through those 8 again exactly.
 //
 // HBM-bound, one read and one write: a wavefront (or a workgroup of four, for
 // groups over 2048 columns) holds its group in registers between the maximum and
@@ -32,22 +35,53 @@ typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 
 constexpr int QT = 256;
 
-// The fp32 bit patterns of 8 consecutive inputs.
+// 8 consecutive inputs as they are: four words of two bf16, or eight fp32.
 template <int IN>
-__device__ __forceinline__ void load8(const void *p, int64_t i, uint32_t (&v)[8]) {
-    if (IN == IN_BF16) {
-        const u32x4 h = __builtin_nontemporal_load((const u32x4 *)((const uint16_t *)p + i));
+struct Raw8 { uint32_t w[IN == IN_BF16 ? 4 : 8]; };
+
+template <int IN>
+__device__ __forceinline__ Raw8<IN> load8(const void *p, int64_t i) {
+    Raw8<IN> r;
+    const u32x4 *q = (const u32x4 *)((const char *)p + i * (IN == IN_BF16 ? 2 : 4));
+    const u32x4 a = __builtin_nontemporal_load(q);
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            v[2 * e] = h[e] << 16;
-            v[2 * e + 1] = h[e] & 0xFFFF0000u;
-        }
-    } else {
-        const u32x4 a = __builtin_nontemporal_load((const u32x4 *)((const float *)p + i));
-        const u32x4 b = __builtin_nontemporal_load((const u32x4 *)((const float *)p + i + 4));
+    for (int e = 0; e < 4; ++e) r.w[e] = a[e];
+    if constexpr (IN == IN_F32) {
+        const u32x4 b = __builtin_nontemporal_load(q + 1);
 #pragma unroll
-        for (int e = 0; e < 4; ++e) { v[e] = a[e]; v[4 + e] = b[e]; }
+        for (int e = 0; e < 4; ++e) r.w[4 + e] = b[e];
     }
+    return r;
+}
+
+// Running maximum of the patterns without their signs (bf16: of the low and the
+// high halves apart), and its fp32 pattern.
+template <int IN>
+__device__ __forceinline__ uint32_t max8(uint32_t m, const Raw8<IN> &r) {
+    if constexpr (IN == IN_BF16) {
+        typedef uint16_t u16x2 __attribute__((ext_vector_type(2)));
+        u16x2 a = __builtin_bit_cast(u16x2, m);
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+            a = __builtin_elementwise_max(a, __builtin_bit_cast(u16x2, r.w[e] & 0x7FFF7FFFu));
+        return __builtin_bit_cast(uint32_t, a);
+    } else {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) m = max(m, r.w[e] & 0x7FFFFFFFu);
+        return m;
+    }
+}
+template <int IN>
+__device__ __forceinline__ uint32_t max_bits(uint32_t m) {
+    return IN == IN_BF16 ? max(m << 16, m & 0xFFFF0000u) : m;
+}
+
+// The fp32 patterns of 8 inputs.
+template <int IN>
+__device__ __forceinline__ void widen8(const Raw8<IN> &r, uint32_t (&v)[8]) {
+#pragma unroll
+    for (int e = 0; e < 8; ++e)
+        v[e] = IN == IN_F32 ? r.w[e % (IN == IN_F32 ? 8 : 4)] : (e & 1) ? r.w[e / 2] & 0xFFFF0000u : r.w[e / 2] << 16;
 }
 
 template <int IN>
@@ -87,6 +121,31 @@ __device__ __forceinline__ uint32_t pack4(int a, int b, int c, int d) {
     return (a & 255) | (b & 255) << 8 | (c & 255) << 16 | (uint32_t)d << 24;
 }
 
+// Eight values a lane to bytes; t is uniform over the wavefront.
+__device__ __forceinline__ u32x2 round8(const uint32_t (&v)[8], const Step &t) {
+    constexpr float MAGIC = 12582912.0f;   // 1.5 * 2^23: the sum's ulp is 1
+    if (!t.zero && t.up == 1.0f) {
+        uint32_t u[8];
+        float worst = 0.0f;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            const float x = __uint_as_float(v[e]), w = __builtin_fmaf(x, t.inv, MAGIC);
+            worst = __builtin_fmaxf(worst, __builtin_fabsf(__builtin_fmaf(x, t.inv, MAGIC - w)));
+            u[e] = __float_as_uint(w);
+        }
+        if (!__any(worst >= 0.5f - 0x1p-15f)) {
+            // the low bytes: bytes 0-3 of a permutation select from its second word
+            const uint32_t a = __builtin_amdgcn_perm(u[1], u[0], 0x0c0c0400), b = __builtin_amdgcn_perm(u[3], u[2], 0x0c0c0400);
+            const uint32_t c = __builtin_amdgcn_perm(u[5], u[4], 0x0c0c0400), d = __builtin_amdgcn_perm(u[7], u[6], 0x0c0c0400);
+            return u32x2{__builtin_amdgcn_perm(b, a, 0x05040100), __builtin_amdgcn_perm(d, c, 0x05040100)};
+        }
+    }
+    int q[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) q[e] = round_one(v[e], t);
+    return u32x2{pack4(q[0], q[1], q[2], q[3]), pack4(q[4], q[5], q[6], q[7])};
+}
+
 __device__ __forceinline__ uint32_t wave_max(uint32_t v) {
 #pragma unroll
     for (int o = 32; o > 0; o >>= 1) v = max(v, (uint32_t)__shfl_xor((int)v, o));
@@ -106,17 +165,14 @@ void quantize_vec(QuantizeArgs a) {
     const int g = (int)(grp - m * a.G);
     const int64_t x0 = m * a.ldx + g * a.Kg, q0 = m * a.ldq + g * a.Kg;
     const int first = (W == 1 ? lane : (int)threadIdx.x) * 8;
-    uint32_t v[NV][8];
+    Raw8<IN> raw[NV] = {};
     uint32_t mx = 0;
 #pragma unroll
     for (int c = 0; c < NV; ++c)
-        if (first + c * W * 512 < a.Kg) load8<IN>(a.X, x0 + first + c * W * 512, v[c]);
+        if (first + c * W * 512 < a.Kg) raw[c] = load8<IN>(a.X, x0 + first + c * W * 512);
 #pragma unroll
-    for (int c = 0; c < NV; ++c)
-        if (first + c * W * 512 < a.Kg)
-#pragma unroll
-            for (int e = 0; e < 8; ++e) mx = max(mx, v[c][e] & 0x7FFFFFFFu);
-    mx = wave_max(mx);
+    for (int c = 0; c < NV; ++c) mx = max8<IN>(mx, raw[c]);
+    mx = wave_max(max_bits<IN>(mx));
     if (W > 1) {
         if (lane == 0) red[wave] = mx;
         __syncthreads();
@@ -128,11 +184,10 @@ void quantize_vec(QuantizeArgs a) {
 #pragma unroll
     for (int c = 0; c < NV; ++c) {
         const int k = first + c * W * 512;
-        if (k >= a.Kg) continue;
-        int q[8];
-#pragma unroll
-        for (int e = 0; e < 8; ++e) q[e] = round_one(v[c][e], t);
-        *(u32x2 *)(a.Q + q0 + k) = u32x2{pack4(q[0], q[1], q[2], q[3]), pack4(q[4], q[5], q[6], q[7])};
+        uint32_t v[8];
+        widen8<IN>(raw[c], v);
+        const u32x2 q = round8(v, t);       // every lane takes part: past the group's end on zeros
+        if (k < a.Kg) *(u32x2 *)(a.Q + q0 + k) = q;
     }
 }
 
