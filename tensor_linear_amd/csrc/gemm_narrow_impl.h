@@ -159,11 +159,12 @@ void gemm_narrow_kernel(GemmArgs g, NarrowSched ts, const void *bias_any, int64_
             if constexpr (SW) {
                 // LDS row r feeds wave column r / 64, W block (r / 16) % 4:
                 // blocks 0-1 gate rows, 2-3 the up rows of the same 32 units.
-                int h = ((r >> 6) << 5) + (((r >> 4) & 1) << 4) + (r & 15);
+                int h = ((r >> 6) << 5) + (OP::INT8 ? quant_w_row(r & 31) : (((r >> 4) & 1) << 4) + (r & 15));
                 h = h < b_rows ? h : b_rows - 1;
                 rb = h + (((r >> 4) & 2) ? up_off : 0);
             } else {
-                rb = r < b_rows ? r : b_rows - 1;
+                rb = OP::INT8 ? quant_w_row(r) : r;
+                rb = rb < b_rows ? rb : b_rows - 1;
             }
             boff[j] = (uint32_t)(rb * g.ldb * ES + chunk * 16);
         }
@@ -332,18 +333,10 @@ void gemm_narrow_kernel(GemmArgs g, NarrowSched ts, const void *bias_any, int64_
         };
         const int64_t m_t = (int64_t)tm * FM, tm_w = m_t + wm * 64, tn_w = (int64_t)tn * TBN + wn * (TBN / 2);
         if constexpr (OP::INT8) {
-            GemmExtra ex;   // what the epilogue reads of it
-            ex.bias = bias_any; ex.bias_shard = bias_shard; ex.up_off = up_off;
-            auto at = [&](int r, int sl) __attribute__((always_inline)) { return (LDS_PTR(q_i32x4))st_addr(r, sl); };
-            auto stage = [&](int jj) __attribute__((always_inline)) {
-#pragma unroll
-                for (int bi = 0; bi < WI; ++bi) *(LDS_PTR(Acc))st_addr(frow, bi * 4 + fq) = acc[bi][jj];
-            };
             if constexpr (SW)
-                quant_store_gated<OUT, 4, 4>(g, ex, qa, vec_store, shard, tm_w, tn_w, lane, stage, at);
+                quant_store_gated<OUT, WI, 4>(g, bias_any, bias_shard, up_off, qa, vec_store, shard, tm_w, tn_w, lane, acc);
             else
-                quant_store<OUT, 4, 1, 16, 2 * WI>(g, ex, qa, vec_store, shard, tm_w, tn_w, lane,
-                    [&](int jj, int) __attribute__((always_inline)) { stage(jj); }, at);
+                quant_store<OUT, WI, 4>(g, bias_any, bias_shard, qa, vec_store, shard, tm_w, tn_w, lane, acc);
         } else {
         const int64_t cbase = (int64_t)shard * g.c_shard;
         const __bf16 *bias = bias_all ? bias_all + (int64_t)shard * bias_shard : nullptr;

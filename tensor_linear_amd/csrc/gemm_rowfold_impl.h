@@ -167,7 +167,7 @@ void gemm_rowfold_kernel(GemmArgs g, FoldSched ts, ReduceArgs ro, int vec_store,
         for (int j = 0; j < LW; ++j) {
             const int r = (j * 4 + wave) * 8 + lane / 8;
             const int chunk = (lane % 8) ^ ((r / 2) % 8);
-            const int rb = r < b_rows ? r : b_rows - 1;
+            const int wr = OP::INT8 ? quant_w_row(r) : r, rb = wr < b_rows ? wr : b_rows - 1;
             boff[j] = (uint32_t)((int64_t)rb * g.ldb * ES + chunk * 16);
         }
     };
@@ -399,13 +399,29 @@ void gemm_rowfold_kernel(GemmArgs g, FoldSched ts, ReduceArgs ro, int vec_store,
             ybase = (Out *)ro.Y + m_t * ro.ldy;
         }
         const Out *bias = (const Out *)ro.bias;
+        if constexpr (OP::INT8) {
+            // lane: columns 32p + 8 (lane / 16) .. + 7 of row lane % 16 of its blocks
+            const int64_t n1 = tn_w + fq * 8;
+            float sw[2][8];
+            QuantBias<OUT> bv[2];
+#pragma unroll
+            for (int p = 0; p < 2; ++p) {
+                quant_load_f32<8>(qa.w_scale, n1 + p * 32, g.N, sw[p]);
+                bv[p] = quant_load_bias<OUT>(ro.bias, 0, n1 + p * 32, g.N);
+            }
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                __builtin_amdgcn_sched_barrier(0);
+                quant_put_rows<OUT, 2>(ybase, ro.ldy, tm_w - m_t + j * 16, g.M - m_t, n1, g.N, vec_store, lane, [&](int p, int e) __attribute__((always_inline)) {
+                    return __builtin_bit_cast(int, __builtin_fmaf(run[2 * p + (e >> 2)][j][e & 3], sw[p][e], quant_bias<OUT>(bv[p], e)));
+                });
+            }
+        } else {
         const int c8 = lane & 7;
         const int64_t ncol = tn_w + c8 * 8;
         float bv[8];
 #pragma unroll
         for (int e = 0; e < 8; ++e) bv[e] = bias && ncol + e < g.N ? (float)bias[ncol + e] : 0.0f;
-        float sw[8] = {};
-        if (OP::INT8) quant_load_f32<8>(qa.w_scale, ncol, g.N, sw);
 #pragma unroll
         for (int jj = 0; jj < 4; ++jj) {        // rows 32jj.. of the wave
             __builtin_amdgcn_sched_barrier(0);
@@ -427,12 +443,6 @@ void gemm_rowfold_kernel(GemmArgs g, FoldSched ts, ReduceArgs ro, int vec_store,
                 const int64_t m = tm_w + jj * 32 + rr;
                 if (m >= g.M) continue;
                 float v[8] = {a0[p][0], a0[p][1], a0[p][2], a0[p][3], a1[p][0], a1[p][1], a1[p][2], a1[p][3]};
-                if constexpr (OP::INT8) {
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) v[e] = __builtin_fmaf(v[e], sw[e], bv[e]);
-                    quant_put8<OUT>(ybase, (m - m_t) * ro.ldy, ncol, g.N, vec_store, v);
-                    continue;
-                }
                 bf16x8 hv;
 #pragma unroll
                 for (int e = 0; e < 8; ++e) hv[e] = (__bf16)(bias ? v[e] + bv[e] : v[e]);
@@ -445,6 +455,7 @@ void gemm_rowfold_kernel(GemmArgs g, FoldSched ts, ReduceArgs ro, int vec_store,
                         if (ncol + e < g.N) row[ncol + e] = hv[e];
                 }
             }
+        }
         }
         drained = false;
     }
@@ -519,7 +530,7 @@ void gemm_rowfold8_kernel(GemmArgs g, FoldSched ts, ReduceArgs ro, int vec_store
         for (int j = 0; j < LW; ++j) {
             const int r = (j * FW8 + wave) * 8 + lane / 8;
             const int chunk = (lane % 8) ^ ((r / 2) % 8);
-            const int rb = r < b_rows ? r : b_rows - 1;
+            const int wr = OP::INT8 ? quant_w_row(r) : r, rb = wr < b_rows ? wr : b_rows - 1;
             boff[j] = (uint32_t)((int64_t)rb * g.ldb * ES + chunk * 16);
         }
     };
@@ -729,13 +740,29 @@ void gemm_rowfold8_kernel(GemmArgs g, FoldSched ts, ReduceArgs ro, int vec_store
             ybase = (Out *)ro.Y + m_t * ro.ldy;
         }
         const Out *bias = (const Out *)ro.bias;
+        if constexpr (OP::INT8) {
+            // lane: columns 32p + 8 (lane / 16) .. + 7 of row lane % 16 of its blocks
+            const int64_t n1 = tn_w + fq * 8;
+            float sw[2][8];
+            QuantBias<OUT> bv[2];
+#pragma unroll
+            for (int p = 0; p < 2; ++p) {
+                quant_load_f32<8>(qa.w_scale, n1 + p * 32, g.N, sw[p]);
+                bv[p] = quant_load_bias<OUT>(ro.bias, 0, n1 + p * 32, g.N);
+            }
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                __builtin_amdgcn_sched_barrier(0);
+                quant_put_rows<OUT, 2>(ybase, ro.ldy, tm_w - m_t + j * 16, g.M - m_t, n1, g.N, vec_store, lane, [&](int p, int e) __attribute__((always_inline)) {
+                    return __builtin_bit_cast(int, __builtin_fmaf(run[2 * p + (e >> 2)][j][e & 3], sw[p][e], quant_bias<OUT>(bv[p], e)));
+                });
+            }
+        } else {
         const int c8 = lane & 7;
         const int64_t ncol = tn_w + c8 * 8;
         float bv[8];
 #pragma unroll
         for (int e = 0; e < 8; ++e) bv[e] = bias && ncol + e < g.N ? (float)bias[ncol + e] : 0.0f;
-        float sw[8] = {};
-        if (OP::INT8) quant_load_f32<8>(qa.w_scale, ncol, g.N, sw);
 #pragma unroll
         for (int jj = 0; jj < 4; ++jj) {        // rows 16jj.. of the wave
             __builtin_amdgcn_sched_barrier(0);
@@ -755,12 +782,6 @@ void gemm_rowfold8_kernel(GemmArgs g, FoldSched ts, ReduceArgs ro, int vec_store
                 const int64_t m = tm_w + jj * 16 + rr;
                 if (m >= g.M) continue;
                 float v[8] = {a0[p][0], a0[p][1], a0[p][2], a0[p][3], a1[p][0], a1[p][1], a1[p][2], a1[p][3]};
-                if constexpr (OP::INT8) {
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) v[e] = __builtin_fmaf(v[e], sw[e], bv[e]);
-                    quant_put8<OUT>(ybase, (m - m_t) * ro.ldy, ncol, g.N, vec_store, v);
-                    continue;
-                }
                 bf16x8 hv;
 #pragma unroll
                 for (int e = 0; e < 8; ++e) hv[e] = (__bf16)(bias ? v[e] + bv[e] : v[e]);
@@ -773,6 +794,7 @@ void gemm_rowfold8_kernel(GemmArgs g, FoldSched ts, ReduceArgs ro, int vec_store
                         if (ncol + e < g.N) row[ncol + e] = hv[e];
                 }
             }
+        }
         }
         drained = false;
     }

@@ -252,7 +252,8 @@ void gemm_skinny_kernel(GemmArgs g, FoldArgs f, GemmExtra ex, QuantArgs qa) {
                         gf = gv;
                         uf = uv;
                     }
-                    store_out<OUT>(g.C, (int64_t)shard * g.c_shard + m * g.ldc + n, silu_f32(gf) * uf);
+                    store_out<OUT>(g.C, (int64_t)shard * g.c_shard + m * g.ldc + n,
+                                   (OP::INT8 ? quant_silu(gf) : silu_f32(gf)) * uf);
                 }
             }
         } else {

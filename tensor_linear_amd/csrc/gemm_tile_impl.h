@@ -196,11 +196,12 @@ void gemm_tile_kernel(GemmArgs g, TileSched ts, int vec_store, GemmExtra ex, Qua
                 // blocks 0-3 gate rows, blocks 4-7 the up rows of the same
                 // 64 hidden units.
                 const int blk = (r >> 4) & 7;
-                int h = ((r >> 7) << 6) + ((blk & 3) << 4) + (r & 15);
+                int h = ((r >> 7) << 6) + (OP::INT8 ? quant_w_row(((blk & 3) << 4) + (r & 15)) : ((blk & 3) << 4) + (r & 15));
                 h = h < b_rows ? h : b_rows - 1;
                 wrow = h + (blk >= 4 ? ex.up_off : 0);
             } else {
-                wrow = r < b_rows ? r : b_rows - 1;
+                wrow = OP::INT8 ? quant_w_row(r) : r;
+                wrow = wrow < b_rows ? wrow : b_rows - 1;
             }
             aoff[j] = (uint32_t)((int64_t)ra * g.lda * ES + chunk * 16);
             boff[j] = (uint32_t)(wrow * g.ldb * ES + chunk * 16);
@@ -395,15 +396,7 @@ void gemm_tile_kernel(GemmArgs g, TileSched ts, int vec_store, GemmExtra ex, Qua
             const bool has_bias = EPI == EPI_BIAS && ex.bias != nullptr;
             const __bf16 *bias = has_bias ? (const __bf16 *)ex.bias + (int64_t)shard * ex.bias_shard : nullptr;
             if constexpr (OP::INT8) {
-                quant_store<OUT, 4, 2, 32, 8>(g, ex, qa, vec_store, shard, tm_w, tn_w, lane,
-                    [&](int j, int ip) __attribute__((always_inline)) {
-#pragma unroll
-                        for (int bj = 0; bj < 2; ++bj)
-#pragma unroll
-                            for (int bi = 0; bi < 4; ++bi)
-                                *(LDS_PTR(Acc))st_addr(bj * 16 + frow, bi * 4 + fq) = acc[4 * ip + bi][2 * j + bj];
-                    },
-                    [&](int r, int sl) __attribute__((always_inline)) { return (LDS_PTR(q_i32x4))st_addr(r, sl); });
+                quant_store<OUT, 8, 8>(g, ex.bias, ex.bias_shard, qa, vec_store, shard, tm_w, tn_w, lane, acc);
             } else
 #pragma unroll
             for (int j = 0; j < 4; ++j) {          // output rows 32j.. of the wave
@@ -517,12 +510,7 @@ void gemm_tile_kernel(GemmArgs g, TileSched ts, int vec_store, GemmExtra ex, Qua
             const int64_t tm_w = (int64_t)tm * TB + wm * 128, tn_w = (int64_t)tn * TBN + wn * 64;
             const bool interior = vec_store && (int64_t)tm * TB + TB <= g.M && (int64_t)tn * TBN + TBN <= g.N;
             if constexpr (OP::INT8) {
-                quant_store_gated<OUT, 8, 8>(g, ex, qa, vec_store, shard, tm_w, tn_w, lane,
-                    [&](int j) __attribute__((always_inline)) {
-#pragma unroll
-                        for (int i = 0; i < 8; ++i) *(LDS_PTR(Acc))sw_addr(frow, i * 4 + fq) = acc[i][j];
-                    },
-                    [&](int r, int sl) __attribute__((always_inline)) { return (LDS_PTR(q_i32x4))sw_addr(r, sl); });
+                quant_store_gated<OUT, 8, 8>(g, ex.bias, ex.bias_shard, ex.up_off, qa, vec_store, shard, tm_w, tn_w, lane, acc);
             } else {
             const bool has_bias = ex.bias != nullptr;
             const int c8 = lane & 7;                       // 8 hidden units from 8*c8

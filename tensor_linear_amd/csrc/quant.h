@@ -25,6 +25,13 @@ __device__ __forceinline__ float quant_value(int32_t acc, float sx, float sw, fl
     return __builtin_fmaf((float)acc * sx, sw, bias);
 }
 
+// silu(v) = v / (1 + e^-v) with the hardware's reciprocal (1 ulp) in place of the
+// divide's ten instructions, which were 4% of a gated layer's time (M = 4096,
+// 4096 -> 2 x 14336: 371 -> 356 us).  For v below -87.3 the reciprocal is 0.
+__device__ __forceinline__ float quant_silu(float v) {
+    return v * __builtin_amdgcn_rcpf(1.0f + __expf(-v));
+}
+
 // Any shape, stride or alignment; every output type, bias and the gated unit.
 // GemmArgs counts elements (bytes of A and B); ex as for the bf16 kernels
 // (x_rows is not taken).

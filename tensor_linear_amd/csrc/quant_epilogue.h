@@ -1,6 +1,8 @@
-// Epilogues of the int8 shard GEMM kernels: int32 sums staged in LDS by a wave,
-// read back row by row, scaled (quant_value), and stored as whole row pieces.
+// Epilogues of the int8 shard GEMM kernels: a wave's int32 sums, scaled
+// (quant_value) and stored from its registers.
 #pragma once
+
+#include <type_traits>
 
 #include "kernels.h"
 #include "quant.h"
@@ -8,8 +10,6 @@
 namespace tpl {
 
 typedef int q_i32x4 __attribute__((ext_vector_type(4)));
-typedef float q_f32x4 __attribute__((ext_vector_type(4)));
-typedef __bf16 q_bf16x8 __attribute__((ext_vector_type(8)));
 
 // N values of fp32 `p` from n on, those past `end` read as element 0.
 template <int N>
@@ -22,170 +22,182 @@ __device__ __forceinline__ void quant_load_f32(const float *p, int64_t n, int64_
     }
 }
 
-// N bias values of the output type from n on (0 without a bias).
-template <int OUT, int N>
-__device__ __forceinline__ void quant_load_bias(const void *b, int64_t base, int64_t n, int64_t end, float *v) {
-#pragma unroll
-    for (int e = 0; e < N; ++e) {
-        const int64_t i = base + (n + e < end ? n + e : 0);
-        v[e] = !b ? 0.0f : OUT == OUT_BF16 ? (float)((const __bf16 *)b)[i] : ((const float *)b)[i];
-    }
-}
-
-// Eight outputs of one row from column n on.
+// Eight bias values of the output type from n on, as they are held (zeros
+// without a bias), and one of them in fp32.
 template <int OUT>
-__device__ __forceinline__ void quant_put8(void *C, int64_t row, int64_t n, int64_t N, bool vec, const float *v) {
-    if (OUT == OUT_BF16) {
-        q_bf16x8 h;
+struct QuantBias { uint32_t w[OUT == OUT_BF16 ? 4 : 8]; };
+template <int OUT>
+__device__ __forceinline__ QuantBias<OUT> quant_load_bias(const void *b, int64_t base, int64_t n, int64_t end) {
+    QuantBias<OUT> r = {};
+    constexpr int ES = OUT == OUT_BF16 ? 2 : 4;
+    if (!b) return r;
+    const char *p = (const char *)b + base * ES;
+    if (n + 8 <= end) {
+        __builtin_memcpy(r.w, p + n * ES, 8 * ES);
+    } else {
 #pragma unroll
-        for (int e = 0; e < 8; ++e) h[e] = (__bf16)v[e];
-        __bf16 *dst = (__bf16 *)C + row + n;
-        if (vec && n + 8 <= N) {
-            __builtin_nontemporal_store(h, (q_bf16x8 *)dst);
-        } else {
+        for (int e = 0; e < 8; ++e) {
+            const int64_t i = n + e < end ? n + e : 0;
+            if (ES == 2) r.w[e / 2] |= (uint32_t)((const uint16_t *)p)[i] << (16 * (e & 1));
+            else r.w[e] = ((const uint32_t *)p)[i];
+        }
+    }
+    return r;
+}
+template <int OUT>
+__device__ __forceinline__ float quant_bias(const QuantBias<OUT> &b, int e) {
+    return __uint_as_float(OUT != OUT_BF16 ? b.w[e] : (e & 1) ? b.w[e / 2] & 0xFFFF0000u : b.w[e / 2] << 16);
+}
+
+// 16 bytes of outputs: 8 (bf16) or 4 (fp32, int32) columns of a row from n on.
+template <int OUT>
+__device__ __forceinline__ void quant_put16(void *C, int64_t row, int64_t n, int64_t N, bool vec, q_i32x4 v) {
+    typedef typename std::conditional<OUT == OUT_BF16, uint16_t, uint32_t>::type T;
+    constexpr int E = OUT == OUT_BF16 ? 8 : 4;
+    T *dst = (T *)C + row + n;
+    if (vec && n + E <= N) {
+        __builtin_nontemporal_store(v, (q_i32x4 *)dst);
+    } else {
 #pragma unroll
-            for (int e = 0; e < 8; ++e)
-                if (n + e < N) dst[e] = h[e];
+        for (int e = 0; e < E; ++e)
+            if (n + e < N) dst[e] = (T)((uint32_t)v[e * 4 / E] >> (E == 8 ? 16 * (e & 1) : 0));
+    }
+}
+
+// Lanes 0-7 of each 16 give b and take the others' a; lanes 8-15 give a and take
+// the others' b: with a and b two 16-byte pieces of a lane's output row, v1 is
+// a piece of rows 0-7 and v2 of rows 8-15, the same piece for eight lanes each.
+__device__ __forceinline__ void quant_swap8(bool hi, q_i32x4 a, q_i32x4 b, q_i32x4 &v1, q_i32x4 &v2) {
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+        const int y = __builtin_amdgcn_mov_dpp(hi ? a[e] : b[e], 0x128 /* row_ror:8 */, 0xf, 0xf, false);
+        v1[e] = hi ? y : a[e];
+        v2[e] = hi ? b[e] : y;
+    }
+}
+
+// Stores NP pairs of blocks of one 16-row block: val(p, e) is the lane's output in
+// column n1 + 32 p + e of row m0 + lane % 16 (n1: 8 (lane / 16) on from the wave's
+// first column), as fp32 or int32 bits.  The lanes exchange 16-byte pieces first,
+// so that a store instruction writes eight rows of 128 bytes (two pairs of bf16,
+// one of fp32) and not sixteen of 64.
+template <int OUT, int NP, class Val>
+__device__ __forceinline__ void quant_put_rows(void *C, int64_t ld, int64_t m0, int64_t M, int64_t n1, int64_t N,
+                                               bool vec, int lane, Val val) {
+    const bool hi = lane & 8;
+    const int64_t r1 = m0 + (lane & 7);
+    auto pack = [&](int p) {
+        q_i32x4 d;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+            d[e] = __builtin_bit_cast(int, bf16x2{(__bf16)__builtin_bit_cast(float, val(p, 2 * e)),
+                                                  (__bf16)__builtin_bit_cast(float, val(p, 2 * e + 1))});
+        }
+        return d;
+    };
+    auto put2 = [&](q_i32x4 a, q_i32x4 b, int64_t n) {
+        q_i32x4 v1, v2;
+        quant_swap8(hi, a, b, v1, v2);
+        if (r1 < M) quant_put16<OUT>(C, r1 * ld, n, N, vec, v1);
+        if (r1 + 8 < M) quant_put16<OUT>(C, (r1 + 8) * ld, n, N, vec, v2);
+    };
+    if constexpr (OUT == OUT_BF16) {
+#pragma unroll
+        for (int p = 0; p + 1 < NP; p += 2) put2(pack(p), pack(p + 1), n1 + 32 * p + (hi ? 32 : 0));
+        if (NP & 1) {
+            const int64_t m = m0 + (lane & 15);
+            if (m < M) quant_put16<OUT>(C, m * ld, n1 + 32 * (NP - 1), N, vec, pack(NP - 1));
         }
     } else {
-        float *dst = (float *)C + row + n;
-        if (vec && n + 8 <= N) {
-            __builtin_nontemporal_store(q_f32x4{v[0], v[1], v[2], v[3]}, (q_f32x4 *)dst);
-            __builtin_nontemporal_store(q_f32x4{v[4], v[5], v[6], v[7]}, (q_f32x4 *)(dst + 4));
-        } else {
 #pragma unroll
-            for (int e = 0; e < 8; ++e)
-                if (n + e < N) dst[e] = v[e];
+        for (int p = 0; p < NP; ++p)
+            put2(q_i32x4{val(p, 0), val(p, 1), val(p, 2), val(p, 3)}, q_i32x4{val(p, 4), val(p, 5), val(p, 6), val(p, 7)},
+                 n1 + 32 * p + (hi ? 4 : 0));
+    }
+}
+
+// The int8 kernels place W rows in LDS so that two neighbouring 16-row blocks of
+// MFMA results hold 8 consecutive output columns in a lane: LDS row r of such a
+// pair of blocks (32 rows) takes W row quant_w_row(r).  Lane l of blocks 2p, 2p + 1
+// then has columns 32 p + 8 (l / 16) .. + 7 of output row l % 16, scaled and stored
+// without a pass through LDS (which the bf16 forms take for whole-line stores).
+__device__ __forceinline__ int quant_w_row(int r) {
+    return (r & ~31) + ((r >> 2) & 3) * 8 + ((r >> 4) & 1) * 4 + (r & 3);
+}
+
+// A wave's NI x NJ blocks (NI even) at rows m0, columns n0 of shard `shard`; two
+// pairs of blocks at a time, so that their scales and bias stay in registers.
+template <int OUT, int NI, int NJ, class AccT>
+__device__ __forceinline__ void quant_store(const GemmArgs &g, const void *bias, int64_t bias_shard,
+                                            const QuantArgs &qa, bool vec, int shard, int64_t m0,
+                                            int64_t n0, int lane, const AccT (&acc)[NI][NJ]) {
+    constexpr int NP = NI >= 4 ? 2 : 1;
+    const int64_t n1 = n0 + (lane >> 4) * 8;
+    char *C = (char *)g.C + (int64_t)shard * g.c_shard * (OUT == OUT_BF16 ? 2 : 4);
+    float sx[NJ];
+    if constexpr (OUT != OUT_I32) {
+#pragma unroll
+        for (int j = 0; j < NJ; ++j) {
+            const int64_t m = m0 + j * 16 + (lane & 15);
+            sx[j] = qa.x_scale[(int64_t)shard * qa.x_shard + (m < g.M ? m : 0) * qa.x_ld];
+        }
+    }
+#pragma unroll
+    for (int i0 = 0; i0 < NI / 2; i0 += NP) {
+        float sw[NP][8];
+        QuantBias<OUT> bv[NP];
+        if constexpr (OUT != OUT_I32) {
+#pragma unroll
+            for (int p = 0; p < NP; ++p) {
+                quant_load_f32<8>(qa.w_scale + (int64_t)shard * qa.w_shard, n1 + (i0 + p) * 32, g.N, sw[p]);
+                bv[p] = quant_load_bias<OUT>(bias, (int64_t)shard * bias_shard, n1 + (i0 + p) * 32, g.N);
+            }
+        }
+#pragma unroll
+        for (int j = 0; j < NJ; ++j) {
+            __builtin_amdgcn_sched_barrier(0);
+            quant_put_rows<OUT, NP>(C, g.ldc, m0 + j * 16, g.M, n1 + i0 * 32, g.N, vec, lane, [&](int p, int e) __attribute__((always_inline)) {
+                const int v = acc[2 * (i0 + p) + (e >> 2)][j][e & 3];
+                if constexpr (OUT == OUT_I32) return v;
+                else return __builtin_bit_cast(int, quant_value(v, sx[j], sw[p][e], quant_bias<OUT>(bv[p], e)));
+            });
         }
     }
 }
 
-// A wave's block of JN * R rows x IP * LPR8 * 8 columns at (m0, n0) of shard
-// `shard`: stage(j, ip) writes the int32 sums of rows R j.. and columns 8 LPR8
-// ip.. to LDS, and addr(row, s) is the 16 bytes of its columns 4 s..4 s + 3.
-template <int OUT, int JN, int IP, int R, int LPR8, class Stage, class Addr>
-__device__ __forceinline__ void quant_store(const GemmArgs &g, const GemmExtra &ex, const QuantArgs &qa,
-                                            bool vec, int shard, int64_t m0, int64_t n0, int lane,
-                                            Stage stage, Addr addr) {
-    const int64_t cbase = (int64_t)shard * g.c_shard;
-    if constexpr (OUT == OUT_I32) {
-        // lane: 4 columns of a row, so that a 256-byte row leaves as whole lines
-        constexpr int LPR = 2 * LPR8, RP = 64 / LPR;
-        const int c = lane % LPR, r0 = lane / LPR;
-#pragma unroll
-        for (int j = 0; j < JN; ++j)
-#pragma unroll
-            for (int ip = 0; ip < IP; ++ip) {
-                __builtin_amdgcn_sched_barrier(0);
-                stage(j, ip);
-                q_i32x4 a[R / RP];
-#pragma unroll
-                for (int p = 0; p < R / RP; ++p) a[p] = *addr(p * RP + r0, c);
-#pragma unroll
-                for (int p = 0; p < R / RP; ++p) {
-                    const int64_t m = m0 + j * R + p * RP + r0, n = n0 + ip * LPR8 * 8 + c * 4;
-                    if (m >= g.M) continue;
-                    int32_t *dst = (int32_t *)g.C + cbase + m * g.ldc + n;
-                    if (vec && n + 4 <= g.N) {
-                        __builtin_nontemporal_store(a[p], (q_i32x4 *)dst);
-                    } else {
-#pragma unroll
-                        for (int e = 0; e < 4; ++e)
-                            if (n + e < g.N) dst[e] = a[p][e];
-                    }
-                }
-            }
-    } else {
-        constexpr int RP = 64 / LPR8;                     // rows per pass
-        const int c8 = lane % LPR8, r0 = lane / LPR8;
-        const float *xs = qa.x_scale + (int64_t)shard * qa.x_shard;
-        const float *ws = qa.w_scale + (int64_t)shard * qa.w_shard;
-        float sw[IP][8], bv[IP][8], sx[JN][R / RP];
-#pragma unroll
-        for (int ip = 0; ip < IP; ++ip) {
-            quant_load_f32<8>(ws, n0 + ip * LPR8 * 8 + c8 * 8, g.N, sw[ip]);
-            quant_load_bias<OUT, 8>(ex.bias, (int64_t)shard * ex.bias_shard, n0 + ip * LPR8 * 8 + c8 * 8, g.N, bv[ip]);
-        }
-#pragma unroll
-        for (int j = 0; j < JN; ++j)
-#pragma unroll
-            for (int p = 0; p < R / RP; ++p) {
-                const int64_t m = m0 + j * R + p * RP + r0;
-                sx[j][p] = xs[(m < g.M ? m : 0) * qa.x_ld];
-            }
-#pragma unroll
-        for (int j = 0; j < JN; ++j)
-#pragma unroll
-            for (int ip = 0; ip < IP; ++ip) {
-                __builtin_amdgcn_sched_barrier(0);
-                stage(j, ip);
-                q_i32x4 a0[R / RP], a1[R / RP];
-#pragma unroll
-                for (int p = 0; p < R / RP; ++p) {
-                    a0[p] = *addr(p * RP + r0, 2 * c8);
-                    a1[p] = *addr(p * RP + r0, 2 * c8 + 1);
-                }
-#pragma unroll
-                for (int p = 0; p < R / RP; ++p) {
-                    const int64_t m = m0 + j * R + p * RP + r0;
-                    if (m >= g.M) continue;
-                    float v[8];
-#pragma unroll
-                    for (int e = 0; e < 8; ++e)
-                        v[e] = quant_value(e < 4 ? a0[p][e & 3] : a1[p][e & 3], sx[j][p], sw[ip][e], bv[ip][e]);
-                    quant_put8<OUT>(g.C, cbase + m * g.ldc, n0 + ip * LPR8 * 8 + c8 * 8, g.N, vec, v);
-                }
-            }
-    }
-}
-
-// The gated unit: a block of JN * 16 rows x LPR8 * 8 hidden units; stage(j)
-// writes 16 rows, gate sums in slots 0 .. 2 LPR8 - 1 and up sums in the next.
-template <int OUT, int JN, int LPR8, class Stage, class Addr>
-__device__ __forceinline__ void quant_store_gated(const GemmArgs &g, const GemmExtra &ex, const QuantArgs &qa,
-                                                  bool vec, int shard, int64_t m0, int64_t n0, int lane,
-                                                  Stage stage, Addr addr) {
-    constexpr int RP = 64 / LPR8;
-    const int c8 = lane % LPR8, r0 = lane / LPR8;
-    const int64_t n = n0 + c8 * 8, cbase = (int64_t)shard * g.c_shard, b0 = (int64_t)shard * ex.bias_shard;
-    const float *xs = qa.x_scale + (int64_t)shard * qa.x_shard;
+// The gated unit: blocks 0 .. NI/2 - 1 gate sums, the rest the up sums of the same
+// hidden units (16 NI / 2 of them from n0 on).
+template <int OUT, int NI, int NJ, class AccT>
+__device__ __forceinline__ void quant_store_gated(const GemmArgs &g, const void *bias, int64_t bias_shard,
+                                                  int64_t up_off, const QuantArgs &qa, bool vec, int shard,
+                                                  int64_t m0, int64_t n0, int lane, const AccT (&acc)[NI][NJ]) {
+    constexpr int U = NI / 2, NP = U / 2;            // gate blocks, pairs of them
+    const int64_t n1 = n0 + (lane >> 4) * 8, b0 = (int64_t)shard * bias_shard;
     const float *ws = qa.w_scale + (int64_t)shard * qa.w_shard;
-    float swg[8], swu[8], bg[8], bu[8], sx[JN][16 / RP];
-    quant_load_f32<8>(ws, n, g.N, swg);
-    quant_load_f32<8>(ws + ex.up_off, n, g.N, swu);
-    quant_load_bias<OUT, 8>(ex.bias, b0, n, g.N, bg);
-    quant_load_bias<OUT, 8>(ex.bias, b0 + ex.up_off, n, g.N, bu);
+    char *C = (char *)g.C + (int64_t)shard * g.c_shard * (OUT == OUT_BF16 ? 2 : 4);
+    float swg[NP][8], swu[NP][8], sx[NJ];
+    QuantBias<OUT> bg[NP], bu[NP];
 #pragma unroll
-    for (int j = 0; j < JN; ++j)
+    for (int j = 0; j < NJ; ++j) {
+        const int64_t m = m0 + j * 16 + (lane & 15);
+        sx[j] = qa.x_scale[(int64_t)shard * qa.x_shard + (m < g.M ? m : 0) * qa.x_ld];
+    }
 #pragma unroll
-        for (int p = 0; p < 16 / RP; ++p) {
-            const int64_t m = m0 + j * 16 + p * RP + r0;
-            sx[j][p] = xs[(m < g.M ? m : 0) * qa.x_ld];
-        }
+    for (int p = 0; p < NP; ++p) {
+        quant_load_f32<8>(ws, n1 + p * 32, g.N, swg[p]);
+        quant_load_f32<8>(ws + up_off, n1 + p * 32, g.N, swu[p]);
+        bg[p] = quant_load_bias<OUT>(bias, b0, n1 + p * 32, g.N);
+        bu[p] = quant_load_bias<OUT>(bias, b0 + up_off, n1 + p * 32, g.N);
+    }
 #pragma unroll
-    for (int j = 0; j < JN; ++j) {
+    for (int j = 0; j < NJ; ++j) {
         __builtin_amdgcn_sched_barrier(0);
-        stage(j);
-        q_i32x4 gq[16 / RP][2], uq[16 / RP][2];
-#pragma unroll
-        for (int p = 0; p < 16 / RP; ++p)
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                gq[p][h] = *addr(p * RP + r0, 2 * c8 + h);
-                uq[p][h] = *addr(p * RP + r0, 2 * LPR8 + 2 * c8 + h);
-            }
-#pragma unroll
-        for (int p = 0; p < 16 / RP; ++p) {
-            const int64_t m = m0 + j * 16 + p * RP + r0;
-            if (m >= g.M) continue;
-            float v[8];
-#pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                const float gg = quant_value(gq[p][e >> 2][e & 3], sx[j][p], swg[e], bg[e]);
-                v[e] = silu_f32(gg) * quant_value(uq[p][e >> 2][e & 3], sx[j][p], swu[e], bu[e]);
-            }
-            quant_put8<OUT>(g.C, cbase + m * g.ldc, n, g.N, vec, v);
-        }
+        quant_put_rows<OUT, NP>(C, g.ldc, m0 + j * 16, g.M, n1, g.N, vec, lane, [&](int p, int e) __attribute__((always_inline)) {
+            const float gg = quant_value(acc[2 * p + (e >> 2)][j][e & 3], sx[j], swg[p][e], quant_bias<OUT>(bg[p], e));
+            const float uu = quant_value(acc[U + 2 * p + (e >> 2)][j][e & 3], sx[j], swu[p][e], quant_bias<OUT>(bu[p], e));
+            return __builtin_bit_cast(int, quant_silu(gg) * uu);
+        });
     }
 }
 

@@ -136,7 +136,7 @@ void quant_generic_kernel(GemmArgs g, int tiles_m, int tiles_n, GemmExtra ex, Qu
                     float v = quant_value(acc[nb][mb][r], sx, sw[n],
                                           ex.bias ? bias_value<OUT>(ex.bias, bsh + n) : 0.0f);
                     if (SWIGLU)
-                        v = silu_f32(v) * quant_value(acc[1][mb][r], sx, sw[ex.up_off + n],
+                        v = quant_silu(v) * quant_value(acc[1][mb][r], sx, sw[ex.up_off + n],
                                                       ex.bias ? bias_value<OUT>(ex.bias, bsh + ex.up_off + n) : 0.0f);
                     if (OUT == OUT_BF16) ((__bf16 *)g.C)[o] = (__bf16)v;
                     else ((float *)g.C)[o] = v;

@@ -147,9 +147,10 @@ def column_plain(x, sx, w, sw, b, P, act):
     slope = (s * (1 + g * (1 - s))).abs()
     # the fast exponential: its argument rounds at u |g| log2(e), its result at 2 u; then
     # a sum, a quotient and a product
-    # below -87 the quotient is subnormal, and from ln(2^128) = 88.73 on the exponential is
-    # infinite and the quotient 0 (the unit's limit): off by at most 88.73 e^-88.73 < 2.7e-37
-    gone = torch.where(g < -87, 2.7e-37, 0.0) * u.abs()
+    # from 1 + e^-g >= 2^126, that is g <= -87.33, on the hardware's reciprocal is subnormal
+    # and comes out 0, as does the unit: off by |g| e^g, which falls with -g, so by at most
+    # 87.34 * 2^-126 < 1.04e-36
+    gone = torch.where(g < -87.3, 1.04e-36, 0.0) * u.abs()
     return y, slope * eg * u.abs() + (g * s).abs() * eu + y.abs() * (1.5 * g.abs() + 8) * U + gone
 
 
