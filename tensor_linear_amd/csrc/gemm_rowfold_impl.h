@@ -409,13 +409,17 @@ void gemm_rowfold_kernel(GemmArgs g, FoldSched ts, ReduceArgs ro, int vec_store,
                 quant_load_f32<8>(qa.w_scale, n1 + p * 32, g.N, sw[p]);
                 bv[p] = quant_load_bias<OUT>(ro.bias, 0, n1 + p * 32, g.N);
             }
+            auto rows = [&](auto fast) __attribute__((always_inline)) {
 #pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                __builtin_amdgcn_sched_barrier(0);
-                quant_put_rows<OUT, 2>(ybase, ro.ldy, tm_w - m_t + j * 16, g.M - m_t, n1, g.N, vec_store, lane, [&](int p, int e) __attribute__((always_inline)) {
-                    return __builtin_bit_cast(int, __builtin_fmaf(run[2 * p + (e >> 2)][j][e & 3], sw[p][e], quant_bias<OUT>(bv[p], e)));
-                });
-            }
+                for (int j = 0; j < 8; ++j) {
+                    __builtin_amdgcn_sched_barrier(0);
+                    quant_put_rows<decltype(fast)::value, OUT, 2>(ybase, ro.ldy, tm_w - m_t + j * 16, g.M - m_t, tn_w, g.N, vec_store, lane, [&](int p, int e) __attribute__((always_inline)) {
+                        return __builtin_bit_cast(int, __builtin_fmaf(run[2 * p + (e >> 2)][j][e & 3], sw[p][e], quant_bias<OUT>(bv[p], e)));
+                    });
+                }
+            };
+            if (vec_store && tm_w + 128 <= g.M && tn_w + 64 <= g.N && ro.ldy < (1 << 24)) rows(std::true_type{});
+            else rows(std::false_type{});
         } else {
         const int c8 = lane & 7;
         const int64_t ncol = tn_w + c8 * 8;
@@ -750,13 +754,17 @@ void gemm_rowfold8_kernel(GemmArgs g, FoldSched ts, ReduceArgs ro, int vec_store
                 quant_load_f32<8>(qa.w_scale, n1 + p * 32, g.N, sw[p]);
                 bv[p] = quant_load_bias<OUT>(ro.bias, 0, n1 + p * 32, g.N);
             }
+            auto rows = [&](auto fast) __attribute__((always_inline)) {
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                __builtin_amdgcn_sched_barrier(0);
-                quant_put_rows<OUT, 2>(ybase, ro.ldy, tm_w - m_t + j * 16, g.M - m_t, n1, g.N, vec_store, lane, [&](int p, int e) __attribute__((always_inline)) {
-                    return __builtin_bit_cast(int, __builtin_fmaf(run[2 * p + (e >> 2)][j][e & 3], sw[p][e], quant_bias<OUT>(bv[p], e)));
-                });
-            }
+                for (int j = 0; j < 4; ++j) {
+                    __builtin_amdgcn_sched_barrier(0);
+                    quant_put_rows<decltype(fast)::value, OUT, 2>(ybase, ro.ldy, tm_w - m_t + j * 16, g.M - m_t, tn_w, g.N, vec_store, lane, [&](int p, int e) __attribute__((always_inline)) {
+                        return __builtin_bit_cast(int, __builtin_fmaf(run[2 * p + (e >> 2)][j][e & 3], sw[p][e], quant_bias<OUT>(bv[p], e)));
+                    });
+                }
+            };
+            if (vec_store && tm_w + 64 <= g.M && tn_w + 64 <= g.N && ro.ldy < (1 << 24)) rows(std::true_type{});
+            else rows(std::false_type{});
         } else {
         const int c8 = lane & 7;
         const int64_t ncol = tn_w + c8 * 8;

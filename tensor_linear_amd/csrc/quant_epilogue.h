@@ -77,15 +77,18 @@ __device__ __forceinline__ void quant_swap8(bool hi, q_i32x4 a, q_i32x4 b, q_i32
 }
 
 // Stores NP pairs of blocks of one 16-row block: val(p, e) is the lane's output in
-// column n1 + 32 p + e of row m0 + lane % 16 (n1: 8 (lane / 16) on from the wave's
-// first column), as fp32 or int32 bits.  The lanes exchange 16-byte pieces first,
+// column n0 + 8 (lane / 16) + 32 p + e of row m0 + lane % 16, as fp32 or int32 bits.  The lanes exchange 16-byte pieces first,
 // so that a store instruction writes eight rows of 128 bytes (two pairs of bf16,
-// one of fp32) and not sixteen of 64.
-template <int OUT, int NP, class Val>
-__device__ __forceinline__ void quant_put_rows(void *C, int64_t ld, int64_t m0, int64_t M, int64_t n1, int64_t N,
+// one of fp32) and not sixteen of 64.  (n0: the wave's first column.)
+// FAST: every output is inside M x N and 16-byte aligned; the stores are a uniform
+// row address and a 32-bit offset of the lane.
+template <bool FAST, int OUT, int NP, class Val>
+__device__ __forceinline__ void quant_put_rows(void *C, int64_t ld, int64_t m0, int64_t M, int64_t n0, int64_t N,
                                                bool vec, int lane, Val val) {
+    constexpr int ES = OUT == OUT_BF16 ? 2 : 4;
     const bool hi = lane & 8;
     const int64_t r1 = m0 + (lane & 7);
+    const int64_t n1 = n0 + (lane >> 4) * 8;
     auto pack = [&](int p) {
         q_i32x4 d;
 #pragma unroll
@@ -96,15 +99,23 @@ __device__ __forceinline__ void quant_put_rows(void *C, int64_t ld, int64_t m0, 
         }
         return d;
     };
-    auto put2 = [&](q_i32x4 a, q_i32x4 b, int64_t n) {
+    // this lane's place among the piece's rows 0-7, `far` columns on in the upper half
+    char *const base = (char *)C + (m0 * ld + n0) * ES;
+    const uint32_t at = (uint32_t)(((int)(lane & 7) * (int)ld + (lane >> 4) * 8 + (hi ? (OUT == OUT_BF16 ? 32 : 4) : 0)) * ES);
+    auto put2 = [&](q_i32x4 a, q_i32x4 b, int64_t n, int p) {
         q_i32x4 v1, v2;
         quant_swap8(hi, a, b, v1, v2);
+        if constexpr (FAST) {
+            __builtin_nontemporal_store(v1, (q_i32x4 *)(base + p * (32 * ES) + at));
+            __builtin_nontemporal_store(v2, (q_i32x4 *)(base + 8 * ld * ES + p * (32 * ES) + at));
+            return;
+        }
         if (r1 < M) quant_put16<OUT>(C, r1 * ld, n, N, vec, v1);
         if (r1 + 8 < M) quant_put16<OUT>(C, (r1 + 8) * ld, n, N, vec, v2);
     };
     if constexpr (OUT == OUT_BF16) {
 #pragma unroll
-        for (int p = 0; p + 1 < NP; p += 2) put2(pack(p), pack(p + 1), n1 + 32 * p + (hi ? 32 : 0));
+        for (int p = 0; p + 1 < NP; p += 2) put2(pack(p), pack(p + 1), n1 + 32 * p + (hi ? 32 : 0), p);
         if (NP & 1) {
             const int64_t m = m0 + (lane & 15);
             if (m < M) quant_put16<OUT>(C, m * ld, n1 + 32 * (NP - 1), N, vec, pack(NP - 1));
@@ -113,7 +124,7 @@ __device__ __forceinline__ void quant_put_rows(void *C, int64_t ld, int64_t m0, 
 #pragma unroll
         for (int p = 0; p < NP; ++p)
             put2(q_i32x4{val(p, 0), val(p, 1), val(p, 2), val(p, 3)}, q_i32x4{val(p, 4), val(p, 5), val(p, 6), val(p, 7)},
-                 n1 + 32 * p + (hi ? 4 : 0));
+                 n1 + 32 * p + (hi ? 4 : 0), p);
     }
 }
 
@@ -126,6 +137,11 @@ __device__ __forceinline__ int quant_w_row(int r) {
     return (r & ~31) + ((r >> 2) & 3) * 8 + ((r >> 4) & 1) * 4 + (r & 3);
 }
 
+// Whether a wave's block that ends before row m and column n takes the FAST form.
+__device__ __forceinline__ bool quant_inside(const GemmArgs &g, bool vec, int64_t m, int64_t n) {
+    return vec && m <= g.M && n <= g.N && g.ldc < (1 << 24);
+}
+
 // A wave's NI x NJ blocks (NI even) at rows m0, columns n0 of shard `shard`; two
 // pairs of blocks at a time, so that their scales and bias stay in registers.
 template <int OUT, int NI, int NJ, class AccT>
@@ -135,6 +151,7 @@ __device__ __forceinline__ void quant_store(const GemmArgs &g, const void *bias,
     constexpr int NP = NI >= 4 ? 2 : 1;
     const int64_t n1 = n0 + (lane >> 4) * 8;
     char *C = (char *)g.C + (int64_t)shard * g.c_shard * (OUT == OUT_BF16 ? 2 : 4);
+    const bool inside = quant_inside(g, vec, m0 + NJ * 16, n0 + NI * 16);
     float sx[NJ];
     if constexpr (OUT != OUT_I32) {
 #pragma unroll
@@ -154,15 +171,19 @@ __device__ __forceinline__ void quant_store(const GemmArgs &g, const void *bias,
                 bv[p] = quant_load_bias<OUT>(bias, (int64_t)shard * bias_shard, n1 + (i0 + p) * 32, g.N);
             }
         }
+        auto rows = [&](auto fast) __attribute__((always_inline)) {
 #pragma unroll
-        for (int j = 0; j < NJ; ++j) {
-            __builtin_amdgcn_sched_barrier(0);
-            quant_put_rows<OUT, NP>(C, g.ldc, m0 + j * 16, g.M, n1 + i0 * 32, g.N, vec, lane, [&](int p, int e) __attribute__((always_inline)) {
-                const int v = acc[2 * (i0 + p) + (e >> 2)][j][e & 3];
-                if constexpr (OUT == OUT_I32) return v;
-                else return __builtin_bit_cast(int, quant_value(v, sx[j], sw[p][e], quant_bias<OUT>(bv[p], e)));
-            });
-        }
+            for (int j = 0; j < NJ; ++j) {
+                __builtin_amdgcn_sched_barrier(0);
+                quant_put_rows<decltype(fast)::value, OUT, NP>(C, g.ldc, m0 + j * 16, g.M, n0 + i0 * 32, g.N, vec, lane, [&](int p, int e) __attribute__((always_inline)) {
+                    const int v = acc[2 * (i0 + p) + (e >> 2)][j][e & 3];
+                    if constexpr (OUT == OUT_I32) return v;
+                    else return __builtin_bit_cast(int, quant_value(v, sx[j], sw[p][e], quant_bias<OUT>(bv[p], e)));
+                });
+            }
+        };
+        if (inside) rows(std::true_type{});
+        else rows(std::false_type{});
     }
 }
 
@@ -190,15 +211,19 @@ __device__ __forceinline__ void quant_store_gated(const GemmArgs &g, const void 
         bg[p] = quant_load_bias<OUT>(bias, b0, n1 + p * 32, g.N);
         bu[p] = quant_load_bias<OUT>(bias, b0 + up_off, n1 + p * 32, g.N);
     }
+    auto rows = [&](auto fast) __attribute__((always_inline)) {
 #pragma unroll
-    for (int j = 0; j < NJ; ++j) {
-        __builtin_amdgcn_sched_barrier(0);
-        quant_put_rows<OUT, NP>(C, g.ldc, m0 + j * 16, g.M, n1, g.N, vec, lane, [&](int p, int e) __attribute__((always_inline)) {
-            const float gg = quant_value(acc[2 * p + (e >> 2)][j][e & 3], sx[j], swg[p][e], quant_bias<OUT>(bg[p], e));
-            const float uu = quant_value(acc[U + 2 * p + (e >> 2)][j][e & 3], sx[j], swu[p][e], quant_bias<OUT>(bu[p], e));
-            return __builtin_bit_cast(int, quant_silu(gg) * uu);
-        });
-    }
+        for (int j = 0; j < NJ; ++j) {
+            __builtin_amdgcn_sched_barrier(0);
+            quant_put_rows<decltype(fast)::value, OUT, NP>(C, g.ldc, m0 + j * 16, g.M, n0, g.N, vec, lane, [&](int p, int e) __attribute__((always_inline)) {
+                const float gg = quant_value(acc[2 * p + (e >> 2)][j][e & 3], sx[j], swg[p][e], quant_bias<OUT>(bg[p], e));
+                const float uu = quant_value(acc[U + 2 * p + (e >> 2)][j][e & 3], sx[j], swu[p][e], quant_bias<OUT>(bu[p], e));
+                return __builtin_bit_cast(int, quant_silu(gg) * uu);
+            });
+        }
+    };
+    if (quant_inside(g, vec, m0 + NJ * 16, n0 + U * 16)) rows(std::true_type{});
+    else rows(std::false_type{});
 }
 
 }  // namespace tpl
