@@ -364,6 +364,9 @@ tp_status tp_linear_row_noalloc(const void *X, int64_t ldx, const void *W, int64
 
 /* ---- 8-bit integers ------------------------------------------------------
  *
+ * (These and the calls on heads below run on the current device, to which the
+ * stream and every buffer must belong.)
+ *
  * The same layers with X and W held as int8 and one fp32 scale for each token
  * and each output channel: x ~ x_scale[m] * X[m, k], w ~ w_scale[n] * W[n, k].
  * The integer sums are exact; they are rounded once to fp32 and scaled.

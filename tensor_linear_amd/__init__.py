@@ -202,6 +202,8 @@ def _mat(t, name):
     ld, unit = t.stride()
     if cols > 1 and unit != 1:
         raise ValueError(f"{name} must have unit column stride")
+    if rows > 1 and ld < cols:   # an expanded row: no leading dimension says that
+        raise ValueError(f"{name} must have a row stride of at least its {cols} columns")
     # A one-row view keeps the row stride of the buffer it was cut from when
     # that stride is a valid leading dim (it places the blocks of a [P, 1, N]
     # output); otherwise its leading dim is its width.
@@ -284,6 +286,8 @@ def _block_out(Y, P, rows, cols, name="Y"):
     block, ldy, unit = Y.stride()
     if cols > 1 and unit != 1:
         raise ValueError(f"{name}[0] must have unit column stride")
+    if rows > 1 and ldy < cols:
+        raise ValueError(f"{name}[0] must have a row stride of at least its {cols} columns")
     ldy = max(ldy, cols, 1)
     if P > 1 and block != rows * ldy:
         raise ValueError(f"{name} blocks must be rows*ldy elements apart")
@@ -308,6 +312,15 @@ def _stream(t, stream):
     if t.is_cuda:
         return _torch()._C._cuda_getCurrentRawStream(t.get_device())
     return 0
+
+
+def _here(t, stream):
+    """_stream for a call whose tensors must be on the current device: a stream
+    of another device would run there or here by the runtime's choice, and the
+    kernels' grids are sized for the current one."""
+    if t.get_device() != _torch()._C._cuda_getDevice():
+        raise ValueError(f"the tensors are on {t.device}, which is not the current device")
+    return _stream(t, stream)
 
 
 # ---- entry points ---------------------------------------------------------
@@ -655,7 +668,7 @@ def tp_quantize_rows(X, Q, scale, stream=None) -> None:
     sp, lds, _ = _token_scales(scale, M, (G,), "scale")
     _same_gpu(X, Q, scale)
     check(_get_lib().tp_quantize_rows(xp, ldx, qp, ldq, sp, lds, M, K, G, _dtype_code(X),
-                                      _stream(X, stream)))
+                                      _here(X, stream)))
 
 
 def tp_linear_column_quant(X, x_scale, W, w_scale, Y, P: int, y_mode: int = TP_Y_CONCAT,
@@ -684,7 +697,7 @@ def tp_linear_column_quant(X, x_scale, W, w_scale, Y, P: int, y_mode: int = TP_Y
     _same_gpu(X, x_scale, W, w_scale, Y, bias)
     check(_get_lib().tp_linear_column_quant(xp, ldx, sp, lds, wp, ldw, wsp, _bias_ptr(bias, dt),
                                             yp, ldy, y_mode, act, M, N, K, P, dt,
-                                            _stream(X, stream)))
+                                            _here(X, stream)))
 
 
 def tp_linear_row_quant(X, x_scale, W, w_scale, Y, P: int, mode: int = TP_ROW_SUM,
@@ -734,7 +747,7 @@ def tp_linear_row_quant(X, x_scale, W, w_scale, Y, P: int, mode: int = TP_ROW_SU
     _same_gpu(X, x_scale, W, w_scale, Y, workspace, bias, y_slices)
     check(_get_lib().tp_linear_row_quant(xp, ldx, sp, lds, G, wp, ldw, wsp, _bias_ptr(bias, dt),
                                          yp, ys, ldy, y_slice_stride, mode, wkp, wkb, M, N, K, P,
-                                         dt, _stream(X, stream)))
+                                         dt, _here(X, stream)))
 
 
 # ---- heads of a fused QKV layer -------------------------------------------
@@ -838,7 +851,7 @@ def tp_qk_norm_rope(X, pos, cos, sin, Q, K, P: int, Hq: int, Hkv: int, q_weight=
     kp, ldk = _rows(K, T, Hkv * D, dt, "K")
     _same_gpu(X, pos, cos, sin, Q, K, q_weight, k_weight, bad)
     check(_get_lib().tp_qk_norm_rope(xp, ldx, x_mode, pp, *rot, qp, ldq, kp, ldk, T, Hq, Hkv, D, P,
-                                     dt, _flag(bad), _stream(X, stream)))
+                                     dt, _flag(bad), _here(X, stream)))
 
 
 def tp_qk_norm_rope_workspace_bytes(T: int, D: int) -> int:
@@ -883,7 +896,7 @@ def tp_qk_norm_rope_backward(X, pos, cos, sin, dQ, dK, dX, P: int, Hq: int, Hkv:
         xp, ldx, x_mode, pp, *rot, qp, ldq, kp, ldk, vp, ldv, dxp, lddx,
         None if dq_weight is None else dq_weight.data_ptr(),
         None if dk_weight is None else dk_weight.data_ptr(), wkp, wkb, T, Hq, Hkv, D, P, dt,
-        _flag(bad), _stream(dX, stream)))
+        _flag(bad), _here(dX, stream)))
 
 
 def tp_kv_append(X, cos, sin, past, cu, table, k_cache, v_cache, P: int, Hq: int, Hkv: int,
@@ -924,4 +937,4 @@ def tp_kv_append(X, cos, sin, past, cu, table, k_cache, v_cache, P: int, Hq: int
     check(_get_lib().tp_kv_append(
         xp, ldx, x_mode, *rot, cu.data_ptr(), past.data_ptr(), B, tp, ldt, max_pages,
         k_cache.data_ptr(), v_cache.data_ptr(), shape[0], shape[1], strides[0], strides[1],
-        strides[2], qp, ldq, T, Hq, Hkv, D, P, dt, _flag(bad), _stream(X, stream)))
+        strides[2], qp, ldq, T, Hq, Hkv, D, P, dt, _flag(bad), _here(X, stream)))

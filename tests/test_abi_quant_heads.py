@@ -164,3 +164,21 @@ def test_binding_refusals():
         a.update(bad)
         with pytest.raises((ValueError, TypeError)):
             tl.tp_kv_append(**a)
+
+
+def test_expanded_rows_are_refused():
+    """A view whose rows share memory has no leading dimension; taken as one it
+    would be read or written past its end."""
+    row = torch.zeros((1, 8))
+    i8 = torch.zeros((4, 8), dtype=torch.int8)
+    with pytest.raises(ValueError, match="row stride"):
+        tl.tp_quantize_rows(row.expand(4, 8), i8, torch.zeros(4))
+    with pytest.raises(ValueError, match="row stride"):
+        tl.tp_linear_column_quant(i8[:1].expand(4, 8), torch.zeros(4), i8, torch.zeros(4), torch.zeros((4, 4)), 1)
+    with pytest.raises(ValueError, match="row stride"):
+        tl.tp_linear_column_quant(i8, torch.zeros(4), i8, torch.zeros(4), torch.zeros((2, 1, 2)).expand(2, 4, 2), 2, tl.TP_Y_SHARDS)
+    with pytest.raises(ValueError, match="row stride"):
+        tl.tp_quantize_rows(torch.zeros((4, 8)), i8, torch.zeros(1).expand(4))
+    c = torch.zeros((9, 4))
+    with pytest.raises(ValueError, match="row stride"):
+        tl.tp_qk_norm_rope(torch.zeros((1, 64)).expand(3, 64), torch.zeros(3, dtype=torch.int64), c, c, torch.zeros((3, 32)), None, 2, 4, 2)

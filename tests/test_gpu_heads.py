@@ -408,3 +408,58 @@ def test_backward_in_a_graph():
         torch.cuda.synchronize()
         got = [a.clone() for a in held]
         assert all(torch.equal(a, b) for a, b in zip(got, step())), f"replay {r}"
+
+
+def test_no_tokens_give_zero_weight_gradients():
+    D, z = 64, lambda *s: torch.zeros(s, dtype=torch.bfloat16, device=DEV)  # noqa: E731
+    cos, sin = (dev(a) for a in tables(4, D))
+    dwq, dwk = torch.full((D,), 3.0, device=DEV), torch.full((D,), 3.0, device=DEV)
+    ws = torch.empty(tl.tp_qk_norm_rope_workspace_bytes(0, D), dtype=torch.uint8, device=DEV)
+    tl.tp_qk_norm_rope_backward(z(0, 4 * D), torch.zeros(0, dtype=torch.int64, device=DEV), cos, sin, z(0, 2 * D), z(0, D), z(0, 4 * D), 1, 2, 1,
+                                q_weight=z(D), k_weight=z(D), dq_weight=dwq, dk_weight=dwk, workspace=ws)
+    assert torch.all(dwq == 0) and torch.all(dwk == 0)
+    # a kind without an output gradient has none of the weight either, and its part of dX is left
+    X, dX = dev(values(1, (3, 4 * D), torch.bfloat16)), torch.full((3, 4 * D), 9.0, dtype=torch.bfloat16, device=DEV)
+    ws = torch.empty(tl.tp_qk_norm_rope_workspace_bytes(3, D), dtype=torch.uint8, device=DEV)
+    dwq.fill_(3.0)
+    tl.tp_qk_norm_rope_backward(X, torch.arange(3, device=DEV), cos, sin, None, dev(values(2, (3, D), torch.bfloat16)), dX, 1, 2, 1, q_weight=z(D) + 1,
+                                k_weight=z(D) + 1, dq_weight=dwq, dk_weight=dwk, workspace=ws)
+    assert torch.all(dwq == 0) and float(dwk.abs().sum()) > 0
+    assert torch.all(dX[:, :2 * D] == 9.0) and torch.all(dX[:, 3 * D:] == 9.0) and not torch.any(dX[:, 2 * D:3 * D] == 9.0)
+
+
+def test_tensors_off_the_current_device_are_refused(monkeypatch):
+    x, q, s = torch.zeros((2, 8), device=DEV), torch.zeros((2, 8), dtype=torch.int8, device=DEV), torch.zeros(2, device=DEV)
+    tl.tp_quantize_rows(x, q, s)
+    monkeypatch.setattr(torch._C, "_cuda_getDevice", lambda: 1)
+    with pytest.raises(ValueError, match="current device"):
+        tl.tp_quantize_rows(x, q, s)
+    with pytest.raises(ValueError, match="current device"):
+        tl.tp_qk_norm_rope(torch.zeros((2, 24), device=DEV), None, None, None, torch.zeros((2, 8), device=DEV), None, 1, 1, 1)
+
+
+def test_two_streams_at_once():
+    """Calls on two streams with their own buffers and workspaces."""
+    T, Hq, Hkv, D = 600, 8, 2, 128
+    t = torch.bfloat16
+    N = (Hq + 2 * Hkv) * D
+    cos, sin = (dev(a) for a in tables(T, D))
+    pos, w = torch.arange(T, device=DEV), dev((1 + 0.1 * values(9, (D,), torch.float32)).to(t))
+    args = [[dev(values(10 * k + i, s, t)) for i, s in enumerate(((T, N), (T, Hq * D), (T, Hkv * D)))] for k in range(2)]
+
+    def run(k, stream=None):
+        X, dq, dk = args[k]
+        out = torch.zeros_like(X), torch.empty(D, device=DEV), torch.empty(D, device=DEV)
+        ws = torch.empty(tl.tp_qk_norm_rope_workspace_bytes(T, D), dtype=torch.uint8, device=DEV)
+        torch.cuda.current_stream().synchronize()
+        tl.tp_qk_norm_rope_backward(X, pos, cos, sin, dq, dk, out[0], 2, Hq, Hkv, dV=dk, q_weight=w, k_weight=w, dq_weight=out[1],
+                                    dk_weight=out[2], workspace=ws, stream=stream)
+        return out, ws
+
+    want = [run(k)[0] for k in range(2)]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    got = [run(k, streams[k].cuda_stream) for k in range(2)]
+    torch.cuda.synchronize()
+    for (g, _), w_ in zip(got, want):
+        assert all(torch.equal(a, b) for a, b in zip(g, w_))
