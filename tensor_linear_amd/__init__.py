@@ -314,13 +314,21 @@ def _stream(t, stream):
     return 0
 
 
-def _here(t, stream):
-    """_stream for a call whose tensors must be on the current device: a stream
-    of another device would run there or here by the runtime's choice, and the
-    kernels' grids are sized for the current one."""
-    if t.get_device() != _torch()._C._cuda_getDevice():
+def _here(stream, t, *others):
+    """The stream handle of a call on tensors (None skipped) that must all be
+    on the current device: a stream of another device would run there or here
+    by the runtime's choice, and the kernels' grids are sized for the current
+    one."""
+    dev = t.get_device()
+    for o in others:
+        if o is not None and o.get_device() != dev:
+            _same_gpu(t, *others)
+    c = _torch()._C
+    if dev < 0:
+        _same_gpu(t)
+    if dev != c._cuda_getDevice():
         raise ValueError(f"the tensors are on {t.device}, which is not the current device")
-    return _stream(t, stream)
+    return c._cuda_getCurrentRawStream(dev) if stream is None else int(stream)
 
 
 # ---- entry points ---------------------------------------------------------
@@ -666,9 +674,8 @@ def tp_quantize_rows(X, Q, scale, stream=None) -> None:
     G = scale.shape[1] if scale.dim() == 2 else 1
     _check_p(G)
     sp, lds, _ = _token_scales(scale, M, (G,), "scale")
-    _same_gpu(X, Q, scale)
     check(_get_lib().tp_quantize_rows(xp, ldx, qp, ldq, sp, lds, M, K, G, _dtype_code(X),
-                                      _here(X, stream)))
+                                      _here(stream, X, Q, scale)))
 
 
 def tp_linear_column_quant(X, x_scale, W, w_scale, Y, P: int, y_mode: int = TP_Y_CONCAT,
@@ -694,10 +701,9 @@ def tp_linear_column_quant(X, x_scale, W, w_scale, Y, P: int, y_mode: int = TP_Y
     else:
         yp, _, _, ldy = _mat(Y, "Y")
         _expect_shape(Y, (M, P * On), "Y")
-    _same_gpu(X, x_scale, W, w_scale, Y, bias)
     check(_get_lib().tp_linear_column_quant(xp, ldx, sp, lds, wp, ldw, wsp, _bias_ptr(bias, dt),
                                             yp, ldy, y_mode, act, M, N, K, P, dt,
-                                            _here(X, stream)))
+                                            _here(stream, X, x_scale, W, w_scale, Y, bias)))
 
 
 def tp_linear_row_quant(X, x_scale, W, w_scale, Y, P: int, mode: int = TP_ROW_SUM,
@@ -744,10 +750,10 @@ def tp_linear_row_quant(X, x_scale, W, w_scale, Y, P: int, mode: int = TP_ROW_SU
         wkp, wkb = workspace.data_ptr(), workspace.numel() * workspace.element_size()
     else:
         wkp, wkb = None, 0
-    _same_gpu(X, x_scale, W, w_scale, Y, workspace, bias, y_slices)
+    on = _here(stream, X, x_scale, W, w_scale, Y, workspace, bias, *(y_slices or ()))
     check(_get_lib().tp_linear_row_quant(xp, ldx, sp, lds, G, wp, ldw, wsp, _bias_ptr(bias, dt),
                                          yp, ys, ldy, y_slice_stride, mode, wkp, wkb, M, N, K, P,
-                                         dt, _here(X, stream)))
+                                         dt, on))
 
 
 # ---- heads of a fused QKV layer -------------------------------------------
@@ -781,56 +787,62 @@ def _rows(t, T, cols, dt, name):
     none."""
     if t is None:
         return None, 0
-    p, _, _, ld = _mat(t, name)
-    _expect_shape(t, (T, cols), name)
-    if _dtype_code(t) != dt:
+    p, rows, n, ld = _mat(t, name)
+    if rows != T or n != cols:
+        _expect_shape(t, (T, cols), name)
+    if _DTYPES.get(t.dtype) != dt:
         raise TypeError(f"{name} must have the dtype of the QKV matrix")
     return p, ld
 
 
 def _rotation(cos, sin, q_weight, k_weight, D, dt, eps, style):
     """The rotation's and norms' arguments in the order of the C calls."""
-    torch = _torch()
-    if (cos is None) != (sin is None):
-        raise ValueError("give both cos and sin, or neither")
     n_pos = R = 0
-    if cos is not None:
-        f32 = torch.float32
-        for t, name in ((cos, "cos"), (sin, "sin")):
-            if t.dtype != f32 or t.dim() != 2 or not t.is_contiguous():
-                raise ValueError(f"{name} must be a contiguous float32 [n_pos, R/2] tensor")
-        shape = cos.shape
-        _expect_shape(sin, shape, "sin")
+    cp = sp = wq = wk = None
+    if cos is not None and sin is not None:
+        shape, f32 = cos.shape, _torch_module.float32
+        if cos.dtype != f32 or sin.dtype != f32 or len(shape) != 2 or not (
+                cos.is_contiguous() and sin.is_contiguous()):
+            raise ValueError("cos and sin must be contiguous float32 [n_pos, R/2] tensors")
+        if sin.shape != shape:
+            _expect_shape(sin, shape, "sin")
         n_pos, R = shape[0], 2 * shape[1]
-    for t, name in ((q_weight, "q_weight"), (k_weight, "k_weight")):
-        if t is not None:
-            _expect_shape(t, (D,), name)
-            if D > 1 and t.stride(0) != 1:
-                raise ValueError(f"{name} must be a contiguous 1-D tensor")
-            if _dtype_code(t) != dt:
-                raise TypeError(f"{name} must have the dtype of the QKV matrix")
-    return (None if cos is None else cos.data_ptr(), None if sin is None else sin.data_ptr(),
-            n_pos, R, style, None if q_weight is None else q_weight.data_ptr(),
-            None if k_weight is None else k_weight.data_ptr(), eps)
+        cp, sp = cos.data_ptr(), sin.data_ptr()
+    elif cos is not sin:
+        raise ValueError("give both cos and sin, or neither")
+    if q_weight is not None:
+        wq = _weight(q_weight, D, dt, "q_weight")
+    if k_weight is not None:
+        wk = _weight(k_weight, D, dt, "k_weight")
+    return cp, sp, n_pos, R, style, wq, wk, eps
+
+
+def _weight(t, D, dt, name):
+    if t.shape != (D,):
+        _expect_shape(t, (D,), name)
+    if D > 1 and t.stride(0) != 1:
+        raise ValueError(f"{name} must be a contiguous 1-D tensor")
+    if _DTYPES.get(t.dtype) != dt:
+        raise TypeError(f"{name} must have the dtype of the QKV matrix")
+    return t.data_ptr()
 
 
 def _positions(pos, T, R):
-    torch = _torch()
     if pos is None:
         if R:
             raise ValueError("pos is needed where heads are rotated")
         return None
-    if pos.dtype != torch.int64 or pos.dim() != 1 or (T > 1 and pos.stride(0) != 1):
+    if pos.shape != (T,):
+        _expect_shape(pos, (T,), "pos")
+    if pos.dtype != _torch_module.int64 or (T > 1 and pos.stride(0) != 1):
         raise ValueError("pos must be a contiguous int64 [T] tensor")
-    _expect_shape(pos, (T,), "pos")
     return pos.data_ptr()
 
 
 def _flag(bad):
-    torch = _torch()
     if bad is None:
         return None
-    if bad.dtype != torch.int32 or bad.numel() < 1:
+    if bad.dtype != _torch_module.int32 or bad.numel() < 1:
         raise ValueError("bad must be an int32 tensor")
     return bad.data_ptr()
 
@@ -849,9 +861,9 @@ def tp_qk_norm_rope(X, pos, cos, sin, Q, K, P: int, Hq: int, Hkv: int, q_weight=
     pp = _positions(pos, T, rot[3])
     qp, ldq = _rows(Q, T, Hq * D, dt, "Q")
     kp, ldk = _rows(K, T, Hkv * D, dt, "K")
-    _same_gpu(X, pos, cos, sin, Q, K, q_weight, k_weight, bad)
+    on = _here(stream, X, pos, cos, sin, Q, K, q_weight, k_weight, bad)
     check(_get_lib().tp_qk_norm_rope(xp, ldx, x_mode, pp, *rot, qp, ldq, kp, ldk, T, Hq, Hkv, D, P,
-                                     dt, _flag(bad), _here(X, stream)))
+                                     dt, _flag(bad), on))
 
 
 def tp_qk_norm_rope_workspace_bytes(T: int, D: int) -> int:
@@ -890,13 +902,13 @@ def tp_qk_norm_rope_backward(X, pos, cos, sin, dQ, dK, dX, P: int, Hq: int, Hkv:
         wkp, wkb = workspace.data_ptr(), workspace.numel() * workspace.element_size()
     else:
         wkp, wkb = None, 0
-    _same_gpu(X, pos, cos, sin, dQ, dK, dV, dX, q_weight, k_weight, dq_weight, dk_weight,
-              workspace, bad)
+    on = _here(stream, dX, X, pos, cos, sin, dQ, dK, dV, q_weight, k_weight, dq_weight, dk_weight,
+               workspace, bad)
     check(_get_lib().tp_qk_norm_rope_backward(
         xp, ldx, x_mode, pp, *rot, qp, ldq, kp, ldk, vp, ldv, dxp, lddx,
         None if dq_weight is None else dq_weight.data_ptr(),
         None if dk_weight is None else dk_weight.data_ptr(), wkp, wkb, T, Hq, Hkv, D, P, dt,
-        _flag(bad), _here(dX, stream)))
+        _flag(bad), on))
 
 
 def tp_kv_append(X, cos, sin, past, cu, table, k_cache, v_cache, P: int, Hq: int, Hkv: int,
@@ -912,13 +924,13 @@ def tp_kv_append(X, cos, sin, past, cu, table, k_cache, v_cache, P: int, Hq: int
     xp, ldx, T, D = _qkv(X, P, Hq, Hkv, x_mode, "X")
     dt = _dtype_code(X)
     rot = _rotation(cos, sin, q_weight, k_weight, D, dt, eps, style)
-    if past.dim() != 1:
-        raise ValueError("past must be [B]")
-    B, i32 = past.shape[0], torch.int32
-    for t, shape, name in ((past, (B,), "past"), (cu, (B + 1,), "cu")):
-        _expect_shape(t, shape, name)
-        if t.dtype != i32 or (shape[0] > 1 and t.stride(0) != 1):
-            raise ValueError(f"{name} must be int32 with unit stride")
+    i32 = torch.int32
+    if past.dtype != i32 or cu.dtype != i32 or past.dim() != 1 or cu.dim() != 1 or not (
+            past.is_contiguous() and cu.is_contiguous()):
+        raise ValueError("past [B] and cu [B + 1] must be int32 with unit stride")
+    B = past.shape[0]
+    if cu.shape[0] != B + 1:
+        _expect_shape(cu, (B + 1,), "cu")
     tp, rows, max_pages, ldt = _mat(table, "table")
     if table.dtype != i32 or rows != B:
         raise ValueError(f"table must be int32 [{B}, max_pages]")
@@ -933,8 +945,8 @@ def tp_kv_append(X, cos, sin, past, cu, table, k_cache, v_cache, P: int, Hq: int
     if _dtype_code(k_cache) != dt or _dtype_code(v_cache) != dt:
         raise TypeError("k_cache and v_cache must have the dtype of the QKV matrix")
     qp, ldq = _rows(Q, T, Hq * D, dt, "Q")
-    _same_gpu(X, cos, sin, past, cu, table, k_cache, v_cache, Q, q_weight, k_weight, bad)
+    on = _here(stream, X, cos, sin, past, cu, table, k_cache, v_cache, Q, q_weight, k_weight, bad)
     check(_get_lib().tp_kv_append(
         xp, ldx, x_mode, *rot, cu.data_ptr(), past.data_ptr(), B, tp, ldt, max_pages,
         k_cache.data_ptr(), v_cache.data_ptr(), shape[0], shape[1], strides[0], strides[1],
-        strides[2], qp, ldq, T, Hq, Hkv, D, P, dt, _flag(bad), _here(X, stream)))
+        strides[2], qp, ldq, T, Hq, Hkv, D, P, dt, _flag(bad), on))
