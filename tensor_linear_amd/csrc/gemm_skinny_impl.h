@@ -39,6 +39,7 @@
 #include "kernels.h"
 #include "mfma_ops.h"
 #include "quant.h"
+#include "quant_math.h"
 
 namespace tpl {
 namespace {

@@ -6,6 +6,7 @@
 
 #include "kernels.h"
 #include "quant.h"
+#include "quant_math.h"
 
 namespace tpl {
 

@@ -12,6 +12,7 @@
 // (K or strides not a multiple of 16, unaligned views); bound by its loads'
 // latency (one stage ahead).
 #include "quant.h"
+#include "quant_math.h"
 
 namespace tpl {
 namespace {
