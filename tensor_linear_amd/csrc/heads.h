@@ -15,7 +15,7 @@ namespace tpl {
 // no norm.  An invalid token sets *bad when bad != NULL.
 struct HeadArgs {
     const void *X; int64_t ldx, x_shard;
-    int64_t T;
+    int64_t T, t0;                          // tokens; the first one of a launch
     int32_t P, hq, hk, D, R, pairs;
     const float *cos, *sin; int64_t n_pos;
     const void *wq, *wk; float eps;

@@ -196,10 +196,10 @@ template <int ES, int LH, bool APPEND>
 __global__ __launch_bounds__(HT)
 void heads_vec(HeadArgs a, int parts) {
     const int lane = threadIdx.x & 63;
-    const int64_t w = (int64_t)blockIdx.x * (HT / 64) + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    if (w >= a.T * parts) return;
-    const int64_t t = w / parts;
-    const int part = (int)(w - t * parts);
+    const uint32_t w = blockIdx.x * (HT / 64) + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);   // < 2^26
+    const int64_t t = a.t0 + w / (uint32_t)parts;
+    if (t >= a.T) return;
+    const int part = (int)(w % (uint32_t)parts);
     const int unit = lane % LH;
     const Runs r = runs_of(unit, a.D, a.R, a.pairs);
     const Span sp = span_of(a, a.Q != nullptr, APPEND || a.K, APPEND);
@@ -300,10 +300,10 @@ void heads_any(HeadArgs a) {
     const int lane = threadIdx.x & 63;
     const Span sp = span_of(a, a.Q != nullptr, APPEND || a.K, APPEND);
     const int slots = sp.per * a.P;
-    const int64_t w = (int64_t)blockIdx.x * (HT / 64) + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    if (w >= a.T * slots) return;
-    const int64_t t = w / slots;
-    const Head h = head_of(a, (int)(w - t * slots), sp, slots);
+    const uint32_t w = blockIdx.x * (HT / 64) + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);   // < 2^26
+    const int64_t t = a.t0 + w / (uint32_t)slots;
+    if (t >= a.T) return;
+    const Head h = head_of(a, (int)(w % (uint32_t)slots), sp, slots);
     const Place pl = APPEND ? find_place(a, t, lane) : given_place(a, t);
     if (!pl.ok && pl.mine && a.bad && lane == 0) *a.bad = 1;
     if (APPEND && !pl.mine) return;
@@ -617,6 +617,20 @@ int lanes_per_head(int D) {
     return l;
 }
 
+// Launches with `waves` wavefronts for each token: as many as the tokens need, since
+// one launch has fewer than 2^32 threads.
+template <class Launch>
+hipError_t launch_tokens(HeadArgs a, int64_t waves, Launch launch) {
+    const int64_t T = a.T, most = waves < (1 << 25) ? (1 << 25) / waves : 1;
+    for (a.t0 = 0; a.t0 < T; a.t0 = a.T) {
+        a.T = T - a.t0 < most ? T : a.t0 + most;
+        launch(a, (unsigned)(((a.T - a.t0) * waves + HT / 64 - 1) / (HT / 64)));
+        const hipError_t e = hipGetLastError();
+        if (e != hipSuccess) return e;
+    }
+    return hipSuccess;
+}
+
 template <int ES, int LH, bool APPEND>
 hipError_t launch_vec(const HeadArgs &a, hipStream_t s) {
     const int64_t slots = (int64_t)span_of(a, a.Q != nullptr, APPEND || a.K, APPEND).per * a.P, hw = 64 / LH;
@@ -625,10 +639,9 @@ hipError_t launch_vec(const HeadArgs &a, hipStream_t s) {
     // wavefront a token, which loads its angles and weights once.
     int64_t parts = (8192 + a.T - 1) / a.T;
     if (parts > groups) parts = groups;
-    const int64_t blocks = (a.T * parts + HT / 64 - 1) / (HT / 64);
-    if (blocks > 0x7FFFFFFFll) return hipErrorInvalidConfiguration;
-    heads_vec<ES, LH, APPEND><<<dim3((unsigned)blocks), dim3(HT), 0, s>>>(a, (int)parts);
-    return hipGetLastError();
+    return launch_tokens(a, parts, [&](const HeadArgs &b, unsigned blocks) {
+        heads_vec<ES, LH, APPEND><<<dim3(blocks), dim3(HT), 0, s>>>(b, (int)parts);
+    });
 }
 
 template <int ES, bool APPEND>
@@ -636,11 +649,9 @@ hipError_t launch_fwd(const HeadArgs &a, hipStream_t s) {
     const Span sp = span_of(a, a.Q != nullptr, APPEND || a.K, APPEND);
     if (a.T == 0 || sp.per == 0) return hipSuccess;
     if (!vec_ok<ES>(a, APPEND, false)) {
-        const int64_t waves = a.T * (int64_t)sp.per * a.P;
-        const int64_t blocks = (waves + HT / 64 - 1) / (HT / 64);
-        if (blocks > 0x7FFFFFFFll) return hipErrorInvalidConfiguration;
-        heads_any<ES, APPEND><<<dim3((unsigned)blocks), dim3(HT), 0, s>>>(a);
-        return hipGetLastError();
+        return launch_tokens(a, (int64_t)sp.per * a.P, [&](const HeadArgs &b, unsigned blocks) {
+            heads_any<ES, APPEND><<<dim3(blocks), dim3(HT), 0, s>>>(b);
+        });
     }
     switch (lanes_per_head(a.D)) {
         case 1: return launch_vec<ES, 1, APPEND>(a, s);

@@ -154,7 +154,7 @@ hipError_t launch_quant_fold(const ReduceArgs &r, const QuantArgs &q, bool per_s
     }
     const int64_t work = vec ? r.M * ((r.N + QF_WCOLS - 1) / QF_WCOLS) * 64 : r.M * r.N;
     const int64_t blocks = (work + QF_THREADS - 1) / QF_THREADS;
-    if (blocks > 0x7FFFFFFFll) return hipErrorInvalidConfiguration;
+    if (blocks > 0xFFFFFFFFll / QF_THREADS) return hipErrorInvalidConfiguration;   // 2^32 threads a launch
     const dim3 grid((unsigned)blocks);
     if (out_type == OUT_BF16 && per_shard) launch_t<OUT_BF16, true>(vec, grid, r, q, s);
     else if (out_type == OUT_BF16) launch_t<OUT_BF16, false>(vec, grid, r, q, s);

@@ -155,7 +155,8 @@ hipError_t launch_quant_generic(const GemmArgs &g, int out_type, const GemmExtra
     if (ex.x_rows > 0 || (out_type == OUT_I32 && (sw || ex.bias))) return hipErrorInvalidValue;
     const int on = sw ? QB / 2 : QB;
     const int64_t tm = (g.M + QB - 1) / QB, tn = (g.N + on - 1) / on;
-    if (tm > 0x7FFFFFFFll || tn > 0x7FFFFFFFll || tm * tn > 0x7FFFFFFFll || tm * tn * g.P > 0x7FFFFFFFll)
+    if (tm > 0x7FFFFFFFll || tn > 0x7FFFFFFFll || tm * tn > 0x7FFFFFFFll ||
+        tm * tn * g.P > 0xFFFFFFFFll / 256)   // 2^32 threads a launch
         return hipErrorInvalidConfiguration;
     const dim3 grid((unsigned)(tm * tn * g.P)), block(256);
     const int a = (int)tm, b = (int)tn;

@@ -12,7 +12,7 @@ hipError_t launch_t(const GemmArgs &g, int out_type, const FoldArgs *fold, const
     const bool sw = ex.act == ACT_SWIGLU;
     const int64_t tn = (g.N + (sw ? 16 : BN) - 1) / (sw ? 16 : BN);
     const int64_t blocks = fold ? tn : tn * g.P;
-    if (tn > 0x7FFFFFFFll || blocks > 0x7FFFFFFFll) return hipErrorInvalidConfiguration;
+    if (tn > 0x7FFFFFFFll || blocks > 0xFFFFFFFFll / SK_THREADS) return hipErrorInvalidConfiguration;
     const dim3 grid((unsigned)blocks), block(SK_THREADS);
     const FoldArgs f = fold ? *fold : FoldArgs{nullptr, 0, 0};
     if (sw) {

@@ -214,9 +214,8 @@ void quantize_any(QuantizeArgs a) {
 
 template <int IN>
 hipError_t launch_t(const QuantizeArgs &a, hipStream_t s) {
-    const int64_t groups = a.M * a.G;
-    if (groups > 0x7FFFFFFFll) return hipErrorInvalidConfiguration;
     constexpr int ES = IN == IN_BF16 ? 2 : 4;
+    const int64_t groups = a.M * a.G;
     const bool vec = a.Kg % 8 == 0 && (a.ldx * ES) % 16 == 0 && (uintptr_t)a.X % 16 == 0 &&
                      a.ldq % 8 == 0 && (uintptr_t)a.Q % 8 == 0 && a.Kg <= 8192;
     const dim3 one((unsigned)groups), four((unsigned)((groups + 3) / 4)), block(QT);
@@ -233,7 +232,18 @@ hipError_t launch_t(const QuantizeArgs &a, hipStream_t s) {
 
 hipError_t launch_quantize_rows(const QuantizeArgs &a, int in_type, hipStream_t s) {
     if (a.M == 0 || a.G == 0) return hipSuccess;
-    return in_type == IN_BF16 ? launch_t<IN_BF16>(a, s) : launch_t<IN_F32>(a, s);
+    // One launch has fewer than 2^32 threads: pieces of at most 2^23 groups.
+    const int64_t most = (1 << 23) / a.G;
+    for (int64_t m = 0; m < a.M; m += most) {
+        QuantizeArgs b = a;
+        b.M = a.M - m < most ? a.M - m : most;
+        b.X = (const char *)a.X + m * a.ldx * (in_type == IN_BF16 ? 2 : 4);
+        b.Q = a.Q + m * a.ldq;
+        b.scale = a.scale + m * a.lds;
+        const hipError_t e = in_type == IN_BF16 ? launch_t<IN_BF16>(b, s) : launch_t<IN_F32>(b, s);
+        if (e != hipSuccess) return e;
+    }
+    return hipSuccess;
 }
 
 }  // namespace tpl

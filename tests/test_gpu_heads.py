@@ -463,3 +463,31 @@ def test_two_streams_at_once():
     torch.cuda.synchronize()
     for (g, _), w_ in zip(got, want):
         assert all(torch.equal(a, b) for a, b in zip(g, w_))
+
+
+def test_more_wavefronts_than_one_launch_holds():
+    # a * 1/2 - b * 2 of small whole numbers: exact in bf16
+    T, H, D = 300001, 160, 3
+    x = torch.randint(-8, 9, (T, H * D), device=DEV).to(torch.bfloat16)
+    cos, sin = torch.full((4, 1), 0.5, device=DEV), torch.full((4, 1), 2.0, device=DEV)
+    out = torch.empty_like(x)
+    tl.tp_qk_norm_rope(x, torch.full((T,), 2, device=DEV), cos, sin, out, None, 1, H, 0)
+    v = x.view(T, H, D)
+    a, b = v[..., 0], v[..., 1]
+    want = torch.stack([a * 0.5 - b * 2, b * 0.5 + a * 2, v[..., 2]], -1)
+    assert torch.equal(out.view(T, H, D), want)
+
+
+def test_append_of_more_tokens_than_one_launch_holds():
+    T, D, page = 2 ** 25 + 77, 16, 65536
+    n = (T + page - 1) // page
+    x = torch.randint(-99, 99, (T, 2 * D), dtype=torch.int8, device=DEV).to(torch.bfloat16)
+    table = torch.randperm(n, device=DEV)[None].to(torch.int32)
+    kc, vc = (torch.zeros(n, page, 1, D, dtype=torch.bfloat16, device=DEV) for _ in range(2))
+    zero = torch.zeros(1, dtype=torch.int32, device=DEV)
+    bad = torch.zeros(1, dtype=torch.int32, device=DEV)
+    cu = torch.tensor([0, T], dtype=torch.int32, device=DEV)
+    tl.tp_kv_append(x, None, None, zero, cu, table, kc, vc, 1, 0, 1, bad=bad)
+    for c, part in ((kc, x[:, :D]), (vc, x[:, D:])):
+        assert torch.equal(c.view(n, page, D)[table[0].long()].view(-1, D)[:T], part)
+    assert not bad.item()

@@ -120,6 +120,15 @@ def test_quantize_special_values(K):
     assert torch.equal(Q.cpu(), want)
 
 
+def test_quantize_more_groups_than_one_launch_holds():
+    x = torch.randint(-126, 127, (2 ** 23 + 5, 3), device=DEV).float()
+    x[:, 1] = 127.0
+    q = torch.empty(x.shape, dtype=torch.int8, device=DEV)
+    s = torch.empty(len(x), 1, device=DEV)
+    tl.tp_quantize_rows(x, q, s)
+    assert torch.equal(q.float(), x) and bool((s == 1).all())
+
+
 # ---- column ------------------------------------------------------------------
 
 COLUMN = [  # M, K, N/P (outputs and, gated, up features), P
