@@ -92,9 +92,12 @@ __device__ __forceinline__ int narrow_tile_of(const NarrowSched &ts, int q) {
 // OP: the operands' type (mfma_ops.h).  TAIL (int8 only): K is not a multiple of
 // the step; the last step's chunks past K are loaded from the row's first chunk
 // of that step (X, in bounds) and from zeros (W).
-template <int OUT, int FM, int TN, bool SW = false, class OP = OpBf16, bool TAIL = false>
-__global__ __attribute__((amdgpu_flat_work_group_size(FM * 2, FM * 2),
-                          amdgpu_waves_per_eu(FM / 128, FM / 128)))
+// KS = 2 (int8 with 128 x 64 tiles, one tile a workgroup): two groups of four waves
+// take half of the K steps each, with stages of their own, and add their sums at
+// the end, each storing half of the rows.  Integers: the split changes no result.
+template <int OUT, int FM, int TN, bool SW = false, class OP = OpBf16, bool TAIL = false, int KS = 1>
+__global__ __attribute__((amdgpu_flat_work_group_size(FM * 2 * KS, FM * 2 * KS),
+                          amdgpu_waves_per_eu(FM / 128 * KS, FM / 128 * KS)))
 void gemm_narrow_kernel(GemmArgs g, NarrowSched ts, const void *bias_any, int64_t bias_shard,
                         int vec_store, int64_t up_off, QuantArgs qa) {
     typedef typename OP::Frag Frag;
@@ -104,6 +107,7 @@ void gemm_narrow_kernel(GemmArgs g, NarrowSched ts, const void *bias_any, int64_
     static_assert(TN == 128 || (TN == 64 && FM == 128), "tile shapes");
     static_assert(!SW || (TN == 128 && (OP::INT8 || OUT == OUT_BF16)), "the gated unit: 128 W rows, bf16 out");
     static_assert(OP::INT8 || !TAIL, "bf16: whole steps of K");
+    static_assert(KS == 1 || (OP::INT8 && TN == 64), "two K halves: 128 x 64 tiles of integers");
     constexpr int TBN = SW ? TN / 2 : TN;  // output columns per tile
     constexpr int NW = FM / 32;            // waves
     constexpr int WI = TN / 32;            // 16-column W blocks per wave
@@ -115,19 +119,23 @@ void gemm_narrow_kernel(GemmArgs g, NarrowSched ts, const void *bias_any, int64_
     constexpr int W_BASE = 3 * OPX;        // three X stages, then three W stages
     constexpr int LX = OPX / 1024 / NW;    // X loads per wave per step (4)
     constexpr int LW = OPW / 1024 / NW;    // W loads per wave per step (2 or 4)
-    __shared__ __attribute__((aligned(1024))) char smem[3 * OPX + 3 * OPW];
-    LDS_PTR(char) lds = (LDS_PTR(char))smem;
-    const uint32_t lds_u = (uint32_t)(uintptr_t)lds;
+    constexpr int STAGES = 3 * OPX + 3 * OPW;
+    __shared__ __attribute__((aligned(1024))) char smem[KS * STAGES];
 
     const int tid = threadIdx.x;
     const int lane = tid & 63;
-    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int wave_wg = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int half = KS == 1 ? 0 : wave_wg / NW;   // of K
+    const int wave = KS == 1 ? wave_wg : wave_wg % NW;
+    LDS_PTR(char) lds = (LDS_PTR(char))smem + half * STAGES;
+    const uint32_t lds_u = (uint32_t)(uintptr_t)lds;
     const int wm = wave >> 1, wn = wave & 1;   // 64 tokens x 64 features each
 
     int ntiles = 0;
     while (narrow_tile_of(ts, ntiles) >= 0) ++ntiles;
     if (ntiles == 0) return;
-    const int nk = OP::INT8 ? (int)((g.K + 127) / 128) : (int)(g.K / FBK);       // K steps per tile
+    const int nk_all = OP::INT8 ? (int)((g.K + 127) / 128) : (int)(g.K / FBK);   // K steps per tile
+    const int nk = (nk_all + KS - 1) / KS, k_first = half * nk;                  // this half's, the first one
     const int total = ntiles * nk;
 
     // ---- load cursor: (tile pq of shard psh, step pkt), two steps ahead of
@@ -200,17 +208,21 @@ void gemm_narrow_kernel(GemmArgs g, NarrowSched ts, const void *bias_any, int64_
     // This lane's chunk (the same for all its loads, NW being even) in the last
     // step of K: its offset in the step where it lies past K, else 0.
     const uint32_t my_chunk = (uint32_t)((lane % 8) ^ ((wave & 1) * 4 + lane / 16)) * 16;
-    const uint32_t cut = TAIL && my_chunk >= g.K - (int64_t)(nk - 1) * 128 ? my_chunk : 0;
+    const uint32_t cut = TAIL && my_chunk >= g.K - (int64_t)(nk_all - 1) * 128 ? my_chunk : 0;
     auto load = [&](int slot, int l) __attribute__((always_inline)) {
+        // the second half's step past an odd number of them: zeros for W, and the
+        // last step's X
+        const bool past = KS == 2 && k_first + pkt >= nk_all;
+        const int k = past ? nk_all - 1 : k_first + pkt;
         if (l < LX) {
             uint32_t off = aoff[l];
-            if (TAIL && pkt == nk - 1) off -= cut;
-            dma(pa + (int64_t)pkt * 128, off, lds_u + slot * OPX + (l * NW + wave) * 1024);
-        } else if (TAIL && pkt == nk - 1) {
-            const char *src = cut ? (const char *)zero_chunk : pb + (int64_t)pkt * 128 + boff[l - LX];
+            if (TAIL && k == nk_all - 1) off -= cut;
+            dma(pa + (int64_t)k * 128, off, lds_u + slot * OPX + (l * NW + wave) * 1024);
+        } else if ((TAIL && k == nk_all - 1) || past) {
+            const char *src = cut || past ? (const char *)zero_chunk : pb + (int64_t)k * 128 + boff[l - LX];
             dma64(src, lds_u + W_BASE + slot * OPW + ((l - LX) * NW + wave) * 1024);
         } else
-            dma(pb + (int64_t)pkt * 128, boff[l - LX],
+            dma(pb + (int64_t)k * 128, boff[l - LX],
                 lds_u + W_BASE + slot * OPW + ((l - LX) * NW + wave) * 1024);
     };
 
@@ -332,7 +344,26 @@ void gemm_narrow_kernel(GemmArgs g, NarrowSched ts, const void *bias_any, int64_
             return ep + (r >> 2) * (NW * 1024) + (r & 3) * 256 + ((s ^ (r & 15)) << 4);
         };
         const int64_t m_t = (int64_t)tm * FM, tm_w = m_t + wm * 64, tn_w = (int64_t)tn * TBN + wn * (TBN / 2);
-        if constexpr (OP::INT8) {
+        if constexpr (KS == 2) {
+            // Half 0 takes the other's sums of X blocks 0-1 and stores them, half 1
+            // those of blocks 2-3.  All loads into LDS have ended before the
+            // sums go there.
+            asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+            __syncthreads();
+            Acc *const all = (Acc *)smem + lane;
+            auto at = [&](int h, int i, int j) -> Acc & { return all[((h * NW + wave) * WI * 2 + i * 2 + j) * 64]; };
+#pragma unroll
+            for (int i = 0; i < WI; ++i)
+#pragma unroll
+                for (int j = 0; j < 2; ++j) at(1 - half, i, j) = half ? acc[i][j] : acc[i][2 + j];
+            __syncthreads();
+            Acc sum[WI][2];
+#pragma unroll
+            for (int i = 0; i < WI; ++i)
+#pragma unroll
+                for (int j = 0; j < 2; ++j) sum[i][j] = (half ? acc[i][2 + j] : acc[i][j]) + at(half, i, j);
+            quant_store<OUT, WI, 2>(g, bias_any, bias_shard, qa, vec_store, shard, tm_w + half * 32, tn_w, lane, sum);
+        } else if constexpr (OP::INT8) {
             if constexpr (SW)
                 quant_store_gated<OUT, WI, 4>(g, bias_any, bias_shard, up_off, qa, vec_store, shard, tm_w, tn_w, lane, acc);
             else

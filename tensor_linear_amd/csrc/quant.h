@@ -41,7 +41,7 @@ bool quant_rowfold_supported(const GemmArgs &g, const ReduceArgs &r, const Quant
 hipError_t launch_quant_rowfold(const GemmArgs &g, const ReduceArgs &r, const QuantArgs &q,
                                 int out_type, hipStream_t s);
 
-// Up to 48 tokens, streaming W; fold != NULL: the P shard products folded with a
+// Up to 32 tokens (48 of the gated unit), streaming W; fold != NULL: the P shard products folded with a
 // scale for each token and shard into fold->Y (C unused).
 bool quant_skinny_supported(const GemmArgs &g, const GemmExtra &ex);
 hipError_t launch_quant_skinny(const GemmArgs &g, int out_type, const FoldArgs *fold,

@@ -15,6 +15,16 @@ void launch_t(const GemmArgs &g, const NarrowSched &ts, int vec, const GemmExtra
         gemm_narrow_kernel<OUT, FM, TN, SW, OpI8, false><<<dim3(grid), dim3(FM * 2), 0, s>>>(g, ts, ex.bias, ex.bias_shard, vec, ex.up_off, q);
 }
 
+// Two groups of waves for the halves of K.
+template <int OUT>
+void launch_halves(const GemmArgs &g, const NarrowSched &ts, int vec, const GemmExtra &ex, const QuantArgs &q,
+                   int grid, hipStream_t s) {
+    if (g.K % 128)
+        gemm_narrow_kernel<OUT, 128, 64, false, OpI8, true, 2><<<dim3(grid), dim3(512), 0, s>>>(g, ts, ex.bias, ex.bias_shard, vec, 0, q);
+    else
+        gemm_narrow_kernel<OUT, 128, 64, false, OpI8, false, 2><<<dim3(grid), dim3(512), 0, s>>>(g, ts, ex.bias, ex.bias_shard, vec, 0, q);
+}
+
 template <int FM, int TN>
 void launch_out(int out_type, bool sw, const GemmArgs &g, const NarrowSched &ts, int vec, const GemmExtra &ex,
                 const QuantArgs &q, int grid, hipStream_t s) {
@@ -55,7 +65,16 @@ hipError_t launch_quant_narrow(const GemmArgs &g, int out_type, const GemmExtra 
     ts.per_xcd = grid / 8;
     const int vw = out_type == OUT_BF16 ? 8 : 4;
     const int vec = g.ldc % vw == 0 && g.c_shard % vw == 0 && aligned16(g.C);
-    if (FM == 256) launch_out<256, 128>(out_type, sw, g, ts, vec, ex, q, grid, s);
+    // The halves of K side by side where one pass of 64-column tiles is all there is
+    // and K is long enough to pay for the join.  Same box, 8 shards, us with weights
+    // from HBM / warm, halves vs one group: 8192 -> 10240, 64 tokens 30.1 / 21.2 vs
+    // 35.6 / 25.9; 4096 -> 4096, 256 tokens 14.3 / 13.8 vs 16.1 / 15.9; 2048 -> 10240, 64
+    // tokens 9.1 / 8.8 vs 10.0 / 9.4; 1024 -> 4096, 128 tokens 7.5 / 7.0 vs 7.4 / 6.6.
+    if (TN == 64 && T <= cus && g.K >= 2048) {
+        if (out_type == OUT_I32) launch_halves<OUT_I32>(g, ts, vec, ex, q, grid, s);
+        else if (out_type == OUT_BF16) launch_halves<OUT_BF16>(g, ts, vec, ex, q, grid, s);
+        else launch_halves<OUT_F32>(g, ts, vec, ex, q, grid, s);
+    } else if (FM == 256) launch_out<256, 128>(out_type, sw, g, ts, vec, ex, q, grid, s);
     else if (TN == 128) launch_out<128, 128>(out_type, sw, g, ts, vec, ex, q, grid, s);
     else launch_out<128, 64>(out_type, sw, g, ts, vec, ex, q, grid, s);
     return hipGetLastError();

@@ -40,7 +40,7 @@ inline bool aligned16(const void *p) { return ((uintptr_t)p & 15u) == 0; }
 }  // namespace
 
 bool quant_skinny_supported(const GemmArgs &g, const GemmExtra &ex) {
-    return ex.x_rows == 0 && g.M >= 1 && g.M <= SKINNY_MAX_M && g.K > 0 && g.K % 16 == 0 &&
+    return ex.x_rows == 0 && g.M >= 1 && g.M <= (ex.act == ACT_SWIGLU ? SKINNY_MAX_M : 32) && g.K > 0 && g.K % 16 == 0 &&
            g.lda % 16 == 0 && g.ldb % 16 == 0 && g.a_shard % 16 == 0 && g.b_shard % 16 == 0 &&
            aligned16(g.A) && aligned16(g.B);
 }
@@ -60,12 +60,8 @@ hipError_t launch_quant_skinny(const GemmArgs &g, int out_type, const FoldArgs *
         if (fold) return launch_t<1, 1, 256, 4>(g, out_type, fold, ex, q, s);
         return launch_t<1, 1, 256, 3>(g, out_type, fold, ex, q, s);
     }
-    if (g.M <= 32) {
-        if (fold) return launch_t<4, 2, 256, 2>(g, out_type, fold, ex, q, s);
-        return launch_t<2, 2, 256, 2>(g, out_type, fold, ex, q, s);
-    }
-    if (fold) return launch_t<2, 4, 128, 3>(g, out_type, fold, ex, q, s);
-    return launch_t<4, 3, 256, 2>(g, out_type, fold, ex, q, s);
+    if (fold) return launch_t<4, 2, 256, 2>(g, out_type, fold, ex, q, s);
+    return launch_t<2, 2, 256, 2>(g, out_type, fold, ex, q, s);
 }
 
 }  // namespace tpl

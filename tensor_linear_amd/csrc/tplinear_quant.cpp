@@ -21,11 +21,13 @@ constexpr int64_t MAX_QUANT_K = 131071;
 
 // The kernel for an int8 shard GEMM.  All give the same bits, so the choice is
 // by speed; same box, 8 shards, us after a read-only 1 GiB flush / warm:
-//  - skinny (streams W) up to 32 tokens, and up to 48 where the 128-row tiles of
-//    all shards would fill at most half of the CUs: 16 tokens skinny vs narrow
-//    4096 -> 28672 28.1 / 20.9 vs 28.6 / 20.7, 8192 -> 28672 45.9 / 37.7 vs 52.1 /
-//    36.3, 8192 -> 10240 22.3 / 17.7 vs 36.6 / 25.4; 40 tokens 4096 -> 28672 44.9 /
-//    35.4 vs 34.8 / 21.6, 8192 -> 10240 35.0 / 28.1 vs 37.6 / 26.0;
+//  - skinny (streams W) up to 32 tokens: 16 tokens skinny vs narrow 4096 -> 28672
+//    28.1 / 20.9 vs 28.6 / 20.7, 8192 -> 28672 45.9 / 37.7 vs 52.1 / 36.3, 32 tokens 8192
+//    -> 10240 24.3 / 19.9 vs 27.4 / 21.1; above that narrow, whose halves of K
+//    stream as well: 48 tokens 8192 -> 10240 31.5 / 26.1 vs 27.8 / 20.2, 1024 -> 4096 8.0 /
+//    7.2 vs 6.9 / 6.2.  The gated unit, which has no such halves, up to 48 where 128
+//    W rows a tile would fill at most a quarter of the CUs: 48 tokens 4096 -> 2 x
+//    4096 14.2 / 12.4 vs 19.0 / 16.8, 8192 -> 2 x 8192 (half) 49.7 / 41.0 vs 43.1 / 31.6;
 //  - narrow tiles where the 256 x 256 ones would fill at most half of the CUs:
 //    narrow vs tile 4096 -> 28672, 256 tokens (112 tiles) 40.2 / 32.2 vs 53.1 /
 //    47.6, 512 tokens (224) 68.2 / 60.9 vs 61.1 / 53.9; 8192 -> 10240, 768 tokens
@@ -37,11 +39,8 @@ hipError_t run_quant(const GemmArgs &g, int out, const GemmExtra &ex, const Quan
                      hipStream_t s) {
     const bool sw = ex.act == ACT_SWIGLU;
     const int64_t cus = device_cu_count();
-    if (quant_skinny_supported(g, ex)) {
-        const int64_t cols = sw ? 64 : 128;   // outputs per 128 W rows
-        const int64_t t128 = (g.N * g.P + cols - 1) / cols;
-        if (g.M <= 32 || 2 * t128 <= cus) return launch_quant_skinny(g, out, nullptr, ex, q, s);
-    }
+    if (quant_skinny_supported(g, ex) && (g.M <= 32 || 4 * ((g.N * g.P + 63) / 64) <= cus))
+        return launch_quant_skinny(g, out, nullptr, ex, q, s);
     if (quant_dma_supported(g, ex, 256)) {
         const int64_t t256 = ((g.M + 255) / 256) * ((g.N + (sw ? 127 : 255)) / (sw ? 128 : 256)) * g.P;
         if (2 * t256 <= cus) return launch_quant_narrow(g, out, ex, q, s);
@@ -56,15 +55,16 @@ hipError_t run_quant(const GemmArgs &g, int out, const GemmExtra &ex, const Quan
 // after a flush, product vs partials: 16 tokens 14336 -> 4096 19.7 vs 24.6, 8192 ->
 // 8192 18.7 vs 27.0, 28672 -> 8192 48.3 vs 55.5, but 28672 -> 2048 31.1 vs 22.8; 32
 // tokens 8192 -> 8192 26.3 vs 28.4, 14336 -> 4096 35.1 vs 24.9; above, with r = P M N
-// / K: 4096 -> 2048 at 200 tokens (r = 800) 21.8 vs 17.0, at 600 (2400) 22.7 vs 30.3;
-// 14336 -> 4096 at 512 (1170) 60.4 vs 51.5, at 768 (1755) 75.3 vs 79.6; 8192 -> 8192 at
-// 128 (1024) 38.8 vs 34.8, at 256 (2048) 39.8 vs 46.9; the second launch itself is
-// about 1.2e6 of P M N (1024 -> 1024 at 64 tokens 11.0 vs 13.3).
+// / K: 14336 -> 4096 at 128 tokens (r = 293) 44.6 vs 23.1, 4096 -> 2048 at 128 (512) 13.0
+// vs 11.8, at 200 (800) 13.0 vs 13.7, 8192 -> 2048 at 300 (600) 21.5 vs 21.6, 28672 ->
+// 8192 at 256 (585) 103.7 vs 83.8, at 384 (878) 150 vs 144 (warm 118 vs 127), 8192 ->
+// 8192 at 128 (1024) 32.7 vs 37.1; the second launch itself is about 1.2e6 of P M N
+// (1024 -> 1024 at 64 tokens 6.1 vs 9.2).
 bool one_product_faster(int64_t M, int64_t N, int64_t K, int32_t P) {
     if (P == 1) return true;
     if (M <= 16 && N >= 16 * (int64_t)device_cu_count()) return true;
     if (M <= 32) return K <= 8192;
-    return (double)P * M * N + 1.2e6 >= 1500.0 * K;
+    return (double)P * M * N + 1.2e6 >= 800.0 * K;
 }
 
 // A scale for each token and shard: the fold inside the product, or int32

@@ -55,7 +55,7 @@ bool quant_dma_supported(const GemmArgs &g, const GemmExtra &, int) {
     return g.K > 0 && g.K % 16 == 0 && g.lda % 16 == 0 && g.ldb % 16 == 0 && g.a_shard % 16 == 0 && g.b_shard % 16 == 0 &&
            (uintptr_t)g.A % 16 == 0 && (uintptr_t)g.B % 16 == 0;
 }
-bool quant_skinny_supported(const GemmArgs &g, const GemmExtra &ex) { return g.M <= 48 && quant_dma_supported(g, ex, 0); }
+bool quant_skinny_supported(const GemmArgs &g, const GemmExtra &ex) { return g.M <= (ex.act == ACT_SWIGLU ? 48 : 32) && quant_dma_supported(g, ex, 0); }
 bool quant_rowfold_supported(const GemmArgs &g, const ReduceArgs &r, const QuantArgs &) {
     return quant_dma_supported(g, GemmExtra{}, 0) && (r.slice_rows >= g.M || r.slice_rows % 256 == 0);
 }
@@ -100,9 +100,11 @@ int main() {
     // Which kernel a column layer takes, around each threshold (256 CUs).
     column(16, 28672, 8192, 8, 0, "skinny");
     column(32, 28672, 8192, 8, 0, "skinny");
-    column(33, 28672, 8192, 8, 0, "narrow");       // 224 tiles of 128 columns: more than half of the CUs
-    column(48, 10240, 8192, 8, 0, "skinny");       // 80 of them
-    column(49, 10240, 8192, 8, 0, "narrow");
+    column(33, 10240, 8192, 8, 0, "narrow");
+    column(32, 28672, 8192, 8, 1, "skinny");
+    column(48, 8192, 8192, 8, 1, "skinny");        // gated: 64 tiles of 128 W rows, a quarter of the CUs
+    column(48, 8320, 8192, 8, 1, "narrow");        // 65
+    column(49, 8192, 8192, 8, 1, "narrow");
     column(256, 28672, 4096, 8, 0, "narrow");      // 112 tiles of 256 x 256
     column(257, 28672, 4096, 8, 0, "tile");        // 224
     column(768, 10240, 8192, 8, 0, "narrow");
@@ -124,13 +126,15 @@ int main() {
     row(2040, 4096, 4096, 8, 8, TP_ROW_SCATTER, "partials + fold"); // slices of 255 rows
     row(4096, 4096, 14336, 8, 1, TP_ROW_SUM, "tile");               // one scale a token: one product
     CHECK(lg.P == 1 && lg.K == 14336 && lg.a_shard == 0 && lg.C == Y && lq.x_shard == 0 && lout == tpl::OUT_BF16);
-    row(512, 4096, 14336, 8, 1, TP_ROW_SUM, "partials + integer fold");
+    row(256, 4096, 14336, 8, 1, TP_ROW_SUM, "partials + integer fold");
+    row(200, 2048, 4096, 8, 1, TP_ROW_SUM, "narrow");
     row(2048, 4096, 4096, 8, 1, TP_ROW_SCATTER, "narrow");          // the slices as shards in M
     CHECK(lg.P == 8 && lg.M == 256 && lg.a_shard == 256 * 4096 && lg.b_shard == 0 && lg.c_shard == 256 * 4096 && lq.x_shard == 256);
     row(300, 520, 512, 4, 4, TP_ROW_PARTIAL, "narrow");
     CHECK(lout == tpl::OUT_F32 && lg.c_shard == 300 * 520 && lq.x_shard == 1 && lq.w_shard == 0);
     setenv("TPLINEAR_ROW_FOLD", "gemm", 1);
-    row(48, 8192, 28672, 8, 8, TP_ROW_FUSED, "skinny fold");
+    row(32, 8192, 28672, 8, 8, TP_ROW_FUSED, "skinny fold");
+    row(33, 8192, 28672, 8, 8, TP_ROW_FUSED, "rowfold");
     row(128, 4096, 14336, 8, 8, TP_ROW_FUSED, "rowfold");
     row(64, 4096, 14336, 8, 1, TP_ROW_FUSED, "narrow");
     unsetenv("TPLINEAR_ROW_FOLD");

@@ -134,7 +134,8 @@ def test_quantize_more_groups_than_one_launch_holds():
 COLUMN = [  # M, K, N/P (outputs and, gated, up features), P
     (1, 16, 1, 1), (3, 128, 17, 3), (16, 256, 64, 2), (17, 144, 33, 8), (5, 100, 20, 2), (33, 2048, 96, 1),
     (48, 4352, 160, 2), (64, 640, 130, 4), (100, 1376, 264, 8), (130, 512, 1000, 2), (257, 1024, 2100, 8),
-    (300, 384, 520, 3), (700, 272, 1288, 8), (40, 33, 70, 2), (260, 129, 66, 1), (1025, 128, 4104, 8), (20, 0, 24, 2)]
+    (300, 384, 520, 3), (700, 272, 1288, 8), (40, 33, 70, 2), (260, 129, 66, 1), (1025, 128, 4104, 8), (20, 0, 24, 2),
+    (70, 2064, 200, 2), (200, 2176, 130, 3), (1, 4112, 40, 1), (129, 4000, 68, 1)]
 
 
 def column_plain(x, sx, w, sw, b, P, act):
@@ -237,7 +238,7 @@ def test_nan_scale_marks_its_row():
 ROW = [  # M, K/P, N, P
     (1, 16, 1, 1), (3, 128, 20, 3), (16, 1024, 64, 8), (16, 512, 8200, 2), (17, 144, 33, 8), (6, 100, 24, 2), (33, 2048, 96, 2),
     (64, 256, 136, 4), (128, 1376, 264, 2), (512, 256, 264, 2), (768, 144, 200, 3), (2048, 48, 136, 8), (48, 1040, 520, 2), (300, 1376, 2056, 3), (520, 256, 1160, 8), (300, 384, 520, 3), (260, 33, 72, 2), (1024, 128, 8200, 4),
-    (12, 0, 24, 2)]
+    (40, 2064, 136, 3), (100, 2304, 72, 2), (48, 2176, 100, 1), (12, 0, 24, 2)]
 
 
 def row_plain(x, sx, w, sw, b, P):
