@@ -23,6 +23,20 @@ struct QuantArgs {
 hipError_t launch_quant_generic(const GemmArgs &g, int out_type, const GemmExtra &ex,
                                 const QuantArgs &q, hipStream_t s);
 
+// Workgroups for T tiles, and their split over the 8 XCDs in contiguous ranges of
+// tiles.  Fewer tiles than CUs are split too (up to 7 workgroups then have none):
+// neighbouring tiles share rows of X or W, and each XCD has an L2 of its own.  Same
+// box, us with weights from HBM / warm, split vs tile b to workgroup b: 8192 -> 10240,
+// 700 tokens 63.5 / 58.3 vs 68.2 / 60.9; 4096 -> 6144, 500 tokens 18.9 / 19.0 vs 21.0 /
+// 21.1; 4096 -> 4096, 256 tokens 13.3 / 13.0 vs 14.3 / 13.9; 4096 -> 28672, 100 tokens
+// 34.0 / 22.1 vs 34.2 / 22.1.
+inline int quant_grid(int64_t T, int cus, int &xcd_split, int &per_xcd) {
+    xcd_split = cus % 8 == 0;
+    const int grid = T >= cus ? cus : xcd_split ? (int)((T + 7) / 8 * 8) : (int)T;
+    per_xcd = grid / 8;
+    return grid;
+}
+
 // Whether the DMA-fed int8 kernels can load g's operands with tiles of `rows`
 // rows: K, leading dims and shard offsets multiples of 16, 16-byte aligned.
 bool quant_dma_supported(const GemmArgs &g, const GemmExtra &ex, int rows);

@@ -60,9 +60,7 @@ hipError_t launch_quant_narrow(const GemmArgs &g, int out_type, const GemmExtra 
     ts.tiles_m = (int)tm;
     ts.tiles_n = (int)tn;
     ts.T = (int)T;
-    const int grid = (int)(T < cus ? T : cus);
-    ts.xcd_split = (grid == cus && cus % 8 == 0 && T >= cus) ? 1 : 0;
-    ts.per_xcd = grid / 8;
+    const int grid = quant_grid(T, cus, ts.xcd_split, ts.per_xcd);
     const int vw = out_type == OUT_BF16 ? 8 : 4;
     const int vec = g.ldc % vw == 0 && g.c_shard % vw == 0 && aligned16(g.C);
     // The halves of K side by side where one pass of 64-column tiles is all there is

@@ -44,9 +44,7 @@ hipError_t launch_quant_rowfold(const GemmArgs &g, const ReduceArgs &r, const Qu
     ts.tiles_n = (int)tn;
     ts.T = (int)T;
     const int cus = device_cu_count();
-    const int grid = (int)(T < cus ? T : cus);
-    ts.xcd_split = (grid == cus && cus % 8 == 0 && T >= cus) ? 1 : 0;
-    ts.per_xcd = grid / 8;
+    const int grid = quant_grid(T, cus, ts.xcd_split, ts.per_xcd);
     const int vw = out_type == OUT_BF16 ? 8 : 4;
     bool vec = r.ldy % vw == 0;
     const bool scat = r.use_slices || r.slice_rows < g.M;

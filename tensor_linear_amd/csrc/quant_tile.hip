@@ -42,9 +42,7 @@ hipError_t launch_quant_tile(const GemmArgs &g, int out_type, const GemmExtra &e
     ts.group_m = out_type == OUT_I32 ? 4 : 8;
     ts.T = (int)T;
     const int cus = device_cu_count();
-    const int grid = (int)(T < cus ? T : cus);
-    ts.xcd_split = (grid == cus && cus % 8 == 0 && T >= cus) ? 1 : 0;
-    ts.per_xcd = grid / 8;
+    const int grid = quant_grid(T, cus, ts.xcd_split, ts.per_xcd);
     const int vw = out_type == OUT_BF16 ? 8 : 4;
     const int vec = g.ldc % vw == 0 && g.c_shard % vw == 0 && aligned16(g.C);
     if (out_type == OUT_I32) launch_t<OUT_I32, EPI_NONE>(g, ts, vec, ex, q, grid, s);
