@@ -48,6 +48,11 @@ __device__ __forceinline__ void get8(const void *p, int64_t i, float *v) {
     }
 }
 
+// Stores past the caches (us, cached stores vs these: queries and keys of 8192 tokens
+// of 64 + 8 heads of 128 64.8 vs 60.4, append of 8870 such tokens 84.3 vs 79.9,
+// gradients of 4096 tokens of 32 + 8 heads 40.5 vs 36.5).  The same for the loads
+// is another 3% for the first two in bf16, but 18% slower in fp32, where X still
+// lies in the last cache, and 3% slower backwards: not taken.
 template <int ES>
 __device__ __forceinline__ void put8(void *p, int64_t i, const float *v) {
     if (ES == 2) {
@@ -55,13 +60,13 @@ __device__ __forceinline__ void put8(void *p, int64_t i, const float *v) {
         bf16x8 h;
 #pragma unroll
         for (int e = 0; e < 8; ++e) h[e] = (__bf16)v[e];
-        *(bf16x8 *)((uint16_t *)p + i) = h;
+        __builtin_nontemporal_store(h, (bf16x8 *)((uint16_t *)p + i));
     } else {
         u32x4 a, b;
 #pragma unroll
         for (int e = 0; e < 4; ++e) { a[e] = __float_as_uint(v[e]); b[e] = __float_as_uint(v[4 + e]); }
-        *(u32x4 *)((float *)p + i) = a;
-        *(u32x4 *)((float *)p + i + 4) = b;
+        __builtin_nontemporal_store(a, (u32x4 *)((float *)p + i));
+        __builtin_nontemporal_store(b, (u32x4 *)((float *)p + i + 4));
     }
 }
 
