@@ -28,21 +28,23 @@ namespace tpl {
 namespace {
 
 typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+// in memory: at any address (the same instructions as for aligned ones)
+typedef uint32_t u32x4_any __attribute__((ext_vector_type(4), aligned(1)));
 
 constexpr int HT = 256;
 
-// 8 consecutive values (16-byte aligned).
+// 8 consecutive values.
 template <int ES>
 __device__ __forceinline__ void get8(const void *p, int64_t i, float *v) {
     if (ES == 2) {
-        const u32x4 h = *(const u32x4 *)((const uint16_t *)p + i);
+        const u32x4 h = *(const u32x4_any *)((const uint16_t *)p + i);
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
             v[2 * e] = __uint_as_float(h[e] << 16);
             v[2 * e + 1] = __uint_as_float(h[e] & 0xFFFF0000u);
         }
     } else {
-        const u32x4 a = *(const u32x4 *)((const float *)p + i), b = *(const u32x4 *)((const float *)p + i + 4);
+        const u32x4 a = *(const u32x4_any *)((const float *)p + i), b = *(const u32x4_any *)((const float *)p + i + 4);
 #pragma unroll
         for (int e = 0; e < 4; ++e) { v[e] = __uint_as_float(a[e]); v[4 + e] = __uint_as_float(b[e]); }
     }
@@ -60,13 +62,13 @@ __device__ __forceinline__ void put8(void *p, int64_t i, const float *v) {
         bf16x8 h;
 #pragma unroll
         for (int e = 0; e < 8; ++e) h[e] = (__bf16)v[e];
-        __builtin_nontemporal_store(h, (bf16x8 *)((uint16_t *)p + i));
+        __builtin_nontemporal_store(__builtin_bit_cast(u32x4, h), (u32x4_any *)((uint16_t *)p + i));
     } else {
         u32x4 a, b;
 #pragma unroll
         for (int e = 0; e < 4; ++e) { a[e] = __float_as_uint(v[e]); b[e] = __float_as_uint(v[4 + e]); }
-        __builtin_nontemporal_store(a, (u32x4 *)((float *)p + i));
-        __builtin_nontemporal_store(b, (u32x4 *)((float *)p + i + 4));
+        __builtin_nontemporal_store(a, (u32x4_any *)((float *)p + i));
+        __builtin_nontemporal_store(b, (u32x4_any *)((float *)p + i + 4));
     }
 }
 
@@ -87,7 +89,7 @@ template <int ES>
 __device__ __forceinline__ Raw8<ES> raw8(const void *p, int64_t i) {
     Raw8<ES> r;
 #pragma unroll
-    for (int h = 0; h < ES / 2; ++h) r.w[h] = *(const u32x4 *)((const char *)p + i * ES + 16 * h);
+    for (int h = 0; h < ES / 2; ++h) r.w[h] = *(const u32x4_any *)((const char *)p + i * ES + 16 * h);
     return r;
 }
 template <int ES>
@@ -298,7 +300,7 @@ __device__ __forceinline__ void pair_at(const HeadArgs &a, int j, int &x, int &y
     y = a.pairs ? 2 * j + 1 : j + a.R / 2;
 }
 
-// Any D, R and alignment: a wavefront per (token, head), one element or pair a lane.
+// Any D and R: a wavefront per (token, head), one element or pair a lane.
 template <int ES, bool APPEND>
 __global__ __launch_bounds__(HT)
 void heads_any(HeadArgs a) {
@@ -496,9 +498,9 @@ void heads_backward_vec(HeadArgs a, int qblocks, int qparts, int kparts, int64_t
         a.partials[(isq ? 0 : kind_stride) + (int64_t)blk * a.D + d] = ((red[0][d] + red[1][d]) + red[2][d]) + red[3][d];
 }
 
-// Any D, R and alignment: a wavefront per token, heads one after another; its
+// Any D and R: a wavefront per token, heads one after another; its
 // weight-gradient sums live in LDS (each lane its own elements).
-constexpr int ANY_D = 1024;   // largest head of the unaligned form
+constexpr int ANY_D = 1024;   // largest head of this form
 template <int ES>
 __global__ __launch_bounds__(HT)
 void heads_backward_any(HeadArgs a, int64_t kind_stride) {
@@ -600,21 +602,8 @@ void weight_grad_sum(const float *partials, int64_t kind_stride, int64_t qblocks
     }
 }
 
-inline bool al16(const void *p) { return ((uintptr_t)p & 15u) == 0; }
-
-// Whether the 16-values-a-lane form takes the call.
-template <int ES>
-bool vec_ok(const HeadArgs &a, bool append, bool backward) {
-    auto st = [](int64_t v) { return v * ES % 16 == 0; };
-    if (a.D % 16 || a.R % 16 || a.D > 512) return false;
-    if (!(al16(a.X) && st(a.ldx) && st(a.x_shard) && al16(a.cos) && al16(a.sin) && al16(a.wq) && al16(a.wk))) return false;
-    if (backward)
-        return al16(a.dQ) && al16(a.dK) && al16(a.dV) && st(a.lddq) && st(a.lddk) && st(a.lddv) &&
-               al16(a.dX) && st(a.lddx) && st(a.dx_shard);
-    if (!(al16(a.Q) && st(a.ldq))) return false;
-    if (append) return al16(a.kc) && al16(a.vc) && st(a.s_page) && st(a.s_slot) && st(a.s_head);
-    return al16(a.K) && st(a.ldk);
-}
+// Whether the 16-values-a-lane form takes the heads.
+bool vec_ok(const HeadArgs &a) { return a.D % 16 == 0 && a.R % 16 == 0 && a.D <= 512; }
 
 int lanes_per_head(int D) {
     int l = 1;
@@ -653,7 +642,7 @@ template <int ES, bool APPEND>
 hipError_t launch_fwd(const HeadArgs &a, hipStream_t s) {
     const Span sp = span_of(a, a.Q != nullptr, APPEND || a.K, APPEND);
     if (a.T == 0 || sp.per == 0) return hipSuccess;
-    if (!vec_ok<ES>(a, APPEND, false)) {
+    if (!vec_ok(a)) {
         return launch_tokens(a, (int64_t)sp.per * a.P, [&](const HeadArgs &b, unsigned blocks) {
             heads_any<ES, APPEND><<<dim3(blocks), dim3(HT), 0, s>>>(b);
         });
@@ -697,7 +686,7 @@ hipError_t launch_bwd(const HeadArgs &a, hipStream_t s) {
     int64_t qb = q ? most : 0, kb = k ? most : 0;   // workgroups that leave sums, of either kind
     if (a.T == 0) qb = kb = 0;
     if (qb + kb > 0) {
-        if (!vec_ok<ES>(a, false, true)) {
+        if (!vec_ok(a)) {
             heads_backward_any<ES><<<dim3((unsigned)most), dim3(HT), 0, s>>>(a, stride);
             qb = kb = most;
         } else {

@@ -15,7 +15,7 @@ namespace {
 using namespace tpl;
 
 constexpr int64_t MAX_HEADS = 1 << 16;   // heads of all shards together
-constexpr int64_t MAX_D = 1024;          // the unaligned backward keeps a head's sums in LDS
+constexpr int64_t MAX_D = 1024;          // the backward for odd sizes keeps a head's sums in LDS
 
 // The QKV matrix, heads and rotation, common to the three entry points.
 tp_status check_heads(int64_t ldx, int32_t x_mode, const float *cos_t, const float *sin_t,
