@@ -3,25 +3,26 @@
 // operands held in 8 bits): acc[m, n] = sum_k x[m, k] w[n, k] exactly in int32
 // on v_mfma_i32_16x16x64_i8, scaled in the epilogue.
 //
-// Tile 64 (M) x 64 (N), four waves in a 2 x 2 grid of 32 x 32 outputs, 128
-// bytes of K a stage: each thread loads two 16-byte chunks of either operand
-// into registers while the stage before is multiplied, and writes them to LDS
-// rows of 144 bytes (the 16 padding bytes turn the 16 rows of a fragment read
-// into different banks).  Chunks past K and rows past M or N are zeros, which
-// add nothing to an integer sum.  It serves what the DMA kernels cannot load
-// (K or strides not a multiple of 16, unaligned views); bound by its loads'
-// latency (one stage ahead).
+// Tiles 128 x 128 (four waves of 64 x 64) or 64 x 64 (four of 16 x 64), 128 bytes of K
+// a stage: each thread loads its 16-byte chunks of the next stage into registers
+// while the current one is multiplied, and then writes them to the other of two
+// LDS buffers, rows of 144 bytes (the 16 padding bytes turn the 16 rows of a
+// fragment read into different banks).  Chunks past K and rows past M or N are
+// zeros, which add nothing to an integer sum.  It serves what the DMA kernels
+// cannot load (K or strides not a multiple of 16, unaligned views) and is bound by
+// its unaligned loads, which often take two lines each: 4096 tokens of 4097 -> 28672
+// 779 us (1.23 POP/s; the DMA kernels with K = 4096 366), three shards of 1999 ->
+// 1112 at 333 tokens 23 us (10.8).  256 bytes a stage for the small tile were slower
+// (1999: 33 us).
 #include "quant.h"
-#include "quant_math.h"
+#include "quant_epilogue.h"
 
 namespace tpl {
 namespace {
 
 typedef int i32x4 __attribute__((ext_vector_type(4)));
 
-constexpr int QB = 64;     // tile edge in M and N
-constexpr int QK = 128;    // K bytes per stage
-constexpr int QROW = QK + 16;
+constexpr int QGROUP = 8;       // tile rows visited as a group
 
 // 16 bytes from p (any alignment), of which the first `n` are in the row.
 __device__ __forceinline__ i32x4 load16(const int8_t *p, int64_t n) {
@@ -34,116 +35,116 @@ __device__ __forceinline__ i32x4 load16(const int8_t *p, int64_t n) {
     return v;
 }
 
-template <int OUT>
-__device__ __forceinline__ float bias_value(const void *b, int64_t i) {
-    if (OUT == OUT_BF16) return (float)((const __bf16 *)b)[i];
-    return ((const float *)b)[i];
-}
+template <int OUT, bool SWIGLU, int T>
+__global__ __launch_bounds__(256, 2)
+void quant_generic_kernel(GemmArgs g, int tiles_m, int tiles_n, int tiles, int vec, GemmExtra ex, QuantArgs qa) {
+    constexpr int ON = SWIGLU ? T / 2 : T;     // output columns per tile
+    constexpr int QK = 128;                    // K bytes per stage
+    constexpr int QROW = QK + 16;              // LDS bytes per row
+    constexpr int CPR = QK / 16;               // 16-byte chunks of a row's stage
+    constexpr int NC = T * CPR / 256;          // chunks a thread loads of either operand
+    constexpr int NJ = T == 128 ? 4 : 1;       // a wave's 16-row blocks of X; it has 4 of W
+    __shared__ __attribute__((aligned(16))) char smem[2][2][T * QROW];
 
-template <int OUT, bool SWIGLU>
-__global__ __launch_bounds__(256)
-void quant_generic_kernel(GemmArgs g, int tiles_m, int tiles_n, GemmExtra ex, QuantArgs qa) {
-    constexpr int ON = SWIGLU ? QB / 2 : QB;   // output columns per tile
-    __shared__ __attribute__((aligned(16))) char Xs[QB * QROW];
-    __shared__ __attribute__((aligned(16))) char Ws[QB * QROW];
-
-    const int per_shard = tiles_m * tiles_n;
-    const int shard = blockIdx.x / per_shard;
-    const int t = blockIdx.x - shard * per_shard;
-    const int64_t m0 = (int64_t)(t / tiles_n) * QB;
-    const int64_t n0 = (int64_t)(t % tiles_n) * ON;
+    // Tiles in contiguous ranges on the XCDs, a shard's tile rows in groups.
+    const int per = (tiles + 7) / 8, logical = (blockIdx.x & 7) * per + (blockIdx.x >> 3);
+    if (logical >= tiles || (int)(blockIdx.x >> 3) >= per) return;
+    const int per_shard = tiles_m * tiles_n, shard = logical / per_shard, t = logical - shard * per_shard;
+    const int first_m = t / (QGROUP * tiles_n) * QGROUP, gsz = min(tiles_m - first_m, QGROUP);
+    const int tr = t - first_m * tiles_n;
+    const int64_t m0 = (int64_t)(first_m + tr % gsz) * T, n0 = (int64_t)(tr / gsz) * ON;
     const int8_t *A = (const int8_t *)g.A + (int64_t)shard * g.a_shard;
     const int8_t *B = (const int8_t *)g.B + (int64_t)shard * g.b_shard;
 
-    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-    const int wm = wave >> 1, wn = wave & 1;
+    const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int wm = T == 128 ? wave >> 1 : wave, wn = T == 128 ? wave & 1 : 0;
 
-    // Chunk c (0, 1) of this thread: tile row (tid + 256 c) / 8, 16-byte
-    // column (tid + 256 c) % 8 of the stage.  For the gated unit W tile rows
-    // 16-31 of each 32 are the up rows of the units in rows 0-15.
-    const int8_t *xrow[2], *wrow[2];
-    int kc[2], at[2];
-    bool xin[2], win[2];
+    // Chunk c of this thread: tile row (tid + 256 c) / CPR, 16-byte column tid % CPR
+    // of the stage.  W rows are placed for the epilogue
+    // (quant_w_row); for the gated unit, of each 64 the last 32 are the up rows.
+    const int8_t *xrow[NC], *wrow[NC];
+    bool xin[NC], win[NC];
+    const int kc = tid % CPR * 16;
 #pragma unroll
-    for (int c = 0; c < 2; ++c) {
-        const int r = (tid + 256 * c) >> 3;
-        kc[c] = ((tid + 256 * c) & 7) * 16;
-        at[c] = r * QROW + kc[c];
+    for (int c = 0; c < NC; ++c) {
+        const int r = (tid + 256 * c) / CPR;
         xin[c] = m0 + r < g.M;
-        xrow[c] = A + (xin[c] ? m0 + r : 0) * g.lda;
-        int64_t n = SWIGLU ? n0 + (r >> 5) * 16 + (r & 15) : n0 + r;
+        xrow[c] = A + (xin[c] ? m0 + r : 0) * g.lda + kc;
+        int64_t n = n0 + (SWIGLU ? (r >> 6) * 32 + quant_w_row(r & 31) : quant_w_row(r));
         win[c] = n < g.N;
         if (!win[c]) n = 0;
-        if (SWIGLU && ((r >> 4) & 1)) n += ex.up_off;
-        wrow[c] = B + n * g.ldb;
+        if (SWIGLU && (r & 32)) n += ex.up_off;
+        wrow[c] = B + n * g.ldb + kc;
     }
-    i32x4 xv[2], wv[2];
+    i32x4 xv[NC], wv[NC];
     auto load = [&](int64_t k0) {
+        const int64_t left = g.K - k0 - kc;
 #pragma unroll
-        for (int c = 0; c < 2; ++c) {
-            const int64_t k = k0 + kc[c], left = g.K - k;
+        for (int c = 0; c < NC; ++c) {
             xv[c] = wv[c] = i32x4{0, 0, 0, 0};
-            if (xin[c] && left > 0) xv[c] = load16(xrow[c] + k, left);
-            if (win[c] && left > 0) wv[c] = load16(wrow[c] + k, left);
+            if (xin[c] && left > 0) xv[c] = load16(xrow[c] + k0, left);
+            if (win[c] && left > 0) wv[c] = load16(wrow[c] + k0, left);
+        }
+    };
+    auto put = [&](int buf) {
+#pragma unroll
+        for (int c = 0; c < NC; ++c) {
+            const int at = (tid + 256 * c) / CPR * QROW + kc;
+            *(i32x4 *)(smem[buf][0] + at) = xv[c];
+            *(i32x4 *)(smem[buf][1] + at) = wv[c];
         }
     };
 
-    i32x4 acc[2][2] = {};
+    i32x4 acc[4][NJ] = {};
     load(0);
+    put(0);
+    __syncthreads();
+    int buf = 0;
     for (int64_t k0 = 0; k0 < g.K; k0 += QK) {
+        const bool more = k0 + QK < g.K;
+        if (more) load(k0 + QK);
 #pragma unroll
-        for (int c = 0; c < 2; ++c) {
-            *(i32x4 *)(Xs + at[c]) = xv[c];
-            *(i32x4 *)(Ws + at[c]) = wv[c];
-        }
-        __syncthreads();
-        if (k0 + QK < g.K) load(k0 + QK);
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
+        for (int h = 0; h < QK / 64; ++h) {
             const int kb = h * 64 + (lane >> 4) * 16;
-            i32x4 a[2], b[2];
+            i32x4 a[4], b[NJ];
 #pragma unroll
-            for (int u = 0; u < 2; ++u) {
-                a[u] = *(const i32x4 *)(Ws + (wn * 32 + u * 16 + (lane & 15)) * QROW + kb);
-                b[u] = *(const i32x4 *)(Xs + (wm * 32 + u * 16 + (lane & 15)) * QROW + kb);
-            }
+            for (int i = 0; i < 4; ++i) a[i] = *(const i32x4 *)(smem[buf][1] + (wn * 64 + i * 16 + (lane & 15)) * QROW + kb);
 #pragma unroll
-            for (int nb = 0; nb < 2; ++nb)
+            for (int j = 0; j < NJ; ++j) b[j] = *(const i32x4 *)(smem[buf][0] + ((wm * NJ + j) * 16 + (lane & 15)) * QROW + kb);
 #pragma unroll
-                for (int mb = 0; mb < 2; ++mb)
-                    acc[nb][mb] = __builtin_amdgcn_mfma_i32_16x16x64_i8(a[nb], b[mb], acc[nb][mb], 0, 0, 0);
+            for (int i = 0; i < 4; ++i)
+#pragma unroll
+                for (int j = 0; j < NJ; ++j) acc[i][j] = __builtin_amdgcn_mfma_i32_16x16x64_i8(a[i], b[j], acc[i][j], 0, 0, 0);
         }
+        buf ^= 1;
+        if (more) put(buf);
         __syncthreads();
     }
+    const int64_t mw = m0 + wm * NJ * 16, nw = n0 + wn * (SWIGLU ? 32 : 64);
+    if constexpr (SWIGLU)
+        quant_store_gated<OUT, 4, NJ>(g, ex.bias, ex.bias_shard, ex.up_off, qa, vec, shard, mw, nw, lane, acc);
+    else
+        quant_store<OUT, 4, NJ>(g, ex.bias, ex.bias_shard, qa, vec, shard, mw, nw, lane, acc);
+}
 
-    // acc[nb][mb][r]: row m = lane % 16, column n = 4 (lane / 16) + r of the block.
-    const int64_t cbase = (int64_t)shard * g.c_shard, bsh = (int64_t)shard * ex.bias_shard;
-#pragma unroll
-    for (int mb = 0; mb < 2; ++mb) {
-        const int64_t m = m0 + wm * 32 + mb * 16 + (lane & 15);
-        if (m >= g.M) continue;
-        const float sx = OUT == OUT_I32 ? 1.0f : qa.x_scale[m * qa.x_ld + (int64_t)shard * qa.x_shard];
-        const float *sw = qa.w_scale + (int64_t)shard * qa.w_shard;
-#pragma unroll
-        for (int nb = 0; nb < (SWIGLU ? 1 : 2); ++nb)
-#pragma unroll
-            for (int r = 0; r < 4; ++r) {
-                const int64_t n = n0 + (SWIGLU ? wn * 16 : wn * 32 + nb * 16) + 4 * (lane >> 4) + r;
-                if (n >= g.N) continue;
-                const int64_t o = cbase + m * g.ldc + n;
-                if constexpr (OUT == OUT_I32) {
-                    ((int32_t *)g.C)[o] = acc[nb][mb][r];
-                } else {
-                    float v = quant_value(acc[nb][mb][r], sx, sw[n],
-                                          ex.bias ? bias_value<OUT>(ex.bias, bsh + n) : 0.0f);
-                    if (SWIGLU)
-                        v = quant_silu(v) * quant_value(acc[1][mb][r], sx, sw[ex.up_off + n],
-                                                      ex.bias ? bias_value<OUT>(ex.bias, bsh + ex.up_off + n) : 0.0f);
-                    if (OUT == OUT_BF16) ((__bf16 *)g.C)[o] = (__bf16)v;
-                    else ((float *)g.C)[o] = v;
-                }
-            }
-    }
+template <int OUT, bool SW>
+hipError_t launch_t(const GemmArgs &g, const GemmExtra &ex, const QuantArgs &q, hipStream_t s) {
+    const int on = SW ? 2 : 1;
+    auto count = [&](int T) { return ((g.M + T - 1) / T) * ((g.N + T / on - 1) / (T / on)); };
+    // The larger tile where it fills the CUs.  Same box, 8 shards, us, 128 vs 64: 4097
+    // -> 28672 at 4096 tokens 779 vs 1357, 517 -> 4096 at 1000 (256 tiles of 128) 15.0 vs
+    // 15.0, 3000 -> 8192 at 300 (192) 36.6 vs 30.1, 1001 -> 10240 at 128 (80) 21.6 vs 14.5.
+    const int T = count(128) * g.P >= device_cu_count() ? 128 : 64;
+    const int64_t tm = (g.M + T - 1) / T, tn = (g.N + T / on - 1) / (T / on);
+    if (tm > 0x7FFFFFFFll || tn > 0x7FFFFFFFll || tm * tn > 0x7FFFFFFFll / QGROUP || tm * tn * g.P > 0xFFFFFFFFll / 256 - 8)
+        return hipErrorInvalidConfiguration;   // 2^32 threads a launch
+    const int tiles = (int)(tm * tn * g.P);
+    const int vw = OUT == OUT_BF16 ? 8 : 4;
+    const int vec = g.ldc % vw == 0 && g.c_shard % vw == 0 && (uintptr_t)g.C % 16 == 0;
+    const dim3 grid((tiles + 7) / 8 * 8), block(256);
+    if (T == 128) quant_generic_kernel<OUT, SW, 128><<<grid, block, 0, s>>>(g, (int)tm, (int)tn, tiles, vec, ex, q);
+    else quant_generic_kernel<OUT, SW, 64><<<grid, block, 0, s>>>(g, (int)tm, (int)tn, tiles, vec, ex, q);
+    return hipGetLastError();
 }
 
 }  // namespace
@@ -153,19 +154,9 @@ hipError_t launch_quant_generic(const GemmArgs &g, int out_type, const GemmExtra
     if (g.M == 0 || g.N == 0 || g.P == 0) return hipSuccess;
     const bool sw = ex.act == ACT_SWIGLU;
     if (ex.x_rows > 0 || (out_type == OUT_I32 && (sw || ex.bias))) return hipErrorInvalidValue;
-    const int on = sw ? QB / 2 : QB;
-    const int64_t tm = (g.M + QB - 1) / QB, tn = (g.N + on - 1) / on;
-    if (tm > 0x7FFFFFFFll || tn > 0x7FFFFFFFll || tm * tn > 0x7FFFFFFFll ||
-        tm * tn * g.P > 0xFFFFFFFFll / 256)   // 2^32 threads a launch
-        return hipErrorInvalidConfiguration;
-    const dim3 grid((unsigned)(tm * tn * g.P)), block(256);
-    const int a = (int)tm, b = (int)tn;
-    if (out_type == OUT_I32) quant_generic_kernel<OUT_I32, false><<<grid, block, 0, s>>>(g, a, b, ex, q);
-    else if (out_type == OUT_BF16 && sw) quant_generic_kernel<OUT_BF16, true><<<grid, block, 0, s>>>(g, a, b, ex, q);
-    else if (out_type == OUT_BF16) quant_generic_kernel<OUT_BF16, false><<<grid, block, 0, s>>>(g, a, b, ex, q);
-    else if (sw) quant_generic_kernel<OUT_F32, true><<<grid, block, 0, s>>>(g, a, b, ex, q);
-    else quant_generic_kernel<OUT_F32, false><<<grid, block, 0, s>>>(g, a, b, ex, q);
-    return hipGetLastError();
+    if (out_type == OUT_I32) return launch_t<OUT_I32, false>(g, ex, q, s);
+    if (out_type == OUT_BF16) return sw ? launch_t<OUT_BF16, true>(g, ex, q, s) : launch_t<OUT_BF16, false>(g, ex, q, s);
+    return sw ? launch_t<OUT_F32, true>(g, ex, q, s) : launch_t<OUT_F32, false>(g, ex, q, s);
 }
 
 }  // namespace tpl

@@ -32,9 +32,8 @@ constexpr int64_t MAX_QUANT_K = 131071;
 //    narrow vs tile 4096 -> 28672, 256 tokens (112 tiles) 40.2 / 32.2 vs 53.1 /
 //    47.6, 512 tokens (224) 68.2 / 60.9 vs 61.1 / 53.9; 8192 -> 10240, 768 tokens
 //    (120) 64.8 / 61.3 vs 90.1 / 82.8, 1024 tokens (160) 114.2 / 102.1 vs 91.1 / 81.1;
-//  - generic where K, a stride or an address is not a multiple of 16 (2000 ->
-//    3336, 16 tokens: skinny 8.0 / 4.7, generic 20.7 / 12.5; 128 tokens: narrow
-//    19.8 / 12.2, generic 24.2 / 16.4).
+//  - generic where K, a stride or an address is not a multiple of 16 (three shards
+//    of 2000 -> 1112 at 333 tokens, narrow 10.8, generic with K = 1999 23.2).
 hipError_t run_quant(const GemmArgs &g, int out, const GemmExtra &ex, const QuantArgs &q,
                      hipStream_t s) {
     const bool sw = ex.act == ACT_SWIGLU;
