@@ -27,48 +27,40 @@
 namespace tpl {
 namespace {
 
+typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
 typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 // in memory: at any address (the same instructions as for aligned ones)
+typedef uint32_t u32x2_any __attribute__((ext_vector_type(2), aligned(1)));
 typedef uint32_t u32x4_any __attribute__((ext_vector_type(4), aligned(1)));
 
 constexpr int HT = 256;
-
-// 8 consecutive values.
-template <int ES>
-__device__ __forceinline__ void get8(const void *p, int64_t i, float *v) {
-    if (ES == 2) {
-        const u32x4 h = *(const u32x4_any *)((const uint16_t *)p + i);
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            v[2 * e] = __uint_as_float(h[e] << 16);
-            v[2 * e + 1] = __uint_as_float(h[e] & 0xFFFF0000u);
-        }
-    } else {
-        const u32x4 a = *(const u32x4_any *)((const float *)p + i), b = *(const u32x4_any *)((const float *)p + i + 4);
-#pragma unroll
-        for (int e = 0; e < 4; ++e) { v[e] = __uint_as_float(a[e]); v[4 + e] = __uint_as_float(b[e]); }
-    }
-}
 
 // Stores past the caches (us, cached stores vs these: queries and keys of 8192 tokens
 // of 64 + 8 heads of 128 64.8 vs 60.4, append of 8870 such tokens 84.3 vs 79.9,
 // gradients of 4096 tokens of 32 + 8 heads 40.5 vs 36.5).  The same for the loads
 // is another 3% for the first two in bf16, but 18% slower in fp32, where X still
 // lies in the last cache, and 3% slower backwards: not taken.
-template <int ES>
-__device__ __forceinline__ void put8(void *p, int64_t i, const float *v) {
-    if (ES == 2) {
+template <int ES, bool FINE>
+__device__ __forceinline__ void put8(void *p, int64_t i, int a, int b, const float *v) {
+    char *q = (char *)p + (i + a) * ES, *q2 = (char *)p + (i + b) * ES;
+    if constexpr (ES == 2) {
         typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
         bf16x8 h;
 #pragma unroll
         for (int e = 0; e < 8; ++e) h[e] = (__bf16)v[e];
-        __builtin_nontemporal_store(__builtin_bit_cast(u32x4, h), (u32x4_any *)((uint16_t *)p + i));
+        const u32x4 w = __builtin_bit_cast(u32x4, h);
+        if constexpr (FINE) {
+            __builtin_nontemporal_store(u32x2{w[0], w[1]}, (u32x2_any *)q);
+            __builtin_nontemporal_store(u32x2{w[2], w[3]}, (u32x2_any *)q2);
+        } else {
+            __builtin_nontemporal_store(w, (u32x4_any *)q);
+        }
     } else {
-        u32x4 a, b;
+        u32x4 c, d;
 #pragma unroll
-        for (int e = 0; e < 4; ++e) { a[e] = __float_as_uint(v[e]); b[e] = __float_as_uint(v[4 + e]); }
-        __builtin_nontemporal_store(a, (u32x4_any *)((float *)p + i));
-        __builtin_nontemporal_store(b, (u32x4_any *)((float *)p + i + 4));
+        for (int e = 0; e < 4; ++e) { c[e] = __float_as_uint(v[e]); d[e] = __float_as_uint(v[4 + e]); }
+        __builtin_nontemporal_store(c, (u32x4_any *)q);
+        __builtin_nontemporal_store(d, (u32x4_any *)(FINE ? q2 : q + 16));
     }
 }
 
@@ -85,11 +77,21 @@ __device__ __forceinline__ void put1(void *p, int64_t i, float v) {
 // 8 consecutive values as they are, and widened.
 template <int ES>
 struct Raw8 { u32x4 w[ES / 2]; };
-template <int ES>
-__device__ __forceinline__ Raw8<ES> raw8(const void *p, int64_t i) {
+// Those at i + a .. + 3 and i + b .. + 3; not FINE: b is a + 4.
+template <int ES, bool FINE>
+__device__ __forceinline__ Raw8<ES> raw8(const void *p, int64_t i, int a, int b) {
     Raw8<ES> r;
+    const char *q = (const char *)p + (i + a) * ES;
+    if constexpr (!FINE) {
 #pragma unroll
-    for (int h = 0; h < ES / 2; ++h) r.w[h] = *(const u32x4_any *)((const char *)p + i * ES + 16 * h);
+        for (int h = 0; h < ES / 2; ++h) r.w[h] = *(const u32x4_any *)(q + 16 * h);
+    } else if constexpr (ES == 2) {
+        const u32x2 lo = *(const u32x2_any *)q, hi = *(const u32x2_any *)((const char *)p + (i + b) * ES);
+        r.w[0] = u32x4{lo[0], lo[1], hi[0], hi[1]};
+    } else {
+        r.w[0] = *(const u32x4_any *)q;
+        r.w[ES / 4] = *(const u32x4_any *)((const char *)p + (i + b) * ES);
+    }
     return r;
 }
 template <int ES>
@@ -147,22 +149,63 @@ __device__ __forceinline__ Place given_place(const HeadArgs &a, int64_t t) {
     return p;
 }
 
-// Lane's two runs of 8 values inside a head: the pairs' halves where it
-// rotates, 16 consecutive values else.
-struct Runs { int a, b; bool on, turn; };
+// A lane's 16 values: four runs of 4 from a, a2, b, b2 on, of which the elements of
+// a and a2 pair with those of b and b2 (halves), or neighbours pair (pairs).
+// turn, turn2: whether the pairs of the values 0-3 and 4-7 of either half (pairs:
+// the first and the last 8 values) rotate.  Where R is a multiple of 16 both do or
+// neither, and a2 = a + 4, b2 = b + 4; where it is only one of 8 (FINE), R / 2 pairs
+// end inside a lane, and the loads are of 4 values.
+struct Runs { int a, a2, b, b2; bool on, turn, turn2; };
+template <bool FINE>
 __device__ __forceinline__ Runs runs_of(int unit, int D, int R, int pairs) {
     Runs r;
     r.on = unit * 16 < D;
     r.turn = unit * 16 < R;
+    r.turn2 = FINE ? unit * 16 + 8 < R : r.turn;
     r.a = r.turn && !pairs ? unit * 8 : unit * 16;
-    r.b = r.turn && !pairs ? R / 2 + unit * 8 : unit * 16 + 8;
+    r.b = r.turn && !pairs ? R / 2 + unit * 8 : unit * 16 + (FINE && !pairs ? 4 : 8);
+    if (!FINE || pairs) {
+        r.a2 = r.a + 4;
+        r.b2 = r.b + 4;
+    } else {
+        r.a2 = r.turn2 ? unit * 8 + 4 : unit * 16 + 8;
+        r.b2 = r.turn2 ? R / 2 + unit * 8 + 4 : unit * 16 + 12;
+    }
     return r;
+}
+// Element e of them.
+__device__ __forceinline__ int run_at(const Runs &r, int e) {
+    return e < 4 ? r.a + e : e < 8 ? r.a2 + e - 4 : e < 12 ? r.b + e - 8 : r.b2 + e - 12;
+}
+
+// 16 values of a row, raw and stored.
+template <int ES, bool FINE>
+__device__ __forceinline__ void load16(const void *p, int64_t i, const Runs &r, Raw8<ES> (&x)[2]) {
+    x[0] = raw8<ES, FINE>(p, i, r.a, r.a2);
+    x[1] = raw8<ES, FINE>(p, i, r.b, r.b2);
+}
+template <int ES, bool FINE>
+__device__ __forceinline__ void store16(void *p, int64_t i, const Runs &r, const float *v) {
+    put8<ES, FINE>(p, i, r.a, r.a2, v);
+    put8<ES, FINE>(p, i, r.b, r.b2, v + 8);
+}
+
+// The cosines and sines of a lane's 8 pairs at table row `pos`.
+template <bool FINE>
+__device__ __forceinline__ void load_angles(const HeadArgs &a, int64_t pos, int unit, const Runs &r, float *c, float *s) {
+    const int64_t i = pos * (a.R / 2) + unit * 8;
+    const int last = FINE && !r.turn2 ? 0 : 4;   // past the table's row: the first four again
+    const Raw8<4> cr = raw8<4, FINE>(a.cos, i, 0, last), sr = raw8<4, FINE>(a.sin, i, 0, last);
+    widen8<4>(cr, c);
+    widen8<4>(sr, s);
 }
 
 // The rotation of a lane's pairs by +angle (back: by -angle).
-__device__ __forceinline__ void turn16(float *v, const float *c, const float *s, bool pairs, bool back) {
+template <bool FINE>
+__device__ __forceinline__ void turn16(float *v, const float *c, const float *s, const Runs &r, bool pairs, bool back) {
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
+        if (FINE && e >= 4 && !r.turn2) continue;
         const int ia = pairs ? 2 * e : e, ib = pairs ? 2 * e + 1 : e + 8;
         const float x = v[ia], y = v[ib], sn = back ? -s[e] : s[e];
         v[ia] = x * c[e] - y * sn;
@@ -199,7 +242,7 @@ __device__ __forceinline__ Head head_of(const HeadArgs &a, int slot, const Span 
 
 // LH: lanes per head.  One wavefront per (token, part): part p of `parts`
 // takes the groups of 64 / LH heads p, p + parts, ...
-template <int ES, int LH, bool APPEND>
+template <int ES, int LH, bool APPEND, bool FINE>
 __global__ __launch_bounds__(HT)
 void heads_vec(HeadArgs a, int parts) {
     const int lane = threadIdx.x & 63;
@@ -208,7 +251,7 @@ void heads_vec(HeadArgs a, int parts) {
     if (t >= a.T) return;
     const int part = (int)(w % (uint32_t)parts);
     const int unit = lane % LH;
-    const Runs r = runs_of(unit, a.D, a.R, a.pairs);
+    const Runs r = runs_of<FINE>(unit, a.D, a.R, a.pairs);
     const Span sp = span_of(a, a.Q != nullptr, APPEND || a.K, APPEND);
     const int slots = sp.per * a.P;
     constexpr int HW = 64 / LH;
@@ -220,8 +263,7 @@ void heads_vec(HeadArgs a, int parts) {
         v.h = head_of(a, g + lane / LH, sp, slots);
         if (v.h.on && r.on) {
             const int64_t x = v.h.shard * a.x_shard + t * a.ldx + v.h.col;
-            v.x[0] = raw8<ES>(a.X, x + r.a);
-            v.x[1] = raw8<ES>(a.X, x + r.b);
+            load16<ES, FINE>(a.X, x, r, v.x);
         }
         return v;
     };
@@ -231,12 +273,9 @@ void heads_vec(HeadArgs a, int parts) {
     if (APPEND && !pl.mine) return;
     float c[8], s[8];
     Raw8<ES> wq[2] = {}, wk[2] = {};
-    if (r.on && r.turn && pl.ok) {
-        get8<4>(a.cos, pl.pos * (a.R / 2) + unit * 8, c);
-        get8<4>(a.sin, pl.pos * (a.R / 2) + unit * 8, s);
-    }
-    if (a.wq && r.on) { wq[0] = raw8<ES>(a.wq, r.a); wq[1] = raw8<ES>(a.wq, r.b); }
-    if (a.wk && r.on) { wk[0] = raw8<ES>(a.wk, r.a); wk[1] = raw8<ES>(a.wk, r.b); }
+    if (r.on && r.turn && pl.ok) load_angles<FINE>(a, pl.pos, unit, r, c, s);
+    if (a.wq && r.on) load16<ES, FINE>(a.wq, 0, r, wq);
+    if (a.wk && r.on) load16<ES, FINE>(a.wk, 0, r, wk);
     for (int g = part * HW; g < slots; g += parts * HW) {
         const Vals cur = next;
         if (g + parts * HW < slots) next = load(g + parts * HW);
@@ -270,24 +309,16 @@ void heads_vec(HeadArgs a, int parts) {
             }
         }
         if (r.turn && h.kind != HEAD_V && pl.ok) {
-            if (a.pairs) turn16(v, c, s, true, false);
-            else turn16(v, c, s, false, false);
+            if (a.pairs) turn16<FINE>(v, c, s, r, true, false);
+            else turn16<FINE>(v, c, s, r, false, false);
         }
         if (!live) continue;
         if (h.kind == HEAD_Q) {
-            if (a.Q) {
-                put8<ES>(a.Q, t * a.ldq + (int64_t)h.head * a.D + r.a, v);
-                put8<ES>(a.Q, t * a.ldq + (int64_t)h.head * a.D + r.b, v + 8);
-            }
+            if (a.Q) store16<ES, FINE>(a.Q, t * a.ldq + (int64_t)h.head * a.D, r, v);
         } else if (APPEND) {
-            if (pl.ok) {
-                void *dst = h.kind == HEAD_K ? a.kc : a.vc;
-                put8<ES>(dst, pl.slot + h.head * a.s_head + r.a, v);
-                put8<ES>(dst, pl.slot + h.head * a.s_head + r.b, v + 8);
-            }
+            if (pl.ok) store16<ES, FINE>(h.kind == HEAD_K ? a.kc : a.vc, pl.slot + h.head * a.s_head, r, v);
         } else if (a.K) {
-            put8<ES>(a.K, t * a.ldk + (int64_t)h.head * a.D + r.a, v);
-            put8<ES>(a.K, t * a.ldk + (int64_t)h.head * a.D + r.b, v + 8);
+            store16<ES, FINE>(a.K, t * a.ldk + (int64_t)h.head * a.D, r, v);
         }
     }
 }
@@ -363,7 +394,7 @@ void heads_any(HeadArgs a) {
 // in partials[kind][block][D], which a second kernel adds in an order of its own:
 // the result does not depend on scheduling.  4096 tokens of 32 + 8 heads of 128:
 // 35.7 us (4.1 TB/s) and 4.4 for the sums.
-template <int ES, int LH>
+template <int ES, int LH, bool FINE>
 __global__ __launch_bounds__(HT)
 void heads_backward_vec(HeadArgs a, int qblocks, int qparts, int kparts, int64_t kind_stride) {
     __shared__ float red[4][LH * 16];
@@ -371,12 +402,17 @@ void heads_backward_vec(HeadArgs a, int qblocks, int qparts, int kparts, int64_t
     const bool isq = (int)blockIdx.x < qblocks;
     const int blk = isq ? blockIdx.x : blockIdx.x - qblocks, nblk = isq ? qblocks : gridDim.x - qblocks;
     const int unit = lane % LH;
-    const Runs r = runs_of(unit, a.D, a.R, a.pairs);
+    const Runs r = runs_of<FINE>(unit, a.D, a.R, a.pairs);
     const void *wt = isq ? a.wq : a.wk, *dy = isq ? a.dQ : a.dK;
     const int64_t ldy = isq ? a.lddq : a.lddk;
     const int nh = isq ? a.hq : a.hk, first = isq ? 0 : a.hq;     // heads of a shard, the first one's place
     float w[16] = {}, gw[16] = {};
-    if (wt && r.on) { get8<ES>(wt, r.a, w); get8<ES>(wt, r.b, w + 8); }
+    if (wt && r.on) {
+        Raw8<ES> wr[2];
+        load16<ES, FINE>(wt, 0, r, wr);
+        widen8<ES>(wr[0], w);
+        widen8<ES>(wr[1], w + 8);
+    }
     constexpr int HW = 64 / LH;
     const int heads = nh * a.P;
     const int groups = dy ? (heads + HW - 1) / HW : 0;            // of gradients, then of value copies
@@ -396,13 +432,11 @@ void heads_backward_vec(HeadArgs a, int qblocks, int qparts, int kparts, int64_t
         if (h < heads && r.on) {
             const void *src = val ? a.dV : dy;
             const int64_t o = t * (val ? a.lddv : ldy) + (int64_t)h * a.D;
-            v.y[0] = raw8<ES>(src, o + r.a);
-            v.y[1] = raw8<ES>(src, o + r.b);
+            load16<ES, FINE>(src, o, r, v.y);
             if (wt && !val) {
                 const int i = h / nh;
                 const int64_t x = i * a.x_shard + t * a.ldx + (int64_t)(first + h - i * nh) * a.D;
-                v.x[0] = raw8<ES>(a.X, x + r.a);
-                v.x[1] = raw8<ES>(a.X, x + r.b);
+                load16<ES, FINE>(a.X, x, r, v.x);
             }
         }
         return v;
@@ -413,10 +447,7 @@ void heads_backward_vec(HeadArgs a, int qblocks, int qparts, int kparts, int64_t
         const Place pl = given_place(a, t);
         u.ok = pl.ok;
         if (!pl.ok && a.bad && lane == 0) *a.bad = 1;
-        if (r.on && r.turn && pl.ok) {
-            get8<4>(a.cos, pl.pos * (a.R / 2) + unit * 8, u.c);
-            get8<4>(a.sin, pl.pos * (a.R / 2) + unit * 8, u.s);
-        }
+        if (r.on && r.turn && pl.ok) load_angles<FINE>(a, pl.pos, unit, r, u.c, u.s);
         return u;
     };
     if (t < a.T && part < all) {
@@ -442,8 +473,8 @@ void heads_backward_vec(HeadArgs a, int qblocks, int qparts, int kparts, int64_t
                     for (int e = 0; e < 16; ++e) v[e] = 0.0f;
                 } else {
                     if (r.turn) {
-                        if (a.pairs) turn16(v, now.c, now.s, true, true);
-                        else turn16(v, now.c, now.s, false, true);
+                        if (a.pairs) turn16<FINE>(v, now.c, now.s, r, true, true);
+                        else turn16<FINE>(v, now.c, now.s, r, false, true);
                     }
                     if (wt) {
                         float x[16], sum = 0.0f, dot = 0.0f;
@@ -472,8 +503,7 @@ void heads_backward_vec(HeadArgs a, int qblocks, int qparts, int kparts, int64_t
             if (live) {
                 const int i = h / nh;
                 const int64_t o = i * a.dx_shard + t * a.lddx + (int64_t)(first + (val ? a.hk : 0) + h - i * nh) * a.D;
-                put8<ES>(a.dX, o + r.a, v);
-                put8<ES>(a.dX, o + r.b, v + 8);
+                store16<ES, FINE>(a.dX, o, r, v);
             }
             if (tn >= a.T) break;
             if (tn != t) {
@@ -491,7 +521,7 @@ void heads_backward_vec(HeadArgs a, int qblocks, int qparts, int kparts, int64_t
         float q = gw[e];
         for (int o = LH; o < 64; o <<= 1) q += __shfl_xor(q, o);
         // the value's place in the head (units past D keep their own cells)
-        if (lane < LH) red[wave][r.on ? (e < 8 ? r.a + e : r.b + e - 8) : unit * 16 + e] = q;
+        if (lane < LH) red[wave][r.on ? run_at(r, e) : unit * 16 + e] = q;
     }
     __syncthreads();
     for (int d = threadIdx.x; d < a.D; d += HT)
@@ -603,7 +633,7 @@ void weight_grad_sum(const float *partials, int64_t kind_stride, int64_t qblocks
 }
 
 // Whether the 16-values-a-lane form takes the heads.
-bool vec_ok(const HeadArgs &a) { return a.D % 16 == 0 && a.R % 16 == 0 && a.D <= 512; }
+bool vec_ok(const HeadArgs &a) { return a.D % 16 == 0 && a.R % 8 == 0 && a.D <= 512; }
 
 int lanes_per_head(int D) {
     int l = 1;
@@ -634,7 +664,8 @@ hipError_t launch_vec(const HeadArgs &a, hipStream_t s) {
     int64_t parts = (8192 + a.T - 1) / a.T;
     if (parts > groups) parts = groups;
     return launch_tokens(a, parts, [&](const HeadArgs &b, unsigned blocks) {
-        heads_vec<ES, LH, APPEND><<<dim3(blocks), dim3(HT), 0, s>>>(b, (int)parts);
+        if (a.R % 16) heads_vec<ES, LH, APPEND, true><<<dim3(blocks), dim3(HT), 0, s>>>(b, (int)parts);
+        else heads_vec<ES, LH, APPEND, false><<<dim3(blocks), dim3(HT), 0, s>>>(b, (int)parts);
     });
 }
 
@@ -674,8 +705,10 @@ void launch_bwd_vec(const HeadArgs &a, int64_t &qb, int64_t &kb, int64_t stride,
     };
     const int qp = fit(qb, a.dQ ? groups(a.hq) : 0);
     const int kp = fit(kb, groups(a.hk) * ((a.dK ? 1 : 0) + (a.dV ? 1 : 0)));
-    if (qb + kb > 0)
-        heads_backward_vec<ES, LH><<<dim3((unsigned)(qb + kb)), dim3(HT), 0, s>>>(a, (int)qb, qp, kp, stride);
+    const dim3 grid((unsigned)(qb + kb));
+    if (qb + kb == 0) return;
+    if (a.R % 16) heads_backward_vec<ES, LH, true><<<grid, dim3(HT), 0, s>>>(a, (int)qb, qp, kp, stride);
+    else heads_backward_vec<ES, LH, false><<<grid, dim3(HT), 0, s>>>(a, (int)qb, qp, kp, stride);
 }
 
 template <int ES>

@@ -71,7 +71,9 @@ CASES = [  # T, Hq, Hkv, D, R, P, pairs, norms, shards, extra
     (6, 3, 1, 7, 6, 1, True, "qk", False, 1), (5, 4, 2, 128, 128, 2, False, "qk", True, 1),
     (2, 2, 2, 512, 64, 1, False, "qk", False, 0), (3, 2, 1, 600, 600, 1, True, "qk", False, 0),
     (4, 8, 8, 32, 0, 8, False, "qk", False, 0), (300, 8, 1, 128, 128, 1, False, "qk", False, 0),
-    (2, 5, 0, 48, 48, 1, False, "q", False, 0), (9001, 2, 1, 32, 32, 1, False, "qk", False, 0)]
+    (2, 5, 0, 48, 48, 1, False, "q", False, 0), (9001, 2, 1, 32, 32, 1, False, "qk", False, 0),
+    (5, 4, 2, 80, 40, 2, False, "qk", True, 0), (6, 6, 3, 80, 40, 3, True, "qk", False, 1), (3, 2, 1, 16, 8, 1, False, "q", False, 0),
+    (4, 4, 2, 48, 24, 2, True, "k", False, 0), (5, 3, 1, 512, 504, 1, False, "qk", False, 3), (200, 4, 4, 128, 120, 4, False, "", True, 0)]
 
 
 def make(case, t):
@@ -231,7 +233,8 @@ APPEND = [  # lens, past, Hq, Hkv, D, R, P, page, pairs, norm, shards, order, ta
     ([2, 9], [1, 6], 3, 1, 10, 6, 1, 3, True, True, False, "hnd", 2),
     ([33, 1], [100, 7], 8, 8, 128, 0, 8, 32, False, True, True, "nhd", 1),
     ([1] * 70, list(range(0, 140, 2)), 2, 1, 32, 32, 1, 16, False, True, False, "nhd", 0),
-    ([0, 0, 1] * 60, [3] * 180, 2, 1, 32, 32, 1, 16, False, False, False, "nhd", 1)]
+    ([0, 0, 1] * 60, [3] * 180, 2, 1, 32, 32, 1, 16, False, False, False, "nhd", 1),
+    ([7, 1], [2, 90], 4, 2, 80, 40, 2, 16, False, True, True, "hnd", 1), ([3, 20], [0, 5], 2, 2, 48, 8, 1, 4, True, True, False, "nhd", 0)]
 
 
 @pytest.mark.parametrize("t", TYPES)
