@@ -30,6 +30,9 @@
 // then the step's one barrier; during substep 1 it reads the next step's
 // substep-0 fragments.  Persistent workgroups walk an XCD-contiguous range
 // of (shard, tile) pairs; the K pipeline runs across tiles.
+//
+// int8 operands (OP): K steps of 128 values, exact sums, and the tile kernel's int8
+// epilogue.
 #pragma once
 
 #include <type_traits>

@@ -20,7 +20,9 @@
 // them.  A wavefront takes several heads of ONE token, so that a token's 16
 // cosines and sines are loaded once per lane and used for every head: for 72
 // heads of 128 the table's bytes would otherwise double the load instructions.
-// With few tokens the heads of a token are spread over more wavefronts.
+// With few tokens the heads of a token are spread over more wavefronts.  bf16 heads
+// of 128: 8192 tokens of 64 + 8 heads 63.3 us (4.8 TB/s), 9700 such tokens with their
+// values into a cache 83 us (4.8 TB/s).
 #include "heads.h"
 #include "kernels.h"
 
@@ -35,11 +37,9 @@ typedef uint32_t u32x4_any __attribute__((ext_vector_type(4), aligned(1)));
 
 constexpr int HT = 256;
 
-// Stores past the caches (us, cached stores vs these: queries and keys of 8192 tokens
-// of 64 + 8 heads of 128 64.8 vs 60.4, append of 8870 such tokens 84.3 vs 79.9,
-// gradients of 4096 tokens of 32 + 8 heads 40.5 vs 36.5).  The same for the loads
-// is another 3% for the first two in bf16, but 18% slower in fp32, where X still
-// lies in the last cache, and 3% slower backwards: not taken.
+// Ordinary stores: past the caches they are faster by themselves (8192 tokens of 64 +
+// 8 heads of 128 60.1 us for 64.5), but the step that reads the result then pays more
+// (with a pass over the queries and keys behind it 124.5 us for 115.8).
 template <int ES, bool FINE>
 __device__ __forceinline__ void put8(void *p, int64_t i, int a, int b, const float *v) {
     char *q = (char *)p + (i + a) * ES, *q2 = (char *)p + (i + b) * ES;
@@ -50,17 +50,17 @@ __device__ __forceinline__ void put8(void *p, int64_t i, int a, int b, const flo
         for (int e = 0; e < 8; ++e) h[e] = (__bf16)v[e];
         const u32x4 w = __builtin_bit_cast(u32x4, h);
         if constexpr (FINE) {
-            __builtin_nontemporal_store(u32x2{w[0], w[1]}, (u32x2_any *)q);
-            __builtin_nontemporal_store(u32x2{w[2], w[3]}, (u32x2_any *)q2);
+            *(u32x2_any *)q = u32x2{w[0], w[1]};
+            *(u32x2_any *)q2 = u32x2{w[2], w[3]};
         } else {
-            __builtin_nontemporal_store(w, (u32x4_any *)q);
+            *(u32x4_any *)q = w;
         }
     } else {
         u32x4 c, d;
 #pragma unroll
         for (int e = 0; e < 4; ++e) { c[e] = __float_as_uint(v[e]); d[e] = __float_as_uint(v[4 + e]); }
-        __builtin_nontemporal_store(c, (u32x4_any *)q);
-        __builtin_nontemporal_store(d, (u32x4_any *)(FINE ? q2 : q + 16));
+        *(u32x4_any *)q = c;
+        *(u32x4_any *)(FINE ? q2 : q + 16) = d;
     }
 }
 
@@ -393,7 +393,7 @@ void heads_any(HeadArgs a) {
 // over the heads of a wavefront and the four wavefronts in a fixed order and left
 // in partials[kind][block][D], which a second kernel adds in an order of its own:
 // the result does not depend on scheduling.  4096 tokens of 32 + 8 heads of 128:
-// 35.7 us (4.1 TB/s) and 4.4 for the sums.
+// 39.6 us in all (3.7 TB/s), 4 of them for the sums.
 template <int ES, int LH, bool FINE>
 __global__ __launch_bounds__(HT)
 void heads_backward_vec(HeadArgs a, int qblocks, int qparts, int kparts, int64_t kind_stride) {

@@ -9,7 +9,9 @@
 //
 // HBM-bound as shard_fold: a wavefront folds 1024 columns of one row, 16 bytes
 // per lane and load, all loads of eight shards in flight before their adds.
-// The row's scales are uniform over the wavefront.
+// The row's scales are uniform over the wavefront.  It serves row layers of few
+// output tiles for their K (rowfold_faster): 256 tokens of 14336 -> 4096 in 8 shards
+// 33.7 us, products and fold together (P M N 4 + M N 2 = 36 MB read and written here).
 #include "quant.h"
 
 namespace tpl {

@@ -1,5 +1,6 @@
 // Launch of the skinny kernel (gemm_skinny_impl.h) on int8 operands: decode
-// shapes, bound by streaming W.
+// shapes, bound by streaming W.  16 tokens, weights from HBM: 8192 -> 28672 43.1 us
+// (5.5 TB/s), 28672 -> 8192 with the fold 44.7 (5.3 TB/s).
 #include "gemm_skinny_impl.h"
 
 namespace tpl {
@@ -48,6 +49,9 @@ bool quant_skinny_supported(const GemmArgs &g, const GemmExtra &ex) {
 hipError_t launch_quant_skinny(const GemmArgs &g, int out_type, const FoldArgs *fold,
                                const GemmExtra &ex, const QuantArgs &q, hipStream_t s) {
     if (g.M == 0 || g.N == 0 || g.P == 0) return hipSuccess;
+    // The bf16 form's blocking: the bytes in flight are the same.  16 tokens, stages
+    // of 2 to 6, 16 to 64 W rows and 128 to 512 bytes of K a row were within 3% of it
+    // or behind, column and fold.
     if (ex.act == ACT_SWIGLU) {
         if (fold || out_type == OUT_I32) return hipErrorInvalidValue;
         if (g.M <= 16) return launch_t<2, 1, 256, 3>(g, out_type, fold, ex, q, s);

