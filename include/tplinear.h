@@ -457,6 +457,7 @@ tp_status tp_linear_row_quant(const int8_t *X, int64_t ldx, const float *x_scale
  * weights are [D] of dtype, shared by the heads and shards (Replicate); a NULL
  * weight means no norm for that kind of head.
  * Arithmetic in fp32, one rounding to dtype (X, weights, outputs, caches).
+ * Outputs must not overlap inputs.
  */
 enum { TP_ROPE_HALVES = 0, TP_ROPE_PAIRS = 1 };
 
@@ -488,7 +489,8 @@ tp_status tp_qk_norm_rope(const void *X, int64_t ldx, int32_t x_mode, const int6
  * dX is whole.  Tokens whose position is outside the table have zero query and
  * key gradients and count nowhere else (bad_flag as above).
  * dq_weight, dk_weight: fp32 [D] or NULL; the sums over all tokens and heads,
- * added in an order fixed by T alone.  They need a workspace of
+ * added in an order fixed by the sizes and by which of dQ, dK and dV are given.
+ * They need a workspace of
  * tp_qk_norm_rope_workspace_bytes(T, D), 256-byte aligned, which calls that may
  * overlap must not share.
  * X is read only where there is a norm (may be NULL without).

@@ -41,6 +41,9 @@ hipError_t launch_quant_tile(const GemmArgs &g, int out_type, const GemmExtra &e
     TileSched ts;
     ts.tiles_m = (int)tm;
     ts.tiles_n = (int)tn;
+    // Groups of 8 tile rows (same box, 8 shards, us with 4 / 8 / 16: 4096 tokens of 4096
+    // -> 28672 386 / 382 / 392, gated 370 / 369 / 373; 2048 tokens of 8192 -> 2 x 28672
+    // gated 728 / 704 / 701); 4 for int32 partials, as the bf16 form's fp32 ones.
     ts.group_m = out_type == OUT_I32 ? 4 : 8;
     ts.T = (int)T;
     const int cus = device_cu_count();
