@@ -11,6 +11,7 @@
 namespace tpl {
 
 typedef int q_i32x4 __attribute__((ext_vector_type(4)));
+typedef int q_i32x4_any __attribute__((ext_vector_type(4), aligned(1)));   // in memory, at any address
 
 // N values of fp32 `p` from n on, those past `end` read as element 0.
 template <int N>
@@ -56,8 +57,10 @@ __device__ __forceinline__ void quant_put16(void *C, int64_t row, int64_t n, int
     typedef typename std::conditional<OUT == OUT_BF16, uint16_t, uint32_t>::type T;
     constexpr int E = OUT == OUT_BF16 ? 8 : 4;
     T *dst = (T *)C + row + n;
-    if (vec && n + E <= N) {
-        __builtin_nontemporal_store(v, (q_i32x4 *)dst);
+    if (n + E <= N) {
+        // rows that straddle lines go through the cache, which puts the lines together
+        if (vec) __builtin_nontemporal_store(v, (q_i32x4 *)dst);
+        else *(q_i32x4_any *)dst = v;
     } else {
 #pragma unroll
         for (int e = 0; e < E; ++e)
