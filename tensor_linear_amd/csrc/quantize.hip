@@ -15,10 +15,10 @@
 // whole number is within 2^-15 of a half -- x * (1/s) is off by less than 2^-16 --
 // does it go through those 8 again exactly.
 //
-// HBM-bound, one read and one write: a wavefront (or a workgroup of four, for
-// groups over 2048 columns) holds its group in registers between the maximum and
-// the rounding, 16-byte loads, so X is read once: 4096 x 14336 bf16 in 8 groups
-// 37.6-39.5 us (4.5-4.7 TB/s), in one group 38 (47 when read twice).  Only groups of
+// HBM-bound, one read and one write: a wavefront (or a workgroup of four or
+// sixteen, for groups over 2048 columns) holds its group in registers between the
+// maximum and the rounding, 16-byte loads, so X is read once: 4096 x 14336 bf16 in
+// 8 groups 37.6-39.5 us (4.5-4.7 TB/s), in one group 38 (47 when read twice).  Only groups of
 // more than 32768 columns are read twice.  The loads need no alignment, and a
 // group's last columns past a multiple of 8 go one by one (4096 x 14342 35 us, with
 // a value a lane 109).  Loads past the caches, ordinary stores: the product that
@@ -177,12 +177,12 @@ __device__ __forceinline__ uint32_t wave_max(uint32_t v) {
     return v;
 }
 
-// W: wavefronts per group (1: four groups per workgroup; 4: one).  NV: chunks
+// W: wavefronts per group (1: four groups per workgroup; else one).  NV: chunks
 // of 8 columns that a lane holds.  TAIL: the groups are no multiple of 8 columns.
 template <int IN, int W, int NV, bool TAIL>
-__global__ __launch_bounds__(QT)
+__global__ __launch_bounds__(W == 1 ? QT : W * 64)
 void quantize_vec(QuantizeArgs a) {
-    __shared__ uint32_t red[4];
+    __shared__ uint32_t red[W];
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int64_t grp = W == 1 ? (int64_t)blockIdx.x * 4 + wave : blockIdx.x;
     if (W == 1 && grp >= a.M * a.G) return;
@@ -201,7 +201,8 @@ void quantize_vec(QuantizeArgs a) {
     if (W > 1) {
         if (lane == 0) red[wave] = mx;
         __syncthreads();
-        mx = max(max(red[0], red[1]), max(red[2], red[3]));
+#pragma unroll
+        for (int w = 0; w < W; ++w) mx = max(mx, red[w]);
     }
     float scale;
     const Step t = step_of(mx, scale);
@@ -248,14 +249,22 @@ void quantize_long(QuantizeArgs a) {
 template <int IN, bool TAIL>
 hipError_t launch_t(const QuantizeArgs &a, hipStream_t s) {
     const int64_t groups = a.M * a.G;
-    const dim3 one((unsigned)groups), four((unsigned)((groups + 3) / 4)), block(QT);
+    const dim3 one((unsigned)groups), four((unsigned)((groups + 3) / 4)), block(QT), large(1024);
+    // Long groups take sixteen wavefronts in place of four where they are few: us of 4
+    // vs 16, bf16: 16 x 8192 5.5 vs 3.9, 256 x 4096 4.3 vs 3.8 (512: 4.6 vs 4.9), 512 x 8192
+    // 7.3 vs 6.2 (1024: 10.6 vs 11.1), 512 x 14336 11.4 vs 9.0 (2048: 23.4 vs 25.5);
+    // above 16384 columns always (16 x 28672 11.6 vs 6.5, 4096 x 28672 73.6 vs 71.1, fp32
+    // 111.5 vs 106.9).
+    const int64_t cus = device_cu_count();
     if (a.Kg <= 512) quantize_vec<IN, 1, 1, TAIL><<<four, block, 0, s>>>(a);
     else if (a.Kg <= 1024) quantize_vec<IN, 1, 2, TAIL><<<four, block, 0, s>>>(a);
     else if (a.Kg <= 2048) quantize_vec<IN, 1, 4, TAIL><<<four, block, 0, s>>>(a);
-    else if (a.Kg <= 4096) quantize_vec<IN, 4, 2, TAIL><<<one, block, 0, s>>>(a);
-    else if (a.Kg <= 8192) quantize_vec<IN, 4, 4, TAIL><<<one, block, 0, s>>>(a);
-    else if (a.Kg <= 16384) quantize_vec<IN, 4, 8, TAIL><<<one, block, 0, s>>>(a);
-    else if (a.Kg <= 32768) quantize_vec<IN, 4, 16, TAIL><<<one, block, 0, s>>>(a);
+    else if (a.Kg <= 4096 && groups > cus) quantize_vec<IN, 4, 2, TAIL><<<one, block, 0, s>>>(a);
+    else if (a.Kg <= 8192 && groups > 2 * cus) quantize_vec<IN, 4, 4, TAIL><<<one, block, 0, s>>>(a);
+    else if (a.Kg <= 8192) quantize_vec<IN, 16, 1, TAIL><<<one, large, 0, s>>>(a);
+    else if (a.Kg <= 16384 && groups > 2 * cus) quantize_vec<IN, 4, 8, TAIL><<<one, block, 0, s>>>(a);
+    else if (a.Kg <= 16384) quantize_vec<IN, 16, 2, TAIL><<<one, large, 0, s>>>(a);
+    else if (a.Kg <= 32768) quantize_vec<IN, 16, 4, TAIL><<<one, large, 0, s>>>(a);
     else quantize_long<IN, TAIL><<<one, block, 0, s>>>(a);
     return hipGetLastError();
 }

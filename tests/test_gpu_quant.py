@@ -71,7 +71,8 @@ def quantize_plain(x, G):
     (1, 1, 1, 0, 0), (3, 8, 1, 0, 0), (5, 24, 3, 0, 0), (2, 30, 2, 1, 1), (7, 512, 1, 8, 0), (9, 1024, 8, 0, 0),
     (4, 4096, 4, 0, 0), (3, 1800, 1, 8, 8), (6, 2056, 1, 0, 0), (2, 8192, 1, 0, 0), (2, 8200, 1, 0, 0),
     (3, 3000, 3, 3, 0), (2, 40000, 1, 0, 0), (1, 24576, 3, 0, 0), (5, 1023, 1, 0, 1), (2, 2051, 1, 0, 0),
-    (3, 6003, 3, 2, 1), (2, 12290, 1, 1, 3), (2, 16392, 1, 0, 0), (3, 16001, 1, 3, 1), (2, 40003, 1, 1, 1), (9, 7, 7, 0, 0)])
+    (3, 6003, 3, 2, 1), (2, 12290, 1, 1, 3), (2, 16392, 1, 0, 0), (3, 16001, 1, 3, 1), (2, 40003, 1, 1, 1), (9, 7, 7, 0, 0),
+    (300, 2056, 1, 0, 0), (270, 4091, 1, 2, 1), (130, 32768, 4, 0, 0), (520, 8001, 1, 0, 0), (520, 8200, 1, 0, 0), (515, 16381, 1, 0, 3)])
 def test_quantize_matches_definition(M, K, G, extra, offset, t):
     print("quantize", M, K, G, extra, offset, t, flush=True)
     x = values(M * 1000 + K, (M, K), t)
