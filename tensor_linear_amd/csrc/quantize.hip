@@ -273,8 +273,8 @@ hipError_t launch_t(const QuantizeArgs &a, hipStream_t s) {
 
 hipError_t launch_quantize_rows(const QuantizeArgs &a, int in_type, hipStream_t s) {
     if (a.M == 0 || a.G == 0) return hipSuccess;
-    // One launch has fewer than 2^32 threads: pieces of at most 2^23 groups.
-    const int64_t most = (1 << 23) / a.G;
+    // One launch has fewer than 2^32 threads: pieces of at most 2^21 groups.
+    const int64_t most = (1 << 21) / a.G;
     for (int64_t m = 0; m < a.M; m += most) {
         QuantizeArgs b = a;
         b.M = a.M - m < most ? a.M - m : most;
