@@ -174,8 +174,9 @@ def _torch():
     global _torch_module, _DTYPES
     if _torch_module is None:
         import torch
-        _torch_module = torch
+        # the table first: another thread that finds the module set uses it
         _DTYPES = {torch.bfloat16: TP_BF16, torch.float32: TP_F32}
+        _torch_module = torch
     return _torch_module
 
 

@@ -1,0 +1,40 @@
+"""The binding's first call made from two threads at once (CPU only)."""
+import sys
+import threading
+import types
+
+import torch
+
+import tensor_linear_amd as tl
+
+
+def test_a_second_thread_in_the_middle_of_the_first_call(monkeypatch):
+    """While the first call is filling the table of types, another thread asks
+    for a type: it must get the type's code, not an empty table's refusal."""
+    found = []
+
+    def other():
+        try:
+            found.append(tl._dtype_code(torch.zeros(1)))
+        except Exception as e:
+            found.append(e)
+
+    class Slow(types.ModuleType):
+        entered = False
+
+        @property
+        def bfloat16(self):
+            if not Slow.entered:              # the first thread is held here until the second is done
+                Slow.entered = True
+                t = threading.Thread(target=other)
+                t.start()
+                t.join()
+            return torch.bfloat16
+
+        float32 = torch.float32
+
+    monkeypatch.setattr(tl, "_torch_module", None)
+    monkeypatch.setattr(tl, "_DTYPES", {})
+    monkeypatch.setitem(sys.modules, "torch", Slow("torch"))
+    assert tl._dtype_code(torch.zeros(1, dtype=torch.bfloat16)) == tl.TP_BF16
+    assert found == [tl.TP_F32]
