@@ -40,11 +40,12 @@ __device__ __forceinline__ float bias_at(const void *b, int64_t n) {
     return ((const float *)b)[n];
 }
 
+// first: the launch's first wavefront.
 template <int OUT, bool PER_SHARD>
 __global__ __launch_bounds__(QF_THREADS)
-void quant_fold_vec(ReduceArgs r, QuantArgs qa) {
+void quant_fold_vec(ReduceArgs r, QuantArgs qa, int64_t first) {
     const int64_t wpr = (r.N + QF_WCOLS - 1) / QF_WCOLS;   // wavefronts per row
-    const int64_t wid = (int64_t)blockIdx.x * (QF_THREADS / 64) +
+    const int64_t wid = first + (int64_t)blockIdx.x * (QF_THREADS / 64) +
                         __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int lane = threadIdx.x & 63;
     if (wid >= r.M * wpr) return;
@@ -106,11 +107,11 @@ void quant_fold_vec(ReduceArgs r, QuantArgs qa) {
     }
 }
 
-// Any N, stride and alignment: one thread per output.
+// Any N, stride and alignment: one thread per output, from `first` on.
 template <int OUT, bool PER_SHARD>
 __global__ __launch_bounds__(QF_THREADS)
-void quant_fold_scalar(ReduceArgs r, QuantArgs qa) {
-    const int64_t idx = (int64_t)blockIdx.x * QF_THREADS + threadIdx.x;
+void quant_fold_scalar(ReduceArgs r, QuantArgs qa, int64_t first) {
+    const int64_t idx = first + (int64_t)blockIdx.x * QF_THREADS + threadIdx.x;
     if (idx >= r.M * r.N) return;
     const int64_t m = idx / r.N;
     const int64_t n = idx - m * r.N;
@@ -133,9 +134,9 @@ void quant_fold_scalar(ReduceArgs r, QuantArgs qa) {
 inline bool aligned16(const void *p) { return ((uintptr_t)p & 15u) == 0; }
 
 template <int OUT, bool PER_SHARD>
-void launch_t(bool vec, dim3 grid, const ReduceArgs &r, const QuantArgs &q, hipStream_t s) {
-    if (vec) quant_fold_vec<OUT, PER_SHARD><<<grid, dim3(QF_THREADS), 0, s>>>(r, q);
-    else quant_fold_scalar<OUT, PER_SHARD><<<grid, dim3(QF_THREADS), 0, s>>>(r, q);
+void launch_t(bool vec, dim3 grid, const ReduceArgs &r, const QuantArgs &q, int64_t first, hipStream_t s) {
+    if (vec) quant_fold_vec<OUT, PER_SHARD><<<grid, dim3(QF_THREADS), 0, s>>>(r, q, first);
+    else quant_fold_scalar<OUT, PER_SHARD><<<grid, dim3(QF_THREADS), 0, s>>>(r, q, first);
 }
 
 }  // namespace
@@ -154,15 +155,20 @@ hipError_t launch_quant_fold(const ReduceArgs &r, const QuantArgs &q, bool per_s
     } else {
         vec = vec && out_ok(r.Y) && r.slice_stride % 4 == 0;
     }
-    const int64_t work = vec ? r.M * ((r.N + QF_WCOLS - 1) / QF_WCOLS) * 64 : r.M * r.N;
-    const int64_t blocks = (work + QF_THREADS - 1) / QF_THREADS;
-    if (blocks > 0xFFFFFFFFll / QF_THREADS) return hipErrorInvalidConfiguration;   // 2^32 threads a launch
-    const dim3 grid((unsigned)blocks);
-    if (out_type == OUT_BF16 && per_shard) launch_t<OUT_BF16, true>(vec, grid, r, q, s);
-    else if (out_type == OUT_BF16) launch_t<OUT_BF16, false>(vec, grid, r, q, s);
-    else if (per_shard) launch_t<OUT_F32, true>(vec, grid, r, q, s);
-    else launch_t<OUT_F32, false>(vec, grid, r, q, s);
-    return hipGetLastError();
+    // As many launches as the outputs need, since one has fewer than 2^32 threads.
+    const int64_t unit = vec ? 64 : 1;                     // threads of a wavefront's part of a row, or of an output
+    const int64_t units = vec ? r.M * ((r.N + QF_WCOLS - 1) / QF_WCOLS) : r.M * r.N, most = ((int64_t)1 << 31) / unit;
+    for (int64_t first = 0; first < units; first += most) {
+        const int64_t n = units - first < most ? units - first : most;
+        const dim3 grid((unsigned)((n * unit + QF_THREADS - 1) / QF_THREADS));
+        if (out_type == OUT_BF16 && per_shard) launch_t<OUT_BF16, true>(vec, grid, r, q, first, s);
+        else if (out_type == OUT_BF16) launch_t<OUT_BF16, false>(vec, grid, r, q, first, s);
+        else if (per_shard) launch_t<OUT_F32, true>(vec, grid, r, q, first, s);
+        else launch_t<OUT_F32, false>(vec, grid, r, q, first, s);
+        const hipError_t e = hipGetLastError();
+        if (e != hipSuccess) return e;
+    }
+    return hipSuccess;
 }
 
 }  // namespace tpl

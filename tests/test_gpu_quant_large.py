@@ -1,0 +1,49 @@
+"""The 8-bit layers where one launch (fewer than 2^32 threads) does not hold the
+work.  Small whole numbers and powers of two as scales: every step is exact, in
+bfloat16 too, and the expected values are computed on the GPU piece by piece."""
+import pytest
+import torch
+
+import tensor_linear_amd as tl
+from gpu_util import DEV, workspace
+
+pytestmark = pytest.mark.gpu
+
+BF = torch.bfloat16
+
+
+def small(seed, shape, most):
+    """Whole numbers of -most .. most as int8, drawn on the GPU."""
+    g = torch.Generator(device=DEV).manual_seed(seed)
+    return torch.randint(-most, most + 1, shape, generator=g, dtype=torch.int8, device=DEV)
+
+
+def powers(n):
+    """n scales of 1/2, 1, 2 in turn."""
+    return torch.tensor([0.5, 1.0, 2.0], device=DEV).repeat(n // 3 + 1)[:n]
+
+
+def need(gib):
+    if torch.cuda.mem_get_info()[0] < gib << 30:
+        pytest.skip(f"needs {gib} GiB of free GPU memory")
+
+
+def pieces(n, step):
+    return [slice(i, min(i + step, n)) for i in range(0, n, step)]
+
+
+@pytest.mark.parametrize("M,N", [(4097, 2 ** 20 + 3), (2 ** 26 + 5, 4)])
+def test_fold_of_more_outputs_than_one_launch_holds(M, N):
+    """A value a thread (N odd) and 16 bytes a lane (a wavefront a row)."""
+    print("fold", M, N, flush=True)
+    need(60)
+    P = 2
+    x, w = small(1, (M, P), 2), small(2, (N, P), 3)
+    sx, sw = powers(M * P).view(M, P), powers(N)
+    bias = small(3, (N,), 5).to(BF)
+    Y = torch.full((M, N), 99.0, dtype=BF, device=DEV)
+    tl.tp_linear_row_quant(x, sx, w, sw, Y, P, tl.TP_ROW_SUM, workspace(tl.TP_ROW_SUM, M, N, P, zero=False), bias=bias)
+    xs, ws = x.float() * sx, w.float() * sw[:, None]
+    for r in pieces(M, max(1, 2 ** 28 // N)):
+        want = xs[r, :1] * ws[:, 0] + xs[r, 1:] * ws[:, 1] + bias.float()
+        assert torch.equal(Y[r], want.to(BF)), r
