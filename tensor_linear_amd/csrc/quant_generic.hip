@@ -127,6 +127,51 @@ void quant_generic_kernel(GemmArgs g, int tiles_m, int tiles_n, int tiles, int v
         quant_store<OUT, 4, NJ>(g, ex.bias, ex.bias_shard, qa, vec, shard, mw, nw, lane, acc);
 }
 
+// One launch has fewer than 2^32 threads: more tiles go by shards, then by halves
+// of the rows or columns.
+template <int OUT, bool SW, int T>
+hipError_t launch_pieces(const GemmArgs &g, const GemmExtra &ex, const QuantArgs &q, hipStream_t s) {
+    constexpr int ON = SW ? T / 2 : T, OS = OUT == OUT_BF16 ? 2 : 4;
+    constexpr int64_t MOST = (1 << 24) - 8;
+    const int64_t tm = (g.M + T - 1) / T, tn = (g.N + ON - 1) / ON;
+    if (tm > MOST || tn > MOST || tm * tn > MOST / g.P) {
+        // rows x cols outputs from row m, column n of shard i on
+        auto part = [&](int32_t i, int64_t m, int64_t n, int64_t rows, int64_t cols) {
+            GemmArgs h = g;
+            GemmExtra e = ex;
+            QuantArgs r = q;
+            h.A = (const char *)g.A + i * g.a_shard + m * g.lda;
+            h.B = (const char *)g.B + i * g.b_shard + n * g.ldb;
+            h.C = (char *)g.C + (i * g.c_shard + m * g.ldc + n) * OS;
+            h.M = rows; h.N = cols; h.P = 1;
+            if (ex.bias) e.bias = (const char *)ex.bias + (i * ex.bias_shard + n) * OS;
+            if (OUT != OUT_I32) {
+                r.x_scale = q.x_scale + i * q.x_shard + m * q.x_ld;
+                r.w_scale = q.w_scale + i * q.w_shard + n;
+            }
+            return launch_pieces<OUT, SW, T>(h, e, r, s);
+        };
+        hipError_t e = hipSuccess;
+        if (g.P > 1) {
+            for (int32_t i = 0; i < g.P && e == hipSuccess; ++i) e = part(i, 0, 0, g.M, g.N);
+        } else if (tm > 1) {
+            const int64_t m = tm / 2 * T;
+            e = part(0, 0, 0, m, g.N);
+            if (e == hipSuccess) e = part(0, m, 0, g.M - m, g.N);
+        } else {
+            const int64_t n = tn / 2 * ON;
+            e = part(0, 0, 0, g.M, n);
+            if (e == hipSuccess) e = part(0, 0, n, g.M, g.N - n);
+        }
+        return e;
+    }
+    const int tiles = (int)(tm * tn * g.P);
+    const int vw = OUT == OUT_BF16 ? 8 : 4;
+    const int vec = g.ldc % vw == 0 && g.c_shard % vw == 0 && (uintptr_t)g.C % 16 == 0;
+    quant_generic_kernel<OUT, SW, T><<<dim3((tiles + 7) / 8 * 8), dim3(256), 0, s>>>(g, (int)tm, (int)tn, tiles, vec, ex, q);
+    return hipGetLastError();
+}
+
 template <int OUT, bool SW>
 hipError_t launch_t(const GemmArgs &g, const GemmExtra &ex, const QuantArgs &q, hipStream_t s) {
     const int on = SW ? 2 : 1;
@@ -135,16 +180,7 @@ hipError_t launch_t(const GemmArgs &g, const GemmExtra &ex, const QuantArgs &q, 
     // -> 28672 at 4096 tokens 779 vs 1357, 517 -> 4096 at 1000 (256 tiles of 128) 15.0 vs
     // 15.0, 3000 -> 8192 at 300 (192) 36.6 vs 30.1, 1001 -> 10240 at 128 (80) 21.6 vs 14.5.
     const int T = count(128) * g.P >= device_cu_count() ? 128 : 64;
-    const int64_t tm = (g.M + T - 1) / T, tn = (g.N + T / on - 1) / (T / on);
-    if (tm > 0x7FFFFFFFll || tn > 0x7FFFFFFFll || tm * tn > 0x7FFFFFFFll / QGROUP || tm * tn * g.P > 0xFFFFFFFFll / 256 - 8)
-        return hipErrorInvalidConfiguration;   // 2^32 threads a launch
-    const int tiles = (int)(tm * tn * g.P);
-    const int vw = OUT == OUT_BF16 ? 8 : 4;
-    const int vec = g.ldc % vw == 0 && g.c_shard % vw == 0 && (uintptr_t)g.C % 16 == 0;
-    const dim3 grid((tiles + 7) / 8 * 8), block(256);
-    if (T == 128) quant_generic_kernel<OUT, SW, 128><<<grid, block, 0, s>>>(g, (int)tm, (int)tn, tiles, vec, ex, q);
-    else quant_generic_kernel<OUT, SW, 64><<<grid, block, 0, s>>>(g, (int)tm, (int)tn, tiles, vec, ex, q);
-    return hipGetLastError();
+    return T == 128 ? launch_pieces<OUT, SW, 128>(g, ex, q, s) : launch_pieces<OUT, SW, 64>(g, ex, q, s);
 }
 
 }  // namespace

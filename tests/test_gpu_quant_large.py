@@ -47,3 +47,38 @@ def test_fold_of_more_outputs_than_one_launch_holds(M, N):
     for r in pieces(M, max(1, 2 ** 28 // N)):
         want = xs[r, :1] * ws[:, 0] + xs[r, 1:] * ws[:, 1] + bias.float()
         assert torch.equal(Y[r], want.to(BF)), r
+
+
+@pytest.mark.parametrize("M,n,P", [(2 ** 25 + 200, 1, 64), (2 ** 31 + 100, 1, 1)])
+def test_generic_column_of_more_tiles_than_one_launch_holds(M, n, P):
+    """An odd K: many shards, and many tokens of one."""
+    print("generic", M, n, P, flush=True)
+    need(60)
+    N = n * P
+    x, w = small(1, (M, 1), 2), small(2, (N, 1), 3)
+    sx, sw = powers(M), powers(N)
+    bias = small(3, (N,), 5).to(BF)
+    for shards in (False, True) if P > 1 else (False,):
+        Y = torch.full((P, M, n) if shards else (M, N), 99.0, dtype=BF, device=DEV)
+        tl.tp_linear_column_quant(x, sx, w, sw, Y, P, tl.TP_Y_SHARDS if shards else tl.TP_Y_CONCAT, bias=bias)
+        for r in pieces(M, 2 ** 28 // N):
+            want = (x[r].float() * sx[r, None] * (w[:, 0].float() * sw) + bias.float()).to(BF)
+            assert torch.equal(Y[:, r, 0].t() if shards else Y[r], want), r
+        del Y
+
+
+def test_generic_gated_column_of_more_tiles_than_one_launch_holds():
+    """Many hidden units of one shard: gate rows, then up rows."""
+    print("generic gated", flush=True)
+    need(60)
+    n = 2 ** 30 + 100
+    x = torch.tensor([[1]], dtype=torch.int8, device=DEV)
+    w = small(2, (2 * n, 1), 3)
+    w[:n] = 100                              # silu(100) is 100 in fp32
+    sw = torch.ones(2 * n, device=DEV)
+    sw[n:] = powers(n)
+    Y = torch.full((1, n), 99.0, device=DEV)
+    tl.tp_linear_column_quant(x, torch.ones(1, device=DEV), w, sw, Y, 1, act=tl.TP_ACT_SWIGLU)
+    for r in pieces(n, 2 ** 28):
+        up = slice(n + r.start, n + r.stop)
+        assert torch.equal(Y[0, r], 100.0 * w[up, 0].float() * sw[up]), r
