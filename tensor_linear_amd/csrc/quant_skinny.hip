@@ -13,9 +13,27 @@ hipError_t launch_t(const GemmArgs &g, int out_type, const FoldArgs *fold, const
     const bool sw = ex.act == ACT_SWIGLU;
     const int64_t tn = (g.N + (sw ? 16 : BN) - 1) / (sw ? 16 : BN);
     const int64_t blocks = fold ? tn : tn * g.P;
-    if (tn > 0x7FFFFFFFll || blocks > 0xFFFFFFFFll / SK_THREADS) return hipErrorInvalidConfiguration;
-    const dim3 grid((unsigned)blocks), block(SK_THREADS);
     const FoldArgs f = fold ? *fold : FoldArgs{nullptr, 0, 0};
+    if (blocks > 0xFFFFFFFFll / SK_THREADS) {
+        // One launch has fewer than 2^32 threads: the columns in halves.
+        const int64_t n = tn / 2 * (sw ? 16 : BN);
+        const int os = out_type == OUT_BF16 ? 2 : 4;
+        GemmArgs h = g;
+        h.N = n;
+        const hipError_t e = launch_t<NB, MB, KB, NST>(h, out_type, fold, ex, q, s);
+        if (e != hipSuccess) return e;
+        h.N = g.N - n;
+        h.B = (const char *)g.B + n * g.ldb;
+        GemmExtra x = ex;
+        QuantArgs r = q;
+        FoldArgs y = f;
+        if (ex.bias) x.bias = (const char *)ex.bias + n * os;
+        if (out_type != OUT_I32) r.w_scale = q.w_scale + n;
+        if (fold) y.Y = (char *)f.Y + n * os;
+        else h.C = (char *)g.C + n * os;
+        return launch_t<NB, MB, KB, NST>(h, out_type, fold ? &y : nullptr, x, r, s);
+    }
+    const dim3 grid((unsigned)blocks), block(SK_THREADS);
     if (sw) {
         if constexpr (NB == 2) {
             if (out_type == OUT_BF16) gemm_skinny_kernel<NB, MB, KB, NST, OUT_BF16, false, true, OpI8><<<grid, block, 0, s>>>(g, f, ex, q);

@@ -28,6 +28,11 @@ def need(gib):
         pytest.skip(f"needs {gib} GiB of free GPU memory")
 
 
+def rows_product(x, w):
+    """x w^T, a row of x at a time."""
+    return torch.stack([(w.float() * row).sum(1) for row in x.float()])
+
+
 def pieces(n, step):
     return [slice(i, min(i + step, n)) for i in range(0, n, step)]
 
@@ -82,3 +87,33 @@ def test_generic_gated_column_of_more_tiles_than_one_launch_holds():
     for r in pieces(n, 2 ** 28):
         up = slice(n + r.start, n + r.stop)
         assert torch.equal(Y[0, r], 100.0 * w[up, 0].float() * sw[up]), r
+
+
+@pytest.mark.parametrize("M", [1, 3])
+def test_skinny_column_of_more_workgroups_than_one_launch_holds(M):
+    print("skinny", M, flush=True)
+    need(60)
+    N, K, P = 2 ** 28 + 64, 16, 2
+    x, w = small(1, (M, K), 1), small(2, (N, K), 3)
+    sx, sw = powers(M), powers(N)
+    bias = small(3, (N,), 5).to(BF)
+    Y = torch.full((M, N), 99.0, dtype=BF, device=DEV)
+    tl.tp_linear_column_quant(x, sx, w, sw, Y, P, bias=bias)
+    for r in pieces(N, 2 ** 26):
+        want = rows_product(x, w[r]) * sx[:, None] * sw[r] + bias[r].float()
+        assert torch.equal(Y[:, r], want.to(BF)), r
+
+
+def test_skinny_fold_of_more_workgroups_than_one_launch_holds():
+    print("skinny fold", flush=True)
+    need(90)
+    M, N, K, P = 1, 2 ** 29 + 64, 32, 2
+    x, w = small(1, (M, K), 1), small(2, (N, K), 2)
+    sx, sw = powers(M * P).view(M, P), powers(N)
+    bias = small(3, (N,), 5).to(BF)
+    Y = torch.full((M, N), 99.0, dtype=BF, device=DEV)
+    tl.tp_linear_row_quant(x, sx, w, sw, Y, P, tl.TP_ROW_FUSED, workspace(tl.TP_ROW_FUSED, M, N, P, zero=False), bias=bias)
+    xs = x.float() * sx.repeat_interleave(K // P, 1)
+    for r in pieces(N, 2 ** 26):
+        want = rows_product(xs, w[r]) * sw[r] + bias[r].float()
+        assert torch.equal(Y[:, r], want.to(BF)), r
