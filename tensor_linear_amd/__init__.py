@@ -627,6 +627,15 @@ def tp_embedding(ids, Y, P: int, E=None, e_shards=None, y_mode: int = TP_Y_CONCA
                                   None if bad is None else bad.data_ptr(), _stream(ids, stream)))
 
 
+def _workspace(t):
+    """Pointer and bytes of a workspace, or of none."""
+    if t is None:
+        return None, 0
+    if not t.is_contiguous():
+        raise ValueError("workspace must be contiguous")
+    return t.data_ptr(), t.numel() * t.element_size()
+
+
 # ---- 8-bit integers -------------------------------------------------------
 
 def _int8_mat(t, name):
@@ -747,10 +756,7 @@ def tp_linear_row_quant(X, x_scale, W, w_scale, Y, P: int, mode: int = TP_ROW_SU
     else:
         dt = _dtype_code(Y)
         yp, ldy = _scatter_out(Y, M, N, P, mode == TP_ROW_SCATTER, y_slice_stride)
-    if workspace is not None:
-        wkp, wkb = workspace.data_ptr(), workspace.numel() * workspace.element_size()
-    else:
-        wkp, wkb = None, 0
+    wkp, wkb = _workspace(workspace)
     on = _here(stream, X, x_scale, W, w_scale, Y, workspace, bias, *(y_slices or ()))
     check(_get_lib().tp_linear_row_quant(xp, ldx, sp, lds, G, wp, ldw, wsp, _bias_ptr(bias, dt),
                                          yp, ys, ldy, y_slice_stride, mode, wkp, wkb, M, N, K, P,
@@ -899,10 +905,7 @@ def tp_qk_norm_rope_backward(X, pos, cos, sin, dQ, dK, dX, P: int, Hq: int, Hkv:
             _expect_shape(t, (D,), name)
             if t.dtype != torch.float32 or (D > 1 and t.stride(0) != 1):
                 raise ValueError(f"{name} must be a contiguous float32 [D] tensor")
-    if workspace is not None:
-        wkp, wkb = workspace.data_ptr(), workspace.numel() * workspace.element_size()
-    else:
-        wkp, wkb = None, 0
+    wkp, wkb = _workspace(workspace)
     on = _here(stream, dX, X, pos, cos, sin, dQ, dK, dV, q_weight, k_weight, dq_weight, dk_weight,
                workspace, bad)
     check(_get_lib().tp_qk_norm_rope_backward(
