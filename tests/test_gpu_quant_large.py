@@ -117,3 +117,20 @@ def test_skinny_fold_of_more_workgroups_than_one_launch_holds():
     for r in pieces(N, 2 ** 26):
         want = rows_product(xs, w[r]) * sw[r] + bias[r].float()
         assert torch.equal(Y[:, r], want.to(BF)), r
+
+
+def test_quantize_more_long_groups_than_one_launch_holds():
+    """2^21 groups, and a few, of a workgroup of 1024 threads each."""
+    print("quantize", flush=True)
+    need(130)
+    M, K = 2 ** 21 + 5, 16392
+    x = torch.empty((M, K), dtype=BF, device=DEV)
+    row = small(1, (K,), 100)
+    x[:] = row.to(BF)
+    last = (torch.arange(M, device=DEV) % 255 - 127).to(torch.int8)     # a value of its own for each row
+    x[:, 0], x[:, K - 1] = 127.0, last.to(BF)
+    q, s = torch.empty((M, K), dtype=torch.int8, device=DEV), torch.empty(M, device=DEV)
+    tl.tp_quantize_rows(x, q, s)
+    assert torch.all(s == 1.0) and torch.all(q[:, 0] == 127) and torch.equal(q[:, K - 1], last)
+    for r in pieces(M, 2 ** 17):
+        assert torch.all(q[r, 1:K - 1] == row[1:K - 1]), r
