@@ -370,6 +370,8 @@ tp_status tp_linear_row_noalloc(const void *X, int64_t ldx, const void *W, int64
  * The same layers with X and W held as int8 and one fp32 scale for each token
  * and each output channel: x ~ x_scale[m] * X[m, k], w ~ w_scale[n] * W[n, k].
  * The integer sums are exact; they are rounded once to fp32 and scaled.
+ * No call is refused for its number of outputs: one that a launch cannot hold
+ * (2^32 threads) takes several.
  */
 
 /*
@@ -399,6 +401,8 @@ tp_status tp_quantize_rows(const void *X, int64_t ldx, int8_t *Q, int64_t ldq, f
  * x_scale: token m's at x_scale[m*ldxs], ldxs >= 1.  w_scale: [N], in the order
  * of W's rows (Shard(0), as the bias).  Output feature n of token m before the
  * activation: fma(float(sum_k X W) * x_scale[m], w_scale[n], bias[n] or 0).
+ * The gated unit's silu takes the hardware's reciprocal (1 ulp) and not a
+ * division: gates below -87.3 give 0, where silu is less than 1.1e-36 in size.
  * out_dtype: TP_BF16 or TP_F32, the type of Y and of the bias.
  * K is at most 131071, so that no int32 sum overflows.
  * Other arguments and errors as tp_linear_column_ex (no x_slices);
@@ -456,7 +460,9 @@ tp_status tp_linear_row_quant(const int8_t *X, int64_t ldx, const float *x_scale
  * Norm: y = x * rsqrt(mean(x^2) + eps) * weight over the D features of a head;
  * weights are [D] of dtype, shared by the heads and shards (Replicate); a NULL
  * weight means no norm for that kind of head.
- * Arithmetic in fp32, one rounding to dtype (X, weights, outputs, caches).
+ * Arithmetic in fp32, one rounding to dtype (X, weights, outputs, caches); a
+ * head whose sum of squares is past fp32 (values of about 1e18 and more) is
+ * normed to zeros.
  * Outputs must not overlap inputs.
  */
 enum { TP_ROPE_HALVES = 0, TP_ROPE_PAIRS = 1 };

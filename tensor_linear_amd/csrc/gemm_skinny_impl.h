@@ -116,9 +116,10 @@ void gemm_skinny_kernel(GemmArgs g, FoldArgs f, GemmExtra ex, QuantArgs qa) {
     // int8, fused fold: the workgroups walk K in step, and rows a multiple of 4 KB
     // apart put their reads of one moment on few memory channels.  The sum does not
     // depend on the order of K, so each workgroup then begins a shard at a stage of
-    // its own and wraps: 16 tokens, 28672 -> 8192 52.6 -> 48.3 us (weights from HBM).
-    // Without such a stride it costs a little (14336 -> 4096 18.7 -> 19.5), and the
-    // column form, whose workgroups are not in step, gains nothing.
+    // its own and wraps: 16 tokens, weights from HBM, 28672 -> 8192 49.5 -> 47.3 us, 32768
+    // -> 8192 58.2 -> 56.9, 8192 -> 8192 20.6 -> 20.1.  Without such a stride it costs a
+    // little (14336 -> 4096 after a flush 24.4 -> 24.8), and the column form, whose
+    // workgroups are not in step, gains nothing.
     const int rot = OP::INT8 && FOLD && g.ldb % 4096 == 0 ? (int)(blockIdx.x % (unsigned)nks) : 0;
     auto turned = [&](int k) { return OP::INT8 && FOLD ? (k + rot < nks ? k + rot : k + rot - nks) : k; };
     auto issue = [&](int t) {

@@ -388,7 +388,8 @@ void heads_any(HeadArgs a) {
 // + waves / parts, ...; with tokens enough that is one part, and a token's angles
 // are loaded once.  The next heads' values and the next token's angles are loaded
 // while the current ones are worked on (the sums, weights and angles leave room
-// for three wavefronts a SIMD, too few to hide the loads by themselves).  The
+// for three wavefronts a SIMD in bf16 with R a multiple of 16, 155 registers, and for
+// two in fp32 or with another R, 171-195: too few to hide the loads by themselves).  The
 // weights' gradient sums of a lane's 16 values stay in registers; they are added
 // over the heads of a wavefront and the four wavefronts in a fixed order and left
 // in partials[kind][block][D], which a second kernel adds in an order of its own:
@@ -750,9 +751,11 @@ hipError_t launch_bwd(const HeadArgs &a, hipStream_t s) {
 
 }  // namespace
 
-// Three wavefronts on each SIMD of 256 CUs (what a wavefront's registers allow;
-// 4096 tokens of 32 + 8 heads of 128, us: 512 workgroups 41.2, 768 35.6, 1024 39.6,
-// 2048 39.6), fewer where a token's heads in parts are fewer.
+// Three wavefronts on each SIMD of 256 CUs (what the registers of the commonest form
+// allow; 4096 tokens of 32 + 8 heads of 128, us: 512 workgroups 41.2, 768 35.6, 1024 39.6,
+// 2048 39.6), fewer where a token's heads in parts are fewer.  Not taken from the
+// device: the workspace's size and the order of the weights' sums depend on the call's
+// sizes alone.
 int64_t qk_backward_blocks(int64_t T) {
     const int64_t b = T < 64 ? 16 * T : 768;
     return b < 1 ? 1 : b > 768 ? 768 : b;

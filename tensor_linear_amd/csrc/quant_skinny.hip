@@ -1,6 +1,9 @@
 // Launch of the skinny kernel (gemm_skinny_impl.h) on int8 operands: decode
-// shapes, bound by streaming W.  16 tokens, weights from HBM: 8192 -> 28672 43.1 us
-// (5.5 TB/s), 28672 -> 8192 with the fold 44.7 (5.3 TB/s).
+// shapes, bound by streaming W.  16 tokens, 8 shards, weights from HBM (several in turn
+// that no cache holds): 8192 -> 28672 43.9 us (5.4 TB/s), 28672 -> 8192 with the fold 47.3
+// (5.0), 4096 -> 28672 26.3 (4.5), 8192 -> 10240 19.3 (4.4).  Few output features leave a
+// CU one or two workgroups, whose stages end in a barrier with nothing beside them:
+// 14336 -> 4096 with the fold 20.7 (2.8), 4096 -> 6144 8.9 (2.8), 4096 -> 4096 7.3 (2.3).
 #include "gemm_skinny_impl.h"
 
 namespace tpl {

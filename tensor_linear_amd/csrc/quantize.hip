@@ -18,9 +18,9 @@
 // HBM-bound, one read and one write: a wavefront (or a workgroup of four or
 // sixteen, for groups over 2048 columns) holds its group in registers between the
 // maximum and the rounding, 16-byte loads, so X is read once: 4096 x 14336 bf16 in
-// 8 groups 37.6-39.5 us (4.5-4.7 TB/s), in one group 38 (47 when read twice).  Only groups of
+// 8 groups or in one 36.6 us (4.8 TB/s; 47 when read twice).  Only groups of
 // more than 32768 columns are read twice.  The loads need no alignment, and a
-// group's last columns past a multiple of 8 go one by one (4096 x 14342 35 us, with
+// group's last columns past a multiple of 8 go one by one (4096 x 14342 38 us, with
 // a value a lane 109).  Loads past the caches, ordinary stores: the product that
 // comes next reads Q, not X.  Stores past the caches are faster by themselves (4096
 // x 4096 12.4 us for 14.7), but with the product behind them 256 x 8192 -> 10240 takes

@@ -50,15 +50,20 @@ hipError_t run_quant(const GemmArgs &g, int out, const GemmExtra &ex, const Quan
 
 // One scale a token: one product over all of K, or P int32 partials and their
 // fold (the same integer sums).  The product has P times fewer workgroups to
-// hide its longer loop; the partials cost 8 P M N bytes.  Same box, 8 shards, us
-// after a flush, product vs partials: 16 tokens 14336 -> 4096 19.7 vs 24.6, 8192 ->
-// 8192 18.7 vs 27.0, 28672 -> 8192 48.3 vs 55.5, but 28672 -> 2048 31.1 vs 22.8; 32
-// tokens 8192 -> 8192 26.3 vs 28.4, 14336 -> 4096 35.1 vs 24.9; above, with r = P M N
-// / K: 14336 -> 4096 at 128 tokens (r = 293) 44.6 vs 23.1, 4096 -> 2048 at 128 (512) 13.0
-// vs 11.8, at 200 (800) 13.0 vs 13.7, 8192 -> 2048 at 300 (600) 21.5 vs 21.6, 28672 ->
-// 8192 at 256 (585) 103.7 vs 83.8, at 384 (878) 150 vs 144 (warm 118 vs 127), 8192 ->
-// 8192 at 128 (1024) 32.7 vs 37.1; the second launch itself is about 1.2e6 of P M N
-// (1024 -> 1024 at 64 tokens 6.1 vs 9.2).
+// hide its longer loop; the partials cost 8 P M N bytes.  8 shards, us, product vs
+// partials, weights from HBM (several in turn that no cache holds, in a graph): 16
+// tokens 14336 -> 4096 16.3 vs 21.1, 8192 -> 8192 15.2 vs 23.5, 28672 -> 8192 47.5 vs
+// 53.0, but 28672 -> 2048 28.2 vs 20.6; 32 tokens 8192 -> 8192 24.4 vs 25.3, 14336 ->
+// 4096 31.9 vs 22.2; above, with r = P M N / K: 14336 -> 4096 at 128 tokens (r = 293) 50.8
+// vs 23.8, 4096 -> 2048 at 128 (512) 16.5 vs 12.4, at 200 (800) 15.5 vs 14.1 (warm 13.1 vs
+// 14.7), 8192 -> 2048 at 300 (600) 28.5 vs 22.2, 28672 -> 8192 at 256 (585) 104 vs 81, at
+// 384 (878) 140 vs 129 (warm 103 vs 125), 8192 -> 8192 at 128 (1024) 32.3 vs 36.1: around
+// the threshold of 800 the partials win with cold weights and the product with warm ones.
+// The second launch itself is about 1.2e6 of P M N (1024 -> 1024 at 64 tokens 6.6 vs 9.4).
+// The rule holds for one output.  Token slices (TP_ROW_SCATTER) take it as well, though
+// each slice is then a product of its own that reads all of W: 8192 -> 8192 after a
+// flush, in slices vs in one output, 16 tokens 77.6 vs 18.0 (partials 26.6), 64 tokens 36.4
+// vs 36.2, 256 tokens 85.7 vs 34.7.
 bool one_product_faster(int64_t M, int64_t N, int64_t K, int32_t P) {
     if (P == 1) return true;
     if (M <= 16 && N >= 16 * (int64_t)device_cu_count()) return true;
@@ -67,20 +72,21 @@ bool one_product_faster(int64_t M, int64_t N, int64_t K, int32_t P) {
 }
 
 // A scale for each token and shard: the fold inside the product, or int32
-// partials and their fold (the same bits).  Same box, 8 shards, us after a flush,
-// fold inside vs partials.  Up to 16 tokens (skinny): 14336 -> 4096 23.2 vs 24.5,
-// 28672 -> 8192 52.4 vs 55.4, 4096 -> 2048 11.8 vs 13.9, 1024 -> 1024 11.2 vs 12.3, but
-// 28672 -> 2048 32.1 vs 23.5 and 14080 -> 2000 22.0 vs 18.7 (fewer workgroups than
-// CUs and a long K); 32 tokens 14336 -> 4096 53.2 vs 25.1.
+// partials and their fold (the same bits).  8 shards, us, fold inside vs partials,
+// weights from HBM as above.  Up to 16 tokens (skinny): 28672 -> 8192 47.3 vs 54.4, 8192
+// -> 8192 20.1 vs 23.7, 14336 -> 4096 20.7 vs 21.3 (warm 20.5 vs 19.0), 4096 -> 2048 8.6 vs
+// 10.4, 1024 -> 1024 7.6 vs 8.0, but 28672 -> 2048 30.4 vs 20.8 and 14080 -> 2000 19.8 vs 16.1
+// (fewer workgroups than CUs and a long K); 32 tokens 14336 -> 4096 50.2 vs 22.2.
 bool skinny_fold_faster(int64_t M, int64_t N, int64_t K) {
     return M <= 16 && (N >= 16 * (int64_t)device_cu_count() || K <= 4096);
 }
 
 // 256 x 128 tiles with the fold in registers walk the shards of a tile in turn,
-// so they need enough tiles, the more the longer the shard's K: K/P = 512 at 64
-// tiles 43.6 vs 37.2, at 96 44.5 vs 54.9; 1024 at 64 68.5 vs 45.6, at 128 68.3 vs 79.4;
-// 1792 at 128 107.6 vs 94.4, at 192 110.3 vs 132.0; 3584 at 192 209.8 vs 200.7, at 256
-// 212.7 vs 272.0; 4096 tokens 14336 -> 4096 220.0 vs 332.4, 28672 -> 8192 757.6 vs 1021.5.
+// so they need enough tiles, the more the longer the shard's K (us, fold vs partials,
+// weights from HBM as above): K/P = 512 at 48 tiles 37.6 vs 30.0, at 64 37.7 vs 36.3, at 96
+// 37.6 vs 55.0; 1024 at 64 61.7 vs 41.8, at 128 61.2 vs 75.4; 1792 at 128 103.6 vs 94.2, at
+// 160 103.6 vs 123.7; 3584 at 192 194.5 vs 197.5, at 256 216 vs 257; 4096 tokens 14336 -> 4096
+// 219 vs 344, 28672 -> 8192 810 vs 1080.
 bool rowfold_faster(int64_t M, int64_t N, int64_t Ks) {
     if (M <= 64) return false;   // its 256-row tile would be three-quarters empty
     const int64_t tiles = ((M + 255) / 256) * ((N + 127) / 128), cus = device_cu_count();

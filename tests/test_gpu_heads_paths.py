@@ -169,3 +169,22 @@ def test_a_head_that_is_not_finite_stays_alone(D, R):
     for a in (Q, dX):
         a[3, 5 * D:6 * D] = 0
     assert torch.equal(Q, Q2) and torch.equal(K, K2) and torch.equal(dX, dX2) and torch.equal(dwk, dwk2)
+
+
+@pytest.mark.parametrize("t", [BF, F32])
+@pytest.mark.parametrize("D,R", [(128, 128), (80, 40), (40, 20)])
+def test_a_sum_of_squares_past_fp32_is_normed_to_zeros(D, R, t):
+    T, Hq, Hkv = 3, 4, 2
+    cos, sin = (dev(a) for a in tables(9, R))
+    x = dev(values(1, (T, (Hq + 2 * Hkv) * D), t))
+    y = x.clone()
+    y[1, 2 * D] = 2.0 ** 65                              # its square is past the largest fp32 value
+    outs = []
+    for x_ in (x, y):
+        Q, K = torch.empty((T, Hq * D), dtype=t, device=DEV), torch.empty((T, Hkv * D), dtype=t, device=DEV)
+        w = torch.ones(D, dtype=t, device=DEV)
+        tl.tp_qk_norm_rope(x_, torch.arange(T, device=DEV), cos, sin, Q, K, 1, Hq, Hkv, q_weight=w, k_weight=w)
+        outs.append((Q, K))
+    assert torch.all(outs[1][0][1, 2 * D:3 * D] == 0)
+    outs[0][0][1, 2 * D:3 * D] = 0
+    assert torch.equal(outs[0][0], outs[1][0]) and torch.equal(outs[0][1], outs[1][1])
