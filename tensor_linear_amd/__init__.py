@@ -807,7 +807,7 @@ def _rotation(cos, sin, q_weight, k_weight, D, dt, eps, style):
     n_pos = R = 0
     cp = sp = wq = wk = None
     if cos is not None and sin is not None:
-        shape, f32 = cos.shape, _torch_module.float32
+        shape, f32 = cos.shape, _torch().float32
         if cos.dtype != f32 or sin.dtype != f32 or len(shape) != 2 or not (
                 cos.is_contiguous() and sin.is_contiguous()):
             raise ValueError("cos and sin must be contiguous float32 [n_pos, R/2] tensors")
@@ -841,7 +841,7 @@ def _positions(pos, T, R):
         return None
     if pos.shape != (T,):
         _expect_shape(pos, (T,), "pos")
-    if pos.dtype != _torch_module.int64 or (T > 1 and pos.stride(0) != 1):
+    if pos.dtype != _torch().int64 or (T > 1 and pos.stride(0) != 1):
         raise ValueError("pos must be a contiguous int64 [T] tensor")
     return pos.data_ptr()
 
@@ -849,7 +849,7 @@ def _positions(pos, T, R):
 def _flag(bad):
     if bad is None:
         return None
-    if bad.dtype != _torch_module.int32 or bad.numel() < 1:
+    if bad.dtype != _torch().int32 or bad.numel() < 1:
         raise ValueError("bad must be an int32 tensor")
     return bad.data_ptr()
 

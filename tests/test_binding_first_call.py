@@ -38,3 +38,16 @@ def test_a_second_thread_in_the_middle_of_the_first_call(monkeypatch):
     monkeypatch.setitem(sys.modules, "torch", Slow("torch"))
     assert tl._dtype_code(torch.zeros(1, dtype=torch.bfloat16)) == tl.TP_BF16
     assert found == [tl.TP_F32]
+
+
+def test_a_second_thread_between_the_table_and_the_module(monkeypatch):
+    """The table is filled, the module not yet published: what the checks of the
+    head steps read must not depend on the module being there."""
+    monkeypatch.setattr(tl, "_DTYPES", {torch.bfloat16: tl.TP_BF16, torch.float32: tl.TP_F32})
+    T, R, D = 3, 4, 8
+    cos = torch.zeros(5, R // 2)
+    for call in (lambda: tl._rotation(cos, cos, None, torch.zeros(D), D, tl.TP_F32, 1e-6, tl.TP_ROPE_HALVES),
+                 lambda: tl._positions(torch.zeros(T, dtype=torch.int64), T, R),
+                 lambda: tl._flag(torch.zeros(1, dtype=torch.int32))):
+        monkeypatch.setattr(tl, "_torch_module", None)
+        assert call() is not None
