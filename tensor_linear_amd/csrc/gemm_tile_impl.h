@@ -81,7 +81,7 @@
 // outputs, which are scaled and stored from the registers (quant_epilogue.h).
 // That epilogue is what one workgroup a CU cannot hide: 4096 tokens of 4096 -> 2 x
 // 14336 with the gated unit took 394 us through LDS and with a divide, and take
-// 356-366 (2.63-2.70 POP/s); without the unit 4096 -> 28672 takes 373.
+// 356-366 (2.63-2.70 POP/s); without the unit 4096 -> 28672 takes 373-387.
 #pragma once
 
 #include <type_traits>
