@@ -11,7 +11,7 @@
 // zeros, which add nothing to an integer sum.  It serves what the DMA kernels
 // cannot load (K or strides not a multiple of 16, unaligned views) and is bound by
 // its unaligned loads, which often take two lines each: 4096 tokens of 4097 -> 28672
-// 779-827 us by the box's temperature (1.2 POP/s; the DMA kernels with K = 4096 373-387), three shards of 1999 ->
+// 779-827 us (1.2 POP/s; the DMA kernels with K = 4096 373-387), three shards of 1999 ->
 // 1112 at 333 tokens 23 us (10.8).  256 bytes a stage for the small tile were slower
 // (1999: 33 us).
 #include "quant.h"
