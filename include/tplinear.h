@@ -548,6 +548,158 @@ tp_status tp_kv_append(const void *X, int64_t ldx, int32_t x_mode, const float *
                        int64_t Hkv, int64_t D, int32_t P, int32_t dtype, int32_t *bad_flag,
                        void *stream);
 
+/* ---- the cache in 8 bits, and attention over it -----------------------------
+ *
+ * An 8-bit cache holds int8 values and one fp32 scale for each token and head of
+ * the keys and of the values: x ~ scale * q.  The scale of (page, slot, head) is
+ * at page*scale_page_stride + slot*scale_slot_stride + head*scale_head_stride.
+ */
+
+/*
+ * tp_kv_append_quant -- tp_kv_append into a cache in 8 bits.
+ *
+ * The keys (normed and rotated, in fp32, not rounded to dtype before) and the
+ * values of each head of D: scale = max |x| / 127, rounded to fp32; q = x / scale,
+ * the exact quotient rounded to the nearest whole number (halves to even), at most
+ * 127 in size.  A head of zeros (or whose scale rounds to 0) has scale 0 and zeros;
+ * one that holds an infinity or a NaN has scale NaN and zeros.
+ * k_scale, v_scale: of the same strides, no two of which may share an element.
+ * Other arguments and errors as tp_kv_append; dtype is that of X, the weights and
+ * Q.  TP_ERR_NULL for a missing scale.
+ */
+tp_status tp_kv_append_quant(const void *X, int64_t ldx, int32_t x_mode, const float *cos_t,
+                             const float *sin_t, int64_t n_pos, int64_t R, int32_t style,
+                             const void *q_weight, const void *k_weight, float eps,
+                             const int32_t *cu, const int32_t *past, int64_t B,
+                             const int32_t *table, int64_t ldt, int64_t max_pages,
+                             int8_t *k_cache, int8_t *v_cache, int64_t n_pages, int64_t page_size,
+                             int64_t page_stride, int64_t slot_stride, int64_t head_stride,
+                             float *k_scale, float *v_scale, int64_t scale_page_stride,
+                             int64_t scale_slot_stride, int64_t scale_head_stride, void *Q,
+                             int64_t ldq, int64_t T, int64_t Hq, int64_t Hkv, int64_t D, int32_t P,
+                             int32_t dtype, int32_t *bad_flag, void *stream);
+
+/*
+ * tp_kv_read -- rows of a paged cache as matrices.
+ *
+ * Row t of sequence s (cu[s] <= t < cu[s+1], cu as in tp_kv_append) is the cache's
+ * row at position past[s] + t - cu[s]: its Hkv heads of keys to K [T, Hkv*D] (ldk >=
+ * Hkv*D), of values to V [T, Hkv*D]; either may be NULL with its cache and scale.
+ * k_scale, v_scale NULL: the cache is of dtype, the rows are copies.  Otherwise it is
+ * int8 and a value is q * scale in fp32, rounded once to dtype.
+ * A position outside [0, max_pages*page_size) or whose page is outside [0, n_pages)
+ * gives zero rows and sets *bad_flag; rows no sequence owns are left alone.
+ * Errors: TP_ERR_NULL (both K and V missing, a cache missing for one that is given, a
+ * scale for one of two and not the other), TP_ERR_SHAPE (sizes, leading dims,
+ * negative strides, D not in 1 .. 1024), TP_ERR_DTYPE, TP_ERR_HIP.
+ */
+tp_status tp_kv_read(const int32_t *cu, const int32_t *past, int64_t B, const int32_t *table,
+                     int64_t ldt, int64_t max_pages, const void *k_cache, const void *v_cache,
+                     int64_t n_pages, int64_t page_size, int64_t page_stride, int64_t slot_stride,
+                     int64_t head_stride, const float *k_scale, const float *v_scale,
+                     int64_t scale_page_stride, int64_t scale_slot_stride,
+                     int64_t scale_head_stride, void *K, int64_t ldk, void *V, int64_t ldv,
+                     int64_t T, int64_t Hkv, int64_t D, int32_t dtype, int32_t *bad_flag,
+                     void *stream);
+
+/*
+ * tp_kv_attention -- attention of new tokens over a paged cache that already holds
+ * their keys and values (tp_kv_append or tp_kv_append_quant of the same cu, past and
+ * table): a decode step's single tokens, chunks and prompts of any lengths in one call.
+ *
+ * Q [T, Hq*D], O [T, Hq*D] (ldq, ldo >= Hq*D): the order of heads of tp_kv_append, so
+ * that O is the input of a row layer whose shard i has the columns of its own heads.
+ * Query head h reads key and value head h / (Hq/Hkv).
+ * Row t of sequence s has the position p = past[s] + t - cu[s] and sees the positions
+ * j <= p, with window > 0 only j > p - window.  With x_j the dot product of its query
+ * and key j times softmax_scale:
+ *   O = sum_j exp(x_j) v_j / sum_j exp(x_j);  lse = log(sum_j exp(x_j)).
+ * lse: fp32 [T, Hq], ldl >= Hq, or NULL.
+ * A position that the row sees but that lies outside [0, max_pages*page_size), or
+ * whose page is outside [0, n_pages), is left out and sets *bad_flag.  A row with
+ * nothing left to see (or only products of minus infinity) has zeros and lse minus
+ * infinity.  What a row does not see has no effect on it, whatever it holds.  Rows no
+ * sequence owns are left alone.
+ * k_scale, v_scale: NULL for caches of dtype, else the caches are int8.
+ * Arithmetic: products, sums and softmax in fp32, one rounding to dtype; with TP_BF16
+ * the weights exp(x_j - max) are rounded to bf16 for the matrix cores' product with
+ * the values (not for their sum).  The order of the sums depends on the sizes and
+ * lengths alone.
+ * workspace: tp_kv_attention_workspace_bytes, 256-byte aligned; calls that may overlap
+ * must not share it.  It need not hold anything before the call.
+ * Errors: TP_ERR_NULL (one scale without the other), TP_ERR_SHAPE (sizes, leading
+ * dims, negative strides, D not in 1 .. 1024, Hkv 0 with Hq > 0, softmax_scale not
+ * positive and finite, window < 0, B or T above 2^31 - 1), TP_ERR_INDIVISIBLE
+ * (Hq % Hkv), TP_ERR_DTYPE, TP_ERR_WORKSPACE, TP_ERR_HIP.
+ */
+tp_status tp_kv_attention(const void *Q, int64_t ldq, const int32_t *cu, const int32_t *past,
+                          int64_t B, const int32_t *table, int64_t ldt, int64_t max_pages,
+                          const void *k_cache, const void *v_cache, int64_t n_pages,
+                          int64_t page_size, int64_t page_stride, int64_t slot_stride,
+                          int64_t head_stride, const float *k_scale, const float *v_scale,
+                          int64_t scale_page_stride, int64_t scale_slot_stride,
+                          int64_t scale_head_stride, float softmax_scale, int64_t window, void *O,
+                          int64_t ldo, float *lse, int64_t ldl, void *workspace, size_t ws_bytes,
+                          int64_t T, int64_t Hq, int64_t Hkv, int64_t D, int32_t dtype,
+                          int32_t *bad_flag, void *stream);
+
+/* Bytes of workspace tp_kv_attention needs, at most 256 MiB; 0 for invalid sizes. */
+size_t tp_kv_attention_workspace_bytes(int64_t T, int64_t B, int64_t Hq, int64_t Hkv, int64_t D);
+
+/* ---- between two blocks ---------------------------------------------------
+ *
+ * tp_residual_norm -- the step between a block's last row layer and the next block's
+ * first column layer, in one pass: the norm after the block, its gate, the sum with
+ * the residual stream, and the norm before the next block.
+ *   u = norm(Y) * post_weight                      (post_weight NULL: u = Y)
+ *   h = residual_scale * R + branch_scale * g * u  (R NULL: no first term; gate NULL: g = 1)
+ *   n = norm(h) * pre_weight                       (pre_weight NULL: n = h)
+ * with norm(x) = x * rsqrt(mean(x^2) + eps) over a row's F features.
+ * Y, R, H, N: [T, F] of dtype, rows ldy, ldr, ldh, ldn >= F apart.  Weights [F] of
+ * dtype.  gate of dtype: [F], the same for every token, with ldg = 0, or [T, F] with
+ * ldg >= F.  H or N may be NULL, not both.
+ * n_scale not NULL: N is int8 and token t's scale is n_scale[t]: the input of
+ * tp_linear_column_quant, with tp_quantize_rows' rule for scales and values.
+ * Arithmetic in fp32, h is not rounded before its norm; one rounding to dtype (or to
+ * int8).  A row whose sum of squares is past fp32 is normed to zeros.
+ * Outputs must not overlap inputs.
+ * Errors: TP_ERR_NULL, TP_ERR_SHAPE (sizes, leading dims, ldg neither 0 nor >= F, eps
+ * negative or NaN, F above 2^20), TP_ERR_DTYPE, TP_ERR_HIP.
+ */
+tp_status tp_residual_norm(const void *Y, int64_t ldy, const void *R, int64_t ldr,
+                           const void *gate, int64_t ldg, const void *post_weight,
+                           const void *pre_weight, float residual_scale, float branch_scale,
+                           float eps, void *H, int64_t ldh, void *N, int64_t ldn, float *n_scale,
+                           int64_t T, int64_t F, int32_t dtype, void *stream);
+
+/*
+ * tp_residual_norm_backward -- the gradients of tp_residual_norm (N of dtype).
+ *
+ * dH, dN: gradients of H and N, [T, F] of dtype; either may be NULL (zero), not both.
+ * dY, dR: [T, F] of dtype, or NULL where not wanted.
+ * dgate: for a gate of [T, F] of dtype with row stride lddg >= F; for one of [F] fp32 [F]
+ * (lddg ignored); or NULL.  dpost_weight, dpre_weight: fp32 [F] or NULL.  The sums over
+ * the tokens are added in an order that the sizes fix.
+ * Y, R, gate and weights as given to tp_residual_norm; h is computed again.
+ * workspace: tp_residual_norm_workspace_bytes(T, F), 256-byte aligned, needed where a
+ * gradient is a sum over the tokens; calls that may overlap must not share it.
+ * Errors: as tp_residual_norm; TP_ERR_NULL also for the gradient of a weight or gate
+ * that is not given, or of R NULL, and where no output is wanted; TP_ERR_WORKSPACE.
+ */
+tp_status tp_residual_norm_backward(const void *Y, int64_t ldy, const void *R, int64_t ldr,
+                                    const void *gate, int64_t ldg, const void *post_weight,
+                                    const void *pre_weight, float residual_scale,
+                                    float branch_scale, float eps, const void *dH, int64_t lddh,
+                                    const void *dN, int64_t lddn, void *dY, int64_t lddy,
+                                    void *dR, int64_t lddr, void *dgate, int64_t lddg,
+                                    float *dpost_weight, float *dpre_weight, void *workspace,
+                                    size_t ws_bytes, int64_t T, int64_t F, int32_t dtype,
+                                    void *stream);
+
+/* Bytes of workspace for the gradients that are sums over the tokens; 0 for invalid
+ * sizes. */
+size_t tp_residual_norm_workspace_bytes(int64_t T, int64_t F);
+
 /* Bytes of workspace tp_linear_row needs for (mode, M, N, P); 0 for
  * TP_ROW_PARTIAL, and for invalid arguments (including P*M*N*4 > 2^60,
  * which tp_linear_row rejects with TP_ERR_SHAPE). */

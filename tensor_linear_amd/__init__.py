@@ -56,7 +56,9 @@ EXPORTS = ("tp_shard_layout", "tp_linear_column", "tp_linear_row", "tp_shard_red
            "tp_row_workspace_bytes", "tp_workspace_zero", "tp_status_str", "tp_version",
            "tp_linear_row_noalloc", "tp_quantize_rows", "tp_linear_column_quant",
            "tp_linear_row_quant", "tp_qk_norm_rope", "tp_qk_norm_rope_backward",
-           "tp_qk_norm_rope_workspace_bytes", "tp_kv_append")
+           "tp_qk_norm_rope_workspace_bytes", "tp_kv_append", "tp_kv_append_quant", "tp_kv_read",
+           "tp_kv_attention", "tp_kv_attention_workspace_bytes", "tp_residual_norm",
+           "tp_residual_norm_backward", "tp_residual_norm_workspace_bytes")
 TP_NOALLOC_SCRATCH_BYTES = 32 << 20
 
 
@@ -125,6 +127,28 @@ def _declare(lib):
     lib.tp_kv_append.argtypes = ([_ptr, _i64, _i32] + rot + [_ptr, _ptr, _i64, _ptr, _i64, _i64,
                                  _ptr, _ptr, _i64, _i64, _i64, _i64, _i64, _ptr, _i64] + heads)
     lib.tp_kv_append.restype = _i32
+    lib.tp_kv_append_quant.argtypes = ([_ptr, _i64, _i32] + rot + [_ptr, _ptr, _i64, _ptr, _i64,
+                                       _i64, _ptr, _ptr] + [_i64] * 5 + [_ptr, _ptr] + [_i64] * 3 +
+                                       [_ptr, _i64] + heads)
+    lib.tp_kv_append_quant.restype = _i32
+    # the sequences and their table, the caches, their scales
+    pages = ([_ptr, _ptr, _i64, _ptr, _i64, _i64, _ptr, _ptr] + [_i64] * 5 + [_ptr, _ptr] +
+             [_i64] * 3)
+    lib.tp_kv_read.argtypes = pages + [_ptr, _i64, _ptr, _i64, _i64, _i64, _i64, _i32, _ptr, _ptr]
+    lib.tp_kv_read.restype = _i32
+    lib.tp_kv_attention.argtypes = ([_ptr, _i64] + pages + [_f32, _i64, _ptr, _i64, _ptr, _i64,
+                                    _ptr, _sz, _i64, _i64, _i64, _i64, _i32, _ptr, _ptr])
+    lib.tp_kv_attention.restype = _i32
+    lib.tp_kv_attention_workspace_bytes.argtypes = [_i64] * 5
+    lib.tp_kv_attention_workspace_bytes.restype = _sz
+    norm = [_ptr, _i64, _ptr, _i64, _ptr, _i64, _ptr, _ptr, _f32, _f32, _f32]
+    lib.tp_residual_norm.argtypes = norm + [_ptr, _i64, _ptr, _i64, _ptr, _i64, _i64, _i32, _ptr]
+    lib.tp_residual_norm.restype = _i32
+    lib.tp_residual_norm_backward.argtypes = (norm + [_ptr, _i64] * 5 + [_ptr, _ptr, _ptr, _sz,
+                                              _i64, _i64, _i32, _ptr])
+    lib.tp_residual_norm_backward.restype = _i32
+    lib.tp_residual_norm_workspace_bytes.argtypes = [_i64, _i64]
+    lib.tp_residual_norm_workspace_bytes.restype = _sz
     lib.tp_row_workspace_bytes.argtypes = [_i32, _i64, _i64, _i32]
     lib.tp_row_workspace_bytes.restype = _sz
     lib.tp_workspace_zero.argtypes = [_ptr, _sz, _ptr]
@@ -915,6 +939,69 @@ def tp_qk_norm_rope_backward(X, pos, cos, sin, dQ, dK, dX, P: int, Hq: int, Hkv:
         _flag(bad), on))
 
 
+def _sequences(past, cu, table):
+    """(B, pointer, row stride, width) of B sequences' lengths and page table."""
+    i32 = _torch().int32
+    if past.dtype != i32 or cu.dtype != i32 or past.dim() != 1 or cu.dim() != 1 or not (
+            past.is_contiguous() and cu.is_contiguous()):
+        raise ValueError("past [B] and cu [B + 1] must be int32 with unit stride")
+    B = past.shape[0]
+    if cu.shape[0] != B + 1:
+        _expect_shape(cu, (B + 1,), "cu")
+    tp, rows, max_pages, ldt = _mat(table, "table")
+    if table.dtype != i32 or rows != B:
+        raise ValueError(f"table must be int32 [{B}, max_pages]")
+    return B, tp, ldt, max_pages
+
+
+def _caches(k_cache, v_cache, Hkv, D):
+    """(shape, strides) of a pair of caches [n_pages, page_size, Hkv, D]."""
+    shape, strides = k_cache.shape, k_cache.stride()
+    if len(shape) != 4 or shape[2] != Hkv or shape[3] != D:
+        raise ValueError(f"k_cache must be [n_pages, page_size, {Hkv}, {D}]")
+    _expect_shape(v_cache, shape, "v_cache")
+    if D > 1 and strides[3] != 1:
+        raise ValueError("k_cache and v_cache must have contiguous features")
+    if strides != v_cache.stride():
+        raise ValueError("k_cache and v_cache must have the same strides")
+    return shape, strides
+
+
+def _cache_scales(k_cache, v_cache, k_scale, v_scale, shape):
+    """(pointers, strides) of an 8-bit cache's scales [n_pages, page_size, Hkv]."""
+    torch = _torch()
+    if k_cache.dtype != torch.int8 or v_cache.dtype != torch.int8:
+        raise TypeError("k_cache and v_cache must be int8 where they have scales")
+    if k_scale is None or v_scale is None:
+        raise ValueError("give both k_scale and v_scale, or neither")
+    if k_scale.dtype != torch.float32 or v_scale.dtype != torch.float32:
+        raise TypeError("k_scale and v_scale must be float32")
+    _expect_shape(k_scale, shape[:3], "k_scale")
+    _expect_shape(v_scale, shape[:3], "v_scale")
+    if k_scale.stride() != v_scale.stride():
+        raise ValueError("k_scale and v_scale must have the same strides")
+    return (k_scale.data_ptr(), v_scale.data_ptr(), *k_scale.stride())
+
+
+def _pages(past, cu, table, k_cache, v_cache, k_scale, v_scale, dt):
+    """The arguments of a call that reads a paged cache, in the order of the C
+    calls, the cache's heads and their size."""
+    B, tp, ldt, max_pages = _sequences(past, cu, table)
+    if k_cache.dim() != 4:
+        raise ValueError("k_cache must be [n_pages, page_size, Hkv, D]")
+    Hkv, D = k_cache.shape[2], k_cache.shape[3]
+    shape, strides = _caches(k_cache, v_cache, Hkv, D)
+    if k_scale is None and v_scale is None:
+        if _dtype_code(k_cache) != dt or _dtype_code(v_cache) != dt:
+            raise TypeError("k_cache and v_cache must have the call's dtype, or be int8 with scales")
+        scales = (None, None, 0, 0, 0)
+    else:
+        scales = _cache_scales(k_cache, v_cache, k_scale, v_scale, shape)
+    return (cu.data_ptr(), past.data_ptr(), B, tp, ldt, max_pages, k_cache.data_ptr(),
+            v_cache.data_ptr(), shape[0], shape[1], strides[0], strides[1], strides[2],
+            *scales), Hkv, D
+
+
 def tp_kv_append(X, cos, sin, past, cu, table, k_cache, v_cache, P: int, Hq: int, Hkv: int,
                  Q=None, q_weight=None, k_weight=None, eps: float = 1e-6,
                  style: int = TP_ROPE_HALVES, x_mode: int = TP_Y_CONCAT, bad=None,
@@ -928,24 +1015,8 @@ def tp_kv_append(X, cos, sin, past, cu, table, k_cache, v_cache, P: int, Hq: int
     xp, ldx, T, D = _qkv(X, P, Hq, Hkv, x_mode, "X")
     dt = _dtype_code(X)
     rot = _rotation(cos, sin, q_weight, k_weight, D, dt, eps, style)
-    i32 = torch.int32
-    if past.dtype != i32 or cu.dtype != i32 or past.dim() != 1 or cu.dim() != 1 or not (
-            past.is_contiguous() and cu.is_contiguous()):
-        raise ValueError("past [B] and cu [B + 1] must be int32 with unit stride")
-    B = past.shape[0]
-    if cu.shape[0] != B + 1:
-        _expect_shape(cu, (B + 1,), "cu")
-    tp, rows, max_pages, ldt = _mat(table, "table")
-    if table.dtype != i32 or rows != B:
-        raise ValueError(f"table must be int32 [{B}, max_pages]")
-    shape, strides = k_cache.shape, k_cache.stride()
-    if len(shape) != 4 or shape[2] != Hkv or shape[3] != D:
-        raise ValueError(f"k_cache must be [n_pages, page_size, {Hkv}, {D}]")
-    _expect_shape(v_cache, shape, "v_cache")
-    if D > 1 and strides[3] != 1:
-        raise ValueError("k_cache and v_cache must have contiguous features")
-    if strides != v_cache.stride():
-        raise ValueError("k_cache and v_cache must have the same strides")
+    B, tp, ldt, max_pages = _sequences(past, cu, table)
+    shape, strides = _caches(k_cache, v_cache, Hkv, D)
     if _dtype_code(k_cache) != dt or _dtype_code(v_cache) != dt:
         raise TypeError("k_cache and v_cache must have the dtype of the QKV matrix")
     qp, ldq = _rows(Q, T, Hq * D, dt, "Q")
@@ -954,3 +1025,179 @@ def tp_kv_append(X, cos, sin, past, cu, table, k_cache, v_cache, P: int, Hq: int
         xp, ldx, x_mode, *rot, cu.data_ptr(), past.data_ptr(), B, tp, ldt, max_pages,
         k_cache.data_ptr(), v_cache.data_ptr(), shape[0], shape[1], strides[0], strides[1],
         strides[2], qp, ldq, T, Hq, Hkv, D, P, dt, _flag(bad), on))
+
+
+def tp_kv_append_quant(X, cos, sin, past, cu, table, k_cache, v_cache, k_scale, v_scale, P: int,
+                       Hq: int, Hkv: int, Q=None, q_weight=None, k_weight=None, eps: float = 1e-6,
+                       style: int = TP_ROPE_HALVES, x_mode: int = TP_Y_CONCAT, bad=None,
+                       stream=None) -> None:
+    """tp_kv_append into a cache in 8 bits: k_cache, v_cache int8 [n_pages,
+    page_size, Hkv, D], k_scale, v_scale float32 [n_pages, page_size, Hkv] (a
+    scale for each token and head), views of one set of strides each."""
+    xp, ldx, T, D = _qkv(X, P, Hq, Hkv, x_mode, "X")
+    dt = _dtype_code(X)
+    rot = _rotation(cos, sin, q_weight, k_weight, D, dt, eps, style)
+    B, tp, ldt, max_pages = _sequences(past, cu, table)
+    shape, strides = _caches(k_cache, v_cache, Hkv, D)
+    scales = _cache_scales(k_cache, v_cache, k_scale, v_scale, shape)
+    qp, ldq = _rows(Q, T, Hq * D, dt, "Q")
+    on = _here(stream, X, cos, sin, past, cu, table, k_cache, v_cache, k_scale, v_scale, Q,
+               q_weight, k_weight, bad)
+    check(_get_lib().tp_kv_append_quant(
+        xp, ldx, x_mode, *rot, cu.data_ptr(), past.data_ptr(), B, tp, ldt, max_pages,
+        k_cache.data_ptr(), v_cache.data_ptr(), shape[0], shape[1], strides[0], strides[1],
+        strides[2], *scales, qp, ldq, T, Hq, Hkv, D, P, dt, _flag(bad), on))
+
+
+def tp_kv_read(past, cu, table, k_cache, v_cache, K, V, k_scale=None, v_scale=None, bad=None,
+               stream=None) -> None:
+    """Rows of a paged cache as matrices: K, V [T, Hkv*D], row t of sequence s
+    the cache's row at position past[s] + t - cu[s] (past, cu, table as in
+    tp_kv_append).  Caches of the type of K and V, or int8 with k_scale and
+    v_scale as in tp_kv_append_quant.  K or V may be None."""
+    out = K if K is not None else V
+    if out is None:
+        raise ValueError("give K, V or both")
+    dt = _dtype_code(out)
+    pages, Hkv, D = _pages(past, cu, table, k_cache, v_cache, k_scale, v_scale, dt)
+    T = out.shape[0]
+    kp, ldk = _rows(K, T, Hkv * D, dt, "K")
+    vp, ldv = _rows(V, T, Hkv * D, dt, "V")
+    on = _here(stream, out, past, cu, table, k_cache, v_cache, k_scale, v_scale, K, V, bad)
+    check(_get_lib().tp_kv_read(*pages, kp, ldk, vp, ldv, T, Hkv, D, dt, _flag(bad), on))
+
+
+def tp_kv_attention_workspace_bytes(T: int, B: int, Hq: int, Hkv: int, D: int) -> int:
+    return int(_get_lib().tp_kv_attention_workspace_bytes(T, B, Hq, Hkv, D))
+
+
+def tp_kv_attention(Q, past, cu, table, k_cache, v_cache, O, workspace=None, k_scale=None,
+                    v_scale=None, scale: float = None, window: int = 0, lse=None, bad=None,
+                    stream=None) -> None:
+    """Attention of new tokens over a paged cache that already holds their keys
+    and values.  Q, O [T, Hq*D]; past int32 [B], cu int32 [B + 1], table int32
+    [B, max_pages] and the caches [n_pages, page_size, Hkv, D] as in
+    tp_kv_append (or int8 with k_scale and v_scale as in tp_kv_append_quant).
+    scale: of the products (None: D ** -0.5); window: how many positions back a
+    token sees, itself included (0: all); lse: float32 [T, Hq], the logarithms of
+    the softmax's sums.  workspace: tp_kv_attention_workspace_bytes(T, B, Hq,
+    Hkv, D)."""
+    dt = _dtype_code(Q)
+    pages, Hkv, D = _pages(past, cu, table, k_cache, v_cache, k_scale, v_scale, dt)
+    qp, T, cols, ldq = _mat(Q, "Q")
+    if D == 0 or cols % D:
+        raise ValueError(f"Q has {cols} columns: no whole heads of {D}")
+    Hq = cols // D
+    op, ldo = _rows(O, T, cols, dt, "O")
+    if O is None:
+        raise ValueError("O is needed")
+    lp, ldl = None, 0
+    if lse is not None:
+        lp, _, _, ldl = _mat(lse, "lse")
+        _expect_shape(lse, (T, Hq), "lse")
+        if lse.dtype != _torch().float32:
+            raise TypeError(f"lse must be float32, got {lse.dtype}")
+    wkp, wkb = _workspace(workspace)
+    on = _here(stream, Q, past, cu, table, k_cache, v_cache, O, k_scale, v_scale, lse, workspace,
+               bad)
+    check(_get_lib().tp_kv_attention(qp, ldq, *pages, D ** -0.5 if scale is None else scale,
+                                     window, op, ldo, lp, ldl, wkp, wkb, T, Hq, Hkv, D, dt,
+                                     _flag(bad), on))
+
+
+# ---- between two blocks ----------------------------------------------------
+
+def _feature_row(t, F, dt, name):
+    """Pointer of a contiguous [F] tensor of dtype code dt, or of none."""
+    if t is None:
+        return None
+    if t.shape != (F,):
+        _expect_shape(t, (F,), name)
+    if F > 1 and t.stride(0) != 1:
+        raise ValueError(f"{name} must be a contiguous 1-D tensor")
+    if _dtype_code(t) != dt:
+        raise TypeError(f"{name} has another dtype than the call")
+    return t.data_ptr()
+
+
+def _norm_input(Y, residual, gate, post_weight, pre_weight, residual_scale, branch_scale, eps):
+    """The inputs of tp_residual_norm in the order of the C calls, T, F and the
+    dtype code."""
+    dt = _dtype_code(Y)
+    yp, T, F, ldy = _mat(Y, "Y")
+    rp, ldr = _rows_of(residual, T, F, dt, "residual")
+    if gate is not None and gate.dim() == 2:
+        gp, ldg = _rows_of(gate, T, F, dt, "gate")
+    else:
+        gp, ldg = _feature_row(gate, F, dt, "gate"), 0
+    return (yp, ldy, rp, ldr, gp, ldg, _feature_row(post_weight, F, dt, "post_weight"),
+            _feature_row(pre_weight, F, dt, "pre_weight"), residual_scale, branch_scale, eps), T, F, dt
+
+
+def _rows_of(t, T, F, dt, name):
+    if t is None:
+        return None, 0
+    p, _, _, ld = _mat(t, name)
+    if t.shape != (T, F):
+        _expect_shape(t, (T, F), name)
+    if _dtype_code(t) != dt:
+        raise TypeError(f"{name} must have the dtype of Y")
+    return p, ld
+
+
+def tp_residual_norm(Y, H, N, residual=None, gate=None, post_weight=None, pre_weight=None,
+                     residual_scale: float = 1.0, branch_scale: float = 1.0, eps: float = 1e-6,
+                     scale=None, stream=None) -> None:
+    """The step between two blocks in one pass: u = norm(Y) * post_weight, h =
+    residual_scale * residual + branch_scale * gate * u to H, norm(h) *
+    pre_weight to N (all [T, F] of one dtype; gate [F] or [T, F], weights [F];
+    a missing weight means no norm there).  With scale (float32 [T]) N is int8:
+    the input of tp_linear_column_quant.  H or N may be None."""
+    args, T, F, dt = _norm_input(Y, residual, gate, post_weight, pre_weight, residual_scale,
+                                 branch_scale, eps)
+    hp, ldh = _rows_of(H, T, F, dt, "H")
+    sp = None
+    if scale is None:
+        np_, ldn = _rows_of(N, T, F, dt, "N")
+    else:
+        if N is None:
+            raise ValueError("scale is the scale of N: give N too")
+        np_, _, _, ldn = _int8_mat(N, "N")
+        _expect_shape(N, (T, F), "N")
+        _expect_shape(scale, (T,), "scale")
+        if scale.dtype != _torch().float32 or (T > 1 and scale.stride(0) != 1):
+            raise ValueError("scale must be a contiguous float32 [T] tensor")
+        sp = scale.data_ptr()
+    on = _here(stream, Y, residual, gate, post_weight, pre_weight, H, N, scale)
+    check(_get_lib().tp_residual_norm(*args, hp, ldh, np_, ldn, sp, T, F, dt, on))
+
+
+def tp_residual_norm_workspace_bytes(T: int, F: int) -> int:
+    return int(_get_lib().tp_residual_norm_workspace_bytes(T, F))
+
+
+def tp_residual_norm_backward(Y, dH, dN, dY=None, dR=None, residual=None, gate=None,
+                              post_weight=None, pre_weight=None, dgate=None, dpost_weight=None,
+                              dpre_weight=None, workspace=None, residual_scale: float = 1.0,
+                              branch_scale: float = 1.0, eps: float = 1e-6, stream=None) -> None:
+    """Gradients of tp_residual_norm: dY and dR ([T, F] of Y's dtype, None where
+    not wanted) from dH and dN (one of them may be None), dgate (float32 [F] for
+    a gate [F], else [T, F] of Y's dtype), dpost_weight and dpre_weight (float32
+    [F]).  Gradients that are sums over the tokens need a workspace of
+    tp_residual_norm_workspace_bytes(T, F)."""
+    args, T, F, dt = _norm_input(Y, residual, gate, post_weight, pre_weight, residual_scale,
+                                 branch_scale, eps)
+    rows = []
+    for t, name in ((dH, "dH"), (dN, "dN"), (dY, "dY"), (dR, "dR")):
+        rows += _rows_of(t, T, F, dt, name)
+    if dgate is not None and gate is not None and gate.dim() == 2:
+        gp, ldg = _rows_of(dgate, T, F, dt, "dgate")
+    else:
+        gp, ldg = _feature_row(dgate, F, TP_F32, "dgate"), 0
+    dpost = _feature_row(dpost_weight, F, TP_F32, "dpost_weight")
+    dpre = _feature_row(dpre_weight, F, TP_F32, "dpre_weight")
+    wkp, wkb = _workspace(workspace)
+    on = _here(stream, Y, residual, gate, post_weight, pre_weight, dH, dN, dY, dR, dgate,
+               dpost_weight, dpre_weight, workspace)
+    check(_get_lib().tp_residual_norm_backward(
+        *args, *rows, gp, ldg, dpost, dpre, wkp, wkb, T, F, dt, on))

@@ -27,7 +27,9 @@ SOURCES = ["tplinear.cpp", "device.cpp", "gemm_tile.hip", "gemm_skinny.hip", "ge
            "noalloc.hip", "tplinear_quant.cpp", "quantize.hip", "quant_generic.hip",
            "quant_tile.hip", "quant_narrow.hip", "quant_rowfold.hip",
            "quant_skinny.hip",
-           "quant_fold.hip", "tplinear_heads.cpp", "heads.hip"]
+           "quant_fold.hip", "tplinear_heads.cpp", "heads.hip",
+           "tplinear_cache.cpp", "heads_quant.hip", "cache_read.hip", "attn_any.hip",
+           "tplinear_norm.cpp", "norm.hip"]
 
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 FLAGS = ["--offload-arch=gfx950", "-O3", "-std=c++17", "-fPIC", "-Wall",

@@ -34,10 +34,13 @@ struct HeadArgs {
     void *dX; int64_t lddx, dx_shard;
     float *dwq, *dwk;
     float *partials;
+    // append to a cache in 8 bits: scales of (page, slot, head) and their strides
+    float *ks, *vs; int64_t ss_page, ss_slot, ss_head;
 };
 
 hipError_t launch_qk_norm_rope(const HeadArgs &a, int elem_bytes, hipStream_t s);
 hipError_t launch_kv_append(const HeadArgs &a, int elem_bytes, hipStream_t s);
+hipError_t launch_kv_append_quant(const HeadArgs &a, int elem_bytes, hipStream_t s);
 hipError_t launch_qk_norm_rope_backward(const HeadArgs &a, int elem_bytes, hipStream_t s);
 
 // Most workgroups that leave weight-gradient sums of either kind (D floats each)
