@@ -28,7 +28,8 @@ SOURCES = ["tplinear.cpp", "device.cpp", "gemm_tile.hip", "gemm_skinny.hip", "ge
            "quant_tile.hip", "quant_narrow.hip", "quant_rowfold.hip",
            "quant_skinny.hip",
            "quant_fold.hip", "tplinear_heads.cpp", "heads.hip",
-           "tplinear_cache.cpp", "heads_quant.hip", "cache_read.hip", "attn_any.hip",
+           "tplinear_cache.cpp", "heads_quant.hip", "cache_read.hip", "attn.cpp", "attn_any.hip",
+           "attn_bf16.hip", "attn_f32.hip", "attn_bf16_int8.hip", "attn_f32_int8.hip",
            "tplinear_norm.cpp", "norm.hip"]
 
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")

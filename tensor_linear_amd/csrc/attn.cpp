@@ -1,0 +1,55 @@
+// Which kernels an attention call takes, and its workspace (host code only).
+#include "attn.h"
+
+#include <cstdint>
+
+#include "attn_plan.h"
+
+namespace tpl {
+
+namespace {
+
+constexpr int64_t MAX_TILE_D = 256;     // largest head of the matrix-core form
+
+// What the matrix-core form takes: heads of whole 16-byte chunks (of whole 8 values in
+// 8 bits), rows of a call that 32 bits count.
+bool tile_ok(int64_t T, int64_t G, int64_t D) { return D <= MAX_TILE_D && D % 8 == 0 && T * G <= INT32_MAX; }
+
+// A cache whose rows lie at multiples of 16 bytes goes to LDS without a stop.
+bool dma_ok(const AttnArgs &a, int es) {
+    const int64_t n = 16 / es;
+    return (uintptr_t)a.c.kc % 16 == 0 && (uintptr_t)a.c.vc % 16 == 0 && a.c.s_page % n == 0 && a.c.s_slot % n == 0 && a.c.s_head % n == 0;
+}
+
+}  // namespace
+
+AttnPlan attention_plan(int64_t T, int64_t B, int64_t Hkv, int32_t G) {
+    AttnPlan p{};
+    // 32 rows a workgroup where the sequences have no more on average
+    p.few = T * G <= 32 * B;
+    const int64_t rows = p.few ? 32 : 128;
+    p.row_tiles = T * G / rows + B;
+    // equal runs while adding up the sequences' tiles in every workgroup is cheap and the
+    // items are too few to even out by themselves
+    p.groups = p.few ? 256 : 512;
+    p.stream = p.few ? p.row_tiles <= 4096 : p.row_tiles <= 512 && p.row_tiles * Hkv <= 2048;
+    return p;
+}
+
+size_t attention_workspace(int64_t T, int64_t B, int64_t Hq, int64_t Hkv, int64_t D) {
+    if (T == 0 || B == 0 || !tile_ok(T, Hq / Hkv, D)) return 0;
+    const AttnPlan p = attention_plan(T, B, Hkv, (int32_t)(Hq / Hkv));
+    if (!p.stream) return 0;
+    const int64_t d = D <= 64 ? 64 : D <= 96 ? 96 : D <= 128 ? 128 : 256, rows = p.few ? 32 : 128;
+    return (size_t)(plan_desc_bytes(p.groups) + plan_stats_bytes(p.groups) + 2 * p.groups * rows * d * 4);
+}
+
+hipError_t launch_kv_attention(const AttnArgs &a, int es, hipStream_t s) {
+    if (!tile_ok(a.c.T, a.G, a.c.D)) return launch_attention_any(a, es, s);
+    const AttnPlan p = attention_plan(a.c.T, a.c.B, a.c.Hkv, a.G);
+    if (!p.stream && p.row_tiles * a.c.Hkv > (1 << 23)) return launch_attention_any(a, es, s);   // more than one launch holds
+    if (a.c.ks) return es == 2 ? launch_attention_bf16_int8(a, p, s) : launch_attention_f32_int8(a, p, s);
+    return es == 2 ? launch_attention_bf16(a, p, dma_ok(a, es), s) : launch_attention_f32(a, p, dma_ok(a, es), s);
+}
+
+}  // namespace tpl

@@ -95,11 +95,9 @@ hipError_t launch(const AttnArgs &a, hipStream_t s) {
 
 }  // namespace
 
-hipError_t launch_kv_attention(const AttnArgs &a, int es, hipStream_t s) {
+hipError_t launch_attention_any(const AttnArgs &a, int es, hipStream_t s) {
     if (a.c.ks) return es == 2 ? launch<2, 1>(a, s) : launch<4, 1>(a, s);
     return es == 2 ? launch<2, 2>(a, s) : launch<4, 4>(a, s);
 }
-
-size_t attention_workspace(int64_t, int64_t, int64_t, int64_t, int64_t) { return 0; }
 
 }  // namespace tpl

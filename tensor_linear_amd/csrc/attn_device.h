@@ -5,6 +5,7 @@
 #include <stdint.h>
 
 #include "attn.h"
+#include "attn_plan.h"
 
 namespace tpl {
 namespace {
@@ -56,6 +57,77 @@ template <int ES>
 __device__ __forceinline__ void store(void *p, int64_t i, float v) {
     if (ES == 2) ((__bf16 *)p)[i] = (__bf16)v;
     else ((float *)p)[i] = v;
+}
+
+// ---- the plan on the device
+
+__device__ __forceinline__ PlanDesc *plan_desc(void *ws) { return (PlanDesc *)ws; }
+__device__ __forceinline__ float *plan_stats(void *ws, int W) { return (float *)((char *)ws + plan_desc_bytes(W)); }
+typedef float plan_f32x4 __attribute__((ext_vector_type(4)));
+__device__ __forceinline__ plan_f32x4 *plan_sums(void *ws, int W) {
+    return (plan_f32x4 *)((char *)ws + plan_desc_bytes(W) + plan_stats_bytes(W));
+}
+
+// A sequence's first row and number of rows among the call's T, and the position of the
+// first of them.  Rows outside the call do not count, whatever cu says.
+struct Sequence { int64_t first, n, past; };
+__device__ __forceinline__ int64_t plan_clamp(int64_t v, int64_t T) { return v < 0 ? 0 : v > T ? T : v; }
+__device__ __forceinline__ Sequence plan_sequence(const CacheArgs &c, int64_t s) {
+    const int64_t from = c.cu[s], to = c.cu[s + 1];
+    Sequence q;
+    q.first = plan_clamp(from, c.T);
+    const int64_t end = plan_clamp(to, c.T);
+    q.n = end > q.first ? end - q.first : 0;
+    q.past = (int64_t)c.past[s] + (q.first - from);
+    return q;
+}
+
+// Index of a sequence's first row tile where sequence s begins at cu[s] G / ROWS + s:
+// floor(x / ROWS) + 1 - floor(y / ROWS) tiles are enough for the rows y .. x - 1.
+__device__ __forceinline__ int64_t plan_index(const CacheArgs &c, int64_t s, int G, int ROWS) {
+    return plan_clamp(c.cu[s], c.T) * G / ROWS + s;
+}
+
+// Row tile r of a sequence: the positions of its first and last row, the positions that
+// its rows see (those of the table), and the tiles of BK that hold them; at least one, so
+// that rows that see nothing are written.
+struct Span { int64_t pos0, pos1, begin, end, first; int tiles; bool outside; };
+__device__ __forceinline__ Span plan_span(const Sequence &q, int r, int G, int ROWS, int BK, int64_t window, int64_t last_pos) {
+    Span s;
+    const uint32_t row = (uint32_t)r * ROWS, rows = (uint32_t)(q.n * G - row < ROWS ? q.n * G - row : ROWS);
+    s.pos0 = q.past + row / G;
+    s.pos1 = q.past + (row + rows - 1) / G;
+    s.begin = s.pos0 - window + 1;
+    if (s.begin < 0) s.begin = 0;
+    s.end = s.pos1 + 1 < last_pos ? s.pos1 + 1 : last_pos;
+    if (s.end < 0) s.end = 0;
+    s.outside = s.pos0 < 0 || s.pos1 >= last_pos;
+    s.first = s.begin / BK;
+    const int64_t n = (s.end + BK - 1) / BK - s.first;
+    s.tiles = n > 0 ? (int)n : 1;
+    return s;
+}
+
+// Four features of a row, d .. d + 3 of D, divided by the row's sum.
+template <int ES>
+__device__ __forceinline__ void write_out(void *O, int64_t at, int d, int D, plan_f32x4 v, bool none, float inv) {
+    float y[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) y[e] = none ? 0.0f : v[e] * inv;
+    if (d + 4 <= D) {
+        if constexpr (ES == 2) {
+            typedef __bf16 bf16x4_ __attribute__((ext_vector_type(4)));
+            typedef uint32_t u32x2_at __attribute__((ext_vector_type(2), aligned(1)));
+            bf16x4_ h;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) h[e] = (__bf16)y[e];
+            typedef uint32_t u32x2_ __attribute__((ext_vector_type(2)));
+            *(u32x2_at *)((char *)O + (at + d) * 2) = __builtin_bit_cast(u32x2_, h);
+        } else {
+            typedef float f32x4_at __attribute__((ext_vector_type(4), aligned(4)));
+            *(f32x4_at *)((float *)O + at + d) = f32x4_at{y[0], y[1], y[2], y[3]};
+        }
+    }
 }
 
 }  // namespace

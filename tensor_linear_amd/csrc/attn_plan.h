@@ -1,0 +1,35 @@
+// How the attention's work is cut: what host and device share of it.
+#pragma once
+
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include "attn.h"
+
+namespace tpl {
+
+// stream: the tiles of all items in `groups` equal runs; else a workgroup for each of
+// the row_tiles * Hkv items.  few: 32 rows a workgroup, else 128.
+struct AttnPlan { int32_t stream, few, groups; int64_t row_tiles; };
+
+// The plan of a call of these sizes (the lengths are on the device: T, B and the heads
+// are all that the host knows).
+AttnPlan attention_plan(int64_t T, int64_t B, int64_t Hkv, int32_t G);
+
+hipError_t launch_attention_any(const AttnArgs &a, int elem_bytes, hipStream_t s);
+hipError_t launch_attention_bf16(const AttnArgs &a, const AttnPlan &p, bool dma, hipStream_t s);
+hipError_t launch_attention_f32(const AttnArgs &a, const AttnPlan &p, bool dma, hipStream_t s);
+hipError_t launch_attention_bf16_int8(const AttnArgs &a, const AttnPlan &p, hipStream_t s);
+hipError_t launch_attention_f32_int8(const AttnArgs &a, const AttnPlan &p, hipStream_t s);
+
+// The item that a run begins and does not finish: sequence s, row tile r, key head h, in
+// `pieces` runs (0: there is none).
+struct PlanDesc { int32_t pieces, r, h, pad; int64_t s; };
+
+// The workspace: descriptors of the runs, then [slot][row] of maximum and sum, then the
+// weighted sums [slot][32 rows][32 features][4][lane] of 4 features each; two slots a run.
+constexpr int64_t PLAN_ROWS = 128;      // largest of an item
+__host__ __device__ inline int64_t plan_desc_bytes(int64_t W) { return W * (int64_t)sizeof(PlanDesc); }
+__host__ __device__ inline int64_t plan_stats_bytes(int64_t W) { return 2 * W * PLAN_ROWS * 8; }
+
+}  // namespace tpl
