@@ -327,12 +327,12 @@ void norm_rows(NormArgs a, int64_t t0) {
 // features' sums of a lane stay in registers; at the end the groups' are added in LDS in
 // order and leave as the workgroup's part of the workspace, which a second kernel adds in
 // an order of its own: the result does not depend on scheduling.
-template <int ES, int W, int G, int C, bool AHEAD, bool TAIL>
+template <int ES, int W, int G, int C, bool AHEAD, bool LONG, bool TAIL>
 __global__ __launch_bounds__(W * G * 64)
 void norm_backward_rows(NormArgs a) {
     constexpr int STEP = W * 512;
     __shared__ float red[2][16][2];
-    __shared__ float sums[G > 1 ? W * 512 * C : 1];
+    __shared__ __attribute__((aligned(16))) float sums[G > 1 || LONG ? W * 512 * C * (LONG ? 2 : 1) : 1];
     int turn = 0;
     const int F = (int)a.F, group = threadIdx.x / (W * 64), lane = threadIdx.x % (W * 64);
     const bool sum_gate = a.dgate && a.ldg == 0;
@@ -351,20 +351,54 @@ void norm_backward_rows(NormArgs a) {
         return v;
     };
     // the weights, and the gate with the branch's factor
-    float wp[C][8], wn[C][8], wg[C][8], dg[C][8] = {}, dp[C][8] = {}, dw[C][8] = {};
+    // (LONG: loaded again for each row, and the weights' sums are in LDS)
+    constexpr int CK = LONG ? 1 : C;
+    float wp_[CK][8], wn_[CK][8], wg_[CK][8], dg[C][8] = {}, dp[CK][8] = {}, dw[CK][8] = {};
+    auto weight = [&](const void *w, int c, float *v) {
+        Raw8<ES> p = {};
+        if (w) p = row8<ES, TAIL>(w, 0, c * STEP + lane * 8, F);
+        widen8<ES>(p, v);
+    };
+    auto gates = [&](const Raw8<ES> *g, int c, float *v) {
+        if (a.gate && a.ldg) widen8<ES>(g[c], v);
+        else weight(a.gate, c, v);
 #pragma unroll
-    for (int c = 0; c < C; ++c) {
-        const int i = c * STEP + lane * 8;
-        Raw8<ES> p = {}, n = {}, g = {};
-        if (a.post) p = row8<ES, TAIL>(a.post, 0, i, F);
-        if (a.pre) n = row8<ES, TAIL>(a.pre, 0, i, F);
-        if (a.gate && !a.ldg) g = row8<ES, TAIL>(a.gate, 0, i, F);
-        widen8<ES>(p, wp[c]);
-        widen8<ES>(n, wn[c]);
-        widen8<ES>(g, wg[c]);
+        for (int e = 0; e < 8; ++e) v[e] = a.gate ? a.beta * v[e] : a.beta;
+    };
+    if constexpr (LONG) {
+        for (int i = threadIdx.x; i < 2 * W * 512 * C; i += W * G * 64) sums[i] = 0.0f;      // each lane its own, below
+        __syncthreads();
+    } else {
 #pragma unroll
-        for (int e = 0; e < 8; ++e) wg[c][e] = a.gate ? a.beta * wg[c][e] : a.beta;
+        for (int c = 0; c < C; ++c) {
+            weight(a.post, c, wp_[c]);
+            weight(a.pre, c, wn_[c]);
+            if (!(a.gate && a.ldg)) gates(nullptr, c, wg_[c]);
+        }
     }
+    auto get = [&](const float (&kept)[CK][8], const void *w, int c, float *v) __attribute__((always_inline)) {
+        if constexpr (LONG) weight(w, c, v);
+        else
+#pragma unroll
+            for (int e = 0; e < 8; ++e) v[e] = kept[c][e];
+    };
+    // adds to the sums of a weight's gradient
+    auto add = [&](float (&kept)[CK][8], int kind, int c, const float *v) __attribute__((always_inline)) {
+        if constexpr (LONG) {
+            typedef float f32x4 __attribute__((ext_vector_type(4)));
+#pragma unroll
+            for (int q = 0; q < 2; ++q) {
+                f32x4 *p = (f32x4 *)sums + (kind * C * 2 + c * 2 + q) * W * 64 + lane;
+                f32x4 x = *p;
+#pragma unroll
+                for (int e = 0; e < 4; ++e) x[e] += v[4 * q + e];
+                *p = x;
+            }
+        } else {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) kept[c][e] += v[e];
+        }
+    };
     const float inv_f = 1.0f / (float)F;
     const int64_t step = (int64_t)gridDim.x * G;
     int64_t t = (int64_t)blockIdx.x * G + group;
@@ -389,24 +423,29 @@ void norm_backward_rows(NormArgs a) {
             row_sum<W, 1>(s, red, turn);
             r1 = rsqrtf(s[0] * inv_f + a.eps);
         }
-        if (a.gate && a.ldg)
+        if constexpr (!LONG)
+            if (a.gate && a.ldg)
 #pragma unroll
-            for (int c = 0; c < C; ++c) {
-                widen8<ES>(cur.g[c], wg[c]);
+                for (int c = 0; c < C; ++c) gates(cur.g, c, wg_[c]);
+        auto gate_of = [&](int c, float *v) __attribute__((always_inline)) {
+            if constexpr (LONG) gates(cur.g, c, v);
+            else
 #pragma unroll
-                for (int e = 0; e < 8; ++e) wg[c][e] *= a.beta;
-            }
+                for (int e = 0; e < 8; ++e) v[e] = wg_[c][e];
+        };
         float h[C][8], x[C][8], sd[2] = {0.0f, 0.0f};      // h; z = dn pre
 #pragma unroll
         for (int c = 0; c < C; ++c) {
             float v[8];
             widen8<ES>(cur.y[c], h[c]);
             if (a.post) {
+                get(wp_, a.post, c, v);
 #pragma unroll
-                for (int e = 0; e < 8; ++e) h[c][e] = h[c][e] * r1 * wp[c][e];
+                for (int e = 0; e < 8; ++e) h[c][e] = h[c][e] * r1 * v[e];
             }
+            gate_of(c, v);
 #pragma unroll
-            for (int e = 0; e < 8; ++e) h[c][e] = wg[c][e] * h[c][e];
+            for (int e = 0; e < 8; ++e) h[c][e] = v[e] * h[c][e];
             if (a.R) {
                 widen8<ES>(cur.r[c], v);
 #pragma unroll
@@ -414,9 +453,10 @@ void norm_backward_rows(NormArgs a) {
             }
             widen8<ES>(cur.dn[c], x[c]);
             if (a.pre) {
+                get(wn_, a.pre, c, v);
 #pragma unroll
                 for (int e = 0; e < 8; ++e) {
-                    x[c][e] *= wn[c][e];
+                    x[c][e] *= v[e];
                     sd[0] = __builtin_fmaf(h[c][e], h[c][e], sd[0]);
                     sd[1] = __builtin_fmaf(x[c][e], h[c][e], sd[1]);
                 }
@@ -440,9 +480,10 @@ void norm_backward_rows(NormArgs a) {
 #pragma unroll
                 for (int e = 0; e < 8; ++e) {
                     const float m = h[c][e] * r2;
-                    if (on) dw[c][e] = __builtin_fmaf(v[e], m, dw[c][e]);
+                    out[e] = v[e] * m;
                     x[c][e] = r2 * (x[c][e] - m * mean);
                 }
+                if (on) add(dw, 1, c, out);
             }
             widen8<ES>(cur.dh[c], v);
 #pragma unroll
@@ -457,9 +498,10 @@ void norm_backward_rows(NormArgs a) {
             if (a.post)
 #pragma unroll
                 for (int e = 0; e < 8; ++e) n[e] *= r1;
+            get(wp_, a.post, c, v);
             if (a.dgate) {
 #pragma unroll
-                for (int e = 0; e < 8; ++e) out[e] = a.beta * x[c][e] * (a.post ? n[e] * wp[c][e] : n[e]);
+                for (int e = 0; e < 8; ++e) out[e] = a.beta * x[c][e] * (a.post ? n[e] * v[e] : n[e]);
                 if (!sum_gate) {
                     if (on) put_row8<ES, TAIL>(a.dgate, t * a.lddg, i, F, out);
                 } else if (on) {
@@ -467,15 +509,18 @@ void norm_backward_rows(NormArgs a) {
                     for (int e = 0; e < 8; ++e) dg[c][e] += out[e];
                 }
             }
+            float w[8];
+            gate_of(c, w);
 #pragma unroll
-            for (int e = 0; e < 8; ++e) x[c][e] *= wg[c][e];
+            for (int e = 0; e < 8; ++e) x[c][e] *= w[e];
             if (a.post) {
 #pragma unroll
                 for (int e = 0; e < 8; ++e) {
-                    if (on) dp[c][e] = __builtin_fmaf(x[c][e], n[e], dp[c][e]);
-                    x[c][e] *= wp[c][e];
+                    out[e] = x[c][e] * n[e];
+                    x[c][e] *= v[e];
                     dot[0] = __builtin_fmaf(x[c][e], n[e], dot[0]);
                 }
+                if (on) add(dp, 0, c, out);
             }
         }
         if (a.post && a.dY) row_sum<W, 1>(dot, red, turn);
@@ -495,8 +540,19 @@ void norm_backward_rows(NormArgs a) {
     }
     if (!a.partials) return;
     float *part = a.partials + (int64_t)blockIdx.x * 3 * F;
-    auto leave = [&](bool wanted, float (&v)[C][8], int kind) {
+    auto leave = [&](bool wanted, auto &v, int kind) {
         if (!wanted) return;
+        constexpr bool IN_LDS = LONG && sizeof(v) != sizeof(dg);     // the weights' sums, not the gate's
+        if constexpr (IN_LDS) {
+#pragma unroll
+            for (int c = 0; c < C; ++c) {
+                float x[8];
+#pragma unroll
+                for (int e = 0; e < 8; ++e) x[e] = sums[(((kind - 1) * C * 2 + c * 2 + e / 4) * W * 64 + lane) * 4 + e % 4];
+                put_row8<4, TAIL>(part, (int64_t)kind * F, c * STEP + lane * 8, F, x);
+            }
+            return;
+        }
         if constexpr (G > 1) {
             for (int g = 1; g < G; ++g) {
                 __syncthreads();
@@ -513,9 +569,10 @@ void norm_backward_rows(NormArgs a) {
                         for (int e = 0; e < 8; ++e) v[c][e] += sums[(c * 8 + e) * W * 64 + lane];
             }
         }
-        if (group == 0)
+        if constexpr (!IN_LDS)
+            if (group == 0)
 #pragma unroll
-            for (int c = 0; c < C; ++c) put_row8<4, TAIL>(part, (int64_t)kind * F, c * STEP + lane * 8, F, v[c]);
+                for (int c = 0; c < C; ++c) put_row8<4, TAIL>(part, (int64_t)kind * F, c * STEP + lane * 8, F, v[c]);
     };
     leave(sum_gate, dg, 0);
     leave(a.dpost != nullptr, dp, 1);
@@ -595,12 +652,12 @@ void launch_backward(const NormArgs &a, int64_t &blocks, hipStream_t s) {
         if (blocks > (a.T + g - 1) / g) blocks = (a.T + g - 1) / g;
         return dim3((unsigned)blocks);
     };
-    if (F <= 512) norm_backward_rows<ES, 1, 8, 1, true, TAIL><<<fit(8), dim3(512), 0, s>>>(a);
-    else if (F <= 1024) norm_backward_rows<ES, 2, 4, 1, true, TAIL><<<fit(4), dim3(512), 0, s>>>(a);
-    else if (F <= 2048) norm_backward_rows<ES, 4, 2, 1, true, TAIL><<<fit(2), dim3(512), 0, s>>>(a);
-    else if (F <= 4096) norm_backward_rows<ES, 8, 1, 1, true, TAIL><<<fit(1), dim3(512), 0, s>>>(a);
-    else if (F <= 8192) norm_backward_rows<ES, 8, 1, 2, false, TAIL><<<fit(1), dim3(512), 0, s>>>(a);
-    else if (F <= 16384) norm_backward_rows<ES, 16, 1, 2, false, TAIL><<<fit(1), dim3(1024), 0, s>>>(a);
+    if (F <= 512) norm_backward_rows<ES, 1, 8, 1, true, false, TAIL><<<fit(8), dim3(512), 0, s>>>(a);
+    else if (F <= 1024) norm_backward_rows<ES, 2, 4, 1, true, false, TAIL><<<fit(4), dim3(512), 0, s>>>(a);
+    else if (F <= 2048) norm_backward_rows<ES, 4, 2, 1, true, false, TAIL><<<fit(2), dim3(512), 0, s>>>(a);
+    else if (F <= 4096) norm_backward_rows<ES, 8, 1, 1, true, false, TAIL><<<fit(1), dim3(512), 0, s>>>(a);
+    else if (F <= 8192) norm_backward_rows<ES, 8, 1, 2, false, false, TAIL><<<fit(1), dim3(512), 0, s>>>(a);
+    else if (F <= 16384) norm_backward_rows<ES, 16, 1, 2, false, true, TAIL><<<fit(1), dim3(1024), 0, s>>>(a);
     else norm_backward_any<ES><<<fit(1), dim3(NT), 0, s>>>(a);
 }
 
