@@ -17,8 +17,8 @@ bool tile_ok(int64_t T, int64_t G, int64_t D) { return D <= MAX_TILE_D && D % 8 
 
 // A cache whose rows lie at multiples of 16 bytes goes to LDS without a stop.
 bool dma_ok(const AttnArgs &a, int es) {
-    const int64_t n = 16 / es;
-    return (uintptr_t)a.c.kc % 16 == 0 && (uintptr_t)a.c.vc % 16 == 0 && a.c.s_page % n == 0 && a.c.s_slot % n == 0 && a.c.s_head % n == 0;
+    const int64_t n = 16 / (a.c.ks ? 1 : es);
+    return a.c.D % n == 0 && (uintptr_t)a.c.kc % 16 == 0 && (uintptr_t)a.c.vc % 16 == 0 && a.c.s_page % n == 0 && a.c.s_slot % n == 0 && a.c.s_head % n == 0;
 }
 
 }  // namespace
@@ -31,8 +31,8 @@ AttnPlan attention_plan(int64_t T, int64_t B, int64_t Hkv, int32_t G) {
     p.row_tiles = T * G / rows + B;
     // equal runs while adding up the sequences' tiles in every workgroup is cheap and the
     // items are too few to even out by themselves
-    p.groups = p.few ? 256 : 512;
-    p.stream = p.few ? p.row_tiles <= 4096 : p.row_tiles <= 512 && p.row_tiles * Hkv <= 2048;
+    p.groups = p.few ? 1024 : 512;
+    p.stream = p.few ? p.row_tiles <= 1024 : p.row_tiles <= 512 && p.row_tiles * Hkv <= 2048;
     return p;
 }
 
@@ -48,8 +48,9 @@ hipError_t launch_kv_attention(const AttnArgs &a, int es, hipStream_t s) {
     if (!tile_ok(a.c.T, a.G, a.c.D)) return launch_attention_any(a, es, s);
     const AttnPlan p = attention_plan(a.c.T, a.c.B, a.c.Hkv, a.G);
     if (!p.stream && p.row_tiles * a.c.Hkv > (1 << 23)) return launch_attention_any(a, es, s);   // more than one launch holds
-    if (a.c.ks) return es == 2 ? launch_attention_bf16_int8(a, p, s) : launch_attention_f32_int8(a, p, s);
-    return es == 2 ? launch_attention_bf16(a, p, dma_ok(a, es), s) : launch_attention_f32(a, p, dma_ok(a, es), s);
+    const bool dma = dma_ok(a, es);
+    if (a.c.ks) return es == 2 ? launch_attention_bf16_int8(a, p, dma, s) : launch_attention_f32_int8(a, p, dma, s);
+    return es == 2 ? launch_attention_bf16(a, p, dma, s) : launch_attention_f32(a, p, dma, s);
 }
 
 }  // namespace tpl

@@ -4,7 +4,7 @@
 namespace tpl {
 
 hipError_t launch_attention_bf16(const AttnArgs &a, const AttnPlan &p, bool dma, hipStream_t s) {
-    return dma ? launch_by_size<2, 2, true>(a, p, s) : launch_by_size<2, 2, false>(a, p, s);
+    return launch_by_size<2, 2>(a, p, dma, s);
 }
 
 }  // namespace tpl

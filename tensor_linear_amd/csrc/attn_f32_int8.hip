@@ -3,8 +3,8 @@
 
 namespace tpl {
 
-hipError_t launch_attention_f32_int8(const AttnArgs &a, const AttnPlan &p, hipStream_t s) {
-    return launch_by_size<4, 1, false>(a, p, s);
+hipError_t launch_attention_f32_int8(const AttnArgs &a, const AttnPlan &p, bool dma, hipStream_t s) {
+    return launch_by_size<4, 1>(a, p, dma, s);
 }
 
 }  // namespace tpl

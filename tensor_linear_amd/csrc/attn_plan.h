@@ -19,8 +19,8 @@ AttnPlan attention_plan(int64_t T, int64_t B, int64_t Hkv, int32_t G);
 hipError_t launch_attention_any(const AttnArgs &a, int elem_bytes, hipStream_t s);
 hipError_t launch_attention_bf16(const AttnArgs &a, const AttnPlan &p, bool dma, hipStream_t s);
 hipError_t launch_attention_f32(const AttnArgs &a, const AttnPlan &p, bool dma, hipStream_t s);
-hipError_t launch_attention_bf16_int8(const AttnArgs &a, const AttnPlan &p, hipStream_t s);
-hipError_t launch_attention_f32_int8(const AttnArgs &a, const AttnPlan &p, hipStream_t s);
+hipError_t launch_attention_bf16_int8(const AttnArgs &a, const AttnPlan &p, bool dma, hipStream_t s);
+hipError_t launch_attention_f32_int8(const AttnArgs &a, const AttnPlan &p, bool dma, hipStream_t s);
 
 // The item that a run begins and does not finish: sequence s, row tile r, key head h, in
 // `pieces` runs (0: there is none).

@@ -2,12 +2,11 @@
 //
 // The new tokens of a sequence and the G query heads that read one key head are the
 // rows of one matrix (row = token * G + head), so the keys and values of a head are
-// read once for all of them.  A workgroup takes 32 WR such rows and walks the keys
-// they see in tiles of BK = 32 WK KB, with the softmax's running maximum and sum:
+// read once for all of them.  A workgroup takes 32 WR such rows, 32 a wavefront, and walks
+// the keys they see in tiles of BK = 32 KB, with the softmax's running maximum and sum:
 //   m' = max(m, max x),  f = 2^(m - m'),  p = 2^(x - m'),  l' = f l + sum p,
 //   o' = f o + p V;   at the end O = o / l,  lse = m ln 2 + log l,
-// x the products times softmax_scale * log2(e).  WR wavefronts have 32 rows each and WK
-// groups of them 32 KB keys of each tile each; the groups' sums meet at the end.
+// x the products times softmax_scale * log2(e).
 //
 // Both products are taken transposed, S^T = K Q^T and O^T = V^T P^T, with 32x32 matrix
 // instructions: a lane then has ONE row (its column l % 32 of S^T and O^T) and 16 of the
@@ -18,11 +17,12 @@
 //
 // K and V tiles lie in LDS as rows of 64, 128 or 256 values, their 16-byte chunks
 // permuted by the row so that reads meet no bank twice: K by chunks of 32 rows, bf16
-// values by the transposing read (4 keys x 16 features a 16-lane group), fp32 values by
-// words.  Two stages: the next tile is fetched while this one is worked on, straight
-// into LDS (16 bytes a lane) where the cache is of the call's type and 16-byte aligned,
-// else by way of registers, where int8 becomes bf16 or fp32 (exactly; a key's scale
-// multiplies its products, a value's scale its weight).
+// values by the transposing read (4 keys x 16 features a 16-lane group, 8 keys in int8),
+// fp32 values by words.  Two stages: the next tile is fetched while this one is worked on,
+// straight into LDS (16 bytes a lane) where the cache is 16-byte aligned, else by way of
+// registers.  int8 becomes bf16 or fp32 (exactly; a key's scale multiplies its products, a
+// value's scale its weight) as a wavefront reads it from LDS where it is alone, on the way
+// into LDS where four read the same keys.
 //
 // What a row does not see must not touch it: keys and values of no position are zeros,
 // products that a row does not see are minus infinity before the maximum, and a tile at
@@ -35,6 +35,8 @@
 // items in a row are cut into equal runs, one for each workgroup: a run's whole items are
 // finished, the others' sums go to the workspace and are joined by a second launch in the
 // order of the tiles.  The lengths are on the device: each workgroup adds them up itself.
+// One thread then reads an item's lengths and tells the others, so that a workgroup stays
+// together and in bounds whatever is in those arrays, were they to change under it.
 #pragma once
 
 #include <hip/hip_runtime.h>
@@ -76,15 +78,42 @@ __device__ __forceinline__ f32x16 product(u32x4 a, u32x4 b, f32x16 c) {
     }
 }
 
+__device__ __forceinline__ int uniform(int v) { return __builtin_amdgcn_readfirstlane(v); }
+
+// An item, and the part of its tiles that a run has; pieces: runs from this one to the
+// item's last.  s < 0: none.
+struct Item { int64_t s; Sequence q; Span sp; int r, h, k0, k1, pieces; };
+
 // Byte permutation of a row of K and of V in LDS (XOR with the byte in the row).
+// K: the 16 rows of a quarter of a read on 16 chunks.  V: the rows of half a read (int8: 0-3
+// and 8-11, 32 bytes each; bf16: 0-3, 64 bytes; fp32: two, 4 apart, 128 bytes) side by side.
 template <int RB>
 __device__ __forceinline__ uint32_t k_swizzle(uint32_t row) {
-    return (RB == 128 ? (row >> 1) & 7 : row & 15) << 4;
+    return (RB == 64 ? (row >> 2) & 3 : RB == 128 ? (row >> 1) & 7 : row & 15) << 4;
 }
-template <int ES, int RB>
+template <int LS, int RB>
 __device__ __forceinline__ uint32_t v_swizzle(uint32_t row) {
-    if (ES == 4) return ((row >> 2) & 1) << 7;
+    if (LS == 1) return RB == 64 ? ((row >> 3) & 1) << 5 : RB == 128 ? ((row >> 1) & 1) << 5 | ((row >> 3) & 1) << 6
+                                                                     : (row & 3) << 5 | ((row >> 3) & 1) << 7;
+    if (LS == 4) return ((row >> 2) & 1) << 7;
     return RB == 128 ? ((row >> 1) & 1) << 6 : (row & 3) << 6;
+}
+
+// int8 values to operands: four words of two bf16 (8 values) or of one fp32 (4).
+template <int ES>
+__device__ __forceinline__ u32x4 from_int8(uint32_t lo, uint32_t hi) {
+    const uint32_t w[2] = {lo, hi};
+    if constexpr (ES == 2) {
+        bf16x8 h;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) h[e] = (__bf16)(float)((int32_t)(w[e / 4] << (24 - 8 * (e & 3))) >> 24);
+        return __builtin_bit_cast(u32x4, h);
+    } else {
+        u32x4 y;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) y[e] = __float_as_uint((float)((int32_t)(lo << (24 - 8 * e)) >> 24));
+        return y;
+    }
 }
 
 __device__ __forceinline__ float other_half(float v) { return __shfl_xor(v, 32); }
@@ -95,11 +124,17 @@ __device__ __forceinline__ int64_t uniform(int64_t v) {
     return (int64_t)((uint64_t)hi << 32 | lo);
 }
 
-template <int ES, int CS, int NB, int WR, int WK, int KB, bool DMA, int OCC>
-__global__ __launch_bounds__(64 * WR * WK, OCC)
+// What lies in LDS: rows of the call's type by way of registers, the same straight from
+// the cache, or int8 straight from the cache.
+enum { STAGE_REGS = 0, STAGE_DMA = 1, STAGE_INT8 = 2 };
+
+template <int ES, int CS, int NB, int WR, int KB, int ST, int OCC>
+__global__ __launch_bounds__(64 * WR, OCC)
 void attention_tile(AttnArgs a, AttnPlan plan) {
-    constexpr int NW = WR * WK, NTH = 64 * NW, ROWS = 32 * WR, BK = 32 * WK * KB;
-    constexpr int DP = NB == 3 ? 128 : NB * 32, RB = DP * ES;          // a row in LDS
+    constexpr int NW = WR, NTH = 64 * NW, ROWS = 32 * WR, BK = 32 * KB;
+    constexpr int LS = ST == STAGE_INT8 ? 1 : ES;                       // bytes of a value in LDS
+    constexpr bool DMA = ST != STAGE_REGS;
+    constexpr int DP = NB == 3 ? 128 : NB * 32, RB = DP * LS;          // a row in LDS
     constexpr int KS = NB * ES;                                         // steps of the first product
     constexpr int CH = RB / 16, LI = BK * CH / NTH;                     // chunks of a row; of a thread and tile
     constexpr int STAGE = 2 * BK * RB;
@@ -111,17 +146,17 @@ void attention_tile(AttnArgs a, AttnPlan plan) {
     __shared__ uint64_t row_mask[2][(BK + 63) / 64];
     __shared__ int64_t scan[NW + 2];
     __shared__ int found[2];
-    __shared__ float merge[2][WK > 1 ? WK : 1][WK > 1 ? ROWS : 1];
+    __shared__ Item next_item;
     LDS_PTR(char) lds = (LDS_PTR(char))smem;
     const uint32_t lds_u = (uint32_t)(uintptr_t)lds;
 
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-    const int wr = wave % WR, wk = wave / WR, half = lane >> 5, col = lane & 31;
+    const int wr = wave, half = lane >> 5, col = lane & 31;
     const CacheArgs &c = a.c;
     const int D = c.D, G = a.G;
     const float cs = a.scale * 1.44269504088896340736f;
     const int64_t last_pos = c.max_pages * (int64_t)c.page;             // positions of the table
-    const int chunks = D * ES / 16;                                     // of a row that hold features
+    const int chunks = D * LS / 16;                                     // of a row in LDS that hold features
 
     auto sequence = [&](int64_t s) { return plan_sequence(c, s); };
     auto span = [&](const Sequence &q, int r) { return plan_span(q, r, G, ROWS, BK, a.window, last_pos); };
@@ -133,9 +168,8 @@ void attention_tile(AttnArgs a, AttnPlan plan) {
     };
 
     // ---- the run of tiles of this workgroup
-    int64_t s = 0, base = 0, u = 0, u1 = 0, all = 0;    // sequence, its first unit, the run [u, u1), units in all
-    int item_r = 0, item_h = 0;
-    int W = plan.groups;                                // runs that have tiles
+    int64_t all = 0, u = 0, u1 = 0, base = 0, seq = 0;   // units in all, the run [u, u1); the first one of sequence seq
+    int W = plan.groups;                                 // runs that have tiles
     int w = blockIdx.x;
     if (plan.stream) {
         const int64_t q = (c.B + NTH - 1) / NTH, sb = tid * q;
@@ -148,6 +182,7 @@ void attention_tile(AttnArgs a, AttnPlan plan) {
             if (lane >= o) run += v;
         }
         if (lane == 63) scan[wave] = run;
+        if (tid == 0) scan[NW] = c.B;
         __syncthreads();
         int64_t before = 0;
         for (int i = 0; i < NW; ++i) {
@@ -161,71 +196,96 @@ void attention_tile(AttnArgs a, AttnPlan plan) {
         if (w >= W) return;
         u = all * w / W;
         u1 = all * (w + 1) / W;
-        const int64_t lo = (before + run - mine) * c.Hkv, hi = (before + run) * c.Hkv;
-        __syncthreads();
-        if (u >= lo && u < hi) {                        // one thread
-            int64_t at = lo, i = sb;
-            while (true) {
+        int64_t at = (before + run - mine) * c.Hkv;
+        if (u >= at && u < (before + run) * c.Hkv) {    // one thread
+            for (int64_t i = sb; i < sb + q && i < c.B; ++i) {
                 const int64_t n = count(sequence(i)) * c.Hkv;
-                if (u < at + n) break;
+                if (u < at + n) {
+                    scan[NW] = i;
+                    scan[NW + 1] = at;
+                    break;
+                }
                 at += n;
-                ++i;
             }
-            scan[NW] = i;
-            scan[NW + 1] = at;
         }
         __syncthreads();
-        s = uniform(scan[NW]);
-        base = uniform(scan[NW + 1]);
-    } else {
-        const int64_t n = (int64_t)plan.row_tiles, i = n - 1 - w / c.Hkv;
-        item_h = w % c.Hkv;
-        // sequence s has the indices from cu[s] G / ROWS + s on, enough for its rows
-        int64_t lo = 0, m = c.B;
-        while (m > 0) {
-            const int64_t step = (m + 63) / 64;
-            const int64_t j = lo + lane * step;
-            const bool below = lane * step < m && plan_index(c, j, G, ROWS) <= i;
-            const int k = __popcll(__ballot(below));
-            if (k == 0) break;
-            const int64_t b = (int64_t)(k - 1) * step;
-            lo += b + 1;
-            m = (m - b < step ? m - b : step) - 1;
-        }
-        s = uniform(lo) - 1;
-        if (s < 0) return;
-        const Sequence q = sequence(s);
-        const int64_t r = i - plan_index(c, s, G, ROWS);
-        if (r >= (q.n * G + ROWS - 1) / ROWS) return;
-        item_r = (int)r;
+        seq = scan[NW];
+        base = scan[NW + 1];
     }
     int stamp = 0;
     if (tid < 2) found[tid] = -1;
 
-    while (true) {
-        // ---- the item and the part of its tiles
-        const Sequence q = sequence(s);
-        Span sp;
-        int k0, k1;
-        int64_t item_u = 0;
+    // The next item and the part of its tiles, by one thread (one wavefront).
+    auto find_item = [&]() {
+        Item m{};
+        m.s = -1;
         if (plan.stream) {
-            const int64_t n = count(q);
-            if (n == 0) { ++s; continue; }
-            const int64_t rel = u - base;
-            item_h = (int)(rel / n);
-            int64_t rem = rel - item_h * n;
-            int r = 0;
-            sp = span(q, 0);
-            while (rem >= sp.tiles) { rem -= sp.tiles; sp = span(q, ++r); }
-            item_r = r;
-            item_u = u - rem;
-            k0 = (int)rem;
-            k1 = (int)(u1 - item_u < sp.tiles ? u1 - item_u : sp.tiles);
+            while (u < u1 && seq < c.B) {
+                const Sequence q = sequence(seq);
+                const int64_t n = count(q);
+                if (u >= base + n * c.Hkv) { base += n * c.Hkv; ++seq; continue; }
+                const int64_t rel = u - base;
+                m.h = (int)(rel / n);
+                int64_t rem = rel - m.h * n;
+                const int nr = (int)((q.n * G + ROWS - 1) / ROWS);
+                Span sp = span(q, 0);
+                int r = 0;
+                while (rem >= sp.tiles && r + 1 < nr) { rem -= sp.tiles; sp = span(q, ++r); }
+                const int64_t item_u = u - rem;
+                m.s = seq; m.q = q; m.sp = sp; m.r = r;
+                m.k0 = (int)rem;
+                m.k1 = (int)(u1 - item_u < sp.tiles ? u1 - item_u : sp.tiles);
+                if (m.k1 <= m.k0) { m.s = -1; break; }
+                int64_t to = ((item_u + sp.tiles) * W - 1) / all;               // the run with the item's last tile
+                if (to >= W) to = W - 1;
+                m.pieces = (int)(to - w + 1);
+                u = item_u + m.k1;
+                break;
+            }
         } else {
-            sp = span(q, item_r);
-            k0 = 0;
-            k1 = sp.tiles;
+            const int64_t i = plan.row_tiles - 1 - w / c.Hkv;
+            // sequence s has the indices from cu[s] G / ROWS + s on, enough for its rows
+            int64_t lo = 0, n = c.B;
+            while (n > 0) {
+                const int64_t step = (n + 63) / 64;
+                const int64_t j = lo + lane * step;
+                const bool below = lane * step < n && plan_index(c, j, G, ROWS) <= i;
+                const int k = __popcll(__ballot(below));
+                if (k == 0) break;
+                const int64_t b = (int64_t)(k - 1) * step;
+                lo += b + 1;
+                n = (n - b < step ? n - b : step) - 1;
+            }
+            const int64_t s = uniform(lo) - 1;
+            if (s >= 0) {
+                const Sequence q = sequence(s);
+                const int64_t r = i - plan_index(c, s, G, ROWS);
+                if (r >= 0 && r < (q.n * G + ROWS - 1) / ROWS) {
+                    m.s = s; m.q = q; m.r = (int)r; m.h = w % c.Hkv;
+                    m.sp = span(q, (int)r);
+                    m.k1 = m.sp.tiles;
+                }
+            }
         }
+        return m;
+    };
+
+    while (true) {
+        if (wave == 0) {
+            const Item m = find_item();
+            if (lane == 0) next_item = m;
+        }
+        __syncthreads();
+        const int64_t s = uniform(next_item.s);
+        if (s < 0) return;
+        Sequence q;
+        q.first = uniform(next_item.q.first); q.n = uniform(next_item.q.n); q.past = uniform(next_item.q.past);
+        Span sp;
+        sp.pos0 = uniform(next_item.sp.pos0); sp.pos1 = uniform(next_item.sp.pos1);
+        sp.begin = uniform(next_item.sp.begin); sp.end = uniform(next_item.sp.end); sp.first = uniform(next_item.sp.first);
+        sp.tiles = uniform(next_item.sp.tiles); sp.outside = next_item.sp.outside;
+        const int item_r = uniform(next_item.r), item_h = uniform(next_item.h), pieces = uniform(next_item.pieces);
+        const int k0 = uniform(next_item.k0), k1 = uniform(next_item.k1);
         if (sp.outside && c.bad && tid == 0) *c.bad = 1;
 
         // ---- this lane's row
@@ -240,8 +300,9 @@ void attention_tile(AttnArgs a, AttnPlan plan) {
 #pragma unroll
         for (int k = 0; k < KS; ++k) {
             qf[k] = u32x4{0, 0, 0, 0};
-            const int ch = 2 * k + half;
-            if (live && ch < chunks) qf[k] = *(const u32x4_any *)((const char *)a.Q + (row * a.ldq + (int64_t)head * D) * ES + ch * 16);
+            // the features that a lane's k-th operand of K has
+            const int ch = ST == STAGE_INT8 ? (2 * (k / ES) + half) * ES + k % ES : 2 * k + half;
+            if (live && ch < D * ES / 16) qf[k] = *(const u32x4_any *)((const char *)a.Q + (row * a.ldq + (int64_t)head * D) * ES + ch * 16);
         }
         f32x16 o[NB];
 #pragma unroll
@@ -296,9 +357,9 @@ void attention_tile(AttnArgs a, AttnPlan plan) {
                 const int64_t at = row_at[st][r];
                 if constexpr (DMA) {
                     const uint32_t dst = lds_u + st * STAGE + (i * NTH + wave * 64) * 16;
-                    const int kc = ch ^ (k_swizzle<RB>(r) >> 4), vc = ch ^ (v_swizzle<ES, RB>(r) >> 4);
-                    const char *ka = at >= 0 && kc < chunks ? (const char *)c.kc + at * ES + kc * 16 : (const char *)no_key;
-                    const char *va = at >= 0 && vc < chunks ? (const char *)c.vc + at * ES + vc * 16 : (const char *)no_key;
+                    const int kc = ch ^ (k_swizzle<RB>(r) >> 4), vc = ch ^ (v_swizzle<LS, RB>(r) >> 4);
+                    const char *ka = at >= 0 && kc < chunks ? (const char *)c.kc + at * CS + kc * 16 : (const char *)no_key;
+                    const char *va = at >= 0 && vc < chunks ? (const char *)c.vc + at * CS + vc * 16 : (const char *)no_key;
                     asm volatile("s_mov_b32 m0, %1\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, off" :: "v"(ka), "s"(dst) : "memory", "m0");
                     asm volatile("s_mov_b32 m0, %1\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, off" :: "v"(va), "s"(dst + BK * RB) : "memory", "m0");
                 } else {
@@ -321,20 +382,6 @@ void attention_tile(AttnArgs a, AttnPlan plan) {
                 }
             }
         };
-        auto widen = [&](u32x4 x) {
-            if constexpr (!QUANT) return x;
-            u32x4 y;
-            if constexpr (ES == 2) {
-                bf16x8 h;
-#pragma unroll
-                for (int e = 0; e < 8; ++e) h[e] = (__bf16)(float)((int32_t)(x[e / 4] << (24 - 8 * (e & 3))) >> 24);
-                y = __builtin_bit_cast(u32x4, h);
-            } else {
-#pragma unroll
-                for (int e = 0; e < 4; ++e) y[e] = __float_as_uint((float)((int32_t)(x[0] << (24 - 8 * e)) >> 24));
-            }
-            return y;
-        };
         auto settle = [&](int k) __attribute__((always_inline)) {      // the fetched tile is in LDS, this thread's part
             if constexpr (DMA) {
                 asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
@@ -343,8 +390,8 @@ void attention_tile(AttnArgs a, AttnPlan plan) {
                 for (int i = 0; i < LI; ++i) {
                     const int n = i * NTH + tid, r = n / CH, ch = n % CH;
                     const uint32_t at = (k & 1) * STAGE + r * RB;
-                    *(LDS_PTR(u32x4))(lds + at + ((ch * 16) ^ k_swizzle<RB>(r))) = widen(kr[i]);
-                    *(LDS_PTR(u32x4))(lds + at + BK * RB + ((ch * 16) ^ v_swizzle<ES, RB>(r))) = widen(vr[i]);
+                    *(LDS_PTR(u32x4))(lds + at + ((ch * 16) ^ k_swizzle<RB>(r))) = QUANT ? from_int8<ES>(kr[i][0], kr[i][1]) : kr[i];
+                    *(LDS_PTR(u32x4))(lds + at + BK * RB + ((ch * 16) ^ v_swizzle<LS, RB>(r))) = QUANT ? from_int8<ES>(vr[i][0], vr[i][1]) : vr[i];
                 }
             }
         };
@@ -375,24 +422,30 @@ void attention_tile(AttnArgs a, AttnPlan plan) {
             }
             f32x16 x[KB];
             uint32_t seen[KB];
-            const uint32_t kl = st * STAGE + (wk * KB * 32 + col) * RB, ks = (half * 16) ^ k_swizzle<RB>(col);
+            const uint32_t kl = st * STAGE + col * RB, ks = (half * 16) ^ k_swizzle<RB>(col);
 #pragma unroll
             for (int b = 0; b < KB; ++b)
 #pragma unroll
                 for (int i = 0; i < 16; ++i) x[b][i] = 0.0f;
 #pragma unroll
-            for (int s2 = 0; s2 < KS; ++s2)
+            for (int s2 = 0; s2 < KS; s2 += ES / LS)
 #pragma unroll
                 for (int b = 0; b < KB; ++b) {
-                    const u32x4 kf = *(LDS_PTR(u32x4))(lds + kl + b * 32 * RB + ((s2 * 32) ^ ks));
-                    x[b] = product<ES>(kf, qf[s2], x[b]);
+                    const u32x4 kf = *(LDS_PTR(u32x4))(lds + kl + b * 32 * RB + ((s2 * LS / ES * 32) ^ ks));
+                    if constexpr (ST != STAGE_INT8) {
+                        x[b] = product<ES>(kf, qf[s2], x[b]);
+                    } else {
+#pragma unroll
+                        for (int e = 0; e < ES; ++e)
+                            x[b] = product<ES>(ES == 2 ? from_int8<ES>(kf[2 * (e & 1)], kf[2 * (e & 1) + 1]) : from_int8<ES>(kf[e], 0), qf[s2 + e], x[b]);
+                    }
                 }
             if constexpr (QUANT) {
 #pragma unroll
                 for (int b = 0; b < KB; ++b)
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
-                        const f32x4 z = *(LDS_PTR(f32x4))(LDS_PTR(float))&row_scale[st][0][(wk * KB + b) * 32 + 8 * i + 4 * half];
+                        const f32x4 z = *(LDS_PTR(f32x4))(LDS_PTR(float))&row_scale[st][0][b * 32 + 8 * i + 4 * half];
 #pragma unroll
                         for (int e = 0; e < 4; ++e) x[b][4 * i + e] *= z[e];
                     }
@@ -400,14 +453,14 @@ void attention_tile(AttnArgs a, AttnPlan plan) {
             bool masked = edge;
 #pragma unroll
             for (int b = 0; b < KB; ++b) {
-                const int n = (wk * KB + b) * 32;
+                const int n = b * 32;
                 seen[b] = __builtin_amdgcn_readfirstlane((uint32_t)(row_mask[st][n / 64] >> (n & 63)));
                 masked |= seen[b] != 0xFFFFFFFFu;
             }
             if (masked) {
 #pragma unroll
                 for (int b = 0; b < KB; ++b) {
-                    const int64_t n = t0 + (wk * KB + b) * 32, up = hi - n, from = lo - n;
+                    const int64_t n = t0 + b * 32, up = hi - n, from = lo - n;
                     uint32_t m = seen[b];
                     m &= up >= 31 ? 0xFFFFFFFFu : up < 0 ? 0u : (2u << (int)up) - 1u;
                     m &= from <= 0 ? 0xFFFFFFFFu : from > 31 ? 0u : 0xFFFFFFFFu << (int)from;
@@ -449,7 +502,7 @@ void attention_tile(AttnArgs a, AttnPlan plan) {
                 for (int b = 0; b < KB; ++b)
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
-                        const f32x4 z = *(LDS_PTR(f32x4))(LDS_PTR(float))&row_scale[st][1][(wk * KB + b) * 32 + 8 * i + 4 * half];
+                        const f32x4 z = *(LDS_PTR(f32x4))(LDS_PTR(float))&row_scale[st][1][b * 32 + 8 * i + 4 * half];
 #pragma unroll
                         for (int e = 0; e < 4; ++e) {
                             x[b][4 * i + e] *= z[e];
@@ -457,12 +510,42 @@ void attention_tile(AttnArgs a, AttnPlan plan) {
                         }
                     }
             }
-            const uint32_t vl = st * STAGE + BK * RB + wk * KB * 32 * RB;
+            const uint32_t vl = st * STAGE + BK * RB;
             auto values = [&](auto put) __attribute__((always_inline)) {
-                if constexpr (ES == 2) {
+                if constexpr (ST == STAGE_INT8) {
+                    // keys 16 s + 8 e + 4 half + i of a step, 4 e + i = (l % 16) / 2
+                    const uint32_t r = (lane & 15) >> 1, key = (r & 3) + (r >> 2) * 8 + 4 * half;
+                    const uint32_t at = vl + key * RB + ((lane >> 4) & 1) * 16 + (lane & 1) * 8, sw = v_swizzle<LS, RB>(key);
+#pragma unroll
+                    for (int b = 0; b < KB; ++b)
+#pragma unroll
+                        for (int s2 = 0; s2 < 2; ++s2) {
+                            u32x4 p[ES / 2];
+                            if constexpr (ES == 2) {
+                                bf16x8 h;
+#pragma unroll
+                                for (int e = 0; e < 8; ++e) h[e] = (__bf16)x[b][8 * s2 + e];
+                                p[0] = __builtin_bit_cast(u32x4, h);
+                            } else {
+#pragma unroll
+                                for (int e = 0; e < 8; ++e) p[e / 4 * (ES / 4)][e % 4] = __float_as_uint(x[b][8 * s2 + e]);
+                            }
+#pragma unroll
+                            for (int d = 0; d < NB; ++d) {
+                                typedef int i32x2 __attribute__((ext_vector_type(2)));
+                                const i32x2 v = __builtin_amdgcn_ds_read_tr8_b64_v2i32((LDS_PTR(i32x2))(lds + at + (b * 32 + s2 * 16) * RB + ((d * 32) ^ sw)));
+                                if constexpr (ES == 2) {
+                                    put(d, b, s2, from_int8<ES>(v[0], v[1]), p[0]);
+                                } else {
+                                    put(d, b, 2 * s2, from_int8<ES>(v[0], 0), p[0]);
+                                    put(d, b, 2 * s2 + 1, from_int8<ES>(v[1], 0), p[ES / 4]);
+                                }
+                            }
+                        }
+                } else if constexpr (ES == 2) {
                     // keys 16 s + 8 e + 4 half + r of a step, r = (l % 16) / 4; features of 16 lanes
                     const uint32_t r = (lane & 15) >> 2;
-                    const uint32_t at = vl + (4 * half + r) * RB + ((lane >> 4) & 1) * 32 + (lane & 3) * 8, sw = v_swizzle<ES, RB>(r);
+                    const uint32_t at = vl + (4 * half + r) * RB + ((lane >> 4) & 1) * 32 + (lane & 3) * 8, sw = v_swizzle<LS, RB>(r);
 #pragma unroll
                     for (int b = 0; b < KB; ++b)
 #pragma unroll
@@ -570,79 +653,33 @@ void attention_tile(AttnArgs a, AttnPlan plan) {
             }
         }
 
-        // ---- the rows' sums: of the two halves, then of the groups of wavefronts
         l += other_half(l);
-        if constexpr (WK > 1) {
-            // each group's rows to the largest of the maxima, then the groups in order
-            __syncthreads();
-            if (half == 0) merge[0][wk][wr * 32 + col] = mx;
-            __syncthreads();
-            float m = mx;
-#pragma unroll
-            for (int i = 0; i < WK; ++i) m = fmaxf(m, merge[0][i][wr * 32 + col]);
-            const float f = m == -INFINITY ? 0.0f : __builtin_amdgcn_exp2f(mx - m);
-            mx = m;
-            l *= f;
-            if (half == 0) merge[1][wk][wr * 32 + col] = l;
+        const bool whole = !plan.stream || (k0 == 0 && k1 == sp.tiles);
+        const int slot = plan.stream ? 2 * w + (k0 == 0 ? 1 : 0) : 0;
+        const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+        if (live) {
 #pragma unroll
             for (int b = 0; b < NB; ++b)
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
                     f32x4 v;
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) v[e] = o[b][4 * i + e] * f;
-                    *(LDS_PTR(f32x4))(lds + ((((wk * WR + wr) * NB + b) * 4 + i) * 64 + lane) * 16) = v;
-                }
-            __syncthreads();
-            l = 0.0f;
-#pragma unroll
-            for (int i = 0; i < WK; ++i) l += merge[1][i][wr * 32 + col];
-        }
-        const bool whole = !plan.stream || (k0 == 0 && k1 == sp.tiles);
-        const int slot = plan.stream ? 2 * w + (k0 == 0 ? 1 : 0) : 0;
-        const float inv = l == 0.0f ? 0.0f : 1.0f / l;
-#pragma unroll
-        for (int b = 0; b < NB; ++b) {
-            if (WK > 1 && b % WK != wk) continue;
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                f32x4 v;
-                if constexpr (WK > 1) {
-                    v = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll
-                    for (int k = 0; k < WK; ++k) v += *(LDS_PTR(f32x4))(lds + ((((k * WR + wr) * NB + b) * 4 + i) * 64 + lane) * 16);
-                } else {
-#pragma unroll
                     for (int e = 0; e < 4; ++e) v[e] = o[b][4 * i + e];
+                    if (whole) write_out<ES>(a.O, row * a.ldo + (int64_t)head * D, b * 32 + 8 * i + 4 * half, D, v, l == 0.0f, inv);
+                    else plan_sums(a.ws, plan.groups)[(((int64_t)slot * WR + wr) * NB + b) * 256 + i * 64 + lane] = v;
                 }
-                if (!whole) {
-                    if (live) plan_sums(a.ws, plan.groups)[(((int64_t)slot * WR + wr) * NB + b) * 256 + i * 64 + lane] = v;
-                    continue;
-                }
-                if (live) write_out<ES>(a.O, row * a.ldo + (int64_t)head * D, b * 32 + 8 * i + 4 * half, D, v, l == 0.0f, inv);
-            }
-        }
-        if (wk == 0 && half == 0 && live) {
-            if (!whole) {
+            if (half == 0 && !whole) {
                 float *ml = plan_stats(a.ws, plan.groups) + ((int64_t)slot * ROWS + wr * 32 + col) * 2;
                 ml[0] = mx;
                 ml[1] = l;
-            } else if (a.lse) {
+            } else if (half == 0 && a.lse) {
                 a.lse[row * a.ldl + head] = l == 0.0f ? -INFINITY : mx * 0.69314718055994530942f + logf(l);
             }
         }
         if (!plan.stream) return;
         if (!whole && k0 == 0 && tid == 0) {
             // this run begins the item: it names the runs that hold the rest
-            const int64_t end = item_u + sp.tiles - 1;
-            const int64_t to = ((end + 1) * W - 1) / all;
-            plan_desc(a.ws)[w] = PlanDesc{(int)(to - w + 1), item_r, item_h, 0, s};
-        }
-        u = item_u + k1;
-        if (u >= u1) return;
-        if (u >= base + count(q) * c.Hkv) {
-            base = u;
-            ++s;
+            plan_desc(a.ws)[w] = PlanDesc{pieces, item_r, item_h, 0, s};
         }
         __syncthreads();
     }
@@ -687,31 +724,35 @@ void attention_join(AttnArgs a, AttnPlan plan) {
     if (a.lse && b == 0 && i == 0 && half == 0) a.lse[row * a.ldl + head] = l == 0.0f ? -INFINITY : m * 0.69314718055994530942f + logf(l);
 }
 
-template <int ES, int CS, int NB, int WR, int WK, int KB, bool DMA, int OCC>
+template <int ES, int CS, int NB, int WR, int KB, int ST, int OCC>
 hipError_t launch_tile(const AttnArgs &a, const AttnPlan &p, hipStream_t s) {
-    const int64_t items = p.row_tiles * a.c.Hkv;
-    const unsigned grid = p.stream ? (unsigned)p.groups : (unsigned)items;
-    attention_tile<ES, CS, NB, WR, WK, KB, DMA, OCC><<<dim3(grid), dim3(64 * WR * WK), 0, s>>>(a, p);
+    const unsigned grid = p.stream ? (unsigned)p.groups : (unsigned)(p.row_tiles * a.c.Hkv);
+    attention_tile<ES, CS, NB, WR, KB, ST, OCC><<<dim3(grid), dim3(64 * WR), 0, s>>>(a, p);
     hipError_t e = hipGetLastError();
     if (e != hipSuccess || !p.stream) return e;
     attention_join<ES, NB, WR><<<dim3((unsigned)p.groups, WR * NB), dim3(256), 0, s>>>(a, p);
     return hipGetLastError();
 }
 
-// Tiles by the bytes of a row in LDS: two stages of K and V, 64 to 128 KB.
-template <int ES, int CS, int NB, bool DMA>
-hipError_t launch_nb(const AttnArgs &a, const AttnPlan &p, hipStream_t s) {
+// dma: the cache goes to LDS without a stop.  Tiles by the bytes of a row in LDS.
+template <int ES, int CS, int NB>
+hipError_t launch_nb(const AttnArgs &a, const AttnPlan &p, bool dma, hipStream_t s) {
     constexpr int RB = (NB == 3 ? 128 : NB * 32) * ES;
-    if (p.few) return launch_tile<ES, CS, NB, 1, RB <= 256 ? 4 : RB == 512 ? 2 : 1, 1, DMA, 1>(a, p, s);
-    return launch_tile<ES, CS, NB, 4, 1, RB <= 256 ? 2 : 1, DMA, NB == 8 ? 1 : 2>(a, p, s);
+    if (p.few) {
+        if (dma) return launch_tile<ES, CS, NB, 1, 1, CS == 1 ? STAGE_INT8 : STAGE_DMA, CS == 1 && NB < 8 ? 2 : 1>(a, p, s);
+        return launch_tile<ES, CS, NB, 1, 1, STAGE_REGS, 1>(a, p, s);
+    }
+    constexpr int KB = RB <= 256 ? 2 : 1, OCC = NB == 8 ? 1 : 2;
+    if (dma && CS != 1) return launch_tile<ES, CS, NB, 4, KB, CS == 1 ? STAGE_REGS : STAGE_DMA, OCC>(a, p, s);
+    return launch_tile<ES, CS, NB, 4, KB, STAGE_REGS, OCC>(a, p, s);
 }
 
-template <int ES, int CS, bool DMA>
-hipError_t launch_by_size(const AttnArgs &a, const AttnPlan &p, hipStream_t s) {
-    if (a.c.D <= 64) return launch_nb<ES, CS, 2, DMA>(a, p, s);
-    if (a.c.D <= 96) return launch_nb<ES, CS, 3, DMA>(a, p, s);
-    if (a.c.D <= 128) return launch_nb<ES, CS, 4, DMA>(a, p, s);
-    return launch_nb<ES, CS, 8, DMA>(a, p, s);
+template <int ES, int CS>
+hipError_t launch_by_size(const AttnArgs &a, const AttnPlan &p, bool dma, hipStream_t s) {
+    if (a.c.D <= 64) return launch_nb<ES, CS, 2>(a, p, dma, s);
+    if (a.c.D <= 96) return launch_nb<ES, CS, 3>(a, p, dma, s);
+    if (a.c.D <= 128) return launch_nb<ES, CS, 4>(a, p, dma, s);
+    return launch_nb<ES, CS, 8>(a, p, dma, s);
 }
 
 }  // namespace

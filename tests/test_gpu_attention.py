@@ -335,6 +335,7 @@ def test_graph_with_growing_sequences():
     ws = workspace(5, 5, 8, 2, 128)
     call = lambda: tl.tp_kv_attention(Q, args["past"], args["cu"], args["table"], args["k_cache"], args["v_cache"], O, ws, lse=L)  # noqa: E731
     side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
     with torch.cuda.stream(side):
         call()
     side.synchronize()

@@ -267,6 +267,7 @@ def test_block_in_a_row():
         tl.tp_residual_norm(y, h, n8, residual=x, pre_weight=pre, scale=ns)
 
     side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
     with torch.cuda.stream(side):
         block()
     side.synchronize()

@@ -295,6 +295,7 @@ def test_graph():
         tl.tp_residual_norm_backward(Y, H, N, dY, dR, dgate=dg, dpost_weight=dp, dpre_weight=dq, workspace=ws, **kw)
 
     side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
     with torch.cuda.stream(side):
         step()
     side.synchronize()
