@@ -23,22 +23,27 @@ bool dma_ok(const AttnArgs &a, int es) {
 
 }  // namespace
 
-AttnPlan attention_plan(int64_t T, int64_t B, int64_t Hkv, int32_t G) {
+AttnPlan attention_plan(int64_t T, int64_t B, int64_t Hkv, int32_t G, int64_t D, int es, bool quant) {
     AttnPlan p{};
     // 32 rows a workgroup where the sequences have no more on average
     p.few = T * G <= 32 * B;
     const int64_t rows = p.few ? 32 : 128;
     p.row_tiles = T * G / rows + B;
-    // equal runs while adding up the sequences' tiles in every workgroup is cheap and the
-    // items are too few to even out by themselves
-    p.groups = p.few ? 1024 : 512;
+    // Equal runs while adding up the sequences' tiles in every workgroup is cheap and the
+    // items are too few to even out by themselves.
     p.stream = p.few ? p.row_tiles <= 1024 : p.row_tiles <= 512 && p.row_tiles * Hkv <= 2048;
+    // As many as 256 CUs hold at once, by LDS (two stages of 32 keys, one wavefront) and by
+    // registers (two wavefronts a SIMD, one for the longest heads).  Not taken from the
+    // device: the workspace's size and the order of the sums depend on the call alone.
+    const int64_t row = (D <= 64 ? 64 : D <= 128 ? 128 : 256) * (quant ? 1 : es);
+    p.groups = 256 * (!p.few ? (D <= 128 ? 2 : 1) : D > 128 && row <= 256 ? 4 : row <= 128 ? 8 : row <= 256 ? 4 : row <= 512 ? 2 : 1);
     return p;
 }
 
 size_t attention_workspace(int64_t T, int64_t B, int64_t Hq, int64_t Hkv, int64_t D) {
     if (T == 0 || B == 0 || !tile_ok(T, Hq / Hkv, D)) return 0;
-    const AttnPlan p = attention_plan(T, B, Hkv, (int32_t)(Hq / Hkv));
+    // the most runs that any type of cache has
+    const AttnPlan p = attention_plan(T, B, Hkv, (int32_t)(Hq / Hkv), D, 2, true);
     if (!p.stream) return 0;
     const int64_t d = D <= 64 ? 64 : D <= 96 ? 96 : D <= 128 ? 128 : 256, rows = p.few ? 32 : 128;
     return (size_t)(plan_desc_bytes(p.groups) + plan_stats_bytes(p.groups) + 2 * p.groups * rows * d * 4);
@@ -46,7 +51,7 @@ size_t attention_workspace(int64_t T, int64_t B, int64_t Hq, int64_t Hkv, int64_
 
 hipError_t launch_kv_attention(const AttnArgs &a, int es, hipStream_t s) {
     if (!tile_ok(a.c.T, a.G, a.c.D)) return launch_attention_any(a, es, s);
-    const AttnPlan p = attention_plan(a.c.T, a.c.B, a.c.Hkv, a.G);
+    const AttnPlan p = attention_plan(a.c.T, a.c.B, a.c.Hkv, a.G, a.c.D, es, a.c.ks != nullptr);
     if (!p.stream && p.row_tiles * a.c.Hkv > (1 << 23)) return launch_attention_any(a, es, s);   // more than one launch holds
     const bool dma = dma_ok(a, es);
     if (a.c.ks) return es == 2 ? launch_attention_bf16_int8(a, p, dma, s) : launch_attention_f32_int8(a, p, dma, s);

@@ -12,9 +12,9 @@ namespace tpl {
 // the row_tiles * Hkv items.  few: 32 rows a workgroup, else 128.
 struct AttnPlan { int32_t stream, few, groups; int64_t row_tiles; };
 
-// The plan of a call of these sizes (the lengths are on the device: T, B and the heads
-// are all that the host knows).
-AttnPlan attention_plan(int64_t T, int64_t B, int64_t Hkv, int32_t G);
+// The plan of a call of these sizes and types (the lengths are on the device: T, B and the
+// heads are all that the host knows).
+AttnPlan attention_plan(int64_t T, int64_t B, int64_t Hkv, int32_t G, int64_t D, int elem_bytes, bool quant);
 
 hipError_t launch_attention_any(const AttnArgs &a, int elem_bytes, hipStream_t s);
 hipError_t launch_attention_bf16(const AttnArgs &a, const AttnPlan &p, bool dma, hipStream_t s);
@@ -22,9 +22,9 @@ hipError_t launch_attention_f32(const AttnArgs &a, const AttnPlan &p, bool dma, 
 hipError_t launch_attention_bf16_int8(const AttnArgs &a, const AttnPlan &p, bool dma, hipStream_t s);
 hipError_t launch_attention_f32_int8(const AttnArgs &a, const AttnPlan &p, bool dma, hipStream_t s);
 
-// The item that a run begins and does not finish: sequence s, row tile r, key head h, in
-// `pieces` runs (0: there is none).
-struct PlanDesc { int32_t pieces, r, h, pad; int64_t s; };
+// The item that a run begins and does not finish: row tile r of a sequence whose rows (of
+// tokens and heads) begin at token `first`, key head h, in `pieces` runs (0: there is none).
+struct PlanDesc { int32_t pieces, r, h; uint32_t rows; int64_t first; };
 
 // The workspace: descriptors of the runs, then [slot][row] of maximum and sum, then the
 // weighted sums [slot][32 rows][32 features][4][lane] of 4 features each; two slots a run.

@@ -26,8 +26,9 @@
 //
 // What a row does not see must not touch it: keys and values of no position are zeros,
 // products that a row does not see are minus infinity before the maximum, and a tile at
-// the edge of what its rows see is looked through for values that are not finite, which
-// then go their own way (weight zero times infinity would be NaN).
+// the edge of what its rows see is looked through for values that are not finite: those
+// become zeros there (weight zero times infinity would be NaN), and the rows that do see
+// them get the infinity afterwards.
 //
 // Work: `items` are (sequence, rows, key head).  Where there are many, a workgroup takes
 // one, the longest first, neighbours in the grid on other key heads (an XCD, every 8th
@@ -35,8 +36,11 @@
 // items in a row are cut into equal runs, one for each workgroup: a run's whole items are
 // finished, the others' sums go to the workspace and are joined by a second launch in the
 // order of the tiles.  The lengths are on the device: each workgroup adds them up itself.
-// One thread then reads an item's lengths and tells the others, so that a workgroup stays
-// together and in bounds whatever is in those arrays, were they to change under it.
+// A run's tiles are one stream, across its items: wavefront 0 looks up the rows of the tile
+// after next (and the next item, when one ends), which all need a tile later, so that the
+// fetches never wait for it.  It alone reads the lengths, and the others go by what it
+// leaves in LDS: a workgroup stays together and in bounds whatever is in those arrays, were
+// they to change under it.
 #pragma once
 
 #include <hip/hip_runtime.h>
@@ -78,11 +82,17 @@ __device__ __forceinline__ f32x16 product(u32x4 a, u32x4 b, f32x16 c) {
     }
 }
 
+template <int ES> struct Bits { typedef uint32_t T; };
+template <> struct Bits<2> { typedef uint16_t T; };
 __device__ __forceinline__ int uniform(int v) { return __builtin_amdgcn_readfirstlane(v); }
 
 // An item, and the part of its tiles that a run has; pieces: runs from this one to the
 // item's last.  s < 0: none.
 struct Item { int64_t s; Sequence q; Span sp; int r, h, k0, k1, pieces; };
+
+// A tile of a run: its rows that hold keys, the position of the first, its item's place in
+// a ring (-1: there is none), whether it is the first and the last of the item's part.
+struct Tile { uint64_t rows; int64_t first; int item, begins, ends, pad; };
 
 // Byte permutation of a row of K and of V in LDS (XOR with the byte in the row).
 // K: the 16 rows of a quarter of a read on 16 chunks.  V: the rows of half a read (int8: 0-3
@@ -142,11 +152,12 @@ void attention_tile(AttnArgs a, AttnPlan plan) {
     static_assert(BK <= NTH, "a thread a row of the tile");
     __shared__ __attribute__((aligned(1024))) char smem[2 * STAGE];
     __shared__ int64_t row_at[2][BK];                 // element offsets of the tiles' rows, -1 for none
-    __shared__ float row_scale[2][2][QUANT ? BK : 1];
-    __shared__ uint64_t row_mask[2][(BK + 63) / 64];
+    __shared__ __attribute__((aligned(16))) float row_scale[2][2][QUANT ? BK : 4];
+    __shared__ Tile tiles[4];                          // of this tile and the two after it
+    __shared__ Item items[4];
     __shared__ int64_t scan[NW + 2];
     __shared__ int found[2];
-    __shared__ Item next_item;
+    __shared__ uint64_t odd[QUANT ? 1 : 2][QUANT ? 1 : DP];   // keys whose value of a feature is not finite: up, down
     LDS_PTR(char) lds = (LDS_PTR(char))smem;
     const uint32_t lds_u = (uint32_t)(uintptr_t)lds;
 
@@ -160,10 +171,11 @@ void attention_tile(AttnArgs a, AttnPlan plan) {
 
     auto sequence = [&](int64_t s) { return plan_sequence(c, s); };
     auto span = [&](const Sequence &q, int r) { return plan_span(q, r, G, ROWS, BK, a.window, last_pos); };
+    auto row_tiles = [&](const Sequence &q) { return ((uint32_t)(q.n * G) + ROWS - 1) / ROWS; };      // T G < 2^31
     auto count = [&](const Sequence &q) {
-        const int nr = (int)((q.n * G + ROWS - 1) / ROWS);
+        const uint32_t nr = row_tiles(q);
         int64_t n = 0;
-        for (int r = 0; r < nr; ++r) n += span(q, r).tiles;
+        for (uint32_t r = 0; r < nr; ++r) n += span(q, r).tiles;
         return n;
     };
 
@@ -172,9 +184,9 @@ void attention_tile(AttnArgs a, AttnPlan plan) {
     int W = plan.groups;                                 // runs that have tiles
     int w = blockIdx.x;
     if (plan.stream) {
-        const int64_t q = (c.B + NTH - 1) / NTH, sb = tid * q;
+        const int64_t per = c.B <= NTH ? 1 : (c.B + NTH - 1) / NTH, sb = tid * per;
         int64_t mine = 0;
-        for (int64_t i = sb; i < sb + q && i < c.B; ++i) mine += count(sequence(i));
+        for (int64_t i = sb; i < sb + per && i < c.B; ++i) mine += count(sequence(i));
         int64_t run = mine;
 #pragma unroll
         for (int o = 1; o < 64; o <<= 1) {
@@ -194,12 +206,12 @@ void attention_tile(AttnArgs a, AttnPlan plan) {
         else w = (w & 7) * (W / 8) + (w >> 3);          // runs next to each other on one XCD
         if (tid == 0) plan_desc(a.ws)[w].pieces = 0;
         if (w >= W) return;
-        u = all * w / W;
-        u1 = all * (w + 1) / W;
+        u = W < plan.groups ? w : all * w / plan.groups;
+        u1 = W < plan.groups ? w + 1 : all * (w + 1) / plan.groups;
         int64_t at = (before + run - mine) * c.Hkv;
         if (u >= at && u < (before + run) * c.Hkv) {    // one thread
-            for (int64_t i = sb; i < sb + q && i < c.B; ++i) {
-                const int64_t n = count(sequence(i)) * c.Hkv;
+            for (int64_t i = sb; i < sb + per && i < c.B; ++i) {
+                const int64_t n = per == 1 ? mine * c.Hkv : count(sequence(i)) * c.Hkv;
                 if (u < at + n) {
                     scan[NW] = i;
                     scan[NW + 1] = at;
@@ -209,40 +221,45 @@ void attention_tile(AttnArgs a, AttnPlan plan) {
             }
         }
         __syncthreads();
-        seq = scan[NW];
-        base = scan[NW + 1];
+        seq = uniform(scan[NW]);
+        base = uniform(scan[NW + 1]);
     }
     int stamp = 0;
     if (tid < 2) found[tid] = -1;
 
-    // The next item and the part of its tiles, by one thread (one wavefront).
+    // The next item and the part of its tiles (wavefront 0).
+    bool first_item = true;
     auto find_item = [&]() {
         Item m{};
         m.s = -1;
         if (plan.stream) {
             while (u < u1 && seq < c.B) {
                 const Sequence q = sequence(seq);
-                const int64_t n = count(q);
+                const int64_t n = uniform(count(q));
                 if (u >= base + n * c.Hkv) { base += n * c.Hkv; ++seq; continue; }
-                const int64_t rel = u - base;
-                m.h = (int)(rel / n);
-                int64_t rem = rel - m.h * n;
-                const int nr = (int)((q.n * G + ROWS - 1) / ROWS);
+                int64_t rem = u - base;
+                m.h = (n * c.Hkv) >> 32 ? (int)(rem / n) : (int)((uint32_t)rem / (uint32_t)n);
+                rem -= m.h * n;
+                const uint32_t nr = row_tiles(q);
                 Span sp = span(q, 0);
-                int r = 0;
+                uint32_t r = 0;
                 while (rem >= sp.tiles && r + 1 < nr) { rem -= sp.tiles; sp = span(q, ++r); }
                 const int64_t item_u = u - rem;
-                m.s = seq; m.q = q; m.sp = sp; m.r = r;
+                m.s = seq; m.q = q; m.sp = sp; m.r = (int)r;
                 m.k0 = (int)rem;
                 m.k1 = (int)(u1 - item_u < sp.tiles ? u1 - item_u : sp.tiles);
                 if (m.k1 <= m.k0) { m.s = -1; break; }
-                int64_t to = ((item_u + sp.tiles) * W - 1) / all;               // the run with the item's last tile
-                if (to >= W) to = W - 1;
-                m.pieces = (int)(to - w + 1);
+                m.pieces = 1;
+                if (m.k1 < sp.tiles) {
+                    int64_t to = ((item_u + sp.tiles) * W - 1) / all;           // the run with the item's last tile
+                    if (to >= W) to = W - 1;
+                    m.pieces = (int)(to - w + 1);
+                }
                 u = item_u + m.k1;
                 break;
             }
-        } else {
+        } else if (first_item) {
+            first_item = false;
             const int64_t i = plan.row_tiles - 1 - w / c.Hkv;
             // sequence s has the indices from cu[s] G / ROWS + s on, enough for its rows
             int64_t lo = 0, n = c.B;
@@ -260,402 +277,384 @@ void attention_tile(AttnArgs a, AttnPlan plan) {
             if (s >= 0) {
                 const Sequence q = sequence(s);
                 const int64_t r = i - plan_index(c, s, G, ROWS);
-                if (r >= 0 && r < (q.n * G + ROWS - 1) / ROWS) {
+                if (r >= 0 && r < row_tiles(q)) {
                     m.s = s; m.q = q; m.r = (int)r; m.h = w % c.Hkv;
                     m.sp = span(q, (int)r);
                     m.k1 = m.sp.tiles;
+                    m.pieces = 1;
                 }
             }
         }
         return m;
     };
 
-    while (true) {
-        if (wave == 0) {
+    // ---- rows of a tile: where they are, and which there are (wavefront 0, in the order
+    // of the run's tiles; numbers of tiles and items go round in rings)
+    int64_t ahead_s = -1, ahead_begin = 0, ahead_end = 0, ahead_first = 0;
+    int ahead_k = 0, ahead_k0 = 0, ahead_k1 = 0, ahead_h = 0, ahead_item = -1;
+    struct Look { int32_t id; uint32_t slot; bool want; };
+    auto look = [&](int n) {
+        if (ahead_s >= 0 && ahead_k + 1 < ahead_k1) {
+            ++ahead_k;
+        } else {
             const Item m = find_item();
-            if (lane == 0) next_item = m;
+            ahead_item = (ahead_item + 1) & 3;
+            if (lane == 0) items[ahead_item] = m;
+            ahead_s = uniform(m.s);
+            ahead_begin = uniform(m.sp.begin);
+            ahead_end = uniform(m.sp.end);
+            ahead_first = uniform(m.sp.first);
+            ahead_h = uniform(m.h);
+            ahead_k = ahead_k0 = uniform(m.k0);
+            ahead_k1 = uniform(m.k1);
         }
-        __syncthreads();
-        const int64_t s = uniform(next_item.s);
-        if (s < 0) return;
-        Sequence q;
-        q.first = uniform(next_item.q.first); q.n = uniform(next_item.q.n); q.past = uniform(next_item.q.past);
-        Span sp;
-        sp.pos0 = uniform(next_item.sp.pos0); sp.pos1 = uniform(next_item.sp.pos1);
-        sp.begin = uniform(next_item.sp.begin); sp.end = uniform(next_item.sp.end); sp.first = uniform(next_item.sp.first);
-        sp.tiles = uniform(next_item.sp.tiles); sp.outside = next_item.sp.outside;
-        const int item_r = uniform(next_item.r), item_h = uniform(next_item.h), pieces = uniform(next_item.pieces);
-        const int k0 = uniform(next_item.k0), k1 = uniform(next_item.k1);
-        if (sp.outside && c.bad && tid == 0) *c.bad = 1;
+        Look e{-1, 0, false};
+        const int64_t t0 = (ahead_first + ahead_k) * BK, p = t0 + lane;
+        if (lane < BK && ahead_s >= 0 && p >= ahead_begin && p < ahead_end) {
+            const uint32_t x = (uint32_t)p, i = c.shift >= 0 ? x >> c.shift : x / c.page;
+            e.slot = x - (c.shift >= 0 ? i << c.shift : i * c.page);
+            e.id = c.table[ahead_s * c.ldt + i];       // i < max_pages: p < last_pos
+            e.want = true;
+        }
+        if (lane == 0) {
+            Tile &t = tiles[n & 3];
+            t.first = t0;
+            t.item = ahead_s >= 0 ? ahead_item : -1;
+            t.begins = ahead_k == ahead_k0;
+            t.ends = ahead_k + 1 == ahead_k1;
+        }
+        return e;
+    };
+    auto place = [&](const Look &e, int n) {
+        const bool ok = e.want && e.id >= 0 && e.id < c.n_pages;
+        if (e.want && !ok && c.bad) *c.bad = 1;
+        const uint64_t m = __ballot(ok);
+        if (lane < BK) row_at[n & 1][lane] = ok ? e.id * c.s_page + (int64_t)e.slot * c.s_slot + ahead_h * c.s_head : -1;
+        if (lane == 0) tiles[n & 3].rows = m;
+    };
+    struct Scales { float k, v; };
+    auto scales = [&](const Look &e) {
+        Scales z{0.0f, 0.0f};
+        if (QUANT && e.want && e.id >= 0 && e.id < c.n_pages) {
+            const int64_t i = e.id * c.ss_page + (int64_t)e.slot * c.ss_slot + ahead_h * c.ss_head;
+            z.k = c.ks[i];
+            z.v = c.vs[i];
+        }
+        return z;
+    };
+    auto put_scales = [&](const Scales &z, int n) {
+        if (QUANT && lane < BK) { row_scale[n & 1][0][lane] = z.k; row_scale[n & 1][1][lane] = z.v; }
+    };
+    // ---- a tile's chunks: thread tid has chunk i NTH + tid of K and of V
+    u32x4 kr[DMA ? 1 : LI], vr[DMA ? 1 : LI];
+    auto fetch = [&](int n) __attribute__((always_inline)) {
+        const int st = n & 1;
+#pragma unroll
+        for (int i = 0; i < LI; ++i) {
+            const int k = i * NTH + tid, r = k / CH, ch = k % CH;
+            const int64_t at = row_at[st][r];
+            if constexpr (DMA) {
+                const uint32_t dst = lds_u + st * STAGE + (i * NTH + wave * 64) * 16;
+                const int kc = ch ^ (k_swizzle<RB>(r) >> 4), vc = ch ^ (v_swizzle<LS, RB>(r) >> 4);
+                const char *ka = at >= 0 && kc < chunks ? (const char *)c.kc + at * CS + kc * 16 : (const char *)no_key;
+                const char *va = at >= 0 && vc < chunks ? (const char *)c.vc + at * CS + vc * 16 : (const char *)no_key;
+                asm volatile("s_mov_b32 m0, %1\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, off" :: "v"(ka), "s"(dst) : "memory", "m0");
+                asm volatile("s_mov_b32 m0, %1\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, off" :: "v"(va), "s"(dst + BK * RB) : "memory", "m0");
+            } else {
+                kr[i] = vr[i] = u32x4{0, 0, 0, 0};
+                if (at >= 0 && ch < chunks) {
+                    const char *ka = (const char *)c.kc + at * CS + ch * (16 / ES) * CS;
+                    const char *va = (const char *)c.vc + at * CS + ch * (16 / ES) * CS;
+                    if constexpr (!QUANT) {
+                        kr[i] = *(const u32x4_any *)ka;
+                        vr[i] = *(const u32x4_any *)va;
+                    } else if constexpr (ES == 2) {
+                        const u32x2 x = *(const u32x2_any *)ka, y = *(const u32x2_any *)va;
+                        kr[i][0] = x[0]; kr[i][1] = x[1];
+                        vr[i][0] = y[0]; vr[i][1] = y[1];
+                    } else {
+                        kr[i][0] = *(const u32_any *)ka;
+                        vr[i][0] = *(const u32_any *)va;
+                    }
+                }
+            }
+        }
+    };
+    auto settle = [&](int n) __attribute__((always_inline)) {      // the fetched tile is in LDS, this thread's part
+        if constexpr (DMA) {
+            asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+        } else {
+#pragma unroll
+            for (int i = 0; i < LI; ++i) {
+                const int k = i * NTH + tid, r = k / CH, ch = k % CH;
+                const uint32_t at = (n & 1) * STAGE + r * RB;
+                *(LDS_PTR(u32x4))(lds + at + ((ch * 16) ^ k_swizzle<RB>(r))) = QUANT ? from_int8<ES>(kr[i][0], kr[i][1]) : kr[i];
+                *(LDS_PTR(u32x4))(lds + at + BK * RB + ((ch * 16) ^ v_swizzle<LS, RB>(r))) = QUANT ? from_int8<ES>(vr[i][0], vr[i][1]) : vr[i];
+            }
+        }
+    };
 
-        // ---- this lane's row
-        const uint32_t R = (uint32_t)item_r * ROWS + wr * 32 + col;         // T G < 2^31
-        const bool live = R < (uint32_t)(q.n * G);
+    // ---- the item that a tile belongs to: this lane's row, its query and its sums
+    bool live = false, several = false, whole = false;
+    int item_r = 0, item_h = 0, pieces = 0, slot = 0, head = 0;
+    uint32_t rows = 0;
+    int64_t first = 0, row = 0, hi = 0, lo = 0, see_all = 0, see_from = 0;
+    bool begins_split = false;
+    u32x4 qf[KS];
+    f32x16 o[NB];
+    float mx = -INFINITY, l = 0.0f;
+    auto enter = [&](int i) __attribute__((always_inline)) {
+        const Item &m = items[i];
+        first = uniform(m.q.first);
+        const int64_t past = uniform(m.q.past), pos0 = uniform(m.sp.pos0), pos1 = uniform(m.sp.pos1);
+        rows = (uint32_t)uniform(m.q.n) * G;                                // T G < 2^31
+        item_r = uniform(m.r);
+        item_h = uniform(m.h);
+        pieces = uniform(m.pieces);
+        const int k0 = uniform(m.k0), k1 = uniform(m.k1), n = uniform(m.sp.tiles);
+        whole = k0 == 0 && k1 == n;
+        begins_split = k0 == 0 && k1 < n;
+        slot = 2 * w + (k0 == 0 ? 1 : 0);
+        if (uniform((int)m.sp.outside) && c.bad && tid == 0) *c.bad = 1;
+        const uint32_t R = (uint32_t)item_r * ROWS + wr * 32 + col;
+        live = R < rows;
         const uint32_t tok = live ? R / (uint32_t)G : 0;
-        const int head = item_h * G + (int)(live ? R - tok * G : 0);
-        const int64_t pos = q.past + tok, row = q.first + tok;
-        const int64_t hi = live ? pos : -1;
-        const int64_t lo = pos - a.window + 1;
-        u32x4 qf[KS];
+        head = item_h * G + (int)(live ? R - tok * G : 0);
+        row = first + tok;
+        hi = live ? past + tok : -1;
+        lo = past + tok - a.window + 1;
+        see_all = pos0;                                                     // keys that every row sees
+        see_from = pos1 - a.window + 1;
+        several = pos1 > pos0;
 #pragma unroll
         for (int k = 0; k < KS; ++k) {
-            qf[k] = u32x4{0, 0, 0, 0};
             // the features that a lane's k-th operand of K has
             const int ch = ST == STAGE_INT8 ? (2 * (k / ES) + half) * ES + k % ES : 2 * k + half;
+            qf[k] = u32x4{0, 0, 0, 0};
             if (live && ch < D * ES / 16) qf[k] = *(const u32x4_any *)((const char *)a.Q + (row * a.ldq + (int64_t)head * D) * ES + ch * 16);
         }
-        f32x16 o[NB];
 #pragma unroll
         for (int b = 0; b < NB; ++b)
 #pragma unroll
-            for (int i = 0; i < 16; ++i) o[b][i] = 0.0f;
-        float mx = -INFINITY, l = 0.0f;
+            for (int e = 0; e < 16; ++e) o[b][e] = 0.0f;
+        mx = -INFINITY;
+        l = 0.0f;
+    };
 
-        // ---- rows of a tile: where they are, and which there are
-        const int32_t *table = c.table + s * c.ldt;
-        struct Look { int32_t id; uint32_t slot; bool want; };
-        auto look = [&](int k) {
-            Look e{-1, 0, false};
-            const int64_t p = ((int64_t)sp.first + k) * BK + tid;
-            if (tid < BK && k < k1 && p >= sp.begin && p < sp.end) {
-                const uint32_t x = (uint32_t)p, i = c.shift >= 0 ? x >> c.shift : x / c.page;
-                e.slot = x - (c.shift >= 0 ? i << c.shift : i * c.page);
-                e.id = table[i];                       // i < max_pages: p < last_pos
-                e.want = true;
-            }
-            return e;
-        };
-        auto place = [&](const Look &e, int k) {
-            if (wave * 64 >= BK) return;
-            const bool ok = e.want && e.id >= 0 && e.id < c.n_pages;
-            if (e.want && !ok && c.bad) *c.bad = 1;
-            const uint64_t m = __ballot(ok);
-            if (tid < BK) row_at[k & 1][tid] = ok ? e.id * c.s_page + (int64_t)e.slot * c.s_slot + item_h * c.s_head : -1;
-            if (lane == 0) row_mask[k & 1][wave] = m;
-        };
-        struct Scales { float k, v; };
-        auto scales = [&](const Look &e) {
-            Scales z{0.0f, 0.0f};
-            if (QUANT && e.want && e.id >= 0 && e.id < c.n_pages) {
-                const int64_t i = e.id * c.ss_page + (int64_t)e.slot * c.ss_slot + item_h * c.ss_head;
-                z.k = c.ks[i];
-                z.v = c.vs[i];
-            }
-            return z;
-        };
-        auto put_scales = [&](const Scales &z, int k) {
-            if (QUANT && tid < BK) { row_scale[k & 1][0][tid] = z.k; row_scale[k & 1][1][tid] = z.v; }
-        };
-
-        // ---- a tile's chunks: thread tid has chunk i NTH + tid of K and of V
-        u32x4 kr[DMA ? 1 : LI], vr[DMA ? 1 : LI];
-        auto fetch = [&](int k) __attribute__((always_inline)) {
-            const int st = k & 1;
+    // ---- one tile
+    auto tile = [&](int n) __attribute__((always_inline)) {
+        const int st = n & 1;
+        const int64_t t0 = uniform(tiles[n & 3].first);
+        const uint64_t valid = (uint64_t)uniform((int64_t)tiles[n & 3].rows);
+        const bool edge = t0 + BK - 1 > see_all || t0 < see_from;
+        // values that are not finite, where rows see different keys
+        bool dirty = false;
+        if (!QUANT && edge && several) {
+            bool any = false;
 #pragma unroll
             for (int i = 0; i < LI; ++i) {
-                const int n = i * NTH + tid, r = n / CH, ch = n % CH;
-                const int64_t at = row_at[st][r];
-                if constexpr (DMA) {
-                    const uint32_t dst = lds_u + st * STAGE + (i * NTH + wave * 64) * 16;
-                    const int kc = ch ^ (k_swizzle<RB>(r) >> 4), vc = ch ^ (v_swizzle<LS, RB>(r) >> 4);
-                    const char *ka = at >= 0 && kc < chunks ? (const char *)c.kc + at * CS + kc * 16 : (const char *)no_key;
-                    const char *va = at >= 0 && vc < chunks ? (const char *)c.vc + at * CS + vc * 16 : (const char *)no_key;
-                    asm volatile("s_mov_b32 m0, %1\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, off" :: "v"(ka), "s"(dst) : "memory", "m0");
-                    asm volatile("s_mov_b32 m0, %1\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, off" :: "v"(va), "s"(dst + BK * RB) : "memory", "m0");
-                } else {
-                    kr[i] = vr[i] = u32x4{0, 0, 0, 0};
-                    if (at >= 0 && ch < chunks) {
-                        const char *ka = (const char *)c.kc + at * CS + ch * (16 / ES) * CS;
-                        const char *va = (const char *)c.vc + at * CS + ch * (16 / ES) * CS;
-                        if constexpr (!QUANT) {
-                            kr[i] = *(const u32x4_any *)ka;
-                            vr[i] = *(const u32x4_any *)va;
-                        } else if constexpr (ES == 2) {
-                            const u32x2 x = *(const u32x2_any *)ka, y = *(const u32x2_any *)va;
-                            kr[i][0] = x[0]; kr[i][1] = x[1];
-                            vr[i][0] = y[0]; vr[i][1] = y[1];
-                        } else {
-                            kr[i][0] = *(const u32_any *)ka;
-                            vr[i][0] = *(const u32_any *)va;
-                        }
-                    }
+                const u32x4 x = *(LDS_PTR(u32x4))(lds + st * STAGE + BK * RB + (i * NTH + tid) * 16);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    if (ES == 2) any |= (x[e] & 0x7F80) == 0x7F80 || (x[e] & 0x7F800000) == 0x7F800000;
+                    else any |= (x[e] & 0x7F800000) == 0x7F800000;
                 }
             }
-        };
-        auto settle = [&](int k) __attribute__((always_inline)) {      // the fetched tile is in LDS, this thread's part
-            if constexpr (DMA) {
-                asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
-            } else {
-#pragma unroll
-                for (int i = 0; i < LI; ++i) {
-                    const int n = i * NTH + tid, r = n / CH, ch = n % CH;
-                    const uint32_t at = (k & 1) * STAGE + r * RB;
-                    *(LDS_PTR(u32x4))(lds + at + ((ch * 16) ^ k_swizzle<RB>(r))) = QUANT ? from_int8<ES>(kr[i][0], kr[i][1]) : kr[i];
-                    *(LDS_PTR(u32x4))(lds + at + BK * RB + ((ch * 16) ^ v_swizzle<LS, RB>(r))) = QUANT ? from_int8<ES>(vr[i][0], vr[i][1]) : vr[i];
-                }
-            }
-        };
-
-        // ---- one tile
-        const int64_t see_all = sp.pos0, see_from = sp.pos1 - a.window + 1;      // keys that every row sees
-        auto tile = [&](int k) __attribute__((always_inline)) {
-            const int st = k & 1;
-            const int64_t t0 = ((int64_t)sp.first + k) * BK;
-            const bool edge = t0 + BK - 1 > see_all || t0 < see_from;
-            // values that are not finite, where rows see different keys
-            bool dirty = false;
-            if (!QUANT && edge && sp.pos1 > sp.pos0) {
-                bool any = false;
-#pragma unroll
-                for (int i = 0; i < LI; ++i) {
-                    const u32x4 x = *(LDS_PTR(u32x4))(lds + st * STAGE + BK * RB + (i * NTH + tid) * 16);
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        if (ES == 2) any |= (x[e] & 0x7F80) == 0x7F80 || (x[e] & 0x7F800000) == 0x7F800000;
-                        else any |= (x[e] & 0x7F800000) == 0x7F800000;
-                    }
-                }
-                ++stamp;
-                if (any) found[stamp & 1] = stamp;
-                __syncthreads();
-                dirty = found[stamp & 1] == stamp;
-            }
-            f32x16 x[KB];
-            uint32_t seen[KB];
-            const uint32_t kl = st * STAGE + col * RB, ks = (half * 16) ^ k_swizzle<RB>(col);
-#pragma unroll
-            for (int b = 0; b < KB; ++b)
-#pragma unroll
-                for (int i = 0; i < 16; ++i) x[b][i] = 0.0f;
-#pragma unroll
-            for (int s2 = 0; s2 < KS; s2 += ES / LS)
-#pragma unroll
-                for (int b = 0; b < KB; ++b) {
-                    const u32x4 kf = *(LDS_PTR(u32x4))(lds + kl + b * 32 * RB + ((s2 * LS / ES * 32) ^ ks));
-                    if constexpr (ST != STAGE_INT8) {
-                        x[b] = product<ES>(kf, qf[s2], x[b]);
-                    } else {
-#pragma unroll
-                        for (int e = 0; e < ES; ++e)
-                            x[b] = product<ES>(ES == 2 ? from_int8<ES>(kf[2 * (e & 1)], kf[2 * (e & 1) + 1]) : from_int8<ES>(kf[e], 0), qf[s2 + e], x[b]);
-                    }
-                }
-            if constexpr (QUANT) {
-#pragma unroll
-                for (int b = 0; b < KB; ++b)
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const f32x4 z = *(LDS_PTR(f32x4))(LDS_PTR(float))&row_scale[st][0][b * 32 + 8 * i + 4 * half];
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) x[b][4 * i + e] *= z[e];
-                    }
-            }
-            bool masked = edge;
-#pragma unroll
-            for (int b = 0; b < KB; ++b) {
-                const int n = b * 32;
-                seen[b] = __builtin_amdgcn_readfirstlane((uint32_t)(row_mask[st][n / 64] >> (n & 63)));
-                masked |= seen[b] != 0xFFFFFFFFu;
-            }
-            if (masked) {
-#pragma unroll
-                for (int b = 0; b < KB; ++b) {
-                    const int64_t n = t0 + b * 32, up = hi - n, from = lo - n;
-                    uint32_t m = seen[b];
-                    m &= up >= 31 ? 0xFFFFFFFFu : up < 0 ? 0u : (2u << (int)up) - 1u;
-                    m &= from <= 0 ? 0xFFFFFFFFu : from > 31 ? 0u : 0xFFFFFFFFu << (int)from;
-                    m >>= 4 * half;
-                    seen[b] = m;
-#pragma unroll
-                    for (int i = 0; i < 16; ++i)
-                        if (!(m >> (8 * (i / 4) + i % 4) & 1)) x[b][i] = -INFINITY;
-                }
-            }
-            float top = x[0][0];
-#pragma unroll
-            for (int b = 0; b < KB; ++b)
-#pragma unroll
-                for (int i = 0; i < 16; ++i) top = fmaxf(top, x[b][i]);
-            top = fmaxf(top, other_half(top));
-            const float next = fmaxf(mx, top * cs);
-            const float zero = next == -INFINITY ? 0.0f : next;
-            if (__any(next > mx)) {
-                const float f = __builtin_amdgcn_exp2f(mx - zero);
-                l *= f;
-#pragma unroll
-                for (int b = 0; b < NB; ++b)
-#pragma unroll
-                    for (int i = 0; i < 16; ++i) o[b][i] *= f;
-                mx = next;
-            }
-            float sum = 0.0f;
-#pragma unroll
-            for (int b = 0; b < KB; ++b)
-#pragma unroll
-                for (int i = 0; i < 16; ++i) {
-                    x[b][i] = __builtin_amdgcn_exp2f(__builtin_fmaf(x[b][i], cs, -zero));
-                    sum += x[b][i];
-                }
-            l += sum;
-            if constexpr (QUANT) {
-#pragma unroll
-                for (int b = 0; b < KB; ++b)
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const f32x4 z = *(LDS_PTR(f32x4))(LDS_PTR(float))&row_scale[st][1][b * 32 + 8 * i + 4 * half];
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) {
-                            x[b][4 * i + e] *= z[e];
-                            if (masked && !(seen[b] >> (8 * i + e) & 1)) x[b][4 * i + e] = 0.0f;   // whatever the scale
-                        }
-                    }
-            }
-            const uint32_t vl = st * STAGE + BK * RB;
-            auto values = [&](auto put) __attribute__((always_inline)) {
-                if constexpr (ST == STAGE_INT8) {
-                    // keys 16 s + 8 e + 4 half + i of a step, 4 e + i = (l % 16) / 2
-                    const uint32_t r = (lane & 15) >> 1, key = (r & 3) + (r >> 2) * 8 + 4 * half;
-                    const uint32_t at = vl + key * RB + ((lane >> 4) & 1) * 16 + (lane & 1) * 8, sw = v_swizzle<LS, RB>(key);
-#pragma unroll
-                    for (int b = 0; b < KB; ++b)
-#pragma unroll
-                        for (int s2 = 0; s2 < 2; ++s2) {
-                            u32x4 p[ES / 2];
-                            if constexpr (ES == 2) {
-                                bf16x8 h;
-#pragma unroll
-                                for (int e = 0; e < 8; ++e) h[e] = (__bf16)x[b][8 * s2 + e];
-                                p[0] = __builtin_bit_cast(u32x4, h);
-                            } else {
-#pragma unroll
-                                for (int e = 0; e < 8; ++e) p[e / 4 * (ES / 4)][e % 4] = __float_as_uint(x[b][8 * s2 + e]);
-                            }
-#pragma unroll
-                            for (int d = 0; d < NB; ++d) {
-                                typedef int i32x2 __attribute__((ext_vector_type(2)));
-                                const i32x2 v = __builtin_amdgcn_ds_read_tr8_b64_v2i32((LDS_PTR(i32x2))(lds + at + (b * 32 + s2 * 16) * RB + ((d * 32) ^ sw)));
-                                if constexpr (ES == 2) {
-                                    put(d, b, s2, from_int8<ES>(v[0], v[1]), p[0]);
-                                } else {
-                                    put(d, b, 2 * s2, from_int8<ES>(v[0], 0), p[0]);
-                                    put(d, b, 2 * s2 + 1, from_int8<ES>(v[1], 0), p[ES / 4]);
-                                }
-                            }
-                        }
-                } else if constexpr (ES == 2) {
-                    // keys 16 s + 8 e + 4 half + r of a step, r = (l % 16) / 4; features of 16 lanes
-                    const uint32_t r = (lane & 15) >> 2;
-                    const uint32_t at = vl + (4 * half + r) * RB + ((lane >> 4) & 1) * 32 + (lane & 3) * 8, sw = v_swizzle<LS, RB>(r);
-#pragma unroll
-                    for (int b = 0; b < KB; ++b)
-#pragma unroll
-                        for (int s2 = 0; s2 < 2; ++s2) {
-                            bf16x8 p;
-#pragma unroll
-                            for (int e = 0; e < 8; ++e) p[e] = (__bf16)x[b][8 * s2 + e];
-#pragma unroll
-                            for (int d = 0; d < NB; ++d) {
-                                LDS_PTR(char) v = lds + at + (b * 32 + s2 * 16) * RB + ((d * 64) ^ sw);
-                                const s16x4 v0 = __builtin_amdgcn_ds_read_tr16_b64_v4i16((LDS_PTR(s16x4))v);
-                                const s16x4 v1 = __builtin_amdgcn_ds_read_tr16_b64_v4i16((LDS_PTR(s16x4))(v + 8 * RB));
-                                put(d, b, s2, __builtin_bit_cast(u32x4, __builtin_shufflevector(v0, v1, 0, 1, 2, 3, 4, 5, 6, 7)), __builtin_bit_cast(u32x4, p));
-                            }
-                        }
-                } else {
-#pragma unroll
-                    for (int b = 0; b < KB; ++b)
-#pragma unroll
-                        for (int i = 0; i < 4; ++i)
-#pragma unroll
-                            for (int d = 0; d < NB; ++d) {
-                                u32x4 v, p;
-#pragma unroll
-                                for (int e = 0; e < 4; ++e) {
-                                    const uint32_t n = b * 32 + 8 * i + e + 4 * half;       // (n >> 2) & 1 = half
-                                    v[e] = *(LDS_PTR(uint32_t))(lds + vl + n * RB + ((d * 128 + col * 4) ^ (half << 7)));
-                                    p[e] = __float_as_uint(x[b][4 * i + e]);
-                                }
-                                put(d, b, i, v, p);
-                            }
-                }
-            };
-            if (!dirty) {
-                values([&](int d, int, int, u32x4 v, u32x4 p) __attribute__((always_inline)) { o[d] = product<ES>(v, p, o[d]); });
-            } else {
-                // Finite values as usual; of the others, counts of those that a row sees by
-                // their kind (a NaN is of both), and then the infinity itself.
-#pragma unroll
-                for (int dd = 0; dd < NB; ++dd) {
-                    __builtin_amdgcn_sched_barrier(0);     // one block after another: few registers
-                    f32x16 up, down;
-#pragma unroll
-                    for (int i = 0; i < 16; ++i) up[i] = down[i] = 0.0f;
-                    values([&](int d, int b, int s2, u32x4 v, u32x4 p) __attribute__((always_inline)) {
-                        if (d != dd) return;
-                        __builtin_amdgcn_sched_barrier(0);
-                        u32x4 fine, pos_, neg, one;
-                        if constexpr (ES == 2) {
-#pragma unroll
-                            for (int e = 0; e < 8; ++e) {
-                                const uint32_t x16 = v[e / 2] >> (16 * (e & 1)) & 0xFFFF, sh = 16 * (e & 1);
-                                const bool odd = (x16 & 0x7F80) == 0x7F80, nan = odd && (x16 & 0x7F);
-                                const uint32_t keep = e & 1 ? 0xFFFF : 0;
-                                fine[e / 2] = (fine[e / 2] & keep) | (odd ? 0u : x16) << sh;
-                                pos_[e / 2] = (pos_[e / 2] & keep) | (odd && (nan || !(x16 & 0x8000)) ? 0x3F80u : 0u) << sh;
-                                neg[e / 2] = (neg[e / 2] & keep) | (odd && (nan || (x16 & 0x8000)) ? 0x3F80u : 0u) << sh;
-                                const uint32_t bit = seen[b] >> (16 * s2 + 8 * (e / 4) + e % 4) & 1;
-                                one[e / 2] = (one[e / 2] & keep) | (bit ? 0x3F80u : 0u) << sh;
-                            }
-                        } else {
-#pragma unroll
-                            for (int e = 0; e < 4; ++e) {
-                                const bool odd = (v[e] & 0x7F800000u) == 0x7F800000u, nan = odd && (v[e] & 0x7FFFFFu);
-                                fine[e] = odd ? 0u : v[e];
-                                pos_[e] = odd && (nan || !(v[e] >> 31)) ? 0x3F800000u : 0u;
-                                neg[e] = odd && (nan || (v[e] >> 31)) ? 0x3F800000u : 0u;
-                                one[e] = seen[b] >> (8 * s2 + e) & 1 ? 0x3F800000u : 0u;
-                            }
-                        }
-                        o[dd] = product<ES>(fine, p, o[dd]);
-                        up = product<ES>(pos_, one, up);
-                        down = product<ES>(neg, one, down);
-                    });
-#pragma unroll
-                    for (int i = 0; i < 16; ++i) {
-                        if (up[i] > 0.0f) o[dd][i] += INFINITY;
-                        if (down[i] > 0.0f) o[dd][i] -= INFINITY;
-                    }
-                }
-            }
-        };
-
-        // ---- the tiles
-        {
-            const Look e0 = look(k0), e1 = look(k0 + 1);
-            Scales z = scales(e0);
-            place(e0, k0);
-            place(e1, k0 + 1);
-            put_scales(z, k0);
-            z = scales(e1);
+            ++stamp;
+            if (any) found[stamp & 1] = stamp;
             __syncthreads();
-            fetch(k0);
-            for (int k = k0; k < k1; ++k) {
-                settle(k);
+            dirty = uniform(found[stamp & 1]) == stamp;
+            if (dirty) {
+                // zeros in their place, and for each feature the keys: a NaN is up and down
+                for (int i = tid; i < 2 * DP; i += NTH) odd[i / DP][i % DP] = 0;
                 __syncthreads();
-                const Look e = look(k + 2);
-                if (k + 1 < k1) fetch(k + 1);
-                tile(k);
-                if (k + 1 < k1) {
-                    put_scales(z, k + 1);
-                    place(e, k + 2);
-                    z = scales(e);
+                for (int i = 0; i < LI; ++i) {
+                    const int k = i * NTH + tid, r = k / CH;
+                    const int d = ((k % CH) * 16 ^ v_swizzle<LS, RB>(r)) / ES;
+                    for (int e = 0; e < 16 / ES; ++e) {
+                        typedef typename Bits<ES>::T B;
+                        LDS_PTR(B) v = (LDS_PTR(B))(lds + st * STAGE + BK * RB + k * 16) + e;
+                        const uint32_t y = ES == 2 ? (uint32_t)*v << 16 : (uint32_t)*v;
+                        if ((y & 0x7F800000) != 0x7F800000) continue;
+                        *v = 0;
+                        const bool nan = (y & 0x7FFFFF) != 0;
+                        if (nan || !(y >> 31)) atomicOr((unsigned long long *)&odd[0][d + e], 1ull << r);
+                        if (nan || y >> 31) atomicOr((unsigned long long *)&odd[QUANT ? 0 : 1][d + e], 1ull << r);
+                    }
                 }
+                __syncthreads();
             }
         }
+        f32x16 x[KB];
+        const uint32_t kl = st * STAGE + col * RB, ks = (half * 16) ^ k_swizzle<RB>(col);
+#pragma unroll
+        for (int b = 0; b < KB; ++b)
+#pragma unroll
+            for (int i = 0; i < 16; ++i) x[b][i] = 0.0f;
+#pragma unroll
+        for (int s2 = 0; s2 < KS; s2 += ES / LS)
+#pragma unroll
+            for (int b = 0; b < KB; ++b) {
+                const u32x4 kf = *(LDS_PTR(u32x4))(lds + kl + b * 32 * RB + ((s2 * LS / ES * 32) ^ ks));
+                if constexpr (ST != STAGE_INT8) {
+                    x[b] = product<ES>(kf, qf[s2], x[b]);
+                } else {
+#pragma unroll
+                    for (int e = 0; e < ES; ++e)
+                        x[b] = product<ES>(ES == 2 ? from_int8<ES>(kf[2 * (e & 1)], kf[2 * (e & 1) + 1]) : from_int8<ES>(kf[e], 0), qf[s2 + e], x[b]);
+                }
+            }
+        if constexpr (QUANT) {
+#pragma unroll
+            for (int b = 0; b < KB; ++b)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const f32x4 z = *(LDS_PTR(f32x4))(LDS_PTR(float))&row_scale[st][0][b * 32 + 8 * i + 4 * half];
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) x[b][4 * i + e] *= z[e];
+                }
+        }
+        // the keys that this lane's row sees
+        uint64_t seen = valid;
+        const bool masked = edge || valid != (BK == 64 ? ~0ull : (1ull << (BK & 63)) - 1);
+        if (masked) {
+            const int64_t up = hi - t0, from = lo - t0;
+            seen &= up >= 63 ? ~0ull : up < 0 ? 0ull : (2ull << (int)up) - 1;
+            seen &= from <= 0 ? ~0ull : from > 63 ? 0ull : ~0ull << (int)from;
+            const uint64_t mine = seen >> (4 * half);
+#pragma unroll
+            for (int b = 0; b < KB; ++b)
+#pragma unroll
+                for (int i = 0; i < 16; ++i)
+                    if (!((uint32_t)(mine >> (32 * b)) >> (8 * (i / 4) + i % 4) & 1)) x[b][i] = -INFINITY;
+        }
+        float top = x[0][0];
+#pragma unroll
+        for (int b = 0; b < KB; ++b)
+#pragma unroll
+            for (int i = 0; i < 16; ++i) top = fmaxf(top, x[b][i]);
+        top = fmaxf(top, other_half(top));
+        const float next = fmaxf(mx, top * cs);
+        const float zero = next == -INFINITY ? 0.0f : next;
+        if (__any(next > mx)) {
+            const float f = __builtin_amdgcn_exp2f(mx - zero);
+            l *= f;
+#pragma unroll
+            for (int b = 0; b < NB; ++b)
+#pragma unroll
+                for (int i = 0; i < 16; ++i) o[b][i] *= f;
+            mx = next;
+        }
+        float sum = 0.0f;
+#pragma unroll
+        for (int b = 0; b < KB; ++b)
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+                x[b][i] = __builtin_amdgcn_exp2f(__builtin_fmaf(x[b][i], cs, -zero));
+                sum += x[b][i];
+            }
+        l += sum;
+        if constexpr (QUANT) {
+#pragma unroll
+            for (int b = 0; b < KB; ++b)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const f32x4 z = *(LDS_PTR(f32x4))(LDS_PTR(float))&row_scale[st][1][b * 32 + 8 * i + 4 * half];
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) x[b][4 * i + e] *= z[e];
+                }
+            if (masked) {                                   // whatever the scale
+                const uint64_t mine = seen >> (4 * half);
+#pragma unroll
+                for (int b = 0; b < KB; ++b)
+#pragma unroll
+                    for (int i = 0; i < 16; ++i)
+                        if (!((uint32_t)(mine >> (32 * b)) >> (8 * (i / 4) + i % 4) & 1)) x[b][i] = 0.0f;
+            }
+        }
+        const uint32_t vl = st * STAGE + BK * RB;
+        if constexpr (ST == STAGE_INT8) {
+            // keys 16 s + 8 e + 4 half + i of a step, 4 e + i = (l % 16) / 2
+            const uint32_t r = (lane & 15) >> 1, key = (r & 3) + (r >> 2) * 8 + 4 * half;
+            const uint32_t at = vl + key * RB + ((lane >> 4) & 1) * 16 + (lane & 1) * 8, sw = v_swizzle<LS, RB>(key);
+#pragma unroll
+            for (int b = 0; b < KB; ++b)
+#pragma unroll
+                for (int s2 = 0; s2 < 2; ++s2) {
+                    u32x4 p[ES / 2];
+                    if constexpr (ES == 2) {
+                        bf16x8 h;
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) h[e] = (__bf16)x[b][8 * s2 + e];
+                        p[0] = __builtin_bit_cast(u32x4, h);
+                    } else {
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) p[e / 4 * (ES / 4)][e % 4] = __float_as_uint(x[b][8 * s2 + e]);
+                    }
+#pragma unroll
+                    for (int d = 0; d < NB; ++d) {
+                        typedef int i32x2 __attribute__((ext_vector_type(2)));
+                        const i32x2 v = __builtin_amdgcn_ds_read_tr8_b64_v2i32((LDS_PTR(i32x2))(lds + at + (b * 32 + s2 * 16) * RB + ((d * 32) ^ sw)));
+                        if constexpr (ES == 2) {
+                            o[d] = product<ES>(from_int8<ES>(v[0], v[1]), p[0], o[d]);
+                        } else {
+                            o[d] = product<ES>(from_int8<ES>(v[0], 0), p[0], o[d]);
+                            o[d] = product<ES>(from_int8<ES>(v[1], 0), p[ES / 4], o[d]);
+                        }
+                    }
+                }
+        } else if constexpr (ES == 2) {
+            // keys 16 s + 8 e + 4 half + r of a step, r = (l % 16) / 4; features of 16 lanes
+            const uint32_t r = (lane & 15) >> 2;
+            const uint32_t at = vl + (4 * half + r) * RB + ((lane >> 4) & 1) * 32 + (lane & 3) * 8, sw = v_swizzle<LS, RB>(r);
+#pragma unroll
+            for (int b = 0; b < KB; ++b)
+#pragma unroll
+                for (int s2 = 0; s2 < 2; ++s2) {
+                    bf16x8 p;
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) p[e] = (__bf16)x[b][8 * s2 + e];
+#pragma unroll
+                    for (int d = 0; d < NB; ++d) {
+                        LDS_PTR(char) v = lds + at + (b * 32 + s2 * 16) * RB + ((d * 64) ^ sw);
+                        const s16x4 v0 = __builtin_amdgcn_ds_read_tr16_b64_v4i16((LDS_PTR(s16x4))v);
+                        const s16x4 v1 = __builtin_amdgcn_ds_read_tr16_b64_v4i16((LDS_PTR(s16x4))(v + 8 * RB));
+                        o[d] = product<ES>(__builtin_bit_cast(u32x4, __builtin_shufflevector(v0, v1, 0, 1, 2, 3, 4, 5, 6, 7)), __builtin_bit_cast(u32x4, p), o[d]);
+                    }
+                }
+        } else {
+#pragma unroll
+            for (int b = 0; b < KB; ++b)
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+#pragma unroll
+                    for (int d = 0; d < NB; ++d) {
+                        u32x4 v, p;
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            const uint32_t k = b * 32 + 8 * i + e + 4 * half;           // (k >> 2) & 1 = half
+                            v[e] = *(LDS_PTR(uint32_t))(lds + vl + k * RB + ((d * 128 + col * 4) ^ (half << 7)));
+                            p[e] = __float_as_uint(x[b][4 * i + e]);
+                        }
+                        o[d] = product<ES>(v, p, o[d]);
+                    }
+        }
+        if (dirty) {
+#pragma unroll
+            for (int d = 0; d < NB; ++d)
+#pragma unroll
+                for (int i = 0; i < 16; ++i) {
+                    __builtin_amdgcn_sched_barrier(0);
+                    const int f = d * 32 + 8 * (i / 4) + 4 * half + i % 4;
+                    if (odd[0][QUANT ? 0 : f] & seen) o[d][i] += INFINITY;
+                    if (odd[QUANT ? 0 : 1][QUANT ? 0 : f] & seen) o[d][i] -= INFINITY;
+                }
+        }
+    };
 
+    // ---- the end of an item's part: rows, or sums for the join
+    auto leave = [&]() __attribute__((always_inline)) {
         l += other_half(l);
-        const bool whole = !plan.stream || (k0 == 0 && k1 == sp.tiles);
-        const int slot = plan.stream ? 2 * w + (k0 == 0 ? 1 : 0) : 0;
         const float inv = l == 0.0f ? 0.0f : 1.0f / l;
         if (live) {
 #pragma unroll
@@ -676,12 +675,40 @@ void attention_tile(AttnArgs a, AttnPlan plan) {
                 a.lse[row * a.ldl + head] = l == 0.0f ? -INFINITY : mx * 0.69314718055994530942f + logf(l);
             }
         }
-        if (!plan.stream) return;
-        if (!whole && k0 == 0 && tid == 0) {
-            // this run begins the item: it names the runs that hold the rest
-            plan_desc(a.ws)[w] = PlanDesc{pieces, item_r, item_h, 0, s};
-        }
+        // a run that begins an item names the runs that hold the rest of it
+        if (begins_split && tid == 0) plan_desc(a.ws)[w] = PlanDesc{pieces, item_r, item_h, rows, first};
+    };
+
+    // ---- the tiles
+    Scales z{0.0f, 0.0f};
+    if (wave == 0) {
+        const Look e0 = look(0);
+        place(e0, 0);
+        z = scales(e0);
+        const Look e1 = look(1);
+        put_scales(z, 0);
+        place(e1, 1);
+        z = scales(e1);
+    }
+    __syncthreads();
+    if (uniform(tiles[0].item) < 0) return;
+    fetch(0);
+    for (int n = 0;; ++n) {
+        settle(n);
         __syncthreads();
+        const bool more = uniform(tiles[(n + 1) & 3].item) >= 0;
+        if (more) fetch(n + 1);
+        Look e{-1, 0, false};
+        if (more && wave == 0) e = look(n + 2);
+        if (uniform(tiles[n & 3].begins)) enter(uniform(tiles[n & 3].item));
+        tile(n);
+        if (uniform(tiles[n & 3].ends)) leave();
+        if (!more) return;
+        if (wave == 0) {
+            put_scales(z, n + 1);
+            place(e, n + 2);
+            z = scales(e);
+        }
     }
 }
 
@@ -696,29 +723,45 @@ void attention_join(AttnArgs a, AttnPlan plan) {
     const PlanDesc d = plan_desc(a.ws)[w];
     if (d.pieces == 0) return;
     const int lane = threadIdx.x & 63, i = threadIdx.x >> 6, half = lane >> 5, col = lane & 31;
-    const Sequence q = plan_sequence(a.c, d.s);
     const uint32_t R = (uint32_t)d.r * ROWS + wr * 32 + col;
-    if (R >= (uint32_t)(q.n * a.G)) return;
+    if (R >= d.rows) return;
     const uint32_t tok = R / (uint32_t)a.G;
-    const int64_t row = q.first + tok;
+    const int64_t row = d.first + tok;
     const int head = d.h * a.G + (int)(R - tok * a.G);
     const float *ml = plan_stats(a.ws, plan.groups) + (int64_t)(wr * 32 + col) * 2;
     const f32x4 *sums = plan_sums(a.ws, plan.groups) + ((int64_t)wr * NB + b) * 256 + i * 64 + lane;
     auto slot = [&](int k) { return k == 0 ? (int64_t)2 * w + 1 : (int64_t)2 * (w + k); };
-    float m = -INFINITY;
-#pragma unroll 8
-    for (int k = 0; k < d.pieces; ++k) m = fmaxf(m, ml[slot(k) * ROWS * 2]);
-    const float zero = m == -INFINITY ? 0.0f : m;
-    float l = 0.0f;
+    // four runs at a time, whose loads leave together, in order
+    float m = -INFINITY, l = 0.0f;
     f32x4 v = {0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll 8
-    for (int k = 0; k < d.pieces; ++k) {
-        const float *s = ml + slot(k) * ROWS * 2;
-        const float f = __builtin_amdgcn_exp2f(s[0] - zero);
-        l = __builtin_fmaf(f, s[1], l);
-        const f32x4 x = sums[slot(k) * WR * NB * 256];
+    for (int k0 = 0; k0 < d.pieces; k0 += 4) {
+        float ms[4], ls[4];
+        f32x4 x[4];
 #pragma unroll
-        for (int e = 0; e < 4; ++e) v[e] = __builtin_fmaf(f, x[e], v[e]);
+        for (int k = 0; k < 4; ++k) {
+            ms[k] = -INFINITY;
+            ls[k] = 0.0f;
+            x[k] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+            if (k0 + k < d.pieces) {
+                const float *s = ml + slot(k0 + k) * ROWS * 2;
+                ms[k] = s[0];
+                ls[k] = s[1];
+                x[k] = sums[slot(k0 + k) * WR * NB * 256];
+            }
+        }
+        const float top = fmaxf(fmaxf(fmaxf(m, ms[0]), fmaxf(ms[1], ms[2])), ms[3]), zero = top == -INFINITY ? 0.0f : top;
+        const float f0 = __builtin_amdgcn_exp2f(m - zero);
+        l *= f0;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) v[e] *= f0;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            const float f = __builtin_amdgcn_exp2f(ms[k] - zero);
+            l = __builtin_fmaf(f, ls[k], l);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) v[e] = __builtin_fmaf(f, x[k][e], v[e]);
+        }
+        m = top;
     }
     write_out<ES>(a.O, row * a.ldo + (int64_t)head * a.c.D, b * 32 + 8 * i + 4 * half, a.c.D, v, l == 0.0f, l == 0.0f ? 0.0f : 1.0f / l);
     if (a.lse && b == 0 && i == 0 && half == 0) a.lse[row * a.ldl + head] = l == 0.0f ? -INFINITY : m * 0.69314718055994530942f + logf(l);
