@@ -67,8 +67,18 @@ typedef __bf16 bf16x4 __attribute__((ext_vector_type(4)));
 typedef short s16x4 __attribute__((ext_vector_type(4)));
 typedef short s16x8 __attribute__((ext_vector_type(8)));
 
-// Source of the chunks of no position.
-static __device__ __attribute__((aligned(16))) const uint32_t no_key[4] = {0, 0, 0, 0};
+// Source of the rows of no position (a row is 1 KB at most).
+static __device__ __attribute__((aligned(16))) const uint32_t no_key[256] = {};
+
+// A chunk of 16, or a word of 4 bytes a lane from the cache to LDS, at `lds` + lane * its
+// size: instructions that the compiler does not track; the waits for them are written out
+// below.
+__device__ __forceinline__ void dma16(const char *from, uint32_t lds) {
+    asm volatile("s_mov_b32 m0, %1\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, off" :: "v"(from), "s"(lds) : "memory", "m0");
+}
+__device__ __forceinline__ void dma4(const char *from, uint32_t lds) {
+    asm volatile("s_mov_b32 m0, %1\n\ts_nop 0\n\tglobal_load_lds_dword %0, off" :: "v"(from), "s"(lds) : "memory", "m0");
+}
 
 // A lane's operand: 16 bytes, chunk 2 s + l / 32 of row l % 32 for step s.
 template <int ES>
@@ -151,15 +161,15 @@ void attention_tile(AttnArgs a, AttnPlan plan) {
     constexpr bool QUANT = CS == 1;
     static_assert(BK <= NTH, "a thread a row of the tile");
     __shared__ __attribute__((aligned(1024))) char smem[2 * STAGE];
-    __shared__ int64_t row_at[2][BK];                 // element offsets of the tiles' rows, -1 for none
-    __shared__ __attribute__((aligned(16))) float row_scale[2][2][QUANT ? BK : 4];
+    __shared__ struct { const char *k, *v; } row_at[2][BK];          // where the tiles' rows are
+    __shared__ __attribute__((aligned(256))) float row_scale[2][2][QUANT ? 64 : 4];
     __shared__ Tile tiles[4];                          // of this tile and the two after it
     __shared__ Item items[4];
     __shared__ int64_t scan[NW + 2];
     __shared__ int found[2];
     __shared__ uint64_t odd[QUANT ? 1 : 2][QUANT ? 1 : DP];   // keys whose value of a feature is not finite: up, down
     LDS_PTR(char) lds = (LDS_PTR(char))smem;
-    const uint32_t lds_u = (uint32_t)(uintptr_t)lds;
+    const uint32_t lds_u = (uint32_t)(uintptr_t)lds, scale_u = (uint32_t)(uintptr_t)(LDS_PTR(float))&row_scale[0][0][0];
 
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int wr = wave, half = lane >> 5, col = lane & 31;
@@ -292,7 +302,11 @@ void attention_tile(AttnArgs a, AttnPlan plan) {
     // of the run's tiles; numbers of tiles and items go round in rings)
     int64_t ahead_s = -1, ahead_begin = 0, ahead_end = 0, ahead_first = 0;
     int ahead_k = 0, ahead_k0 = 0, ahead_k1 = 0, ahead_h = 0, ahead_item = -1;
-    struct Look { int32_t id; uint32_t slot; bool want; };
+    // Entries of the table: lane i has entry `window + i` of the sequence's, so that a tile
+    // needs a load only where it leaves them.
+    int32_t entry = -1;
+    int64_t window = 0;
+    const char *scale_k = (const char *)no_key, *scale_v = (const char *)no_key;     // of this lane's row of the last tile looked up
     auto look = [&](int n) {
         if (ahead_s >= 0 && ahead_k + 1 < ahead_k1) {
             ++ahead_k;
@@ -307,82 +321,102 @@ void attention_tile(AttnArgs a, AttnPlan plan) {
             ahead_h = uniform(m.h);
             ahead_k = ahead_k0 = uniform(m.k0);
             ahead_k1 = uniform(m.k1);
+            window = -64;                               // another sequence's
         }
-        Look e{-1, 0, false};
         const int64_t t0 = (ahead_first + ahead_k) * BK, p = t0 + lane;
-        if (lane < BK && ahead_s >= 0 && p >= ahead_begin && p < ahead_end) {
-            const uint32_t x = (uint32_t)p, i = c.shift >= 0 ? x >> c.shift : x / c.page;
-            e.slot = x - (c.shift >= 0 ? i << c.shift : i * c.page);
-            e.id = c.table[ahead_s * c.ldt + i];       // i < max_pages: p < last_pos
-            e.want = true;
+        const bool want = lane < BK && ahead_s >= 0 && p >= ahead_begin && p < ahead_end;
+        // pages of the tile's first and last position that count (0 where there is none)
+        const int64_t lo_p = t0 > ahead_begin ? t0 : ahead_begin, hi_p = t0 + BK < ahead_end ? t0 + BK : ahead_end;
+        const uint32_t x = (uint32_t)p, i = c.shift >= 0 ? x >> c.shift : x / c.page;
+        if (ahead_s >= 0 && hi_p > lo_p) {
+            const uint32_t a0 = (uint32_t)lo_p, a1 = (uint32_t)(hi_p - 1);
+            const int64_t i0 = (uint32_t)uniform((int)(c.shift >= 0 ? a0 >> c.shift : a0 / c.page));
+            const int64_t i1 = (uint32_t)uniform((int)(c.shift >= 0 ? a1 >> c.shift : a1 / c.page));
+            if (i0 < window || i1 >= window + 64) {     // i1 - i0 < BK
+                window = i0;
+                entry = window + lane < c.max_pages ? c.table[ahead_s * c.ldt + window + lane] : -1;
+            }
+        }
+        const int64_t id = __shfl(entry, (int)(i - window) & 63);
+        const uint32_t slot = x - (c.shift >= 0 ? i << c.shift : i * c.page);
+        const bool ok = want && id >= 0 && id < c.n_pages;
+        if (want && !ok && c.bad) *c.bad = 1;
+        const uint64_t m = __ballot(ok);
+        if (lane < BK) {
+            const int64_t at = (id * c.s_page + (int64_t)slot * c.s_slot + ahead_h * c.s_head) * CS;
+            row_at[n & 1][lane].k = ok ? (const char *)c.kc + at : (const char *)no_key;
+            row_at[n & 1][lane].v = ok ? (const char *)c.vc + at : (const char *)no_key;
         }
         if (lane == 0) {
             Tile &t = tiles[n & 3];
+            t.rows = m;
             t.first = t0;
             t.item = ahead_s >= 0 ? ahead_item : -1;
             t.begins = ahead_k == ahead_k0;
             t.ends = ahead_k + 1 == ahead_k1;
         }
-        return e;
-    };
-    auto place = [&](const Look &e, int n) {
-        const bool ok = e.want && e.id >= 0 && e.id < c.n_pages;
-        if (e.want && !ok && c.bad) *c.bad = 1;
-        const uint64_t m = __ballot(ok);
-        if (lane < BK) row_at[n & 1][lane] = ok ? e.id * c.s_page + (int64_t)e.slot * c.s_slot + ahead_h * c.s_head : -1;
-        if (lane == 0) tiles[n & 3].rows = m;
-    };
-    struct Scales { float k, v; };
-    auto scales = [&](const Look &e) {
-        Scales z{0.0f, 0.0f};
-        if (QUANT && e.want && e.id >= 0 && e.id < c.n_pages) {
-            const int64_t i = e.id * c.ss_page + (int64_t)e.slot * c.ss_slot + ahead_h * c.ss_head;
-            z.k = c.ks[i];
-            z.v = c.vs[i];
+        if (QUANT) {
+            const int64_t at = id * c.ss_page + (int64_t)slot * c.ss_slot + ahead_h * c.ss_head;
+            scale_k = ok ? (const char *)(c.ks + at) : (const char *)no_key;
+            scale_v = ok ? (const char *)(c.vs + at) : (const char *)no_key;
         }
-        return z;
     };
-    auto put_scales = [&](const Scales &z, int n) {
-        if (QUANT && lane < BK) { row_scale[n & 1][0][lane] = z.k; row_scale[n & 1][1][lane] = z.v; }
-    };
+
     // ---- a tile's chunks: thread tid has chunk i NTH + tid of K and of V
     u32x4 kr[DMA ? 1 : LI], vr[DMA ? 1 : LI];
+    float scale_kr = 0.0f, scale_vr = 0.0f;
     auto fetch = [&](int n) __attribute__((always_inline)) {
         const int st = n & 1;
+        const char *ka[LI], *va[LI];
+#pragma unroll
+        for (int i = 0; i < LI; ++i) {
+            const int r = (i * NTH + tid) / CH;
+            ka[i] = row_at[st][r].k;
+            va[i] = row_at[st][r].v;
+        }
 #pragma unroll
         for (int i = 0; i < LI; ++i) {
             const int k = i * NTH + tid, r = k / CH, ch = k % CH;
-            const int64_t at = row_at[st][r];
             if constexpr (DMA) {
                 const uint32_t dst = lds_u + st * STAGE + (i * NTH + wave * 64) * 16;
                 const int kc = ch ^ (k_swizzle<RB>(r) >> 4), vc = ch ^ (v_swizzle<LS, RB>(r) >> 4);
-                const char *ka = at >= 0 && kc < chunks ? (const char *)c.kc + at * CS + kc * 16 : (const char *)no_key;
-                const char *va = at >= 0 && vc < chunks ? (const char *)c.vc + at * CS + vc * 16 : (const char *)no_key;
-                asm volatile("s_mov_b32 m0, %1\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, off" :: "v"(ka), "s"(dst) : "memory", "m0");
-                asm volatile("s_mov_b32 m0, %1\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, off" :: "v"(va), "s"(dst + BK * RB) : "memory", "m0");
+                dma16(kc < chunks ? ka[i] + kc * 16 : (const char *)no_key, dst);
+                dma16(vc < chunks ? va[i] + vc * 16 : (const char *)no_key, dst + BK * RB);
             } else {
                 kr[i] = vr[i] = u32x4{0, 0, 0, 0};
-                if (at >= 0 && ch < chunks) {
-                    const char *ka = (const char *)c.kc + at * CS + ch * (16 / ES) * CS;
-                    const char *va = (const char *)c.vc + at * CS + ch * (16 / ES) * CS;
+                if (ch < chunks) {
+                    const char *kp = ka[i] + ch * (16 / ES) * CS, *vp = va[i] + ch * (16 / ES) * CS;
                     if constexpr (!QUANT) {
-                        kr[i] = *(const u32x4_any *)ka;
-                        vr[i] = *(const u32x4_any *)va;
+                        kr[i] = *(const u32x4_any *)kp;
+                        vr[i] = *(const u32x4_any *)vp;
                     } else if constexpr (ES == 2) {
-                        const u32x2 x = *(const u32x2_any *)ka, y = *(const u32x2_any *)va;
+                        const u32x2 x = *(const u32x2_any *)kp, y = *(const u32x2_any *)vp;
                         kr[i][0] = x[0]; kr[i][1] = x[1];
                         vr[i][0] = y[0]; vr[i][1] = y[1];
                     } else {
-                        kr[i][0] = *(const u32_any *)ka;
-                        vr[i][0] = *(const u32_any *)va;
+                        kr[i][0] = *(const u32_any *)kp;
+                        vr[i][0] = *(const u32_any *)vp;
                     }
                 }
             }
         }
+        if (QUANT && wave == 0) {          // the scales of the tile that was looked up last, in lane order
+            if constexpr (DMA) {
+                dma4(scale_k, scale_u + st * 512);
+                dma4(scale_v, scale_u + st * 512 + 256);
+            } else {
+                scale_kr = *(const float *)scale_k;
+                scale_vr = *(const float *)scale_v;
+            }
+        }
     };
-    auto settle = [&](int n) __attribute__((always_inline)) {      // the fetched tile is in LDS, this thread's part
+    // The fetched tile is in LDS, this thread's part; DMA: all but the last `later` of the
+    // instructions have done their work.
+    auto settle = [&](int n, bool later) __attribute__((always_inline)) {
         if constexpr (DMA) {
-            asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+            constexpr int LATER = 2 * LI + (QUANT ? 2 : 0);          // of one fetch; the counter holds 63
+            if (later) asm volatile("s_waitcnt vmcnt(%0)" :: "n"(LATER < 63 ? LATER : 63) : "memory");
+            else asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
         } else {
 #pragma unroll
             for (int i = 0; i < LI; ++i) {
@@ -390,6 +424,10 @@ void attention_tile(AttnArgs a, AttnPlan plan) {
                 const uint32_t at = (n & 1) * STAGE + r * RB;
                 *(LDS_PTR(u32x4))(lds + at + ((ch * 16) ^ k_swizzle<RB>(r))) = QUANT ? from_int8<ES>(kr[i][0], kr[i][1]) : kr[i];
                 *(LDS_PTR(u32x4))(lds + at + BK * RB + ((ch * 16) ^ v_swizzle<LS, RB>(r))) = QUANT ? from_int8<ES>(vr[i][0], vr[i][1]) : vr[i];
+            }
+            if (QUANT && wave == 0) {
+                row_scale[n & 1][0][QUANT ? lane : 0] = scale_kr;
+                row_scale[n & 1][1][QUANT ? lane : 0] = scale_vr;
             }
         }
     };
@@ -679,36 +717,45 @@ void attention_tile(AttnArgs a, AttnPlan plan) {
         if (begins_split && tid == 0) plan_desc(a.ws)[w] = PlanDesc{pieces, item_r, item_h, rows, first};
     };
 
-    // ---- the tiles
-    Scales z{0.0f, 0.0f};
-    if (wave == 0) {
-        const Look e0 = look(0);
-        place(e0, 0);
-        z = scales(e0);
-        const Look e1 = look(1);
-        put_scales(z, 0);
-        place(e1, 1);
-        z = scales(e1);
-    }
+    // ---- the tiles.  Each is looked up before the fetch of the one before it, whose scales
+    // are then no longer needed.
+    if (wave == 0) look(0);
     __syncthreads();
     if (uniform(tiles[0].item) < 0) return;
     fetch(0);
+    if (wave == 0) look(1);
+    if constexpr (WR == 1 && DMA) {
+        // A wavefront by itself: the next tile's fetch leaves before this one's is there, as
+        // soon as its place in LDS is free.
+        for (int n = 0;; ++n) {
+            __syncthreads();                            // of one wavefront: its LDS reads are done
+            asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+            const bool more = uniform(tiles[(n + 1) & 3].item) >= 0;
+            if (more) {
+                fetch(n + 1);
+                settle(n, true);
+                look(n + 2);
+            } else {
+                settle(n, false);
+            }
+            if (uniform(tiles[n & 3].begins)) enter(uniform(tiles[n & 3].item));
+            tile(n);
+            if (uniform(tiles[n & 3].ends)) leave();
+            if (!more) return;
+        }
+    }
     for (int n = 0;; ++n) {
-        settle(n);
+        settle(n, false);
         __syncthreads();
         const bool more = uniform(tiles[(n + 1) & 3].item) >= 0;
-        if (more) fetch(n + 1);
-        Look e{-1, 0, false};
-        if (more && wave == 0) e = look(n + 2);
+        if (more) {
+            fetch(n + 1);
+            if (wave == 0) look(n + 2);
+        }
         if (uniform(tiles[n & 3].begins)) enter(uniform(tiles[n & 3].item));
         tile(n);
         if (uniform(tiles[n & 3].ends)) leave();
         if (!more) return;
-        if (wave == 0) {
-            put_scales(z, n + 1);
-            place(e, n + 2);
-            z = scales(e);
-        }
     }
 }
 
