@@ -80,6 +80,16 @@ __device__ __forceinline__ void dma4(const char *from, uint32_t lds) {
     asm volatile("s_mov_b32 m0, %1\n\ts_nop 0\n\tglobal_load_lds_dword %0, off" :: "v"(from), "s"(lds) : "memory", "m0");
 }
 
+// The WR wavefronts meet: what each wrote to LDS before is there after it.  Written out,
+// since hipcc leaves out the wait for LDS before a __syncthreads() that comes right behind
+// a wait in inline assembly: rows looked up by wavefront 0 were then read by the others
+// before they were there.
+template <int WR>
+__device__ __forceinline__ void meet() {
+    if constexpr (WR > 1) asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
+    else asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+}
+
 // A lane's operand: 16 bytes, chunk 2 s + l / 32 of row l % 32 for step s.
 template <int ES>
 __device__ __forceinline__ f32x16 product(u32x4 a, u32x4 b, f32x16 c) {
@@ -205,7 +215,7 @@ void attention_tile(AttnArgs a, AttnPlan plan) {
         }
         if (lane == 63) scan[wave] = run;
         if (tid == 0) scan[NW] = c.B;
-        __syncthreads();
+        meet<WR>();
         int64_t before = 0;
         for (int i = 0; i < NW; ++i) {
             if (i < wave) before += scan[i];
@@ -230,7 +240,7 @@ void attention_tile(AttnArgs a, AttnPlan plan) {
                 at += n;
             }
         }
-        __syncthreads();
+        meet<WR>();
         seq = uniform(scan[NW]);
         base = uniform(scan[NW + 1]);
     }
@@ -335,6 +345,8 @@ void attention_tile(AttnArgs a, AttnPlan plan) {
             if (i0 < window || i1 >= window + 64) {     // i1 - i0 < BK
                 window = i0;
                 entry = window + lane < c.max_pages ? c.table[ahead_s * c.ldt + window + lane] : -1;
+                // waited for here, once in 64 pages, and not by every use below
+                asm volatile("s_waitcnt vmcnt(0)" : "+v"(entry) :: "memory");
             }
         }
         const int64_t id = __shfl(entry, (int)(i - window) & 63);
@@ -500,12 +512,12 @@ void attention_tile(AttnArgs a, AttnPlan plan) {
             }
             ++stamp;
             if (any) found[stamp & 1] = stamp;
-            __syncthreads();
+            meet<WR>();
             dirty = uniform(found[stamp & 1]) == stamp;
             if (dirty) {
                 // zeros in their place, and for each feature the keys: a NaN is up and down
                 for (int i = tid; i < 2 * DP; i += NTH) odd[i / DP][i % DP] = 0;
-                __syncthreads();
+                meet<WR>();
                 for (int i = 0; i < LI; ++i) {
                     const int k = i * NTH + tid, r = k / CH;
                     const int d = ((k % CH) * 16 ^ v_swizzle<LS, RB>(r)) / ES;
@@ -520,7 +532,7 @@ void attention_tile(AttnArgs a, AttnPlan plan) {
                         if (nan || y >> 31) atomicOr((unsigned long long *)&odd[QUANT ? 0 : 1][d + e], 1ull << r);
                     }
                 }
-                __syncthreads();
+                meet<WR>();
             }
         }
         f32x16 x[KB];
@@ -717,41 +729,23 @@ void attention_tile(AttnArgs a, AttnPlan plan) {
         if (begins_split && tid == 0) plan_desc(a.ws)[w] = PlanDesc{pieces, item_r, item_h, rows, first};
     };
 
-    // ---- the tiles.  Each is looked up before the fetch of the one before it, whose scales
-    // are then no longer needed.
-    if (wave == 0) look(0);
-    __syncthreads();
-    if (uniform(tiles[0].item) < 0) return;
-    fetch(0);
-    if (wave == 0) look(1);
-    if constexpr (WR == 1 && DMA) {
-        // A wavefront by itself: the next tile's fetch leaves before this one's is there, as
-        // soon as its place in LDS is free.
-        for (int n = 0;; ++n) {
-            __syncthreads();                            // of one wavefront: its LDS reads are done
-            asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
-            const bool more = uniform(tiles[(n + 1) & 3].item) >= 0;
-            if (more) {
-                fetch(n + 1);
-                settle(n, true);
-                look(n + 2);
-            } else {
-                settle(n, false);
-            }
-            if (uniform(tiles[n & 3].begins)) enter(uniform(tiles[n & 3].item));
-            tile(n);
-            if (uniform(tiles[n & 3].ends)) leave();
-            if (!more) return;
+    // ---- the tiles.  In one loop, so that each step is there once (a launch begins without
+    // instructions in the caches): tile n + 2 is looked up, tile n + 1 fetched, tile n worked
+    // on.  A wavefront by itself (ALONE) fetches the next tile before this one is there, as
+    // soon as its place in LDS is free; four wait for theirs first, and then for each other.
+    constexpr bool ALONE = WR == 1 && DMA;
+    for (int n = -2;; ++n) {
+        if (!ALONE && n >= 0) settle(n, false);
+        meet<WR>();                                     // also: this wavefront's reads of the last tile are done
+        bool more = true;
+        if (n >= -1) {
+            more = uniform(tiles[(n + 1) & 3].item) >= 0;
+            if (n < 0 && !more) return;
+            if (more) fetch(n + 1);
         }
-    }
-    for (int n = 0;; ++n) {
-        settle(n, false);
-        __syncthreads();
-        const bool more = uniform(tiles[(n + 1) & 3].item) >= 0;
-        if (more) {
-            fetch(n + 1);
-            if (wave == 0) look(n + 2);
-        }
+        if (ALONE && n >= 0) settle(n, more);
+        if (more && wave == 0) look(n + 2);
+        if (n < 0) continue;
         if (uniform(tiles[n & 3].begins)) enter(uniform(tiles[n & 3].item));
         tile(n);
         if (uniform(tiles[n & 3].ends)) leave();
