@@ -11,9 +11,14 @@ namespace {
 
 constexpr int64_t MAX_TILE_D = 256;     // largest head of the matrix-core form
 
-// What the matrix-core form takes: heads of whole 16-byte chunks (of whole 8 values in
-// 8 bits), rows of a call that 32 bits count.
-bool tile_ok(int64_t T, int64_t G, int64_t D) { return D <= MAX_TILE_D && D % 8 == 0 && T * G <= INT32_MAX; }
+// What the matrix-core form takes: heads of whole 16-byte chunks (of whole 8 values in 8
+// bits); rows, positions and windows that 32 bits hold, with room for their sums.
+constexpr int64_t FAR = PLAN_FAR;
+bool tile_ok(int64_t T, int64_t B, int64_t G, int64_t D) { return D <= MAX_TILE_D && D % 8 == 0 && T < FAR && B < FAR && T * G < INT32_MAX - 128; }
+bool positions_ok(const AttnArgs &a) {
+    const int64_t last = a.c.max_pages * (int64_t)a.c.page;
+    return a.c.max_pages < FAR && last < FAR && (a.window >= 2 * FAR || last + a.window <= FAR);
+}
 
 // A cache whose rows lie at multiples of 16 bytes goes to LDS without a stop.
 bool dma_ok(const AttnArgs &a, int es) {
@@ -41,7 +46,7 @@ AttnPlan attention_plan(int64_t T, int64_t B, int64_t Hkv, int32_t G, int64_t D,
 }
 
 size_t attention_workspace(int64_t T, int64_t B, int64_t Hq, int64_t Hkv, int64_t D) {
-    if (T == 0 || B == 0 || !tile_ok(T, Hq / Hkv, D)) return 0;
+    if (T == 0 || B == 0 || !tile_ok(T, B, Hq / Hkv, D)) return 0;
     // the most runs that any type of cache has
     const AttnPlan p = attention_plan(T, B, Hkv, (int32_t)(Hq / Hkv), D, 2, true);
     if (!p.stream) return 0;
@@ -50,8 +55,12 @@ size_t attention_workspace(int64_t T, int64_t B, int64_t Hq, int64_t Hkv, int64_
 }
 
 hipError_t launch_kv_attention(const AttnArgs &a, int es, hipStream_t s) {
-    if (!tile_ok(a.c.T, a.G, a.c.D)) return launch_attention_any(a, es, s);
-    const AttnPlan p = attention_plan(a.c.T, a.c.B, a.c.Hkv, a.G, a.c.D, es, a.c.ks != nullptr);
+    if (!tile_ok(a.c.T, a.c.B, a.G, a.c.D) || !positions_ok(a)) return launch_attention_any(a, es, s);
+    AttnPlan p = attention_plan(a.c.T, a.c.B, a.c.Hkv, a.G, a.c.D, es, a.c.ks != nullptr);
+    p.last_pos = (int32_t)(a.c.max_pages * (int64_t)a.c.page);
+    p.window = (int32_t)(a.window < 2 * FAR ? a.window : 2 * FAR);
+    // units of a run: tiles of 32 keys and changes of items, counted in 32 bits
+    if (p.stream && p.row_tiles * (p.last_pos / 32 + 8) * a.c.Hkv >= INT32_MAX) p.stream = 0;
     if (!p.stream && p.row_tiles * a.c.Hkv > (1 << 23)) return launch_attention_any(a, es, s);   // more than one launch holds
     const bool dma = dma_ok(a, es);
     if (a.c.ks) return es == 2 ? launch_attention_bf16_int8(a, p, dma, s) : launch_attention_f32_int8(a, p, dma, s);

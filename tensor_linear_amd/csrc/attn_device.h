@@ -68,43 +68,48 @@ __device__ __forceinline__ plan_f32x4 *plan_sums(void *ws, int W) {
     return (plan_f32x4 *)((char *)ws + plan_desc_bytes(W) + plan_stats_bytes(W));
 }
 
+// 32 bits hold what the matrix-core form takes (attn.cpp): rows of tokens and heads,
+// positions of the table below FAR, tokens fewer than FAR, windows of 2 FAR (none) or so
+// short that a row FAR positions on sees nothing of the table.  So a past beyond FAR may be
+// taken for FAR, and one before -FAR for -FAR.
+constexpr int FAR = PLAN_FAR;
+
 // A sequence's first row and number of rows among the call's T, and the position of the
 // first of them.  Rows outside the call do not count, whatever cu says.
-struct Sequence { int64_t first, n, past; };
-__device__ __forceinline__ int64_t plan_clamp(int64_t v, int64_t T) { return v < 0 ? 0 : v > T ? T : v; }
-__device__ __forceinline__ Sequence plan_sequence(const CacheArgs &c, int64_t s) {
-    const int64_t from = c.cu[s], to = c.cu[s + 1];
+struct Sequence { int first, n, past; };
+__device__ __forceinline__ int plan_clamp(int v, int T) { return v < 0 ? 0 : v > T ? T : v; }
+__device__ __forceinline__ Sequence plan_sequence(const CacheArgs &c, int s) {
+    const int from = c.cu[s], to = c.cu[s + 1], past = c.past[s], T = (int)c.T;
     Sequence q;
-    q.first = plan_clamp(from, c.T);
-    const int64_t end = plan_clamp(to, c.T);
+    q.first = plan_clamp(from, T);
+    const int end = plan_clamp(to, T);
     q.n = end > q.first ? end - q.first : 0;
-    q.past = (int64_t)c.past[s] + (q.first - from);
+    q.past = past < -FAR ? -FAR : past > FAR ? FAR : past;
+    if (from < 0) q.past = from < -FAR || q.past > FAR + from ? FAR : q.past - from;   // rows before the call's first
     return q;
 }
 
 // Index of a sequence's first row tile where sequence s begins at cu[s] G / ROWS + s:
 // floor(x / ROWS) + 1 - floor(y / ROWS) tiles are enough for the rows y .. x - 1.
-__device__ __forceinline__ int64_t plan_index(const CacheArgs &c, int64_t s, int G, int ROWS) {
-    return plan_clamp(c.cu[s], c.T) * G / ROWS + s;
+__device__ __forceinline__ int plan_index(const CacheArgs &c, int s, int G, int ROWS) {
+    return plan_clamp(c.cu[s], (int)c.T) * G / ROWS + s;
 }
 
 // Row tile r of a sequence: the positions of its first and last row, the positions that
 // its rows see (those of the table), and the tiles of BK that hold them; at least one, so
 // that rows that see nothing are written.
-struct Span { int64_t pos0, pos1, begin, end, first; int tiles; bool outside; };
-__device__ __forceinline__ Span plan_span(const Sequence &q, int r, int G, int ROWS, int BK, int64_t window, int64_t last_pos) {
+struct Span { int pos0, pos1, begin, end, first, tiles; };
+__device__ __forceinline__ Span plan_span(const Sequence &q, int r, int G, int ROWS, int BK, int window, int last_pos) {
     Span s;
-    const uint32_t row = (uint32_t)r * ROWS, rows = (uint32_t)(q.n * G - row < ROWS ? q.n * G - row : ROWS);
-    s.pos0 = q.past + row / G;
-    s.pos1 = q.past + (row + rows - 1) / G;
-    s.begin = s.pos0 - window + 1;
-    if (s.begin < 0) s.begin = 0;
+    const uint32_t row = (uint32_t)r * ROWS, all = (uint32_t)(q.n * G), rows = all - row < (uint32_t)ROWS ? all - row : ROWS;
+    s.pos0 = q.past + (int)(row / (uint32_t)G);
+    s.pos1 = q.past + (int)((row + rows - 1) / (uint32_t)G);
+    s.begin = s.pos0 - window + 1 > 0 ? s.pos0 - window + 1 : 0;
     s.end = s.pos1 + 1 < last_pos ? s.pos1 + 1 : last_pos;
     if (s.end < 0) s.end = 0;
-    s.outside = s.pos0 < 0 || s.pos1 >= last_pos;
     s.first = s.begin / BK;
-    const int64_t n = (s.end + BK - 1) / BK - s.first;
-    s.tiles = n > 0 ? (int)n : 1;
+    const int n = (s.end + BK - 1) / BK - s.first;
+    s.tiles = n > 0 ? n : 1;
     return s;
 }
 

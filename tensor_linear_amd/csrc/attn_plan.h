@@ -8,9 +8,12 @@
 
 namespace tpl {
 
+constexpr int32_t PLAN_FAR = 1 << 29;   // what positions and counts of tokens are below
+
 // stream: the tiles of all items in `groups` equal runs; else a workgroup for each of
 // the row_tiles * Hkv items.  few: 32 rows a workgroup, else 128.
-struct AttnPlan { int32_t stream, few, groups; int64_t row_tiles; };
+// last_pos: positions of the table; window: 2 PLAN_FAR for none.
+struct AttnPlan { int32_t stream, few, groups, last_pos, window; int64_t row_tiles; };
 
 // The plan of a call of these sizes and types (the lengths are on the device: T, B and the
 // heads are all that the host knows).
@@ -24,7 +27,7 @@ hipError_t launch_attention_f32_int8(const AttnArgs &a, const AttnPlan &p, bool 
 
 // The item that a run begins and does not finish: row tile r of a sequence whose rows (of
 // tokens and heads) begin at token `first`, key head h, in `pieces` runs (0: there is none).
-struct PlanDesc { int32_t pieces, r, h; uint32_t rows; int64_t first; };
+struct PlanDesc { int32_t pieces, r, h, rows, first, pad[3]; };
 
 // The workspace: descriptors of the runs, then [slot][row] of maximum and sum, then the
 // weighted sums [slot][32 rows][32 features][4][lane] of 4 features each; two slots a run.

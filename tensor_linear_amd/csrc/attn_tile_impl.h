@@ -102,17 +102,25 @@ __device__ __forceinline__ f32x16 product(u32x4 a, u32x4 b, f32x16 c) {
     }
 }
 
+// A value that all lanes have, as a scalar.
+__device__ __forceinline__ uint64_t uniform64(uint64_t v) {
+    return (uint64_t)(uint32_t)__builtin_amdgcn_readfirstlane((uint32_t)(v >> 32)) << 32 | (uint32_t)__builtin_amdgcn_readfirstlane((uint32_t)v);
+}
 template <int ES> struct Bits { typedef uint32_t T; };
 template <> struct Bits<2> { typedef uint16_t T; };
 __device__ __forceinline__ int uniform(int v) { return __builtin_amdgcn_readfirstlane(v); }
 
 // An item, and the part of its tiles that a run has; pieces: runs from this one to the
 // item's last.  s < 0: none.
-struct Item { int64_t s; Sequence q; Span sp; int r, h, k0, k1, pieces; };
+struct Item { int s; Sequence q; Span sp; int r, h, k0, k1, pieces; };
 
 // A tile of a run: its rows that hold keys, the position of the first, its item's place in
 // a ring (-1: there is none), whether it is the first and the last of the item's part.
-struct Tile { uint64_t rows; int64_t first; int item, begins, ends, pad; };
+struct Tile { uint64_t rows; int first, item, begins, ends; };
+
+// Tiles that the change from one item to the next costs a run in time (a wavefront by
+// itself: the query's loads, the sums' way out, the next item's lengths).
+constexpr int CHANGE = 2;
 
 // Byte permutation of a row of K and of V in LDS (XOR with the byte in the row).
 // K: the 16 rows of a quarter of a read on 16 chunks.  V: the rows of half a read (int8: 0-3
@@ -175,7 +183,7 @@ void attention_tile(AttnArgs a, AttnPlan plan) {
     __shared__ __attribute__((aligned(256))) float row_scale[2][2][QUANT ? 64 : 4];
     __shared__ Tile tiles[4];                          // of this tile and the two after it
     __shared__ Item items[4];
-    __shared__ int64_t scan[NW + 2];
+    __shared__ int scan[NW + 2];
     __shared__ int found[2];
     __shared__ uint64_t odd[QUANT ? 1 : 2][QUANT ? 1 : DP];   // keys whose value of a feature is not finite: up, down
     LDS_PTR(char) lds = (LDS_PTR(char))smem;
@@ -186,52 +194,55 @@ void attention_tile(AttnArgs a, AttnPlan plan) {
     const CacheArgs &c = a.c;
     const int D = c.D, G = a.G;
     const float cs = a.scale * 1.44269504088896340736f;
-    const int64_t last_pos = c.max_pages * (int64_t)c.page;             // positions of the table
+    const int last_pos = plan.last_pos, window_of = plan.window;         // positions of the table; FAR: all
     const int chunks = D * LS / 16;                                     // of a row in LDS that hold features
 
-    auto sequence = [&](int64_t s) { return plan_sequence(c, s); };
-    auto span = [&](const Sequence &q, int r) { return plan_span(q, r, G, ROWS, BK, a.window, last_pos); };
-    auto row_tiles = [&](const Sequence &q) { return ((uint32_t)(q.n * G) + ROWS - 1) / ROWS; };      // T G < 2^31
+    auto sequence = [&](int s) { return plan_sequence(c, s); };
+    auto span = [&](const Sequence &q, int r) { return plan_span(q, r, G, ROWS, BK, window_of, last_pos); };
+    auto row_tiles = [&](const Sequence &q) { return (q.n * G + ROWS - 1) / ROWS; };
+    // units of one head of a sequence: its tiles, and the changes between its items
     auto count = [&](const Sequence &q) {
-        const uint32_t nr = row_tiles(q);
-        int64_t n = 0;
-        for (uint32_t r = 0; r < nr; ++r) n += span(q, r).tiles;
+        const int nr = row_tiles(q);
+        int n = nr * CHANGE;
+        for (int r = 0; r < nr; ++r) n += span(q, r).tiles;
         return n;
     };
 
-    // ---- the run of tiles of this workgroup
-    int64_t all = 0, u = 0, u1 = 0, base = 0, seq = 0;   // units in all, the run [u, u1); the first one of sequence seq
-    int W = plan.groups;                                 // runs that have tiles
+    // ---- the run of units of this workgroup
+    int all = 0, u = 0, u1 = 0, base = 0, seq = 0;       // units in all, the run [u, u1); the first one of sequence seq
+    int W = plan.groups;                                 // runs that have units
     int w = blockIdx.x;
+    const int B = (int)c.B;
     if (plan.stream) {
-        const int64_t per = c.B <= NTH ? 1 : (c.B + NTH - 1) / NTH, sb = tid * per;
-        int64_t mine = 0;
-        for (int64_t i = sb; i < sb + per && i < c.B; ++i) mine += count(sequence(i));
-        int64_t run = mine;
+        const int per = B <= NTH ? 1 : (B + NTH - 1) / NTH, sb = tid * per;
+        int mine = 0;
+        for (int i = sb; i < sb + per && i < B; ++i) mine += count(sequence(i));
+        int run = mine;
 #pragma unroll
         for (int o = 1; o < 64; o <<= 1) {
-            const int64_t v = __shfl_up(run, o);
+            const int v = __shfl_up(run, o);
             if (lane >= o) run += v;
         }
         if (lane == 63) scan[wave] = run;
-        if (tid == 0) scan[NW] = c.B;
+        if (tid == 0) scan[NW] = B;
         meet<WR>();
-        int64_t before = 0;
+        int before = 0;
         for (int i = 0; i < NW; ++i) {
             if (i < wave) before += scan[i];
             all += scan[i];
         }
         all = uniform(all) * c.Hkv;
-        if (all < W) W = (int)all;
+        if (all < W) W = all;
         else w = (w & 7) * (W / 8) + (w >> 3);          // runs next to each other on one XCD
         if (tid == 0) plan_desc(a.ws)[w].pieces = 0;
         if (w >= W) return;
-        u = W < plan.groups ? w : all * w / plan.groups;
-        u1 = W < plan.groups ? w + 1 : all * (w + 1) / plan.groups;
-        int64_t at = (before + run - mine) * c.Hkv;
+        auto cut = [&](int i) { return W < plan.groups ? i : (int)((int64_t)all * i / plan.groups); };
+        u = cut(w);
+        u1 = cut(w + 1);
+        int at = (before + run - mine) * c.Hkv;
         if (u >= at && u < (before + run) * c.Hkv) {    // one thread
-            for (int64_t i = sb; i < sb + per && i < c.B; ++i) {
-                const int64_t n = per == 1 ? mine * c.Hkv : count(sequence(i)) * c.Hkv;
+            for (int i = sb; i < sb + per && i < B; ++i) {
+                const int n = (per == 1 ? mine : count(sequence(i))) * c.Hkv;
                 if (u < at + n) {
                     scan[NW] = i;
                     scan[NW + 1] = at;
@@ -253,53 +264,54 @@ void attention_tile(AttnArgs a, AttnPlan plan) {
         Item m{};
         m.s = -1;
         if (plan.stream) {
-            while (u < u1 && seq < c.B) {
+            while (u < u1 && seq < B) {
                 const Sequence q = sequence(seq);
-                const int64_t n = uniform(count(q));
+                const int n = uniform(count(q));
                 if (u >= base + n * c.Hkv) { base += n * c.Hkv; ++seq; continue; }
-                int64_t rem = u - base;
-                m.h = (n * c.Hkv) >> 32 ? (int)(rem / n) : (int)((uint32_t)rem / (uint32_t)n);
+                int rem = u - base;
+                m.h = (uint32_t)rem / (uint32_t)n;
                 rem -= m.h * n;
-                const uint32_t nr = row_tiles(q);
+                const int nr = row_tiles(q);
                 Span sp = span(q, 0);
-                uint32_t r = 0;
-                while (rem >= sp.tiles && r + 1 < nr) { rem -= sp.tiles; sp = span(q, ++r); }
-                const int64_t item_u = u - rem;
-                m.s = seq; m.q = q; m.sp = sp; m.r = (int)r;
-                m.k0 = (int)rem;
-                m.k1 = (int)(u1 - item_u < sp.tiles ? u1 - item_u : sp.tiles);
-                if (m.k1 <= m.k0) { m.s = -1; break; }
+                int r = 0;
+                while (rem >= CHANGE + sp.tiles && r + 1 < nr) { rem -= CHANGE + sp.tiles; sp = span(q, ++r); }
+                const int item_u = u - rem, end = item_u + CHANGE + sp.tiles;       // the item's units
+                m.q = q; m.sp = sp; m.r = r;
+                m.k0 = rem > CHANGE ? rem - CHANGE : 0;
+                m.k1 = (u1 < end ? u1 : end) - item_u - CHANGE;
+                u = end;
+                if (m.k1 <= m.k0) continue;                 // none of its tiles: all in the next run
+                m.s = seq;
                 m.pieces = 1;
-                if (m.k1 < sp.tiles) {
-                    int64_t to = ((item_u + sp.tiles) * W - 1) / all;           // the run with the item's last tile
+                if (end > u1) {
+                    int to = (int)(((int64_t)end * W - 1) / all);               // the run with the item's last tile
                     if (to >= W) to = W - 1;
-                    m.pieces = (int)(to - w + 1);
+                    m.pieces = to - w + 1;
                 }
-                u = item_u + m.k1;
                 break;
             }
         } else if (first_item) {
             first_item = false;
-            const int64_t i = plan.row_tiles - 1 - w / c.Hkv;
+            const int i = (int)plan.row_tiles - 1 - w / c.Hkv;
             // sequence s has the indices from cu[s] G / ROWS + s on, enough for its rows
-            int64_t lo = 0, n = c.B;
+            int lo = 0, n = B;
             while (n > 0) {
-                const int64_t step = (n + 63) / 64;
-                const int64_t j = lo + lane * step;
+                const int step = (n + 63) / 64;
+                const int j = lo + lane * step;
                 const bool below = lane * step < n && plan_index(c, j, G, ROWS) <= i;
                 const int k = __popcll(__ballot(below));
                 if (k == 0) break;
-                const int64_t b = (int64_t)(k - 1) * step;
+                const int b = (k - 1) * step;
                 lo += b + 1;
                 n = (n - b < step ? n - b : step) - 1;
             }
-            const int64_t s = uniform(lo) - 1;
+            const int s = uniform(lo) - 1;
             if (s >= 0) {
                 const Sequence q = sequence(s);
-                const int64_t r = i - plan_index(c, s, G, ROWS);
+                const int r = i - plan_index(c, s, G, ROWS);
                 if (r >= 0 && r < row_tiles(q)) {
-                    m.s = s; m.q = q; m.r = (int)r; m.h = w % c.Hkv;
-                    m.sp = span(q, (int)r);
+                    m.s = s; m.q = q; m.r = r; m.h = w % c.Hkv;
+                    m.sp = span(q, r);
                     m.k1 = m.sp.tiles;
                     m.pieces = 1;
                 }
@@ -310,13 +322,14 @@ void attention_tile(AttnArgs a, AttnPlan plan) {
 
     // ---- rows of a tile: where they are, and which there are (wavefront 0, in the order
     // of the run's tiles; numbers of tiles and items go round in rings)
-    int64_t ahead_s = -1, ahead_begin = 0, ahead_end = 0, ahead_first = 0;
+    int ahead_s = -1, ahead_begin = 0, ahead_end = 0, ahead_first = 0;
     int ahead_k = 0, ahead_k0 = 0, ahead_k1 = 0, ahead_h = 0, ahead_item = -1;
     // Entries of the table: lane i has entry `window + i` of the sequence's, so that a tile
     // needs a load only where it leaves them.
     int32_t entry = -1;
-    int64_t window = 0;
+    int window = 0;
     const char *scale_k = (const char *)no_key, *scale_v = (const char *)no_key;     // of this lane's row of the last tile looked up
+    auto page_of = [&](uint32_t p) { return (int)(c.shift >= 0 ? p >> c.shift : p / c.page); };
     auto look = [&](int n) {
         if (ahead_s >= 0 && ahead_k + 1 < ahead_k1) {
             ++ahead_k;
@@ -333,29 +346,26 @@ void attention_tile(AttnArgs a, AttnPlan plan) {
             ahead_k1 = uniform(m.k1);
             window = -64;                               // another sequence's
         }
-        const int64_t t0 = (ahead_first + ahead_k) * BK, p = t0 + lane;
+        const int t0 = (ahead_first + ahead_k) * BK, p = t0 + lane;
         const bool want = lane < BK && ahead_s >= 0 && p >= ahead_begin && p < ahead_end;
-        // pages of the tile's first and last position that count (0 where there is none)
-        const int64_t lo_p = t0 > ahead_begin ? t0 : ahead_begin, hi_p = t0 + BK < ahead_end ? t0 + BK : ahead_end;
-        const uint32_t x = (uint32_t)p, i = c.shift >= 0 ? x >> c.shift : x / c.page;
+        // pages of the tile's first and last position that count
+        const int lo_p = t0 > ahead_begin ? t0 : ahead_begin, hi_p = t0 + BK < ahead_end ? t0 + BK : ahead_end;
         if (ahead_s >= 0 && hi_p > lo_p) {
-            const uint32_t a0 = (uint32_t)lo_p, a1 = (uint32_t)(hi_p - 1);
-            const int64_t i0 = (uint32_t)uniform((int)(c.shift >= 0 ? a0 >> c.shift : a0 / c.page));
-            const int64_t i1 = (uint32_t)uniform((int)(c.shift >= 0 ? a1 >> c.shift : a1 / c.page));
+            const int i0 = uniform(page_of(lo_p)), i1 = uniform(page_of(hi_p - 1));
             if (i0 < window || i1 >= window + 64) {     // i1 - i0 < BK
                 window = i0;
-                entry = window + lane < c.max_pages ? c.table[ahead_s * c.ldt + window + lane] : -1;
+                entry = window + lane < (int)c.max_pages ? c.table[ahead_s * c.ldt + window + lane] : -1;
                 // waited for here, once in 64 pages, and not by every use below
                 asm volatile("s_waitcnt vmcnt(0)" : "+v"(entry) :: "memory");
             }
         }
-        const int64_t id = __shfl(entry, (int)(i - window) & 63);
-        const uint32_t slot = x - (c.shift >= 0 ? i << c.shift : i * c.page);
+        const int i = page_of(p), id = __shfl(entry, (i - window) & 63);
+        const uint32_t slot = (uint32_t)p - (c.shift >= 0 ? (uint32_t)i << c.shift : (uint32_t)i * c.page);
         const bool ok = want && id >= 0 && id < c.n_pages;
         if (want && !ok && c.bad) *c.bad = 1;
         const uint64_t m = __ballot(ok);
         if (lane < BK) {
-            const int64_t at = (id * c.s_page + (int64_t)slot * c.s_slot + ahead_h * c.s_head) * CS;
+            const int64_t at = ((int64_t)id * c.s_page + (int64_t)slot * c.s_slot + ahead_h * c.s_head) * CS;
             row_at[n & 1][lane].k = ok ? (const char *)c.kc + at : (const char *)no_key;
             row_at[n & 1][lane].v = ok ? (const char *)c.vc + at : (const char *)no_key;
         }
@@ -368,7 +378,7 @@ void attention_tile(AttnArgs a, AttnPlan plan) {
             t.ends = ahead_k + 1 == ahead_k1;
         }
         if (QUANT) {
-            const int64_t at = id * c.ss_page + (int64_t)slot * c.ss_slot + ahead_h * c.ss_head;
+            const int64_t at = (int64_t)id * c.ss_page + (int64_t)slot * c.ss_slot + ahead_h * c.ss_head;
             scale_k = ok ? (const char *)(c.ks + at) : (const char *)no_key;
             scale_v = ok ? (const char *)(c.vs + at) : (const char *)no_key;
         }
@@ -447,8 +457,7 @@ void attention_tile(AttnArgs a, AttnPlan plan) {
     // ---- the item that a tile belongs to: this lane's row, its query and its sums
     bool live = false, several = false, whole = false;
     int item_r = 0, item_h = 0, pieces = 0, slot = 0, head = 0;
-    uint32_t rows = 0;
-    int64_t first = 0, row = 0, hi = 0, lo = 0, see_all = 0, see_from = 0;
+    int rows = 0, first = 0, row = 0, hi = 0, lo = 0, see_all = 0, see_from = 0;
     bool begins_split = false;
     u32x4 qf[KS];
     f32x16 o[NB];
@@ -456,8 +465,8 @@ void attention_tile(AttnArgs a, AttnPlan plan) {
     auto enter = [&](int i) __attribute__((always_inline)) {
         const Item &m = items[i];
         first = uniform(m.q.first);
-        const int64_t past = uniform(m.q.past), pos0 = uniform(m.sp.pos0), pos1 = uniform(m.sp.pos1);
-        rows = (uint32_t)uniform(m.q.n) * G;                                // T G < 2^31
+        const int past = uniform(m.q.past), pos0 = uniform(m.sp.pos0), pos1 = uniform(m.sp.pos1);
+        rows = uniform(m.q.n) * G;
         item_r = uniform(m.r);
         item_h = uniform(m.h);
         pieces = uniform(m.pieces);
@@ -465,23 +474,23 @@ void attention_tile(AttnArgs a, AttnPlan plan) {
         whole = k0 == 0 && k1 == n;
         begins_split = k0 == 0 && k1 < n;
         slot = 2 * w + (k0 == 0 ? 1 : 0);
-        if (uniform((int)m.sp.outside) && c.bad && tid == 0) *c.bad = 1;
-        const uint32_t R = (uint32_t)item_r * ROWS + wr * 32 + col;
+        if ((pos0 < 0 || pos1 >= last_pos) && c.bad && tid == 0) *c.bad = 1;
+        const int R = item_r * ROWS + wr * 32 + col;
         live = R < rows;
-        const uint32_t tok = live ? R / (uint32_t)G : 0;
-        head = item_h * G + (int)(live ? R - tok * G : 0);
+        const int tok = live ? (int)((uint32_t)R / (uint32_t)G) : 0;
+        head = item_h * G + (live ? R - tok * G : 0);
         row = first + tok;
         hi = live ? past + tok : -1;
-        lo = past + tok - a.window + 1;
+        lo = past + tok - window_of + 1;
         see_all = pos0;                                                     // keys that every row sees
-        see_from = pos1 - a.window + 1;
+        see_from = pos1 - window_of + 1;
         several = pos1 > pos0;
 #pragma unroll
         for (int k = 0; k < KS; ++k) {
             // the features that a lane's k-th operand of K has
             const int ch = ST == STAGE_INT8 ? (2 * (k / ES) + half) * ES + k % ES : 2 * k + half;
             qf[k] = u32x4{0, 0, 0, 0};
-            if (live && ch < D * ES / 16) qf[k] = *(const u32x4_any *)((const char *)a.Q + (row * a.ldq + (int64_t)head * D) * ES + ch * 16);
+            if (live && ch < D * ES / 16) qf[k] = *(const u32x4_any *)((const char *)a.Q + ((int64_t)row * a.ldq + (int64_t)head * D) * ES + ch * 16);
         }
 #pragma unroll
         for (int b = 0; b < NB; ++b)
@@ -494,8 +503,8 @@ void attention_tile(AttnArgs a, AttnPlan plan) {
     // ---- one tile
     auto tile = [&](int n) __attribute__((always_inline)) {
         const int st = n & 1;
-        const int64_t t0 = uniform(tiles[n & 3].first);
-        const uint64_t valid = (uint64_t)uniform((int64_t)tiles[n & 3].rows);
+        const int t0 = uniform(tiles[n & 3].first);
+        const uint64_t valid = uniform64(tiles[n & 3].rows);
         const bool edge = t0 + BK - 1 > see_all || t0 < see_from;
         // values that are not finite, where rows see different keys
         bool dirty = false;
@@ -568,9 +577,9 @@ void attention_tile(AttnArgs a, AttnPlan plan) {
         uint64_t seen = valid;
         const bool masked = edge || valid != (BK == 64 ? ~0ull : (1ull << (BK & 63)) - 1);
         if (masked) {
-            const int64_t up = hi - t0, from = lo - t0;
-            seen &= up >= 63 ? ~0ull : up < 0 ? 0ull : (2ull << (int)up) - 1;
-            seen &= from <= 0 ? ~0ull : from > 63 ? 0ull : ~0ull << (int)from;
+            const int up = hi - t0, from = lo - t0;
+            seen &= up >= 63 ? ~0ull : up < 0 ? 0ull : (2ull << up) - 1;
+            seen &= from <= 0 ? ~0ull : from > 63 ? 0ull : ~0ull << from;
             const uint64_t mine = seen >> (4 * half);
 #pragma unroll
             for (int b = 0; b < KB; ++b)
@@ -714,7 +723,7 @@ void attention_tile(AttnArgs a, AttnPlan plan) {
                     f32x4 v;
 #pragma unroll
                     for (int e = 0; e < 4; ++e) v[e] = o[b][4 * i + e];
-                    if (whole) write_out<ES>(a.O, row * a.ldo + (int64_t)head * D, b * 32 + 8 * i + 4 * half, D, v, l == 0.0f, inv);
+                    if (whole) write_out<ES>(a.O, (int64_t)row * a.ldo + (int64_t)head * D, b * 32 + 8 * i + 4 * half, D, v, l == 0.0f, inv);
                     else plan_sums(a.ws, plan.groups)[(((int64_t)slot * WR + wr) * NB + b) * 256 + i * 64 + lane] = v;
                 }
             if (half == 0 && !whole) {
@@ -722,7 +731,7 @@ void attention_tile(AttnArgs a, AttnPlan plan) {
                 ml[0] = mx;
                 ml[1] = l;
             } else if (half == 0 && a.lse) {
-                a.lse[row * a.ldl + head] = l == 0.0f ? -INFINITY : mx * 0.69314718055994530942f + logf(l);
+                a.lse[(int64_t)row * a.ldl + head] = l == 0.0f ? -INFINITY : mx * 0.69314718055994530942f + logf(l);
             }
         }
         // a run that begins an item names the runs that hold the rest of it
@@ -764,11 +773,10 @@ void attention_join(AttnArgs a, AttnPlan plan) {
     const PlanDesc d = plan_desc(a.ws)[w];
     if (d.pieces == 0) return;
     const int lane = threadIdx.x & 63, i = threadIdx.x >> 6, half = lane >> 5, col = lane & 31;
-    const uint32_t R = (uint32_t)d.r * ROWS + wr * 32 + col;
+    const int R = d.r * ROWS + wr * 32 + col;
     if (R >= d.rows) return;
-    const uint32_t tok = R / (uint32_t)a.G;
+    const int tok = (int)((uint32_t)R / (uint32_t)a.G), head = d.h * a.G + R - tok * a.G;
     const int64_t row = d.first + tok;
-    const int head = d.h * a.G + (int)(R - tok * a.G);
     const float *ml = plan_stats(a.ws, plan.groups) + (int64_t)(wr * 32 + col) * 2;
     const f32x4 *sums = plan_sums(a.ws, plan.groups) + ((int64_t)wr * NB + b) * 256 + i * 64 + lane;
     auto slot = [&](int k) { return k == 0 ? (int64_t)2 * w + 1 : (int64_t)2 * (w + k); };
