@@ -41,7 +41,7 @@ AttnPlan attention_plan(int64_t T, int64_t B, int64_t Hkv, int32_t G, int64_t D,
     // registers (two wavefronts a SIMD, one for the longest heads).  Not taken from the
     // device: the workspace's size and the order of the sums depend on the call alone.
     const int64_t row = (D <= 64 ? 64 : D <= 128 ? 128 : 256) * (quant ? 1 : es);
-    p.groups = 256 * (!p.few ? (D <= 128 ? 2 : 1) : D > 128 && row <= 256 ? 4 : row <= 128 ? 8 : row <= 256 ? 4 : row <= 512 ? 2 : 1);
+    p.groups = 256 * (!p.few ? (D <= 128 ? 2 : 1) : row <= 128 ? 8 : row <= 256 ? 4 : row <= 512 ? 2 : 1);
     return p;
 }
 

@@ -106,6 +106,7 @@ __device__ __forceinline__ f32x16 product(u32x4 a, u32x4 b, f32x16 c) {
 __device__ __forceinline__ uint64_t uniform64(uint64_t v) {
     return (uint64_t)(uint32_t)__builtin_amdgcn_readfirstlane((uint32_t)(v >> 32)) << 32 | (uint32_t)__builtin_amdgcn_readfirstlane((uint32_t)v);
 }
+template <int N> struct Const { static constexpr int value = N; };
 template <int ES> struct Bits { typedef uint32_t T; };
 template <> struct Bits<2> { typedef uint16_t T; };
 __device__ __forceinline__ int uniform(int v) { return __builtin_amdgcn_readfirstlane(v); }
@@ -166,9 +167,11 @@ __device__ __forceinline__ int64_t uniform(int64_t v) {
 // the cache, or int8 straight from the cache.
 enum { STAGE_REGS = 0, STAGE_DMA = 1, STAGE_INT8 = 2 };
 
-template <int ES, int CS, int NB, int WR, int KB, int ST, int OCC>
+// FULL: D is 32 NB, all of a row in LDS.
+template <int ES, int CS, int NB, int WR, int KB, int ST, int OCC, bool FULL>
 __global__ __launch_bounds__(64 * WR, OCC)
 void attention_tile(AttnArgs a, AttnPlan plan) {
+    constexpr bool ALONE = WR == 1 && ST != STAGE_REGS;                 // see the loop at the end
     constexpr int NW = WR, NTH = 64 * NW, ROWS = 32 * WR, BK = 32 * KB;
     constexpr int LS = ST == STAGE_INT8 ? 1 : ES;                       // bytes of a value in LDS
     constexpr bool DMA = ST != STAGE_REGS;
@@ -387,42 +390,37 @@ void attention_tile(AttnArgs a, AttnPlan plan) {
     // ---- a tile's chunks: thread tid has chunk i NTH + tid of K and of V
     u32x4 kr[DMA ? 1 : LI], vr[DMA ? 1 : LI];
     float scale_kr = 0.0f, scale_vr = 0.0f;
-    auto fetch = [&](int n) __attribute__((always_inline)) {
+    auto place = [&](int n) { return (n & 1) * STAGE; };                     // of tile n in LDS
+    // K (or V) of tile n: K with the scales of the tile that was looked up last.
+    auto fetch = [&](int n, auto is_v) __attribute__((always_inline)) {
+        constexpr bool V = decltype(is_v)::value;
         const int st = n & 1;
-        const char *ka[LI], *va[LI];
+        const char *from[LI];
 #pragma unroll
-        for (int i = 0; i < LI; ++i) {
-            const int r = (i * NTH + tid) / CH;
-            ka[i] = row_at[st][r].k;
-            va[i] = row_at[st][r].v;
-        }
+        for (int i = 0; i < LI; ++i) from[i] = V ? row_at[st][(i * NTH + tid) / CH].v : row_at[st][(i * NTH + tid) / CH].k;
 #pragma unroll
         for (int i = 0; i < LI; ++i) {
             const int k = i * NTH + tid, r = k / CH, ch = k % CH;
             if constexpr (DMA) {
-                const uint32_t dst = lds_u + st * STAGE + (i * NTH + wave * 64) * 16;
-                const int kc = ch ^ (k_swizzle<RB>(r) >> 4), vc = ch ^ (v_swizzle<LS, RB>(r) >> 4);
-                dma16(kc < chunks ? ka[i] + kc * 16 : (const char *)no_key, dst);
-                dma16(vc < chunks ? va[i] + vc * 16 : (const char *)no_key, dst + BK * RB);
+                const int at = ch ^ ((V ? v_swizzle<LS, RB>(r) : k_swizzle<RB>(r)) >> 4);
+                dma16(FULL || at < chunks ? from[i] + at * 16 : (const char *)no_key, lds_u + place(n) + (V ? BK * RB : 0) + (i * NTH + wave * 64) * 16);
             } else {
-                kr[i] = vr[i] = u32x4{0, 0, 0, 0};
+                u32x4 &x = V ? vr[i] : kr[i];
+                x = u32x4{0, 0, 0, 0};
                 if (ch < chunks) {
-                    const char *kp = ka[i] + ch * (16 / ES) * CS, *vp = va[i] + ch * (16 / ES) * CS;
+                    const char *p = from[i] + ch * (16 / ES) * CS;
                     if constexpr (!QUANT) {
-                        kr[i] = *(const u32x4_any *)kp;
-                        vr[i] = *(const u32x4_any *)vp;
+                        x = *(const u32x4_any *)p;
                     } else if constexpr (ES == 2) {
-                        const u32x2 x = *(const u32x2_any *)kp, y = *(const u32x2_any *)vp;
-                        kr[i][0] = x[0]; kr[i][1] = x[1];
-                        vr[i][0] = y[0]; vr[i][1] = y[1];
+                        const u32x2 y = *(const u32x2_any *)p;
+                        x[0] = y[0]; x[1] = y[1];
                     } else {
-                        kr[i][0] = *(const u32_any *)kp;
-                        vr[i][0] = *(const u32_any *)vp;
+                        x[0] = *(const u32_any *)p;
                     }
                 }
             }
         }
-        if (QUANT && wave == 0) {          // the scales of the tile that was looked up last, in lane order
+        if (QUANT && !V && wave == 0) {
             if constexpr (DMA) {
                 dma4(scale_k, scale_u + st * 512);
                 dma4(scale_v, scale_u + st * 512 + 256);
@@ -432,13 +430,10 @@ void attention_tile(AttnArgs a, AttnPlan plan) {
             }
         }
     };
-    // The fetched tile is in LDS, this thread's part; DMA: all but the last `later` of the
-    // instructions have done their work.
-    auto settle = [&](int n, bool later) __attribute__((always_inline)) {
+    // What was fetched is in LDS, this thread's part.
+    auto settle_all = [&](int n) __attribute__((always_inline)) {
         if constexpr (DMA) {
-            constexpr int LATER = 2 * LI + (QUANT ? 2 : 0);          // of one fetch; the counter holds 63
-            if (later) asm volatile("s_waitcnt vmcnt(%0)" :: "n"(LATER < 63 ? LATER : 63) : "memory");
-            else asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+            asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
         } else {
 #pragma unroll
             for (int i = 0; i < LI; ++i) {
@@ -452,6 +447,12 @@ void attention_tile(AttnArgs a, AttnPlan plan) {
                 row_scale[n & 1][1][QUANT ? lane : 0] = scale_vr;
             }
         }
+    };
+    // Of this tile, while the next one's instructions are under way (66 at most; the counter
+    // holds 63).
+    auto settle_first = [&]() __attribute__((always_inline)) {
+        constexpr int LATER = 2 * LI + (QUANT ? 2 : 0);
+        asm volatile("s_waitcnt vmcnt(%0)" :: "n"(LATER < 63 ? LATER : 63) : "memory");
     };
 
     // ---- the item that a tile belongs to: this lane's row, its query and its sums
@@ -506,46 +507,8 @@ void attention_tile(AttnArgs a, AttnPlan plan) {
         const int t0 = uniform(tiles[n & 3].first);
         const uint64_t valid = uniform64(tiles[n & 3].rows);
         const bool edge = t0 + BK - 1 > see_all || t0 < see_from;
-        // values that are not finite, where rows see different keys
-        bool dirty = false;
-        if (!QUANT && edge && several) {
-            bool any = false;
-#pragma unroll
-            for (int i = 0; i < LI; ++i) {
-                const u32x4 x = *(LDS_PTR(u32x4))(lds + st * STAGE + BK * RB + (i * NTH + tid) * 16);
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    if (ES == 2) any |= (x[e] & 0x7F80) == 0x7F80 || (x[e] & 0x7F800000) == 0x7F800000;
-                    else any |= (x[e] & 0x7F800000) == 0x7F800000;
-                }
-            }
-            ++stamp;
-            if (any) found[stamp & 1] = stamp;
-            meet<WR>();
-            dirty = uniform(found[stamp & 1]) == stamp;
-            if (dirty) {
-                // zeros in their place, and for each feature the keys: a NaN is up and down
-                for (int i = tid; i < 2 * DP; i += NTH) odd[i / DP][i % DP] = 0;
-                meet<WR>();
-                for (int i = 0; i < LI; ++i) {
-                    const int k = i * NTH + tid, r = k / CH;
-                    const int d = ((k % CH) * 16 ^ v_swizzle<LS, RB>(r)) / ES;
-                    for (int e = 0; e < 16 / ES; ++e) {
-                        typedef typename Bits<ES>::T B;
-                        LDS_PTR(B) v = (LDS_PTR(B))(lds + st * STAGE + BK * RB + k * 16) + e;
-                        const uint32_t y = ES == 2 ? (uint32_t)*v << 16 : (uint32_t)*v;
-                        if ((y & 0x7F800000) != 0x7F800000) continue;
-                        *v = 0;
-                        const bool nan = (y & 0x7FFFFF) != 0;
-                        if (nan || !(y >> 31)) atomicOr((unsigned long long *)&odd[0][d + e], 1ull << r);
-                        if (nan || y >> 31) atomicOr((unsigned long long *)&odd[QUANT ? 0 : 1][d + e], 1ull << r);
-                    }
-                }
-                meet<WR>();
-            }
-        }
         f32x16 x[KB];
-        const uint32_t kl = st * STAGE + col * RB, ks = (half * 16) ^ k_swizzle<RB>(col);
+        const uint32_t kl = place(n) + col * RB, ks = (half * 16) ^ k_swizzle<RB>(col);
 #pragma unroll
         for (int b = 0; b < KB; ++b)
 #pragma unroll
@@ -631,7 +594,45 @@ void attention_tile(AttnArgs a, AttnPlan plan) {
                         if (!((uint32_t)(mine >> (32 * b)) >> (8 * (i / 4) + i % 4) & 1)) x[b][i] = 0.0f;
             }
         }
-        const uint32_t vl = st * STAGE + BK * RB;
+        // values that are not finite, where rows see different keys
+        bool dirty = false;
+        if (!QUANT && edge && several) {
+            bool any = false;
+#pragma unroll
+            for (int i = 0; i < LI; ++i) {
+                const u32x4 x = *(LDS_PTR(u32x4))(lds + place(n) + BK * RB + (i * NTH + tid) * 16);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    if (ES == 2) any |= (x[e] & 0x7F80) == 0x7F80 || (x[e] & 0x7F800000) == 0x7F800000;
+                    else any |= (x[e] & 0x7F800000) == 0x7F800000;
+                }
+            }
+            ++stamp;
+            if (any) found[stamp & 1] = stamp;
+            meet<WR>();
+            dirty = uniform(found[stamp & 1]) == stamp;
+            if (dirty) {
+                // zeros in their place, and for each feature the keys: a NaN is up and down
+                for (int i = tid; i < 2 * DP; i += NTH) odd[i / DP][i % DP] = 0;
+                meet<WR>();
+                for (int i = 0; i < LI; ++i) {
+                    const int k = i * NTH + tid, r = k / CH;
+                    const int d = ((k % CH) * 16 ^ v_swizzle<LS, RB>(r)) / ES;
+                    for (int e = 0; e < 16 / ES; ++e) {
+                        typedef typename Bits<ES>::T B;
+                        LDS_PTR(B) v = (LDS_PTR(B))(lds + place(n) + BK * RB + k * 16) + e;
+                        const uint32_t y = ES == 2 ? (uint32_t)*v << 16 : (uint32_t)*v;
+                        if ((y & 0x7F800000) != 0x7F800000) continue;
+                        *v = 0;
+                        const bool nan = (y & 0x7FFFFF) != 0;
+                        if (nan || !(y >> 31)) atomicOr((unsigned long long *)&odd[0][d + e], 1ull << r);
+                        if (nan || y >> 31) atomicOr((unsigned long long *)&odd[QUANT ? 0 : 1][d + e], 1ull << r);
+                    }
+                }
+                meet<WR>();
+            }
+        }
+        const uint32_t vl = place(n) + BK * RB;
         if constexpr (ST == STAGE_INT8) {
             // keys 16 s + 8 e + 4 half + i of a step, 4 e + i = (l % 16) / 2
             const uint32_t r = (lane & 15) >> 1, key = (r & 3) + (r >> 2) * 8 + 4 * half;
@@ -742,17 +743,22 @@ void attention_tile(AttnArgs a, AttnPlan plan) {
     // instructions in the caches): tile n + 2 is looked up, tile n + 1 fetched, tile n worked
     // on.  A wavefront by itself (ALONE) fetches the next tile before this one is there, as
     // soon as its place in LDS is free; four wait for theirs first, and then for each other.
-    constexpr bool ALONE = WR == 1 && DMA;
     for (int n = -2;; ++n) {
-        if (!ALONE && n >= 0) settle(n, false);
+        if (!ALONE && n >= 0) settle_all(n);
         meet<WR>();                                     // also: this wavefront's reads of the last tile are done
         bool more = true;
         if (n >= -1) {
             more = uniform(tiles[(n + 1) & 3].item) >= 0;
             if (n < 0 && !more) return;
-            if (more) fetch(n + 1);
+            if (more) {
+                fetch(n + 1, Const<0>());
+                fetch(n + 1, Const<1>());
+            }
         }
-        if (ALONE && n >= 0) settle(n, more);
+        if (ALONE && n >= 0) {
+            if (more) settle_first();
+            else settle_all(n);
+        }
         if (more && wave == 0) look(n + 2);
         if (n < 0) continue;
         if (uniform(tiles[n & 3].begins)) enter(uniform(tiles[n & 3].item));
@@ -762,81 +768,116 @@ void attention_tile(AttnArgs a, AttnPlan plan) {
     }
 }
 
-// Joins the sums of the items that more than one run holds: workgroup (w, y) the item
-// that run w begins, block y of its rows and features; its first sums are in slot 2 w + 1,
-// the later ones in slots 2 (w + 1), 2 (w + 2), ...
+// Joins the sums of the items that more than one run holds: workgroup (w, y) 32 rows and 32
+// features of the item that run w begins; its first sums are in slot 2 w + 1, the later ones
+// in slots 2 (w + 1), 2 (w + 2), ...  Of few runs a wavefront adds up 8 of the features, in
+// the runs' order; of many (a long sequence with few heads) it takes every fourth run with
+// all of the features, and then the four are added in order.
+constexpr int JOIN = 256, JOIN_ALONE = 8;
+template <int N> struct JoinSums { float m, l; f32x4 x[N]; };
+
+template <int N>
+__device__ __forceinline__ void join_add(JoinSums<N> &s, float m, float l, const f32x4 (&y)[N]) {
+    const float top = fmaxf(s.m, m), zero = top == -INFINITY ? 0.0f : top;
+    const float f0 = __builtin_amdgcn_exp2f(s.m - zero), f1 = __builtin_amdgcn_exp2f(m - zero);
+    s.m = top;
+    s.l = __builtin_fmaf(f1, l, s.l * f0);
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) s.x[i][e] = __builtin_fmaf(f1, y[i][e], s.x[i][e] * f0);
+}
+
 template <int ES, int NB, int WR>
-__global__ __launch_bounds__(256)
+__global__ __launch_bounds__(JOIN)
 void attention_join(AttnArgs a, AttnPlan plan) {
-    constexpr int ROWS = 32 * WR;
+    constexpr int ROWS = 32 * WR, JW = JOIN / 64;
+    __shared__ JoinSums<4> parts[JW][64];
     const int w = blockIdx.x, wr = blockIdx.y / NB, b = blockIdx.y % NB;
     const PlanDesc d = plan_desc(a.ws)[w];
     if (d.pieces == 0) return;
-    const int lane = threadIdx.x & 63, i = threadIdx.x >> 6, half = lane >> 5, col = lane & 31;
+    const int lane = threadIdx.x & 63, v = threadIdx.x >> 6, half = lane >> 5, col = lane & 31;
     const int R = d.r * ROWS + wr * 32 + col;
-    if (R >= d.rows) return;
-    const int tok = (int)((uint32_t)R / (uint32_t)a.G), head = d.h * a.G + R - tok * a.G;
+    const bool live = R < d.rows;
+    const int tok = live ? (int)((uint32_t)R / (uint32_t)a.G) : 0, head = d.h * a.G + (live ? R - tok * a.G : 0);
     const int64_t row = d.first + tok;
     const float *ml = plan_stats(a.ws, plan.groups) + (int64_t)(wr * 32 + col) * 2;
-    const f32x4 *sums = plan_sums(a.ws, plan.groups) + ((int64_t)wr * NB + b) * 256 + i * 64 + lane;
     auto slot = [&](int k) { return k == 0 ? (int64_t)2 * w + 1 : (int64_t)2 * (w + k); };
-    // four runs at a time, whose loads leave together, in order
-    float m = -INFINITY, l = 0.0f;
-    f32x4 v = {0.0f, 0.0f, 0.0f, 0.0f};
-    for (int k0 = 0; k0 < d.pieces; k0 += 4) {
-        float ms[4], ls[4];
-        f32x4 x[4];
+    const f32x4 *sums = plan_sums(a.ws, plan.groups) + ((int64_t)wr * NB + b) * 256 + lane;
+    const bool few = d.pieces <= JOIN_ALONE;
+    JoinSums<4> s{-INFINITY, 0.0f, {}};
+    JoinSums<1> t{-INFINITY, 0.0f, {}};
+    if (live && few) {
+        // four runs at a time, whose loads leave together
+        for (int k0 = 0; k0 < d.pieces; k0 += 4) {
+            f32x4 y[4][1];
+            float m[4], l[4];
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-            ms[k] = -INFINITY;
-            ls[k] = 0.0f;
-            x[k] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-            if (k0 + k < d.pieces) {
-                const float *s = ml + slot(k0 + k) * ROWS * 2;
-                ms[k] = s[0];
-                ls[k] = s[1];
-                x[k] = sums[slot(k0 + k) * WR * NB * 256];
+            for (int j = 0; j < 4; ++j) {
+                m[j] = -INFINITY;
+                l[j] = 0.0f;
+                y[j][0] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+                if (k0 + j < d.pieces) {
+                    const float *p = ml + slot(k0 + j) * ROWS * 2;
+                    m[j] = p[0];
+                    l[j] = p[1];
+                    y[j][0] = sums[slot(k0 + j) * WR * NB * 256 + v * 64];
+                }
             }
+#pragma unroll
+            for (int j = 0; j < 4; ++j) join_add<1>(t, m[j], l[j], y[j]);
         }
-        const float top = fmaxf(fmaxf(fmaxf(m, ms[0]), fmaxf(ms[1], ms[2])), ms[3]), zero = top == -INFINITY ? 0.0f : top;
-        const float f0 = __builtin_amdgcn_exp2f(m - zero);
-        l *= f0;
+    } else if (live) {
+#pragma unroll 4
+        for (int k = v; k < d.pieces; k += JW) {
+            const float *p = ml + slot(k) * ROWS * 2;
+            f32x4 y[4];
 #pragma unroll
-        for (int e = 0; e < 4; ++e) v[e] *= f0;
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-            const float f = __builtin_amdgcn_exp2f(ms[k] - zero);
-            l = __builtin_fmaf(f, ls[k], l);
-#pragma unroll
-            for (int e = 0; e < 4; ++e) v[e] = __builtin_fmaf(f, x[k][e], v[e]);
+            for (int i = 0; i < 4; ++i) y[i] = sums[slot(k) * WR * NB * 256 + i * 64];
+            join_add<4>(s, p[0], p[1], y);
         }
-        m = top;
     }
-    write_out<ES>(a.O, row * a.ldo + (int64_t)head * a.c.D, b * 32 + 8 * i + 4 * half, a.c.D, v, l == 0.0f, l == 0.0f ? 0.0f : 1.0f / l);
-    if (a.lse && b == 0 && i == 0 && half == 0) a.lse[row * a.ldl + head] = l == 0.0f ? -INFINITY : m * 0.69314718055994530942f + logf(l);
+    if (!few) {
+        parts[v][lane] = s;
+        __syncthreads();
+#pragma unroll
+        for (int k = 0; k < JW; ++k) {
+            const f32x4 y[1] = {parts[k][lane].x[v]};
+            join_add<1>(t, parts[k][lane].m, parts[k][lane].l, y);
+        }
+    }
+    if (!live) return;
+    const bool none = t.l == 0.0f;
+    write_out<ES>(a.O, row * a.ldo + (int64_t)head * a.c.D, b * 32 + 8 * v + 4 * half, a.c.D, t.x[0], none, none ? 0.0f : 1.0f / t.l);
+    if (a.lse && b == 0 && v == 0 && half == 0) a.lse[row * a.ldl + head] = none ? -INFINITY : t.m * 0.69314718055994530942f + logf(t.l);
 }
 
-template <int ES, int CS, int NB, int WR, int KB, int ST, int OCC>
+template <int ES, int CS, int NB, int WR, int KB, int ST, int OCC, bool FULL>
 hipError_t launch_tile(const AttnArgs &a, const AttnPlan &p, hipStream_t s) {
     const unsigned grid = p.stream ? (unsigned)p.groups : (unsigned)(p.row_tiles * a.c.Hkv);
-    attention_tile<ES, CS, NB, WR, KB, ST, OCC><<<dim3(grid), dim3(64 * WR), 0, s>>>(a, p);
+    attention_tile<ES, CS, NB, WR, KB, ST, OCC, FULL><<<dim3(grid), dim3(64 * WR), 0, s>>>(a, p);
     hipError_t e = hipGetLastError();
     if (e != hipSuccess || !p.stream) return e;
-    attention_join<ES, NB, WR><<<dim3((unsigned)p.groups, WR * NB), dim3(256), 0, s>>>(a, p);
+    attention_join<ES, NB, WR><<<dim3((unsigned)p.groups, WR * NB), dim3(JOIN), 0, s>>>(a, p);
     return hipGetLastError();
 }
 
 // dma: the cache goes to LDS without a stop.  Tiles by the bytes of a row in LDS.
+template <int ES, int CS, int NB, bool FULL>
+hipError_t launch_full(const AttnArgs &a, const AttnPlan &p, bool dma, hipStream_t s) {
+    constexpr int RB = (NB == 3 ? 128 : NB * 32) * ES, OCC = NB == 8 ? 1 : 2;
+    if (p.few) {
+        if (dma) return launch_tile<ES, CS, NB, 1, 1, CS == 1 ? STAGE_INT8 : STAGE_DMA, OCC, FULL>(a, p, s);
+        return launch_tile<ES, CS, NB, 1, 1, STAGE_REGS, 1, false>(a, p, s);
+    }
+    constexpr int KB = RB <= 256 ? 2 : 1;
+    if (dma && CS != 1) return launch_tile<ES, CS, NB, 4, KB, CS == 1 ? STAGE_REGS : STAGE_DMA, OCC, CS != 1 && FULL>(a, p, s);
+    return launch_tile<ES, CS, NB, 4, KB, STAGE_REGS, OCC, false>(a, p, s);
+}
 template <int ES, int CS, int NB>
 hipError_t launch_nb(const AttnArgs &a, const AttnPlan &p, bool dma, hipStream_t s) {
-    constexpr int RB = (NB == 3 ? 128 : NB * 32) * ES;
-    if (p.few) {
-        if (dma) return launch_tile<ES, CS, NB, 1, 1, CS == 1 ? STAGE_INT8 : STAGE_DMA, CS == 1 && NB < 8 ? 2 : 1>(a, p, s);
-        return launch_tile<ES, CS, NB, 1, 1, STAGE_REGS, 1>(a, p, s);
-    }
-    constexpr int KB = RB <= 256 ? 2 : 1, OCC = NB == 8 ? 1 : 2;
-    if (dma && CS != 1) return launch_tile<ES, CS, NB, 4, KB, CS == 1 ? STAGE_REGS : STAGE_DMA, OCC>(a, p, s);
-    return launch_tile<ES, CS, NB, 4, KB, STAGE_REGS, OCC>(a, p, s);
+    if (NB != 3 && a.c.D == 32 * NB) return launch_full<ES, CS, NB, NB != 3>(a, p, dma, s);
+    return launch_full<ES, CS, NB, false>(a, p, dma, s);
 }
 
 template <int ES, int CS>
