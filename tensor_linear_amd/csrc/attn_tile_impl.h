@@ -64,6 +64,8 @@ typedef uint32_t u32x2_any __attribute__((ext_vector_type(2), aligned(1)));
 typedef uint32_t u32x4_any __attribute__((ext_vector_type(4), aligned(1)));
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 typedef __bf16 bf16x4 __attribute__((ext_vector_type(4)));
+typedef _Float16 f16x2 __attribute__((ext_vector_type(2)));
+typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
 typedef short s16x4 __attribute__((ext_vector_type(4)));
 typedef short s16x8 __attribute__((ext_vector_type(8)));
 
@@ -100,6 +102,11 @@ __device__ __forceinline__ f32x16 product(u32x4 a, u32x4 b, f32x16 c) {
         for (int j = 0; j < 4; ++j) c = __builtin_amdgcn_mfma_f32_32x32x2f32(__uint_as_float(a[j]), __uint_as_float(b[j]), c, 0, 0, 0);
         return c;
     }
+}
+
+// The second product of an int8 cache in a bf16 call: values and weights in fp16.
+__device__ __forceinline__ f32x16 product_half(u32x4 a, u32x4 b, f32x16 c) {
+    return __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(f16x8, a), __builtin_bit_cast(f16x8, b), c, 0, 0, 0);
 }
 
 // A value that all lanes have, as a scalar.
@@ -155,6 +162,17 @@ __device__ __forceinline__ u32x4 from_int8(uint32_t lo, uint32_t hi) {
     }
 }
 
+// int8 values to fp16, 8 of them: a byte with its sign flipped is v + 128, below the
+// exponent of 1024 it makes 1152 + v.
+__device__ __forceinline__ u32x4 half_from_int8(uint32_t lo, uint32_t hi) {
+    const uint32_t w[2] = {lo ^ 0x80808080u, hi ^ 0x80808080u};
+    u32x4 y;
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+        y[e] = __builtin_bit_cast(uint32_t, __builtin_bit_cast(f16x2, __builtin_amdgcn_perm(0x64646464u, w[e / 2], e & 1 ? 0x04030402u : 0x04010400u)) - f16x2{1152, 1152});
+    return y;
+}
+
 __device__ __forceinline__ float other_half(float v) { return __shfl_xor(v, 32); }
 
 // A value that all lanes have, as a scalar.
@@ -180,6 +198,7 @@ void attention_tile(AttnArgs a, AttnPlan plan) {
     constexpr int CH = RB / 16, LI = BK * CH / NTH;                     // chunks of a row; of a thread and tile
     constexpr int STAGE = 2 * BK * RB;
     constexpr bool QUANT = CS == 1;
+    constexpr bool HALF = QUANT && ES == 2;                             // values and weights in fp16: see below
     static_assert(BK <= NTH, "a thread a row of the tile");
     __shared__ __attribute__((aligned(1024))) char smem[2 * STAGE];
     __shared__ struct { const char *k, *v; } row_at[2][BK];          // where the tiles' rows are
@@ -440,7 +459,7 @@ void attention_tile(AttnArgs a, AttnPlan plan) {
                 const int k = i * NTH + tid, r = k / CH, ch = k % CH;
                 const uint32_t at = (n & 1) * STAGE + r * RB;
                 *(LDS_PTR(u32x4))(lds + at + ((ch * 16) ^ k_swizzle<RB>(r))) = QUANT ? from_int8<ES>(kr[i][0], kr[i][1]) : kr[i];
-                *(LDS_PTR(u32x4))(lds + at + BK * RB + ((ch * 16) ^ v_swizzle<LS, RB>(r))) = QUANT ? from_int8<ES>(vr[i][0], vr[i][1]) : vr[i];
+                *(LDS_PTR(u32x4))(lds + at + BK * RB + ((ch * 16) ^ v_swizzle<LS, RB>(r))) = HALF ? half_from_int8(vr[i][0], vr[i][1]) : QUANT ? from_int8<ES>(vr[i][0], vr[i][1]) : vr[i];
             }
             if (QUANT && wave == 0) {
                 row_scale[n & 1][0][QUANT ? lane : 0] = scale_kr;
@@ -463,6 +482,12 @@ void attention_tile(AttnArgs a, AttnPlan plan) {
     u32x4 qf[KS];
     f32x16 o[NB];
     float mx = -INFINITY, l = 0.0f;
+    // HALF: weights times scales go into the second product as fp16, which rounds them by
+    // 2^-12 at most (bf16: 2^-9, as much as the output's own rounding), and have to lie where
+    // fp16 is exact: all weights are 2^shift times the softmax's, l and o with them, so that
+    // the largest of a row (top_w) is between 2^4 and 2^15.  The shift begins at 2^16, for
+    // scales of values of order one, and hardly ever changes.
+    float shift = 16.0f, top_w = 0.0f;
     auto enter = [&](int i) __attribute__((always_inline)) {
         const Item &m = items[i];
         first = uniform(m.q.first);
@@ -499,6 +524,8 @@ void attention_tile(AttnArgs a, AttnPlan plan) {
             for (int e = 0; e < 16; ++e) o[b][e] = 0.0f;
         mx = -INFINITY;
         l = 0.0f;
+        shift = 16.0f;
+        top_w = 0.0f;
     };
 
     // ---- one tile
@@ -561,18 +588,20 @@ void attention_tile(AttnArgs a, AttnPlan plan) {
         if (__any(next > mx)) {
             const float f = __builtin_amdgcn_exp2f(mx - zero);
             l *= f;
+            if (HALF) top_w *= f;
 #pragma unroll
             for (int b = 0; b < NB; ++b)
 #pragma unroll
                 for (int i = 0; i < 16; ++i) o[b][i] *= f;
             mx = next;
         }
+        const float less = HALF ? shift - zero : -zero;
         float sum = 0.0f;
 #pragma unroll
         for (int b = 0; b < KB; ++b)
 #pragma unroll
             for (int i = 0; i < 16; ++i) {
-                x[b][i] = __builtin_amdgcn_exp2f(__builtin_fmaf(x[b][i], cs, -zero));
+                x[b][i] = __builtin_amdgcn_exp2f(__builtin_fmaf(x[b][i], cs, less));
                 sum += x[b][i];
             }
         l += sum;
@@ -592,6 +621,32 @@ void attention_tile(AttnArgs a, AttnPlan plan) {
 #pragma unroll
                     for (int i = 0; i < 16; ++i)
                         if (!((uint32_t)(mine >> (32 * b)) >> (8 * (i / 4) + i % 4) & 1)) x[b][i] = 0.0f;
+            }
+        }
+        if constexpr (HALF) {
+            float most = x[0][0];
+#pragma unroll
+            for (int b = 0; b < KB; ++b)
+#pragma unroll
+                for (int i = 0; i < 16; ++i) most = fmaxf(most, fabsf(x[b][i]));
+            top_w = fmaxf(top_w, fmaxf(most, other_half(most)));
+            if (__any(top_w >= 32768.0f || (top_w < 16.0f && top_w > 0.0f))) {
+                // the row's largest to 2^12 (an infinite scale stays infinite)
+                const int e = (int)(__float_as_uint(top_w) >> 23) - 127;
+                const bool off = top_w > 0.0f && e < 128 && (e >= 15 || e < 4);
+                const float to = off ? fminf(fmaxf(shift + (float)(12 - e), -100.0f), 100.0f) : shift;
+                const float f = __builtin_amdgcn_exp2f(to - shift);
+                shift = to;
+                top_w *= f;
+                l *= f;
+#pragma unroll
+                for (int b = 0; b < KB; ++b)
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) x[b][i] *= f;
+#pragma unroll
+                for (int b = 0; b < NB; ++b)
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) o[b][i] *= f;
             }
         }
         // values that are not finite, where rows see different keys
@@ -643,9 +698,9 @@ void attention_tile(AttnArgs a, AttnPlan plan) {
                 for (int s2 = 0; s2 < 2; ++s2) {
                     u32x4 p[ES / 2];
                     if constexpr (ES == 2) {
-                        bf16x8 h;
+                        f16x8 h;
 #pragma unroll
-                        for (int e = 0; e < 8; ++e) h[e] = (__bf16)x[b][8 * s2 + e];
+                        for (int e = 0; e < 8; ++e) h[e] = (_Float16)x[b][8 * s2 + e];
                         p[0] = __builtin_bit_cast(u32x4, h);
                     } else {
 #pragma unroll
@@ -656,7 +711,7 @@ void attention_tile(AttnArgs a, AttnPlan plan) {
                         typedef int i32x2 __attribute__((ext_vector_type(2)));
                         const i32x2 v = __builtin_amdgcn_ds_read_tr8_b64_v2i32((LDS_PTR(i32x2))(lds + at + (b * 32 + s2 * 16) * RB + ((d * 32) ^ sw)));
                         if constexpr (ES == 2) {
-                            o[d] = product<ES>(from_int8<ES>(v[0], v[1]), p[0], o[d]);
+                            o[d] = product_half(half_from_int8(v[0], v[1]), p[0], o[d]);
                         } else {
                             o[d] = product<ES>(from_int8<ES>(v[0], 0), p[0], o[d]);
                             o[d] = product<ES>(from_int8<ES>(v[1], 0), p[ES / 4], o[d]);
@@ -671,15 +726,25 @@ void attention_tile(AttnArgs a, AttnPlan plan) {
             for (int b = 0; b < KB; ++b)
 #pragma unroll
                 for (int s2 = 0; s2 < 2; ++s2) {
-                    bf16x8 p;
+                    u32x4 p;
+                    if constexpr (HALF) {
+                        f16x8 h;
 #pragma unroll
-                    for (int e = 0; e < 8; ++e) p[e] = (__bf16)x[b][8 * s2 + e];
+                        for (int e = 0; e < 8; ++e) h[e] = (_Float16)x[b][8 * s2 + e];
+                        p = __builtin_bit_cast(u32x4, h);
+                    } else {
+                        bf16x8 h;
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) h[e] = (__bf16)x[b][8 * s2 + e];
+                        p = __builtin_bit_cast(u32x4, h);
+                    }
 #pragma unroll
                     for (int d = 0; d < NB; ++d) {
                         LDS_PTR(char) v = lds + at + (b * 32 + s2 * 16) * RB + ((d * 64) ^ sw);
                         const s16x4 v0 = __builtin_amdgcn_ds_read_tr16_b64_v4i16((LDS_PTR(s16x4))v);
                         const s16x4 v1 = __builtin_amdgcn_ds_read_tr16_b64_v4i16((LDS_PTR(s16x4))(v + 8 * RB));
-                        o[d] = product<ES>(__builtin_bit_cast(u32x4, __builtin_shufflevector(v0, v1, 0, 1, 2, 3, 4, 5, 6, 7)), __builtin_bit_cast(u32x4, p), o[d]);
+                        const u32x4 y = __builtin_bit_cast(u32x4, __builtin_shufflevector(v0, v1, 0, 1, 2, 3, 4, 5, 6, 7));
+                        o[d] = HALF ? product_half(y, p, o[d]) : product<ES>(y, p, o[d]);
                     }
                 }
         } else {
@@ -715,6 +780,14 @@ void attention_tile(AttnArgs a, AttnPlan plan) {
     // ---- the end of an item's part: rows, or sums for the join
     auto leave = [&]() __attribute__((always_inline)) {
         l += other_half(l);
+        if constexpr (HALF) {
+            const float f = __builtin_amdgcn_exp2f(-shift);
+            l *= f;
+#pragma unroll
+            for (int b = 0; b < NB; ++b)
+#pragma unroll
+                for (int i = 0; i < 16; ++i) o[b][i] *= f;
+        }
         const float inv = l == 0.0f ? 0.0f : 1.0f / l;
         if (live) {
 #pragma unroll

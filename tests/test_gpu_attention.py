@@ -2,7 +2,7 @@
 the CPU.
 
 Tolerances.  u = 2^-24, u_w = 2^-8 for bf16 (the weights' rounding for the product
-with the values; none in fp32), u_out = finfo(type).eps / 2, n the keys a row sees,
+with the values, 2^-11 where the cache is int8; none in fp32), u_out = finfo(type).eps / 2, n the keys a row sees,
 A = sum w |v| / sum w.  A product with a key has D roundings of the sum of |q k|, and
 three more (the scales): delta = (D + 4) u scale sum |q k| at most, plus 4 u |x - max|
 for the exponential's argument and 4 u for the exponential.  Numerator and denominator
@@ -10,6 +10,11 @@ are each off by delta + n u relative to A (n additions, and a rescaling for each
 32 keys at least: n u in all counts both twice over), so
   |o - o*| <= 1.02 A (u_w + 2 (delta + (n + 16) u)) + u_out |o*|,
   |lse - lse*| <= 1.02 (delta + (n + 16) u) + 4 u |lse*|.
+Where the cache is int8 and the type bf16, a weight times its scale is rounded to fp16,
+to 2^-25 at best (half of its smallest step), in units in which the largest of the row, M,
+is 2^4 or more: by 2^-29 M or less, which a value's code multiplies.  So for codes c
+  |o - o*| gains 2^-29 M sum |c| / sum w,
+which counts in a feature whose code is zero at the largest scales.
 """
 import math
 
@@ -33,9 +38,10 @@ def workspace(T, B, Hq, Hkv, D):
 
 class Cached:
     """Sequences with `past` tokens before their `lens` new ones in a paged cache; all that no sequence holds is NaN
-    (an 8-bit cache: scales)."""
+    (an 8-bit cache: scales).  v_scales: exponents of two, smallest and largest, of further factors of the values' scales."""
 
-    def __init__(self, lens, past, Hkv, D, page, t, int8=False, seed=0, order="slot", pad=0, lead=0, tail=0, extra_pages=3):
+    def __init__(self, lens, past, Hkv, D, page, t, int8=False, seed=0, order="slot", pad=0, lead=0, tail=0, extra_pages=3,
+                 v_scales=(0, 0)):
         g = torch.Generator().manual_seed(seed)
         self.lens, self.past, self.Hkv, self.D, self.page, self.t, self.int8 = lens, past, Hkv, D, page, t, int8
         total = [max(0, n + p) for n, p in zip(lens, past)]
@@ -59,6 +65,7 @@ class Cached:
             return view(torch.full(mem + [D + pad], NAN).to(t)[..., :D]), None
         (self.kc, self.ks), (self.vc, self.vs) = make(), make()
         self.k, self.v = [], []       # in 64 bits, [keys, Hkv, D]
+        self.v_scale = []             # int8: [keys, Hkv]
         for s, n in enumerate(total):
             mine, ids = ids[:need[s]], ids[need[s]:]
             self.table[s, :need[s]] = torch.tensor(mine, dtype=torch.int32)
@@ -67,6 +74,8 @@ class Cached:
                 if int8:
                     x = torch.randint(-127, 128, (n, Hkv, D), generator=g).to(torch.int8)
                     f = (torch.rand((n, Hkv), generator=g) + 0.5) / 64
+                    if c is self.vc and v_scales != (0, 0):
+                        f *= 2.0 ** torch.randint(v_scales[0], v_scales[1] + 1, (n, Hkv), generator=g)
                     wide.append(x.double() * f.double()[..., None])
                 else:
                     x = torch.randn((n, Hkv, D), generator=g).to(t)
@@ -78,6 +87,8 @@ class Cached:
                         sc[mine[j // page], :len(rows)] = f[j:j + page]
             self.k.append(wide[0])
             self.v.append(wide[1])
+            if int8:
+                self.v_scale.append(f.double())
 
     def dev(self):
         place = lambda x: None if x is None else _like(x)  # noqa: E731
@@ -99,7 +110,7 @@ def reference(c, Q, Hq, window, scale, see=lambda s, j: True):
     o = torch.zeros(c.T, Hq, D, dtype=torch.float64)
     lse = torch.full((c.T, Hq), -math.inf, dtype=torch.float64)
     eo, el = torch.zeros_like(o), torch.zeros_like(lse)
-    u_w = 2.0 ** -8 if c.t == BF else 0.0
+    u_w = 0.0 if c.t == F32 else 2.0 ** -11 if c.int8 and c.D % 8 == 0 and c.D <= 256 else 2.0 ** -8
     q = Q.double().view(c.T, Hq, D)
     for s in range(len(c.lens)):
         for i in range(c.lens[s]):
@@ -118,7 +129,10 @@ def reference(c, Q, Hq, window, scale, see=lambda s, j: True):
             lse[t] = m + l.log()
             A = (w[..., None] * v.abs()).sum(0) / l[:, None]
             delta = ((D + 4) * U * mag + 4 * U * (x - m).abs()).max(0).values + (len(js) + 20) * U
-            eo[t] = 1.02 * A * (u_w + 2 * delta[:, None]) + torch.finfo(c.t).eps / 2 * o[t].abs()
+            if c.int8 and c.t == BF:
+                sc = c.v_scale[s][js].repeat_interleave(G, 1)                      # [n, Hq]
+                eo[t] = 1.02 * 2.0 ** -29 * ((w * sc).max(0).values / l)[:, None] * (v / sc[..., None]).abs().sum(0)
+            eo[t] += 1.02 * A * (u_w + 2 * delta[:, None]) + torch.finfo(c.t).eps / 2 * o[t].abs()
             el[t] = 1.02 * delta + 4 * U * lse[t].abs()
     return o, lse, eo, el
 
@@ -207,6 +221,15 @@ def test_long(lens, past, shape, t, int8):
     """Keys enough that several workgroups share a row, and rows enough that they do not."""
     Hq, Hkv, D, page = shape
     check(Cached(lens, past, Hkv, D, page, t, int8, seed=11), Hq)
+
+
+@pytest.mark.parametrize("t", [BF, F32])
+@pytest.mark.parametrize("v_scales", [(-90, -90), (-60, -50), (60, 60), (-40, 40), (-12, 3)])
+@pytest.mark.parametrize("lens,past,shape", [([1, 1], [700, 5], (8, 2, 128, 16)), ([40, 3], [100, 0], (4, 2, 64, 16)), ([1], [3000], (4, 1, 96, 16))])
+def test_scales_of_any_size(lens, past, shape, v_scales, t):
+    """8-bit values whose scales are tiny or huge, or both in one row."""
+    Hq, Hkv, D, page = shape
+    check(Cached(lens, past, Hkv, D, page, t, True, seed=4, v_scales=v_scales), Hq)
 
 
 @pytest.mark.parametrize("t,int8", TYPES)
