@@ -29,11 +29,12 @@ void attention_any(AttnArgs a, int64_t w0, int64_t waves) {
     const int32_t *table = a.c.table + s * a.c.ldt;
     const int64_t p = (int64_t)a.c.past[s] + (t - a.c.cu[s]);
     const int64_t first = p - a.window + 1 > 0 ? p - a.window + 1 : 0;
+    const int64_t held = a.c.max_pages * (int64_t)a.c.page, last = p < held ? p : held - 1;   // positions of the table
     const int64_t q0 = t * a.ldq + (int64_t)h * D;
     float m = -INFINITY, l = 0.0f, o[FEATURES] = {};
     bool bad = false;
-    for (int64_t j0 = first; j0 <= p; j0 += 64) {
-        const bool seen = j0 + lane <= p;
+    for (int64_t j0 = first; j0 <= last; j0 += 64) {
+        const bool seen = j0 + lane <= last;
         Row r{-1, 0};
         if (seen) r = row_of(a.c, table, (uint32_t)(j0 + lane));
         bad |= seen && r.page < 0;
@@ -72,7 +73,7 @@ void attention_any(AttnArgs a, int64_t w0, int64_t waves) {
                 if (lane + 64 * i < D) o[i] = __builtin_fmaf(ej, cached<CS>(a.c.vc, v0 + lane + 64 * i), o[i]);
         }
     }
-    if (p < 0) bad = true;
+    if (p < 0 || p >= held) bad = true;
     if (__any(bad) && lane == 0 && a.c.bad) *a.c.bad = 1;
     const float inv = l == 0.0f ? 0.0f : 1.0f / l;
 #pragma unroll

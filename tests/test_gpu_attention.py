@@ -417,3 +417,99 @@ def test_long_cache_offsets():
     tl.tp_kv_attention(Q.to(DEV), args["past"], args["cu"], table, kc, vc, O, workspace(6, 2, 4, 1, D))
     want, _, eo, _ = reference(c, Q, 4, 0, D ** -0.5)
     assert ((O.cpu().double().view(6, 4, D) - want).abs() <= eo).all()
+
+
+@pytest.mark.parametrize("t,int8", TYPES)
+@pytest.mark.parametrize("Hq,Hkv,D", [(8, 2, 128), (4, 4, 64), (3, 1, 50)])
+@pytest.mark.parametrize("T", [9, 300])
+def test_lengths_that_are_none(T, Hq, Hkv, D, t, int8):
+    """Row offsets out of order or outside the call and any past: nothing outside the call's rows is touched."""
+    big = 2 ** 31 - 1
+    c = Cached([T // 3] * 3, [40, 50, 20], Hkv, D, 16, t, int8, seed=5)
+    args, scales = c.dev()
+    ws = workspace(c.T, 3, Hq, Hkv, D)
+    Q = torch.randn((c.T, Hq * D), generator=torch.Generator().manual_seed(1)).to(t).to(DEV)
+    for cu in ([0, T, 0, T], [T, 5, 3, 0], [-7, 4, big, -big - 1], [5, 5, 5, big], [-big, -5, -3, -1], [big] * 4, [-big - 1, big, -big - 1, big]):
+        for past in ([0, 9, 30], [big, -big - 1, big], [-big - 1] * 3, [-5, big, 0]):
+            O, L = torch.full((c.T + 8, Hq * D), 9.0, dtype=t, device=DEV), torch.full((c.T + 8, Hq), 9.0, device=DEV)
+            print("lengths", T, Hq, Hkv, D, t, int8, cu, past, flush=True)
+            tl.tp_kv_attention(Q, torch.tensor(past, dtype=torch.int32, device=DEV), torch.tensor(cu, dtype=torch.int32, device=DEV), args["table"],
+                               args["k_cache"], args["v_cache"], O[4:-4], ws, **scales, lse=L[4:-4])
+            torch.cuda.synchronize()
+            assert (O[:4] == 9.0).all() and (O[-4:] == 9.0).all() and (L[:4] == 9.0).all() and (L[-4:] == 9.0).all()
+
+
+@pytest.mark.parametrize("t,int8", TYPES)
+@pytest.mark.parametrize("Hq,Hkv,D", [(8, 2, 128), (3, 1, 50)])
+@pytest.mark.parametrize("n", [1, 50])
+def test_positions_past_the_table(n, Hq, Hkv, D, t, int8):
+    """A past far beyond the table sees all that the table holds, or with a window nothing, as one just beyond it does."""
+    c = Cached([n, n], [200, 90], Hkv, D, 16, t, int8, seed=5)
+    c.table %= c.n_pages
+    c.ks, c.vs = (None if x is None else torch.where(x.isnan(), torch.ones_like(x), x) for x in (c.ks, c.vs))
+    c.kc, c.vc = (x if int8 else torch.where(x.isnan(), torch.ones_like(x), x) for x in (c.kc, c.vc))
+    args, scales = c.dev()
+    ws = workspace(c.T, 2, Hq, Hkv, D)
+    Q = torch.randn((c.T, Hq * D), generator=torch.Generator().manual_seed(1)).to(t).to(DEV)
+    end = c.max_pages * c.page
+
+    def call(past, window):
+        O, L, flag = torch.empty_like(Q), torch.empty((c.T, Hq), device=DEV), torch.zeros(1, dtype=torch.int32, device=DEV)
+        args["past"].fill_(past)
+        tl.tp_kv_attention(Q, args["past"], args["cu"], args["table"], args["k_cache"], args["v_cache"], O, ws, **scales, window=window, lse=L, bad=flag)
+        assert flag.item() == 1
+        return O, L
+    want, wl = call(end, 0)
+    assert torch.isfinite(want).all() and torch.isfinite(wl).all()
+    for past in (2 ** 29 + 5, 2 ** 31 - 1 - n):
+        O, L = call(past, 0)
+        assert torch.equal(O, want) and torch.equal(L, wl)
+        O, L = call(past, 77)
+        assert (O == 0).all() and (L == -math.inf).all()
+
+
+def test_rows_of_many_tokens_again():
+    """Calls whose items fill the GPU by themselves, bit for bit the same again."""
+    c = Cached([500, 3, 257, 128], [100, 900, 0, 64], 2, 128, 16, BF, seed=9)
+    args, _ = c.dev()
+    Q = torch.randn((c.T, 16 * 128), generator=torch.Generator().manual_seed(1)).to(BF).to(DEV)
+    ws = workspace(c.T, 4, 16, 2, 128)
+
+    def call():
+        O = torch.empty_like(Q)
+        tl.tp_kv_attention(Q, args["past"], args["cu"], args["table"], args["k_cache"], args["v_cache"], O, ws)
+        return O
+    first = call()
+    for _ in range(5):
+        assert torch.equal(call(), first)
+
+
+def test_two_graphs_in_one_workspace():
+    """Two captured calls of different sizes that share a workspace, replayed in turn with eager calls between them."""
+    cs = [Cached([1] * 7, [900, 3, 40, 0, 2000, 77, 1], 2, 128, 16, BF), Cached([90, 1], [300, 2500], 2, 128, 16, BF)]
+    n = max(tl.tp_kv_attention_workspace_bytes(c.T, len(c.lens), 8, 2, 128) for c in cs)
+    ws = torch.full((max(n, 256),), 255, dtype=torch.uint8, device=DEV)
+    calls, outs, graphs = [], [], []
+    for c in cs:
+        args, _ = c.dev()
+        Q = torch.randn((c.T, 8 * 128), generator=torch.Generator().manual_seed(1)).to(BF).to(DEV)
+        O = torch.empty_like(Q)
+        calls.append(lambda a=args, q=Q, o=O: tl.tp_kv_attention(q, a["past"], a["cu"], a["table"], a["k_cache"], a["v_cache"], o, ws))
+        outs.append(O)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    for call in calls:
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph, stream=side):
+            call()
+        graphs.append(graph)
+    for call in calls:
+        call()
+    want = [o.clone() for o in outs]
+    for k in (0, 1, 1, 0, 1, 0):
+        outs[k].zero_()
+        graphs[k].replay()
+        torch.cuda.synchronize()
+        assert torch.equal(outs[k], want[k])
+        calls[1 - k]()
+        assert torch.equal(outs[1 - k], want[1 - k])
