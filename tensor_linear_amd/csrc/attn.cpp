@@ -30,6 +30,12 @@ bool dma_ok(const AttnArgs &a, int es) {
 
 AttnPlan attention_plan(int64_t T, int64_t B, int64_t Hkv, int32_t G, int64_t D, int es, bool quant) {
     AttnPlan p{};
+    // Of 2^(31 + i) / G rounded up, 2^i >= G, x < 2^31 times what was added is less than
+    // 2^(31 + i) / G, which no quotient feels.
+    int i = 0;
+    while (((int64_t)1 << i) < G) ++i;
+    p.by_shift = 31 + i;
+    p.by_g = (uint32_t)((((uint64_t)1 << p.by_shift) + (uint64_t)G - 1) / (uint64_t)G);
     // 32 rows a workgroup where the sequences have no more on average
     p.few = T * G <= 32 * B;
     const int64_t rows = p.few ? 32 : 128;

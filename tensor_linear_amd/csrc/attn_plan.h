@@ -12,8 +12,9 @@ constexpr int32_t PLAN_FAR = 1 << 29;   // what positions and counts of tokens a
 
 // stream: the tiles of all items in `groups` equal runs; else a workgroup for each of
 // the row_tiles * Hkv items.  few: 32 rows a workgroup, else 128.
-// last_pos: positions of the table; window: 2 PLAN_FAR for none.
-struct AttnPlan { int32_t stream, few, groups, last_pos, window; int64_t row_tiles; };
+// last_pos: positions of the table; window: 2 PLAN_FAR for none.  by_g, by_shift: x / G is
+// x by_g >> by_shift for x < 2^31.
+struct AttnPlan { int32_t stream, few, groups, last_pos, window; uint32_t by_g; int32_t by_shift; int64_t row_tiles; };
 
 // The plan of a call of these sizes and types (the lengths are on the device: T, B and the
 // heads are all that the host knows).

@@ -205,7 +205,12 @@ void attention_tile(AttnArgs a, AttnPlan plan) {
     __shared__ __attribute__((aligned(256))) float row_scale[2][2][QUANT ? 64 : 4];
     __shared__ Tile tiles[4];                          // of this tile and the two after it
     __shared__ Item items[4];
-    __shared__ int scan[NW + 2];
+    __shared__ int scan[NW];
+    // Where a run is (wavefront 0's, in LDS since scalar registers are short): its units
+    // left, the sequence of the next with its row tiles, the next item's head and row tile;
+    // of the first one the units before the sequence and those of one of its heads.
+    __shared__ struct { int u, u1, all, W, first, seq, base, units, nr, h, r; Sequence q; } walk;
+    __shared__ Sequence known[NTH];                    // the call's sequences, if they are no more
     __shared__ int found[2];
     __shared__ uint64_t odd[QUANT ? 1 : 2][QUANT ? 1 : DP];   // keys whose value of a feature is not finite: up, down
     LDS_PTR(char) lds = (LDS_PTR(char))smem;
@@ -220,25 +225,43 @@ void attention_tile(AttnArgs a, AttnPlan plan) {
     const int chunks = D * LS / 16;                                     // of a row in LDS that hold features
 
     auto sequence = [&](int s) { return plan_sequence(c, s); };
-    auto span = [&](const Sequence &q, int r) { return plan_span(q, r, G, ROWS, BK, window_of, last_pos); };
+    auto span = [&](const Sequence &q, int r) { return plan_span(plan, q, r, G, ROWS, BK); };
     auto row_tiles = [&](const Sequence &q) { return (q.n * G + ROWS - 1) / ROWS; };
-    // units of one head of a sequence: its tiles, and the changes between its items
+    // Units of one head of each lane's sequence (its tiles, and the changes between its
+    // items): by the lane where they are few, else by all lanes for one after another.
     auto count = [&](const Sequence &q) {
         const int nr = row_tiles(q);
         int n = nr * CHANGE;
-        for (int r = 0; r < nr; ++r) n += span(q, r).tiles;
+        if (!__any(nr > 16)) {
+            for (int r = 0; r < nr; ++r) n += span(q, r).tiles;
+            return n;
+        }
+        for (uint64_t todo = __ballot(nr > 0); todo; todo &= todo - 1) {
+            const int j = __builtin_ctzll(todo);
+            const Sequence p{0, __shfl(q.n, j), __shfl(q.past, j)};
+            int v = 0;
+            for (int r = lane; r < row_tiles(p); r += 64) v += span(p, r).tiles;
+#pragma unroll
+            for (int o = 32; o > 0; o >>= 1) v += __shfl_xor(v, o);
+            if (lane == j) n += v;
+        }
         return n;
     };
 
     // ---- the run of units of this workgroup
-    int all = 0, u = 0, u1 = 0, base = 0, seq = 0;       // units in all, the run [u, u1); the first one of sequence seq
-    int W = plan.groups;                                 // runs that have units
     int w = blockIdx.x;
     const int B = (int)c.B;
     if (plan.stream) {
+        int all = 0, W = plan.groups;                   // units in all, runs that have any
         const int per = B <= NTH ? 1 : (B + NTH - 1) / NTH, sb = tid * per;
         int mine = 0;
-        for (int i = sb; i < sb + per && i < B; ++i) mine += count(sequence(i));
+        for (int i = sb; i < sb + per; ++i) {           // in step: count() takes whole wavefronts
+            Sequence q{};
+            if (i < B) q = sequence(i);
+            const int n = count(q);
+            mine += n;
+            if (per == 1) known[tid] = q;
+        }
         int run = mine;
 #pragma unroll
         for (int o = 1; o < 64; o <<= 1) {
@@ -246,7 +269,6 @@ void attention_tile(AttnArgs a, AttnPlan plan) {
             if (lane >= o) run += v;
         }
         if (lane == 63) scan[wave] = run;
-        if (tid == 0) scan[NW] = B;
         meet<WR>();
         int before = 0;
         for (int i = 0; i < NW; ++i) {
@@ -259,46 +281,105 @@ void attention_tile(AttnArgs a, AttnPlan plan) {
         if (tid == 0) plan_desc(a.ws)[w].pieces = 0;
         if (w >= W) return;
         auto cut = [&](int i) { return W < plan.groups ? i : (int)((int64_t)all * i / plan.groups); };
-        u = cut(w);
-        u1 = cut(w + 1);
+        const int u = cut(w);
+        if (tid == 0) {
+            walk.u = u;
+            walk.u1 = cut(w + 1);
+            walk.all = all;
+            walk.W = W;
+            walk.seq = B;
+            walk.first = 1;
+        }
+        meet<WR>();
         int at = (before + run - mine) * c.Hkv;
-        if (u >= at && u < (before + run) * c.Hkv) {    // one thread
-            for (int i = sb; i < sb + per && i < B; ++i) {
-                const int n = (per == 1 ? mine : count(sequence(i))) * c.Hkv;
-                if (u < at + n) {
-                    scan[NW] = i;
-                    scan[NW + 1] = at;
-                    break;
+        const bool here = u >= at && u < (before + run) * c.Hkv;       // one thread
+        if (per == 1) {
+            if (here) {
+                walk.seq = tid;
+                walk.base = at;
+                walk.units = mine;
+            }
+        } else {
+            bool open = here;
+            for (int i = sb; i < sb + per && __any(open); ++i) {
+                Sequence q{};
+                if (i < B) q = sequence(i);
+                const int n = count(q);
+                if (open && u < at + n * c.Hkv) {
+                    walk.seq = i;
+                    walk.base = at;
+                    walk.units = n;
+                    open = false;
                 }
-                at += n;
+                at += n * c.Hkv;
             }
         }
         meet<WR>();
-        seq = uniform(scan[NW]);
-        base = uniform(scan[NW + 1]);
     }
     int stamp = 0;
     if (tid < 2) found[tid] = -1;
 
-    // The next item and the part of its tiles (wavefront 0).
+    // The next item and the part of its tiles (wavefront 0): the run's first by search, the
+    // ones after it in order.
     bool first_item = true;
+    auto known_sequence = [&](int i) {
+        Sequence q;
+        if (B <= NTH) q = known[i];
+        else q = sequence(i);
+        return Sequence{uniform(q.first), uniform(q.n), uniform(q.past)};
+    };
     auto find_item = [&]() {
         Item m{};
         m.s = -1;
         if (plan.stream) {
+            int u = uniform(walk.u), seq = uniform(walk.seq), h = uniform(walk.h), r = uniform(walk.r), nr = uniform(walk.nr);
+            const int u1 = uniform(walk.u1);
+            Sequence q{uniform(walk.q.first), uniform(walk.q.n), uniform(walk.q.past)};
+            bool begin = uniform(walk.first);
             while (u < u1 && seq < B) {
-                const Sequence q = sequence(seq);
-                const int n = uniform(count(q));
-                if (u >= base + n * c.Hkv) { base += n * c.Hkv; ++seq; continue; }
-                int rem = u - base;
-                m.h = (uint32_t)rem / (uint32_t)n;
-                rem -= m.h * n;
-                const int nr = row_tiles(q);
-                Span sp = span(q, 0);
-                int r = 0;
-                while (rem >= CHANGE + sp.tiles && r + 1 < nr) { rem -= CHANGE + sp.tiles; sp = span(q, ++r); }
+                int rem = 0;
+                if (begin) {
+                    begin = false;
+                    const int units = uniform(walk.units);
+                    q = known_sequence(seq);
+                    nr = row_tiles(q);
+                    rem = u - uniform(walk.base);
+                    if (units <= 0 || rem < 0) break;       // sums past 32 bits, of lengths that no call has
+                    h = (uint32_t)rem / (uint32_t)units;
+                    if (h >= c.Hkv) break;
+                    rem -= h * units;
+                    // the row tile in which the units up to `rem` end, of 64 at a time
+                    bool got = false;
+                    for (int r0 = 0; r0 < nr && !got; r0 += 64) {
+                        const int t = r0 + lane < nr ? CHANGE + span(q, r0 + lane).tiles : 0;
+                        int v = t;
+#pragma unroll
+                        for (int o = 1; o < 64; o <<= 1) {
+                            const int y = __shfl_up(v, o);
+                            if (lane >= o) v += y;
+                        }
+                        const uint64_t beyond = __ballot(rem < v && t > 0);
+                        got = beyond != 0;
+                        const int j = got ? __builtin_ctzll(beyond) : 63;
+                        r = r0 + j;
+                        rem -= uniform(__shfl(got ? v - t : v, j));
+                    }
+                    if (!got) break;
+                } else if (++r >= nr) {
+                    r = 0;
+                    if (++h >= c.Hkv) {
+                        h = 0;
+                        r = -1;                             // the next step's is the sequence's first, if it has rows
+                        if (++seq >= B) break;
+                        q = known_sequence(seq);
+                        nr = row_tiles(q);
+                        if (nr == 0) h = c.Hkv;
+                        continue;
+                    }
+                }
+                const Span sp = span(q, r);
                 const int item_u = u - rem, end = item_u + CHANGE + sp.tiles;       // the item's units
-                m.q = q; m.sp = sp; m.r = r;
+                m.q = q; m.sp = sp; m.r = r; m.h = h;
                 m.k0 = rem > CHANGE ? rem - CHANGE : 0;
                 m.k1 = (u1 < end ? u1 : end) - item_u - CHANGE;
                 u = end;
@@ -306,12 +387,20 @@ void attention_tile(AttnArgs a, AttnPlan plan) {
                 m.s = seq;
                 m.pieces = 1;
                 if (end > u1) {
-                    int to = (int)(((int64_t)end * W - 1) / all);               // the run with the item's last tile
+                    const int W = uniform(walk.W);
+                    int to = (int)(((int64_t)end * W - 1) / uniform(walk.all));     // the run with the item's last tile
                     if (to >= W) to = W - 1;
                     m.pieces = to - w + 1;
                 }
                 break;
             }
+            walk.u = u;
+            walk.seq = seq;
+            walk.h = h;
+            walk.r = r;
+            walk.nr = nr;
+            walk.q = q;
+            walk.first = 0;
         } else if (first_item) {
             first_item = false;
             const int i = (int)plan.row_tiles - 1 - w / c.Hkv;
@@ -344,8 +433,8 @@ void attention_tile(AttnArgs a, AttnPlan plan) {
 
     // ---- rows of a tile: where they are, and which there are (wavefront 0, in the order
     // of the run's tiles; numbers of tiles and items go round in rings)
-    int ahead_s = -1, ahead_begin = 0, ahead_end = 0, ahead_first = 0;
-    int ahead_k = 0, ahead_k0 = 0, ahead_k1 = 0, ahead_h = 0, ahead_item = -1;
+    int ahead_s = -1, ahead_begin = 0, ahead_end = 0, ahead_t0 = 0;
+    int ahead_left = 0, ahead_h = 0, ahead_item = -1;
     // Entries of the table: lane i has entry `window + i` of the sequence's, so that a tile
     // needs a load only where it leaves them.
     int32_t entry = -1;
@@ -353,8 +442,10 @@ void attention_tile(AttnArgs a, AttnPlan plan) {
     const char *scale_k = (const char *)no_key, *scale_v = (const char *)no_key;     // of this lane's row of the last tile looked up
     auto page_of = [&](uint32_t p) { return (int)(c.shift >= 0 ? p >> c.shift : p / c.page); };
     auto look = [&](int n) {
-        if (ahead_s >= 0 && ahead_k + 1 < ahead_k1) {
-            ++ahead_k;
+        const bool begins = ahead_left == 0;
+        if (!begins) {
+            --ahead_left;
+            ahead_t0 += BK;
         } else {
             const Item m = find_item();
             ahead_item = (ahead_item + 1) & 3;
@@ -362,13 +453,12 @@ void attention_tile(AttnArgs a, AttnPlan plan) {
             ahead_s = uniform(m.s);
             ahead_begin = uniform(m.sp.begin);
             ahead_end = uniform(m.sp.end);
-            ahead_first = uniform(m.sp.first);
+            ahead_t0 = (uniform(m.sp.first) + uniform(m.k0)) * BK;
             ahead_h = uniform(m.h);
-            ahead_k = ahead_k0 = uniform(m.k0);
-            ahead_k1 = uniform(m.k1);
+            ahead_left = ahead_s >= 0 ? uniform(m.k1) - uniform(m.k0) - 1 : 0;
             window = -64;                               // another sequence's
         }
-        const int t0 = (ahead_first + ahead_k) * BK, p = t0 + lane;
+        const int t0 = ahead_t0, p = t0 + lane;
         const bool want = lane < BK && ahead_s >= 0 && p >= ahead_begin && p < ahead_end;
         // pages of the tile's first and last position that count
         const int lo_p = t0 > ahead_begin ? t0 : ahead_begin, hi_p = t0 + BK < ahead_end ? t0 + BK : ahead_end;
@@ -396,8 +486,8 @@ void attention_tile(AttnArgs a, AttnPlan plan) {
             t.rows = m;
             t.first = t0;
             t.item = ahead_s >= 0 ? ahead_item : -1;
-            t.begins = ahead_k == ahead_k0;
-            t.ends = ahead_k + 1 == ahead_k1;
+            t.begins = begins;
+            t.ends = ahead_left == 0;
         }
         if (QUANT) {
             const int64_t at = (int64_t)id * c.ss_page + (int64_t)slot * c.ss_slot + ahead_h * c.ss_head;
@@ -503,7 +593,7 @@ void attention_tile(AttnArgs a, AttnPlan plan) {
         if ((pos0 < 0 || pos1 >= last_pos) && c.bad && tid == 0) *c.bad = 1;
         const int R = item_r * ROWS + wr * 32 + col;
         live = R < rows;
-        const int tok = live ? (int)((uint32_t)R / (uint32_t)G) : 0;
+        const int tok = live ? plan_token(plan, R) : 0;
         head = item_h * G + (live ? R - tok * G : 0);
         row = first + tok;
         hi = live ? past + tok : -1;

@@ -139,6 +139,11 @@ int main() {
     c = Call(); c.T = 1000; c.B = 1000; c.max_pages = 1 << 18; taken(c, "bf16"); CHECK(!lp.stream);   // units of all runs past 2^31
     c = Call(); c.page = 48; taken(c, "bf16"); CHECK(la.c.shift == -1 && la.c.page == 48);
 
+    for (int64_t G = 1; G <= 65536; ++G) {
+        const tpl::AttnPlan p = tpl::attention_plan(64, 1, 1, (int32_t)G, 64, 2, false);
+        for (const uint32_t x : {0u, (uint32_t)G - 1, (uint32_t)G, (uint32_t)(INT32_MAX / G * G), (uint32_t)(INT32_MAX / G * G - 1), (uint32_t)INT32_MAX})
+            CHECK((uint32_t)((uint64_t)x * p.by_g >> p.by_shift) == x / (uint32_t)G);
+    }
     // The workspace of the sizes holds the plan of every type.
     for (int i = 0; i < 200000; ++i) {
         const int64_t G = draw(1, 16), Hkv = draw(1, 16), D = 8 * draw(1, 33), B = draw(1, i % 3 ? 64 : 4000), T = draw(1, i % 2 ? 200 : 1 << 20);
@@ -147,6 +152,8 @@ int main() {
         for (int k = 0; k < 4 && D <= 256; ++k) {
             const tpl::AttnPlan p = tpl::attention_plan(T, B, Hkv, (int32_t)G, D, k & 1 ? 4 : 2, k & 2);
             CHECK(p.groups >= 8 && p.groups % 8 == 0);
+            for (const uint32_t x : {0u, 1u, (uint32_t)G - 1, (uint32_t)G, (uint32_t)draw(0, INT32_MAX), (uint32_t)(draw(0, INT32_MAX / G) * G), (uint32_t)INT32_MAX})
+                CHECK((uint32_t)((uint64_t)x * p.by_g >> p.by_shift) == x / (uint32_t)G);
             if (p.stream) CHECK(n >= (size_t)(tpl::plan_desc_bytes(p.groups) + tpl::plan_stats_bytes(p.groups) + 2 * p.groups * (p.few ? 32 : 128) * d * 4));
         }
         CHECK(n <= 300u << 20);
