@@ -30,12 +30,7 @@ bool dma_ok(const AttnArgs &a, int es) {
 
 AttnPlan attention_plan(int64_t T, int64_t B, int64_t Hkv, int32_t G, int64_t D, int es, bool quant) {
     AttnPlan p{};
-    // Of 2^(31 + i) / G rounded up, 2^i >= G, x < 2^31 times what was added is less than
-    // 2^(31 + i) / G, which no quotient feels.
-    int i = 0;
-    while (((int64_t)1 << i) < G) ++i;
-    p.by_shift = 31 + i;
-    p.by_g = (uint32_t)((((uint64_t)1 << p.by_shift) + (uint64_t)G - 1) / (uint64_t)G);
+    p.g = divisor(G);
     // 32 rows a workgroup where the sequences have no more on average
     p.few = T * G <= 32 * B;
     const int64_t rows = p.few ? 32 : 128;
@@ -65,6 +60,8 @@ hipError_t launch_kv_attention(const AttnArgs &a, int es, hipStream_t s) {
     AttnPlan p = attention_plan(a.c.T, a.c.B, a.c.Hkv, a.G, a.c.D, es, a.c.ks != nullptr);
     p.last_pos = (int32_t)(a.c.max_pages * (int64_t)a.c.page);
     p.window = (int32_t)(a.window < 2 * FAR ? a.window : 2 * FAR);
+    p.page = divisor(a.c.page);
+    p.n_pages = (uint32_t)(a.c.n_pages < (int64_t)1 << 31 ? a.c.n_pages : (int64_t)1 << 31);
     // units of a run: tiles of 32 keys and changes of items, counted in 32 bits
     if (p.stream && p.row_tiles * (p.last_pos / 32 + 8) * a.c.Hkv >= INT32_MAX) p.stream = 0;
     if (!p.stream && p.row_tiles * a.c.Hkv > (1 << 23)) return launch_attention_any(a, es, s);   // more than one launch holds

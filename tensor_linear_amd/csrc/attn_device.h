@@ -99,13 +99,13 @@ __device__ __forceinline__ int plan_index(const CacheArgs &c, int s, int G, int 
 // its rows see (those of the table), and the tiles of BK that hold them; at least one, so
 // that rows that see nothing are written.
 struct Span { int pos0, pos1, begin, end, first, tiles; };
-__device__ __forceinline__ int plan_token(const AttnPlan &p, uint32_t row) { return (int)((uint64_t)row * p.by_g >> p.by_shift); }   // row / G
+__device__ __forceinline__ int plan_divide(uint32_t x, const Divisor &d) { return (int)((uint64_t)x * d.by >> d.shift); }
 __device__ __forceinline__ Span plan_span(const AttnPlan &p, const Sequence &q, int r, int G, int ROWS, int BK) {
     const int window = p.window, last_pos = p.last_pos;
     Span s;
     const uint32_t row = (uint32_t)r * ROWS, all = (uint32_t)(q.n * G), rows = all - row < (uint32_t)ROWS ? all - row : ROWS;
-    s.pos0 = q.past + plan_token(p, row);
-    s.pos1 = q.past + plan_token(p, row + rows - 1);
+    s.pos0 = q.past + plan_divide(row, p.g);
+    s.pos1 = q.past + plan_divide(row + rows - 1, p.g);
     s.begin = s.pos0 - window + 1 > 0 ? s.pos0 - window + 1 : 0;
     s.end = s.pos1 + 1 < last_pos ? s.pos1 + 1 : last_pos;
     if (s.end < 0) s.end = 0;

@@ -10,11 +10,19 @@ namespace tpl {
 
 constexpr int32_t PLAN_FAR = 1 << 29;   // what positions and counts of tokens are below
 
+// x / d = x by >> shift for x < 2^31: 2^(31 + i) / d rounded up, 2^i >= d, times x is too
+// large by less than 2^(31 + i) / d, which no quotient feels.
+struct Divisor { uint32_t by; int32_t shift; };
+inline Divisor divisor(int64_t d) {
+    int i = 0;
+    while (((int64_t)1 << i) < d) ++i;
+    return Divisor{(uint32_t)((((uint64_t)1 << (31 + i)) + (uint64_t)d - 1) / (uint64_t)d), 31 + i};
+}
+
 // stream: the tiles of all items in `groups` equal runs; else a workgroup for each of
 // the row_tiles * Hkv items.  few: 32 rows a workgroup, else 128.
-// last_pos: positions of the table; window: 2 PLAN_FAR for none.  by_g, by_shift: x / G is
-// x by_g >> by_shift for x < 2^31.
-struct AttnPlan { int32_t stream, few, groups, last_pos, window; uint32_t by_g; int32_t by_shift; int64_t row_tiles; };
+// last_pos: positions of the table; window: 2 PLAN_FAR for none; n_pages: 2^31 at most.
+struct AttnPlan { int32_t stream, few, groups, last_pos, window; uint32_t n_pages; int64_t row_tiles; Divisor g, page; };
 
 // The plan of a call of these sizes and types (the lengths are on the device: T, B and the
 // heads are all that the host knows).

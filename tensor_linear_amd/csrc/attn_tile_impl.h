@@ -122,9 +122,11 @@ __device__ __forceinline__ int uniform(int v) { return __builtin_amdgcn_readfirs
 // item's last.  s < 0: none.
 struct Item { int s; Sequence q; Span sp; int r, h, k0, k1, pieces; };
 
-// A tile of a run: its rows that hold keys, the position of the first, its item's place in
-// a ring (-1: there is none), whether it is the first and the last of the item's part.
-struct Tile { uint64_t rows; int first, item, begins, ends; };
+// A tile of a run: its rows that hold keys, the position of the first; what: its item's
+// place in a ring, with BEGINS in the first tile of the item's part and ENDS in its last
+// (-1: there is none).
+struct __attribute__((aligned(16))) Tile { uint64_t rows; int first, what; };
+enum { ITEMS = 4, BEGINS = 4, ENDS = 8 };
 
 // Tiles that the change from one item to the next costs a run in time (a wavefront by
 // itself: the query's loads, the sums' way out, the next item's lengths).
@@ -203,8 +205,8 @@ void attention_tile(AttnArgs a, AttnPlan plan) {
     __shared__ __attribute__((aligned(1024))) char smem[2 * STAGE];
     __shared__ struct { const char *k, *v; } row_at[2][BK];          // where the tiles' rows are
     __shared__ __attribute__((aligned(256))) float row_scale[2][2][QUANT ? 64 : 4];
-    __shared__ Tile tiles[4];                          // of this tile and the two after it
-    __shared__ Item items[4];
+    __shared__ Tile tiles[2];                          // the next tile and the one after it
+    __shared__ Item items[ITEMS];
     __shared__ int scan[NW];
     // Where a run is (wavefront 0's, in LDS since scalar registers are short): its units
     // left, the sequence of the next with its row tiles, the next item's head and row tile;
@@ -433,14 +435,13 @@ void attention_tile(AttnArgs a, AttnPlan plan) {
 
     // ---- rows of a tile: where they are, and which there are (wavefront 0, in the order
     // of the run's tiles; numbers of tiles and items go round in rings)
-    int ahead_s = -1, ahead_begin = 0, ahead_end = 0, ahead_t0 = 0;
-    int ahead_left = 0, ahead_h = 0, ahead_item = -1;
+    int ahead_s = -1, ahead_begin = 0, ahead_end = 0, ahead_t0 = 0, ahead_left = 0, ahead_item = -1;
+    int64_t ahead_at = 0, ahead_sat = 0;               // of the head in the cache's rows, and among the scales
     // Entries of the table: lane i has entry `window + i` of the sequence's, so that a tile
     // needs a load only where it leaves them.
     int32_t entry = -1;
     int window = 0;
     const char *scale_k = (const char *)no_key, *scale_v = (const char *)no_key;     // of this lane's row of the last tile looked up
-    auto page_of = [&](uint32_t p) { return (int)(c.shift >= 0 ? p >> c.shift : p / c.page); };
     auto look = [&](int n) {
         const bool begins = ahead_left == 0;
         if (!begins) {
@@ -448,49 +449,40 @@ void attention_tile(AttnArgs a, AttnPlan plan) {
             ahead_t0 += BK;
         } else {
             const Item m = find_item();
-            ahead_item = (ahead_item + 1) & 3;
+            ahead_item = (ahead_item + 1) % ITEMS;
             if (lane == 0) items[ahead_item] = m;
             ahead_s = uniform(m.s);
             ahead_begin = uniform(m.sp.begin);
-            ahead_end = uniform(m.sp.end);
+            ahead_end = ahead_s >= 0 ? uniform(m.sp.end) : 0;       // of no item no position is looked up
             ahead_t0 = (uniform(m.sp.first) + uniform(m.k0)) * BK;
-            ahead_h = uniform(m.h);
+            ahead_at = uniform(m.h) * c.s_head;
+            ahead_sat = uniform(m.h) * c.ss_head;
             ahead_left = ahead_s >= 0 ? uniform(m.k1) - uniform(m.k0) - 1 : 0;
             window = -64;                               // another sequence's
         }
         const int t0 = ahead_t0, p = t0 + lane;
-        const bool want = lane < BK && ahead_s >= 0 && p >= ahead_begin && p < ahead_end;
-        // pages of the tile's first and last position that count
-        const int lo_p = t0 > ahead_begin ? t0 : ahead_begin, hi_p = t0 + BK < ahead_end ? t0 + BK : ahead_end;
-        if (ahead_s >= 0 && hi_p > lo_p) {
-            const int i0 = uniform(page_of(lo_p)), i1 = uniform(page_of(hi_p - 1));
-            if (i0 < window || i1 >= window + 64) {     // i1 - i0 < BK
-                window = i0;
-                entry = window + lane < (int)c.max_pages ? c.table[ahead_s * c.ldt + window + lane] : -1;
-                // waited for here, once in 64 pages, and not by every use below
-                asm volatile("s_waitcnt vmcnt(0)" : "+v"(entry) :: "memory");
-            }
+        const bool want = lane < BK && p >= ahead_begin && p < ahead_end;
+        const int i = plan_divide(p, plan.page);
+        if (__any(want && (uint32_t)(i - window) >= 64)) {
+            // from the tile's first position that counts on; its last is in less than BK pages
+            window = uniform(plan_divide(t0 > ahead_begin ? t0 : ahead_begin, plan.page));
+            entry = window + lane < (int)c.max_pages ? c.table[ahead_s * c.ldt + window + lane] : -1;
+            // waited for here, once in 64 pages, and not by every use below
+            asm volatile("s_waitcnt vmcnt(0)" : "+v"(entry) :: "memory");
         }
-        const int i = page_of(p), id = __shfl(entry, (i - window) & 63);
-        const uint32_t slot = (uint32_t)p - (c.shift >= 0 ? (uint32_t)i << c.shift : (uint32_t)i * c.page);
-        const bool ok = want && id >= 0 && id < c.n_pages;
-        if (want && !ok && c.bad) *c.bad = 1;
-        const uint64_t m = __ballot(ok);
+        const uint32_t id = (uint32_t)__builtin_amdgcn_ds_bpermute((i - window) * 4, entry);     // of lane (i - window) % 64
+        const uint32_t slot = (uint32_t)p - (uint32_t)i * c.page;
+        const bool ok = want && id < plan.n_pages;
+        if (__any(want && !ok) && c.bad) *c.bad = 1;
+        const uint64_t rows = __ballot(ok);
         if (lane < BK) {
-            const int64_t at = ((int64_t)id * c.s_page + (int64_t)slot * c.s_slot + ahead_h * c.s_head) * CS;
+            const int64_t at = ((int64_t)((uint64_t)id * (uint64_t)c.s_page + (uint64_t)slot * (uint64_t)c.s_slot) + ahead_at) * CS;
             row_at[n & 1][lane].k = ok ? (const char *)c.kc + at : (const char *)no_key;
             row_at[n & 1][lane].v = ok ? (const char *)c.vc + at : (const char *)no_key;
         }
-        if (lane == 0) {
-            Tile &t = tiles[n & 3];
-            t.rows = m;
-            t.first = t0;
-            t.item = ahead_s >= 0 ? ahead_item : -1;
-            t.begins = begins;
-            t.ends = ahead_left == 0;
-        }
+        if (lane == 0) tiles[n & 1] = Tile{rows, t0, ahead_s < 0 ? -1 : ahead_item | (begins ? BEGINS : 0) | (ahead_left == 0 ? ENDS : 0)};
         if (QUANT) {
-            const int64_t at = (int64_t)id * c.ss_page + (int64_t)slot * c.ss_slot + ahead_h * c.ss_head;
+            const int64_t at = (int64_t)((uint64_t)id * (uint64_t)c.ss_page + (uint64_t)slot * (uint64_t)c.ss_slot) + ahead_sat;
             scale_k = ok ? (const char *)(c.ks + at) : (const char *)no_key;
             scale_v = ok ? (const char *)(c.vs + at) : (const char *)no_key;
         }
@@ -593,7 +585,7 @@ void attention_tile(AttnArgs a, AttnPlan plan) {
         if ((pos0 < 0 || pos1 >= last_pos) && c.bad && tid == 0) *c.bad = 1;
         const int R = item_r * ROWS + wr * 32 + col;
         live = R < rows;
-        const int tok = live ? plan_token(plan, R) : 0;
+        const int tok = live ? plan_divide(R, plan.g) : 0;
         head = item_h * G + (live ? R - tok * G : 0);
         row = first + tok;
         hi = live ? past + tok : -1;
@@ -619,10 +611,8 @@ void attention_tile(AttnArgs a, AttnPlan plan) {
     };
 
     // ---- one tile
-    auto tile = [&](int n) __attribute__((always_inline)) {
+    auto tile = [&](int n, int t0, uint64_t valid) __attribute__((always_inline)) {
         const int st = n & 1;
-        const int t0 = uniform(tiles[n & 3].first);
-        const uint64_t valid = uniform64(tiles[n & 3].rows);
         const bool edge = t0 + BK - 1 > see_all || t0 < see_from;
         f32x16 x[KB];
         const uint32_t kl = place(n) + col * RB, ks = (half * 16) ^ k_swizzle<RB>(col);
@@ -906,12 +896,15 @@ void attention_tile(AttnArgs a, AttnPlan plan) {
     // instructions in the caches): tile n + 2 is looked up, tile n + 1 fetched, tile n worked
     // on.  A wavefront by itself (ALONE) fetches the next tile before this one is there, as
     // soon as its place in LDS is free; four wait for theirs first, and then for each other.
+    Tile now{0, 0, -1}, next{0, 0, -1};
     for (int n = -2;; ++n) {
         if (!ALONE && n >= 0) settle_all(n);
         meet<WR>();                                     // also: this wavefront's reads of the last tile are done
         bool more = true;
         if (n >= -1) {
-            more = uniform(tiles[(n + 1) & 3].item) >= 0;
+            const Tile t = tiles[(n + 1) & 1];
+            next = Tile{uniform64(t.rows), uniform(t.first), uniform(t.what)};
+            more = next.what >= 0;
             if (n < 0 && !more) return;
             if (more) {
                 fetch(n + 1, Const<0>());
@@ -923,11 +916,13 @@ void attention_tile(AttnArgs a, AttnPlan plan) {
             else settle_all(n);
         }
         if (more && wave == 0) look(n + 2);
-        if (n < 0) continue;
-        if (uniform(tiles[n & 3].begins)) enter(uniform(tiles[n & 3].item));
-        tile(n);
-        if (uniform(tiles[n & 3].ends)) leave();
-        if (!more) return;
+        if (n >= 0) {
+            if (now.what & BEGINS) enter(now.what % ITEMS);
+            tile(n, now.first, now.rows);
+            if (now.what & ENDS) leave();
+            if (!more) return;
+        }
+        now = next;
     }
 }
 

@@ -142,7 +142,13 @@ int main() {
     for (int64_t G = 1; G <= 65536; ++G) {
         const tpl::AttnPlan p = tpl::attention_plan(64, 1, 1, (int32_t)G, 64, 2, false);
         for (const uint32_t x : {0u, (uint32_t)G - 1, (uint32_t)G, (uint32_t)(INT32_MAX / G * G), (uint32_t)(INT32_MAX / G * G - 1), (uint32_t)INT32_MAX})
-            CHECK((uint32_t)((uint64_t)x * p.by_g >> p.by_shift) == x / (uint32_t)G);
+            CHECK((uint32_t)((uint64_t)x * p.g.by >> p.g.shift) == x / (uint32_t)G);
+    }
+    for (int i = 0; i < 100000; ++i) {
+        const int64_t d = i < 2 ? 0xFFFFFFFFll - i : draw(1, i % 2 ? 5000 : 0xFFFFFFFFll);
+        const tpl::Divisor v = tpl::divisor(d);
+        for (const int64_t x : {(int64_t)0, d - 1, d, draw(0, INT32_MAX), INT32_MAX / d * d, (int64_t)INT32_MAX})
+            CHECK(x > INT32_MAX || (int64_t)((uint64_t)x * v.by >> v.shift) == x / d);
     }
     // The workspace of the sizes holds the plan of every type.
     for (int i = 0; i < 200000; ++i) {
@@ -153,7 +159,7 @@ int main() {
             const tpl::AttnPlan p = tpl::attention_plan(T, B, Hkv, (int32_t)G, D, k & 1 ? 4 : 2, k & 2);
             CHECK(p.groups >= 8 && p.groups % 8 == 0);
             for (const uint32_t x : {0u, 1u, (uint32_t)G - 1, (uint32_t)G, (uint32_t)draw(0, INT32_MAX), (uint32_t)(draw(0, INT32_MAX / G) * G), (uint32_t)INT32_MAX})
-                CHECK((uint32_t)((uint64_t)x * p.by_g >> p.by_shift) == x / (uint32_t)G);
+                CHECK((uint32_t)((uint64_t)x * p.g.by >> p.g.shift) == x / (uint32_t)G);
             if (p.stream) CHECK(n >= (size_t)(tpl::plan_desc_bytes(p.groups) + tpl::plan_stats_bytes(p.groups) + 2 * p.groups * (p.few ? 32 : 128) * d * 4));
         }
         CHECK(n <= 300u << 20);
