@@ -36,8 +36,10 @@ AttnPlan attention_plan(int64_t T, int64_t B, int64_t Hkv, int32_t G, int64_t D,
     const int64_t rows = p.few ? 32 : 128;
     p.row_tiles = T * G / rows + B;
     // Equal runs while adding up the sequences' tiles in every workgroup is cheap and the
-    // items are too few to even out by themselves.
-    p.stream = p.few ? p.row_tiles <= 1024 : p.row_tiles <= 512 && p.row_tiles * Hkv <= 2048;
+    // items are too few to even out by themselves: 200 tokens of pasts up to 1000, 8 key
+    // heads, 108 us for 126, 1500 309 for 325, but 3000 over int8 270 for 240; 12 chunks
+    // over a window of 1024 121 us for 133, but a prompt of 4 x 1024 tokens 172 for 143.
+    p.stream = p.few ? p.row_tiles <= 2048 : p.row_tiles <= 512 && p.row_tiles * Hkv <= 2048;
     // As many as 256 CUs hold at once, by LDS (two stages of 32 keys, one wavefront) and by
     // registers (two wavefronts a SIMD, one for the longest heads).  Not taken from the
     // device: the workspace's size and the order of the sums depend on the call alone.
@@ -65,6 +67,16 @@ hipError_t launch_kv_attention(const AttnArgs &a, int es, hipStream_t s) {
     // units of a run: tiles of 32 keys and changes of items, counted in 32 bits
     if (p.stream && p.row_tiles * (p.last_pos / 32 + 8) * a.c.Hkv >= INT32_MAX) p.stream = 0;
     if (!p.stream && p.row_tiles * a.c.Hkv > (1 << 23)) return launch_attention_any(a, es, s);   // more than one launch holds
+    // Prompts from their first tokens on: the items' lengths go from one tile of 64 keys to
+    // L, which taking the longest first evens out.  By themselves they then take the time of
+    // 3/4 L tiles or all tiles' share of a workgroup, the runs that share and 6 tiles more,
+    // the sums' way by the workspace (64 query and 8 key heads of 128, one prompt of 512,
+    // 1024 and 2048 tokens: 29, 50 and 115 us for 40, 63 and 136; but with 8 query heads and
+    // one key head 4096 tokens 146 for 78).
+    if (p.stream && !p.few && p.window >= p.last_pos && 2 * a.c.T >= a.c.B * (int64_t)p.last_pos) {
+        const int64_t L = p.last_pos / 64, items = p.row_tiles * a.c.Hkv;
+        if (L * (3 * p.groups - 2 * items) <= 24 * (int64_t)p.groups) p.stream = 0;
+    }
     const bool dma = dma_ok(a, es);
     if (a.c.ks) return es == 2 ? launch_attention_bf16_int8(a, p, dma, s) : launch_attention_f32_int8(a, p, dma, s);
     return es == 2 ? launch_attention_bf16(a, p, dma, s) : launch_attention_f32(a, p, dma, s);

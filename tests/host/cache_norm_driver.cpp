@@ -114,6 +114,18 @@ int main() {
     c.T = 20000;
     taken(c, "bf16");
     CHECK(!lp.few && !lp.stream && tp_kv_attention_workspace_bytes(c.T, c.B, c.Hq, c.Hkv, c.D) == 0);
+    c.T = 2048; c.B = 1; c.Hq = 64; c.max_pages = 32;    // a prompt from its first token on
+    taken(c, "bf16");
+    CHECK(!lp.few && !lp.stream);
+    c.max_pages = 128;                              // or the end of a longer one
+    taken(c, "bf16");
+    CHECK(lp.stream);
+    c.max_pages = 32; c.window = 500;
+    taken(c, "bf16");
+    CHECK(lp.stream);
+    c.window = 0; c.Hq = 4; c.Hkv = 1;
+    taken(c, "bf16");
+    CHECK(lp.stream);
     // What goes to LDS without a stop: rows at multiples of 16 bytes.
     for (const bool q : {false, true}) {
         const int64_t n = q ? 16 : 8;

@@ -218,7 +218,8 @@ def test_strides(order, pad, extra, shift, t, int8):
     ([9], [4000], (32, 4, 128, 16)), ([300], [0], (8, 2, 128, 16)), ([130, 260], [500, 0], (4, 1, 96, 64)), ([200], [900], (4, 4, 256, 16)),
     ([1], [2000], (40, 1, 256, 16)), ([65], [700], (2, 2, 128, 16)), ([1, 700], [900, 0], (2, 1, 128, 16)),
     ([1100, 20], [3, 200], (16, 2, 64, 16)), ([0, 5, 0, 1600, 0], [9, 9, 9, 100, 9], (8, 1, 32, 16)), ([1] * 70, [30 * i % 97 for i in range(70)], (2, 1, 64, 16)),
-    ([1 + 40 * (i % 7 == 3) for i in range(300)], [i % 50 for i in range(300)], (4, 1, 32, 16))])
+    ([1 + 40 * (i % 7 == 3) for i in range(300)], [i % 50 for i in range(300)], (4, 1, 32, 16)),
+    ([11 + i % 5 - 11 * (i % 9 == 4) for i in range(300)], [i % 70 for i in range(300)], (4, 1, 32, 16)), ([1] * 700, [i % 40 for i in range(700)], (2, 1, 32, 16))])
 def test_long(lens, past, shape, t, int8):
     """Keys enough that several workgroups share a row, and rows enough that they do not."""
     Hq, Hkv, D, page = shape
