@@ -11,10 +11,10 @@ namespace {
 
 constexpr int64_t MAX_TILE_D = 256;     // largest head of the matrix-core form
 
-// What the matrix-core form takes: heads of whole 16-byte chunks (of whole 8 values in 8
-// bits); rows, positions and windows that 32 bits hold, with room for their sums.
+// What the matrix-core form takes: heads of 8 to 256; rows, positions and windows that 32
+// bits hold, with room for their sums.
 constexpr int64_t FAR = PLAN_FAR;
-bool tile_ok(int64_t T, int64_t B, int64_t G, int64_t D) { return D <= MAX_TILE_D && D % 8 == 0 && T < FAR && B < FAR && T * G < INT32_MAX - 128; }
+bool tile_ok(int64_t T, int64_t B, int64_t G, int64_t D) { return D >= 8 && D <= MAX_TILE_D && T < FAR && B < FAR && T * G < INT32_MAX - 128; }
 bool positions_ok(const AttnArgs &a) {
     const int64_t last = a.c.max_pages * (int64_t)a.c.page;
     return a.c.max_pages < FAR && last < FAR && (a.window >= 2 * FAR || last + a.window <= FAR);

@@ -115,13 +115,15 @@ __device__ __forceinline__ Span plan_span(const AttnPlan &p, const Sequence &q, 
     return s;
 }
 
-// Four features of a row, d .. d + 3 of D, divided by the row's sum.
-template <int ES>
+// Four features of a row, d .. d + 3 of D, divided by the row's sum.  ENDS: a row may end
+// inside them; FULL: it does not before them either.
+enum { ROW_FULL = 0, ROW_FOURS = 1, ROW_ENDS = 2 };
+template <int ES, int ROW>
 __device__ __forceinline__ void write_out(void *O, int64_t at, int d, int D, plan_f32x4 v, bool none, float inv) {
     float y[4];
 #pragma unroll
     for (int e = 0; e < 4; ++e) y[e] = none ? 0.0f : v[e] * inv;
-    if (d + 4 <= D) {
+    if (ROW == ROW_FULL || d + 4 <= D) {
         if constexpr (ES == 2) {
             typedef __bf16 bf16x4_ __attribute__((ext_vector_type(4)));
             typedef uint32_t u32x2_at __attribute__((ext_vector_type(2), aligned(1)));
@@ -134,6 +136,10 @@ __device__ __forceinline__ void write_out(void *O, int64_t at, int d, int D, pla
             typedef float f32x4_at __attribute__((ext_vector_type(4), aligned(4)));
             *(f32x4_at *)((float *)O + at + d) = f32x4_at{y[0], y[1], y[2], y[3]};
         }
+    } else if (ROW == ROW_ENDS && d < D) {
+#pragma unroll
+        for (int e = 0; e < 3; ++e)
+            if (d + e < D) store<ES>(O, at + d + e, y[e]);
     }
 }
 

@@ -20,7 +20,7 @@
 // values by the transposing read (4 keys x 16 features a 16-lane group, 8 keys in int8),
 // fp32 values by words.  Two stages: the next tile is fetched while this one is worked on,
 // straight into LDS (16 bytes a lane) where the cache is 16-byte aligned, else by way of
-// registers.  int8 becomes bf16 or fp32 (exactly; a key's scale multiplies its products, a
+// registers, of rows that end inside a chunk too.  int8 becomes bf16 or fp32 (exactly; a key's scale multiplies its products, a
 // value's scale its weight) as a wavefront reads it from LDS where it is alone, on the way
 // into LDS where four read the same keys.
 //
@@ -41,6 +41,20 @@
 // fetches never wait for it.  It alone reads the lengths, and the others go by what it
 // leaves in LDS: a workgroup stays together and in bounds whatever is in those arrays, were
 // they to change under it.
+//
+// Measured (both launches, a captured graph; inputs that no cache holds).  One token each of
+// 64 sequences of 8000 at most, 64 query and 8 key heads of 128: 214 us, 5.0 TB/s, the rate
+// of a copy; 16000 at most of 32 query heads over int8 213 us, 4.6 TB/s, where a tile's 500
+// vector instructions (its values become bf16 and fp16 in each wavefront) take 52% of the
+// cycles.  A prompt of 4096 tokens, the same heads: 391 us, 703 TFLOP/s:
+// the matrix cores are busy 29% and the vector units 44% of the cycles, four wavefronts that
+// wait for each other every 64 keys the rest.  12 chunks of 600 tokens at most, 24 query and
+// 8 key heads of 96, a window of 1024 over int8: 114 us, 251 TFLOP/s, 630 vector instructions
+// for 24 products a wavefront and tile, and 11 us the join.  4 sequences of 300 keys: 16 us, where the
+// first tile is worked on after 9, lengths, page table, rows and keys read one after another.
+// Split: 64 keys a tile instead of 32 where four wavefronts share them (fewer meetings), two
+// workgroups a CU.  One wavefront a workgroup for 32 rows: four wavefronts that cut the keys
+// of one tile among them and joined their sums in LDS took 257 us for the first case.
 #pragma once
 
 #include <hip/hip_runtime.h>
@@ -175,6 +189,13 @@ __device__ __forceinline__ u32x4 half_from_int8(uint32_t lo, uint32_t hi) {
     return y;
 }
 
+// The bytes of x from bit n on (0 .. 120), zeros behind them.
+__device__ __forceinline__ u32x4 shift_down(u32x4 x, int n) {
+    const uint64_t lo = (uint64_t)x[1] << 32 | x[0], hi = (uint64_t)x[3] << 32 | x[2];
+    const uint64_t l = n >= 64 ? hi >> (n & 63) : n > 0 ? lo >> n | hi << (64 - n) : lo, h = n >= 64 ? 0 : hi >> n;
+    return u32x4{(uint32_t)l, (uint32_t)(l >> 32), (uint32_t)h, (uint32_t)(h >> 32)};
+}
+
 __device__ __forceinline__ float other_half(float v) { return __shfl_xor(v, 32); }
 
 // A value that all lanes have, as a scalar.
@@ -184,17 +205,17 @@ __device__ __forceinline__ int64_t uniform(int64_t v) {
 }
 
 // What lies in LDS: rows of the call's type by way of registers, the same straight from
-// the cache, or int8 straight from the cache.
-enum { STAGE_REGS = 0, STAGE_DMA = 1, STAGE_INT8 = 2 };
+// the cache, or int8 straight from the cache.  ODD: as REGS, of rows that end inside a chunk;
+// the last is loaded so that it ends with the row, and moved to its place.
+enum { STAGE_REGS = 0, STAGE_DMA = 1, STAGE_INT8 = 2, STAGE_ODD = 3 };
 
 // FULL: D is 32 NB, all of a row in LDS.
 template <int ES, int CS, int NB, int WR, int KB, int ST, int OCC, bool FULL>
 __global__ __launch_bounds__(64 * WR, OCC)
 void attention_tile(AttnArgs a, AttnPlan plan) {
-    constexpr bool ALONE = WR == 1 && ST != STAGE_REGS;                 // see the loop at the end
+    constexpr bool DMA = ST == STAGE_DMA || ST == STAGE_INT8, ALONE = WR == 1 && DMA;   // see the loop at the end
     constexpr int NW = WR, NTH = 64 * NW, ROWS = 32 * WR, BK = 32 * KB;
     constexpr int LS = ST == STAGE_INT8 ? 1 : ES;                       // bytes of a value in LDS
-    constexpr bool DMA = ST != STAGE_REGS;
     constexpr int DP = NB == 3 ? 128 : NB * 32, RB = DP * LS;          // a row in LDS
     constexpr int KS = NB * ES;                                         // steps of the first product
     constexpr int CH = RB / 16, LI = BK * CH / NTH;                     // chunks of a row; of a thread and tile
@@ -224,7 +245,10 @@ void attention_tile(AttnArgs a, AttnPlan plan) {
     const int D = c.D, G = a.G;
     const float cs = a.scale * 1.44269504088896340736f;
     const int last_pos = plan.last_pos, window_of = plan.window;         // positions of the table; FAR: all
-    const int chunks = D * LS / 16;                                     // of a row in LDS that hold features
+    const int chunks = ST == STAGE_ODD ? (D * LS + 15) / 16 : D * LS / 16;      // of a row in LDS that hold features
+    constexpr int CB = 16 / ES * CS;                                    // bytes of a chunk in the cache (by way of registers)
+    // where this thread's chunk, always the same of a row, is loaded
+    const int load_at = ST == STAGE_ODD && (tid % CH + 1) * CB > D * CS ? D * CS - CB : tid % CH * CB;
 
     auto sequence = [&](int s) { return plan_sequence(c, s); };
     auto span = [&](const Sequence &q, int r) { return plan_span(plan, q, r, G, ROWS, BK); };
@@ -509,7 +533,7 @@ void attention_tile(AttnArgs a, AttnPlan plan) {
                 u32x4 &x = V ? vr[i] : kr[i];
                 x = u32x4{0, 0, 0, 0};
                 if (ch < chunks) {
-                    const char *p = from[i] + ch * (16 / ES) * CS;
+                    const char *p = from[i] + load_at;
                     if constexpr (!QUANT) {
                         x = *(const u32x4_any *)p;
                     } else if constexpr (ES == 2) {
@@ -540,6 +564,10 @@ void attention_tile(AttnArgs a, AttnPlan plan) {
             for (int i = 0; i < LI; ++i) {
                 const int k = i * NTH + tid, r = k / CH, ch = k % CH;
                 const uint32_t at = (n & 1) * STAGE + r * RB;
+                if (ST == STAGE_ODD) {
+                    kr[i] = shift_down(kr[i], ch < chunks ? 8 * (ch * CB - load_at) : 0);
+                    vr[i] = shift_down(vr[i], ch < chunks ? 8 * (ch * CB - load_at) : 0);
+                }
                 *(LDS_PTR(u32x4))(lds + at + ((ch * 16) ^ k_swizzle<RB>(r))) = QUANT ? from_int8<ES>(kr[i][0], kr[i][1]) : kr[i];
                 *(LDS_PTR(u32x4))(lds + at + BK * RB + ((ch * 16) ^ v_swizzle<LS, RB>(r))) = HALF ? half_from_int8(vr[i][0], vr[i][1]) : QUANT ? from_int8<ES>(vr[i][0], vr[i][1]) : vr[i];
             }
@@ -598,7 +626,9 @@ void attention_tile(AttnArgs a, AttnPlan plan) {
             // the features that a lane's k-th operand of K has
             const int ch = ST == STAGE_INT8 ? (2 * (k / ES) + half) * ES + k % ES : 2 * k + half;
             qf[k] = u32x4{0, 0, 0, 0};
-            if (live && ch < D * ES / 16) qf[k] = *(const u32x4_any *)((const char *)a.Q + ((int64_t)row * a.ldq + (int64_t)head * D) * ES + ch * 16);
+            const char *p = (const char *)a.Q + ((int64_t)row * a.ldq + (int64_t)head * D) * ES;
+            if (live && ch < D * ES / 16) qf[k] = *(const u32x4_any *)(p + ch * 16);
+            else if (ST == STAGE_ODD && live && ch < chunks) qf[k] = shift_down(*(const u32x4_any *)(p + D * ES - 16), 8 * ((ch + 1) * 16 - D * ES));
         }
 #pragma unroll
         for (int b = 0; b < NB; ++b)
@@ -877,7 +907,7 @@ void attention_tile(AttnArgs a, AttnPlan plan) {
                     f32x4 v;
 #pragma unroll
                     for (int e = 0; e < 4; ++e) v[e] = o[b][4 * i + e];
-                    if (whole) write_out<ES>(a.O, (int64_t)row * a.ldo + (int64_t)head * D, b * 32 + 8 * i + 4 * half, D, v, l == 0.0f, inv);
+                    if (whole) write_out<ES, FULL ? ROW_FULL : ST == STAGE_ODD ? ROW_ENDS : ROW_FOURS>(a.O, (int64_t)row * a.ldo + (int64_t)head * D, b * 32 + 8 * i + 4 * half, D, v, l == 0.0f, inv);
                     else plan_sums(a.ws, plan.groups)[(((int64_t)slot * WR + wr) * NB + b) * 256 + i * 64 + lane] = v;
                 }
             if (half == 0 && !whole) {
@@ -946,7 +976,7 @@ __device__ __forceinline__ void join_add(JoinSums<N> &s, float m, float l, const
         for (int e = 0; e < 4; ++e) s.x[i][e] = __builtin_fmaf(f1, y[i][e], s.x[i][e] * f0);
 }
 
-template <int ES, int NB, int WR>
+template <int ES, int NB, int WR, bool ODD>
 __global__ __launch_bounds__(JOIN)
 void attention_join(AttnArgs a, AttnPlan plan) {
     constexpr int ROWS = 32 * WR, JW = JOIN / 64;
@@ -1006,7 +1036,7 @@ void attention_join(AttnArgs a, AttnPlan plan) {
     }
     if (!live) return;
     const bool none = t.l == 0.0f;
-    write_out<ES>(a.O, row * a.ldo + (int64_t)head * a.c.D, b * 32 + 8 * v + 4 * half, a.c.D, t.x[0], none, none ? 0.0f : 1.0f / t.l);
+    write_out<ES, ODD ? ROW_ENDS : ROW_FOURS>(a.O, row * a.ldo + (int64_t)head * a.c.D, b * 32 + 8 * v + 4 * half, a.c.D, t.x[0], none, none ? 0.0f : 1.0f / t.l);
     if (a.lse && b == 0 && v == 0 && half == 0) a.lse[row * a.ldl + head] = none ? -INFINITY : t.m * 0.69314718055994530942f + logf(t.l);
 }
 
@@ -1016,7 +1046,7 @@ hipError_t launch_tile(const AttnArgs &a, const AttnPlan &p, hipStream_t s) {
     attention_tile<ES, CS, NB, WR, KB, ST, OCC, FULL><<<dim3(grid), dim3(64 * WR), 0, s>>>(a, p);
     hipError_t e = hipGetLastError();
     if (e != hipSuccess || !p.stream) return e;
-    attention_join<ES, NB, WR><<<dim3((unsigned)p.groups, WR * NB), dim3(JOIN), 0, s>>>(a, p);
+    attention_join<ES, NB, WR, ST == STAGE_ODD><<<dim3((unsigned)p.groups, WR * NB), dim3(JOIN), 0, s>>>(a, p);
     return hipGetLastError();
 }
 
@@ -1024,11 +1054,14 @@ hipError_t launch_tile(const AttnArgs &a, const AttnPlan &p, hipStream_t s) {
 template <int ES, int CS, int NB, bool FULL>
 hipError_t launch_full(const AttnArgs &a, const AttnPlan &p, bool dma, hipStream_t s) {
     constexpr int RB = (NB == 3 ? 128 : NB * 32) * ES, OCC = NB == 8 ? 1 : 2;
+    const bool odd = a.c.D % (16 / ES);
     if (p.few) {
+        if (odd) return launch_tile<ES, CS, NB, 1, 1, STAGE_ODD, 1, false>(a, p, s);
         if (dma) return launch_tile<ES, CS, NB, 1, 1, CS == 1 ? STAGE_INT8 : STAGE_DMA, OCC, FULL>(a, p, s);
         return launch_tile<ES, CS, NB, 1, 1, STAGE_REGS, 1, false>(a, p, s);
     }
     constexpr int KB = RB <= 256 ? 2 : 1;
+    if (odd) return launch_tile<ES, CS, NB, 4, KB, STAGE_ODD, OCC, false>(a, p, s);
     if (dma && CS != 1) return launch_tile<ES, CS, NB, 4, KB, CS == 1 ? STAGE_REGS : STAGE_DMA, OCC, CS != 1 && FULL>(a, p, s);
     return launch_tile<ES, CS, NB, 4, KB, STAGE_REGS, OCC, false>(a, p, s);
 }

@@ -321,7 +321,7 @@ void norm_rows(NormArgs a, int64_t t0) {
 
 // Gradients, bound by latency and HBM: two wavefronts a SIMD, whose registers hold the
 // weights widened and the sums, with three sums over the row one after another (4096 x
-// 4096 bf16 with both norms and a gate 54 us with the second launch, 3.7 TB/s; 8192 x 2048
+// 4096 bf16 with both norms and a gate 52 us with the second launch, 3.9 TB/s; 8192 x 2048
 // 49; 2048 x 8192 64).  G groups of W wavefronts a workgroup, each with rows of its own one after
 // another; the next row's values are loaded while the current ones are worked on.  The
 // features' sums of a lane stay in registers; at the end the groups' are added in LDS in

@@ -138,7 +138,11 @@ int main() {
         taken(c, q ? "bf16 int8" : "bf16"); CHECK(ldma == !q);
     }
     // What 32 bits, or the tiles, do not hold.
-    for (const int64_t d : {1, 4, 100, 127, 264, 1000}) { c = Call(); c.D = d; taken(c, "any"); }
+    for (const int64_t d : {1, 7, 257, 264, 1000}) { c = Call(); c.D = d; taken(c, "any"); }
+    for (const int64_t d : {9, 12, 100, 127, 250}) {
+        c = Call(); c.D = d; taken(c, "bf16"); CHECK(!ldma);
+        c.int8 = true; taken(c, "bf16 int8"); CHECK(!ldma);
+    }
     c = Call(); c.max_pages = int64_t(1) << 30; taken(c, "any");
     c = Call(); c.max_pages = 1 << 20; c.page = 1 << 12; taken(c, "any");                       // 2^32 positions
     c = Call(); c.page = int64_t(1) << 33; c.max_pages = 1; c.ss = 1; c.sp = 0; taken(c, "any"); // one page of all
@@ -164,10 +168,10 @@ int main() {
     }
     // The workspace of the sizes holds the plan of every type.
     for (int i = 0; i < 200000; ++i) {
-        const int64_t G = draw(1, 16), Hkv = draw(1, 16), D = 8 * draw(1, 33), B = draw(1, i % 3 ? 64 : 4000), T = draw(1, i % 2 ? 200 : 1 << 20);
+        const int64_t G = draw(1, 16), Hkv = draw(1, 16), D = i % 4 ? draw(1, 264) : 8 * draw(1, 33), B = draw(1, i % 3 ? 64 : 4000), T = draw(1, i % 2 ? 200 : 1 << 20);
         const size_t n = tp_kv_attention_workspace_bytes(T, B, Hkv * G, Hkv, D);
         const int64_t d = D <= 64 ? 64 : D <= 96 ? 96 : D <= 128 ? 128 : 256;
-        for (int k = 0; k < 4 && D <= 256; ++k) {
+        for (int k = 0; k < 4 && D >= 8 && D <= 256; ++k) {
             const tpl::AttnPlan p = tpl::attention_plan(T, B, Hkv, (int32_t)G, D, k & 1 ? 4 : 2, k & 2);
             CHECK(p.groups >= 8 && p.groups % 8 == 0);
             for (const uint32_t x : {0u, 1u, (uint32_t)G - 1, (uint32_t)G, (uint32_t)draw(0, INT32_MAX), (uint32_t)(draw(0, INT32_MAX / G) * G), (uint32_t)INT32_MAX})

@@ -110,7 +110,7 @@ def reference(c, Q, Hq, window, scale, see=lambda s, j: True):
     o = torch.zeros(c.T, Hq, D, dtype=torch.float64)
     lse = torch.full((c.T, Hq), -math.inf, dtype=torch.float64)
     eo, el = torch.zeros_like(o), torch.zeros_like(lse)
-    u_w = 0.0 if c.t == F32 else 2.0 ** -11 if c.int8 and c.D % 8 == 0 and c.D <= 256 else 2.0 ** -8
+    u_w = 0.0 if c.t == F32 else 2.0 ** -11 if c.int8 and 8 <= c.D <= 256 else 2.0 ** -8
     q = Q.double().view(c.T, Hq, D)
     for s in range(len(c.lens)):
         for i in range(c.lens[s]):
