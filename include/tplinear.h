@@ -589,6 +589,7 @@ tp_status tp_kv_append_quant(const void *X, int64_t ldx, int32_t x_mode, const f
  * int8 and a value is q * scale in fp32, rounded once to dtype.
  * A position outside [0, max_pages*page_size) or whose page is outside [0, n_pages)
  * gives zero rows and sets *bad_flag; rows no sequence owns are left alone.
+ * K and V must not overlap the cache.
  * Errors: TP_ERR_NULL (both K and V missing, a cache missing for one that is given, a
  * scale for one of two and not the other), TP_ERR_SHAPE (sizes, leading dims,
  * negative strides, D not in 1 .. 1024), TP_ERR_DTYPE, TP_ERR_HIP.
@@ -622,9 +623,10 @@ tp_status tp_kv_read(const int32_t *cu, const int32_t *past, int64_t B, const in
  * sequence owns are left alone.
  * k_scale, v_scale: NULL for caches of dtype, else the caches are int8.
  * Arithmetic: products, sums and softmax in fp32, one rounding to dtype; with TP_BF16
- * the weights exp(x_j - max) are rounded to bf16 for the matrix cores' product with
- * the values (not for their sum).  The order of the sums depends on the sizes and
- * lengths alone.
+ * the weights exp(x_j - max) are rounded to bf16, over an int8 cache with the value's
+ * scale to fp16, for the matrix cores' product with the values (not for their sum).  The
+ * order of the sums depends on the sizes and lengths alone.
+ * O and lse must not overlap inputs.
  * workspace: tp_kv_attention_workspace_bytes, 256-byte aligned; calls that may overlap
  * must not share it.  It need not hold anything before the call.
  * Errors: TP_ERR_NULL (one scale without the other), TP_ERR_SHAPE (sizes, leading

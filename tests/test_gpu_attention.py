@@ -179,7 +179,7 @@ def check(c, Hq, window=0, scale=None, extra=0, shift=0, see=lambda s, j: True, 
 SHAPES = [  # Hq, Hkv, D, page
     (1, 1, 128, 16), (8, 1, 128, 16), (8, 8, 64, 16), (6, 2, 80, 16), (12, 4, 96, 5), (4, 4, 256, 32), (32, 2, 128, 64), (33, 1, 64, 1),
     (3, 1, 7, 16), (4, 2, 40, 48), (2, 1, 72, 16), (5, 5, 100, 16), (4, 2, 192, 16), (2, 2, 300, 16), (64, 1, 128, 256), (20, 2, 120, 16),
-    (2, 1, 600, 16), (10, 2, 16, 16), (7, 7, 8, 3), (80, 1, 32, 16)]
+    (2, 1, 600, 16), (4, 2, 33, 16), (6, 3, 127, 16), (2, 1, 250, 8), (3, 1, 9, 4), (8, 2, 204, 16), (16, 4, 12, 16), (10, 2, 16, 16), (7, 7, 8, 3), (80, 1, 32, 16)]
 TYPES = [(BF, False), (F32, False), (BF, True), (F32, True)]
 
 
