@@ -46,9 +46,10 @@
 // 64 sequences of 8000 at most, 64 query and 8 key heads of 128: 214 us, 5.0 TB/s, the rate
 // of a copy; 16000 at most of 32 query heads over int8 213 us, 4.6 TB/s, where a tile's 500
 // vector instructions (its values become bf16 and fp16 in each wavefront) take 52% of the
-// cycles.  A prompt of 4096 tokens, the same heads: 391 us, 703 TFLOP/s:
-// the matrix cores are busy 29% and the vector units 44% of the cycles, four wavefronts that
-// wait for each other every 64 keys the rest.  12 chunks of 600 tokens at most, 24 query and
+// cycles.  A prompt of 4096 tokens, the same heads: 391-425 us by the
+// chip's temperature, 650-700 TFLOP/s: the matrix cores are busy 29% and the vector units 44%
+// of the cycles, four wavefronts that wait for each other every 64 keys the rest (wavefront
+// 0's look-ups 8%).  12 chunks of 600 tokens at most, 24 query and
 // 8 key heads of 96, a window of 1024 over int8: 114 us, 251 TFLOP/s, 630 vector instructions
 // for 24 products a wavefront and tile, and 11 us the join.  4 sequences of 300 keys: 16 us, where the
 // first tile is worked on after 9, lengths, page table, rows and keys read one after another.
