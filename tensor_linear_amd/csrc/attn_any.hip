@@ -29,7 +29,8 @@ void attention_any(AttnArgs a, int64_t w0, int64_t waves) {
     const int32_t *table = a.c.table + s * a.c.ldt;
     const int64_t p = (int64_t)a.c.past[s] + (t - a.c.cu[s]);
     const int64_t first = p - a.window + 1 > 0 ? p - a.window + 1 : 0;
-    const int64_t held = a.c.max_pages * (int64_t)a.c.page, last = p < held ? p : held - 1;   // positions of the table
+    // positions of the table that 32 bits hold
+    const int64_t most = 0xFFFFFFFF, all = a.c.max_pages * (int64_t)a.c.page, held = all < most ? all : most, last = p < held ? p : held - 1;
     const int64_t q0 = t * a.ldq + (int64_t)h * D;
     float m = -INFINITY, l = 0.0f, o[FEATURES] = {};
     bool bad = false;

@@ -81,7 +81,8 @@ void read_rows(ReadArgs a, int64_t w0, int64_t waves, int parts) {
     if (s < 0) return;
     const int64_t p = (int64_t)a.c.past[s] + (t - a.c.cu[s]);
     Row r{-1, 0};
-    if (p >= 0) r = row_of(a.c, a.c.table + s * a.c.ldt, (uint32_t)p);
+    // (a sequence that begins before the call's first row may have positions past 32 bits)
+    if (p >= 0 && p < 0xFFFFFFFF) r = row_of(a.c, a.c.table + s * a.c.ldt, (uint32_t)p);
     const bool ok = r.page >= 0;
     if (!ok && a.c.bad && lane == 0) *a.c.bad = 1;
     const int64_t row = r.page * a.c.s_page + r.slot * a.c.s_slot;
