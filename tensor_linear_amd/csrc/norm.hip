@@ -275,7 +275,7 @@ void norm_rows(NormArgs a, int64_t t0) {
         for (int e = 0; e < 8; ++e) s[0] = __builtin_fmaf(h[c][e], h[c][e], s[0]);
         if (a.H) put_row8<ES, TAIL>(a.H, t * a.ldh, c * STEP + lane * 8, F, h[c]);
     }
-    if (!a.N) return;
+    if (!a.N && !a.scale) return;       // rows of no features may have a scale alone
     if (a.pre) {
         row_sum<W, 1>(s, red, turn);
         const float r2 = rsqrtf(s[0] / (float)F + a.eps);
@@ -296,8 +296,8 @@ void norm_rows(NormArgs a, int64_t t0) {
 #pragma unroll
     for (int c = 0; c < C; ++c)
 #pragma unroll
-        for (int e = 0; e < 8; ++e)     // past the row's end zeros, whatever its factors
-            if (!TAIL || c * STEP + lane * 8 + e < F) m = max(m, __float_as_uint(h[c][e]) & 0x7FFFFFFFu);
+        for (int e = 0; e < 8; ++e)     // nothing past the row's end, whatever its factors
+            if (c * STEP + lane * 8 + (TAIL ? e : 0) < F) m = max(m, __float_as_uint(h[c][e]) & 0x7FFFFFFFu);
     float scale;
     const Step st = step_of(row_max<W>(m, red, turn), scale);
     if (lane == 0) a.scale[t] = scale;

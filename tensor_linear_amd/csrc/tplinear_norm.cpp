@@ -45,9 +45,9 @@ tp_status tp_residual_norm(const void *Y, int64_t ldy, const void *R, int64_t ld
     const tp_status st = check_norm(Y, ldy, R, ldr, gate, ldg, eps, T, F, dtype);
     if (st != TP_OK) return st;
     if (!rows_ok(H, ldh, T, F) || !rows_ok(N, ldn, T, F)) return TP_ERR_SHAPE;
-    if (n_scale && !N) return TP_ERR_NULL;
+    if (n_scale && !N && F > 0) return TP_ERR_NULL;
     if (T == 0 || (F == 0 && !n_scale)) return TP_OK;
-    if ((F > 0 && !Y) || (!H && !N)) return TP_ERR_NULL;
+    if (F > 0 && (!Y || (!H && !N))) return TP_ERR_NULL;
     NormArgs a = norm_args(Y, ldy, R, ldr, gate, ldg, post_weight, pre_weight, residual_scale, branch_scale, eps, T, F);
     a.H = H; a.ldh = H ? ldh : 0; a.N = N; a.ldn = N ? ldn : 0; a.scale = n_scale;
     return hip_status(launch_residual_norm(a, dtype == TP_BF16 ? 2 : 4, (hipStream_t)stream));
