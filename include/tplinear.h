@@ -612,7 +612,8 @@ tp_status tp_kv_read(const int32_t *cu, const int32_t *past, int64_t B, const in
  * that O is the input of a row layer whose shard i has the columns of its own heads.
  * Query head h reads key and value head h / (Hq/Hkv).
  * Row t of sequence s has the position p = past[s] + t - cu[s] and sees the positions
- * j <= p, with window > 0 only j > p - window.  With x_j the dot product of its query
+ * j <= p, with window > 0 only j > p - window (0 is all; windows between 2^29 less the
+ * table's positions and 2^29 take a slow form).  With x_j the dot product of its query
  * and key j times softmax_scale:
  *   O = sum_j exp(x_j) v_j / sum_j exp(x_j);  lse = log(sum_j exp(x_j)).
  * lse: fp32 [T, Hq], ldl >= Hq, or NULL.

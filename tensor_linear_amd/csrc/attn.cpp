@@ -11,13 +11,14 @@ namespace {
 
 constexpr int64_t MAX_TILE_D = 256;     // largest head of the matrix-core form
 
-// What the matrix-core form takes: heads of 8 to 256; rows, positions and windows that 32
-// bits hold, with room for their sums.
+// What the matrix-core form takes: heads of 8 to 256; rows and positions of the table that
+// 32 bits hold, with room for their sums; windows of any length but those, far longer than
+// any sequence, from FAR less the table's positions to FAR.
 constexpr int64_t FAR = PLAN_FAR;
 bool tile_ok(int64_t T, int64_t B, int64_t G, int64_t D) { return D >= 8 && D <= MAX_TILE_D && T < FAR && B < FAR && T * G < INT32_MAX - 128; }
 bool positions_ok(const AttnArgs &a) {
     const int64_t last = a.c.max_pages * (int64_t)a.c.page;
-    return a.c.max_pages < FAR && last < FAR && (a.window >= 2 * FAR || last + a.window <= FAR);
+    return a.c.max_pages < FAR && last < FAR && (a.window > FAR || last + a.window <= FAR);
 }
 
 // A cache whose rows lie at multiples of 16 bytes goes to LDS without a stop.
@@ -62,6 +63,7 @@ hipError_t launch_kv_attention(const AttnArgs &a, int es, hipStream_t s) {
     AttnPlan p = attention_plan(a.c.T, a.c.B, a.c.Hkv, a.G, a.c.D, es, a.c.ks != nullptr);
     p.last_pos = (int32_t)(a.c.max_pages * (int64_t)a.c.page);
     p.window = (int32_t)(a.window < 2 * FAR ? a.window : 2 * FAR);
+    p.excess = (uint32_t)(a.window - p.window < (int64_t)UINT32_MAX ? a.window - p.window : (int64_t)UINT32_MAX);
     p.page = divisor(a.c.page);
     p.n_pages = (uint32_t)(a.c.n_pages < (int64_t)1 << 31 ? a.c.n_pages : (int64_t)1 << 31);
     // units of a run: tiles of 32 keys and changes of items, counted in 32 bits

@@ -69,23 +69,29 @@ __device__ __forceinline__ plan_f32x4 *plan_sums(void *ws, int W) {
 }
 
 // 32 bits hold what the matrix-core form takes (attn.cpp): rows of tokens and heads,
-// positions of the table below FAR, tokens fewer than FAR, windows of 2 FAR (none) or so
-// short that a row FAR positions on sees nothing of the table.  So a past beyond FAR may be
-// taken for FAR, and one before -FAR for -FAR.
+// positions of the table and tokens below FAR, windows to 2 FAR.  A past before -FAR may be
+// taken for -FAR, whose rows are all before the table.  Beyond FAR, where rows are behind the
+// table, it counts for the first position that a row sees alone, past - window + 1: so a
+// window that is `excess` longer than 2 FAR brings it nearer by as much, and it is held
+// between FAR, whose rows see all of the table if the window is 2 FAR, and 3 FAR - 2, whose
+// rows see nothing of it (and whose positions, of FAR - 2 tokens on, are below 2^31 - 1).
 constexpr int FAR = PLAN_FAR;
 
 // A sequence's first row and number of rows among the call's T, and the position of the
 // first of them.  Rows outside the call do not count, whatever cu says.
 struct Sequence { int first, n, past; };
 __device__ __forceinline__ int plan_clamp(int v, int T) { return v < 0 ? 0 : v > T ? T : v; }
-__device__ __forceinline__ Sequence plan_sequence(const CacheArgs &c, int s) {
-    const int from = c.cu[s], to = c.cu[s + 1], past = c.past[s], T = (int)c.T;
+__device__ __forceinline__ Sequence plan_sequence(const CacheArgs &c, uint32_t excess, int s) {
+    const int from = c.cu[s], to = c.cu[s + 1], T = (int)c.T;
     Sequence q;
     q.first = plan_clamp(from, T);
     const int end = plan_clamp(to, T);
     q.n = end > q.first ? end - q.first : 0;
-    q.past = past < -FAR ? -FAR : past > FAR ? FAR : past;
-    if (from < 0) q.past = from < -FAR || q.past > FAR + from ? FAR : q.past - from;   // rows before the call's first
+    // rows before the call's first count: the past is past + FAR - most, of up to 33 bits
+    const int past = c.past[s], most = from < 0 ? FAR + from : FAR;
+    const uint32_t beyond = (uint32_t)past - (uint32_t)most, behind = beyond > excess ? beyond - excess : 0;
+    if (past > most) q.past = FAR + (int)(behind < 2 * FAR - 2 ? behind : 2 * FAR - 2);
+    else q.past = past + (FAR - most) > -FAR ? past + (FAR - most) : -FAR;
     return q;
 }
 

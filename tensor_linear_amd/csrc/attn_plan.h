@@ -21,8 +21,9 @@ inline Divisor divisor(int64_t d) {
 
 // stream: the tiles of all items in `groups` equal runs; else a workgroup for each of
 // the row_tiles * Hkv items.  few: 32 rows a workgroup, else 128.
-// last_pos: positions of the table; window: 2 PLAN_FAR for none; n_pages: 2^31 at most.
-struct AttnPlan { int32_t stream, few, groups, last_pos, window; uint32_t n_pages; int64_t row_tiles; Divisor g, page; };
+// last_pos: positions of the table; window: 2 PLAN_FAR at most, excess: what it is longer, 2^32 - 1 at most;
+// n_pages: 2^31 at most.
+struct AttnPlan { int32_t stream, few, groups, last_pos, window; uint32_t n_pages; int64_t row_tiles; Divisor g, page; uint32_t excess; };
 
 // The plan of a call of these sizes and types (the lengths are on the device: T, B and the
 // heads are all that the host knows).

@@ -251,7 +251,7 @@ void attention_tile(AttnArgs a, AttnPlan plan) {
     // where this thread's chunk, always the same of a row, is loaded
     const int load_at = ST == STAGE_ODD && (tid % CH + 1) * CB > D * CS ? D * CS - CB : tid % CH * CB;
 
-    auto sequence = [&](int s) { return plan_sequence(c, s); };
+    auto sequence = [&](int s) { return plan_sequence(c, plan.excess, s); };
     auto span = [&](const Sequence &q, int r) { return plan_span(plan, q, r, G, ROWS, BK); };
     auto row_tiles = [&](const Sequence &q) { return (q.n * G + ROWS - 1) / ROWS; };
     // Units of one head of each lane's sequence (its tiles, and the changes between its

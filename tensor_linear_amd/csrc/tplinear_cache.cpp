@@ -143,7 +143,8 @@ tp_status tp_kv_attention(const void *Q, int64_t ldq, const int32_t *cu, const i
     a.c = cache_args(cu, past, B, table, ldt, max_pages, k_cache, v_cache, n_pages, page_size, page_stride, slot_stride, head_stride,
                      k_scale, v_scale, scale_page_stride, scale_slot_stride, scale_head_stride, T, Hkv, D, bad_flag);
     a.Q = Q; a.ldq = ldq; a.O = O; a.ldo = ldo; a.lse = lse; a.ldl = lse ? ldl : 0;
-    a.scale = softmax_scale; a.window = window > 0 ? window : (int64_t)1 << 62;
+    const int64_t all = (int64_t)1 << 62;
+    a.scale = softmax_scale; a.window = window > 0 && window < all ? window : all;
     a.G = (int32_t)(Hq / Hkv);
     a.ws = workspace;
     return hip_status(launch_kv_attention(a, dtype == TP_BF16 ? 2 : 4, (hipStream_t)stream));
