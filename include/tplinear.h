@@ -625,8 +625,10 @@ tp_status tp_kv_read(const int32_t *cu, const int32_t *past, int64_t B, const in
  * k_scale, v_scale: NULL for caches of dtype, else the caches are int8.
  * Arithmetic: products, sums and softmax in fp32, one rounding to dtype; with TP_BF16
  * the weights exp(x_j - max) are rounded to bf16, over an int8 cache with the value's
- * scale to fp16, for the matrix cores' product with the values (not for their sum).  The
- * order of the sums depends on the sizes and lengths alone.
+ * scale to fp16 (2^-11 of itself, 2^-29 of the row's largest at best; scales may be any
+ * fp32 numbers), for the matrix cores' product with the values (not for their sum).  A sum
+ * of weights times values past fp32 is infinite.  The order of the sums depends on the
+ * sizes and lengths alone.
  * O and lse must not overlap inputs.
  * workspace: tp_kv_attention_workspace_bytes, 256-byte aligned; calls that may overlap
  * must not share it.  It need not hold anything before the call.

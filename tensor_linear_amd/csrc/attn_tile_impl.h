@@ -594,11 +594,18 @@ void attention_tile(AttnArgs a, AttnPlan plan) {
     f32x16 o[NB];
     float mx = -INFINITY, l = 0.0f;
     // HALF: weights times scales go into the second product as fp16, which rounds them by
-    // 2^-12 at most (bf16: 2^-9, as much as the output's own rounding), and have to lie where
-    // fp16 is exact: all weights are 2^shift times the softmax's, l and o with them, so that
-    // the largest of a row (top_w) is between 2^4 and 2^15.  The shift begins at 2^16, for
-    // scales of values of order one, and hardly ever changes.
+    // 2^-11 at most (bf16: 2^-8, as much as the output's own rounding) where they are its normal
+    // numbers, and smaller ones to multiples of 2^-24: all weights are 2^shift times the
+    // softmax's, o with them, so that the largest of a row (top_w) is between 2^4 and 2^15.  The
+    // shift begins at 2^16, for scales of values of order one, and hardly ever changes.  As far
+    // as it is in 0 .. NEAR it is in the exponential's argument, where it costs nothing (l has it
+    // too), and what is missing of it (far) is put in behind the product with the scale.  A row
+    // that sees scales past MOST_SCALE, where that product might not be finite, has none of it in
+    // the argument for that tile.  With a shift of MOST fp32's smallest values are fp16's.
+    constexpr float NEAR = 60.0f, MOST = 125.0f, MOST_SCALE = 0x1p67f;
     float shift = 16.0f, top_w = 0.0f;
+    uint64_t far = 0;                                                       // the lanes whose shift is not in 0 .. NEAR
+    auto near_of = [&](float v) { return fminf(fmaxf(v, 0.0f), NEAR); };
     auto enter = [&](int i) __attribute__((always_inline)) {
         const Item &m = items[i];
         first = uniform(m.q.first);
@@ -639,6 +646,7 @@ void attention_tile(AttnArgs a, AttnPlan plan) {
         l = 0.0f;
         shift = 16.0f;
         top_w = 0.0f;
+        far = 0;
     };
 
     // ---- one tile
@@ -664,7 +672,9 @@ void attention_tile(AttnArgs a, AttnPlan plan) {
                         x[b] = product<ES>(ES == 2 ? from_int8<ES>(kf[2 * (e & 1)], kf[2 * (e & 1) + 1]) : from_int8<ES>(kf[e], 0), qf[s2 + e], x[b]);
                 }
             }
+        uint64_t apart = 0;         // HALF: where scales are that they and the shift may take past fp32, or shifts that are far
         if constexpr (QUANT) {
+            if constexpr (HALF) apart = far | __ballot(!(fabsf(row_scale[st][1][lane & (BK - 1)]) <= MOST_SCALE));
 #pragma unroll
             for (int b = 0; b < KB; ++b)
 #pragma unroll
@@ -706,7 +716,17 @@ void attention_tile(AttnArgs a, AttnPlan plan) {
                 for (int i = 0; i < 16; ++i) o[b][i] *= f;
             mx = next;
         }
-        const float less = HALF ? shift - zero : -zero;
+        float held = shift;                                                 // HALF: the shift in the exponents
+        if constexpr (HALF) {
+            if (__builtin_expect(apart != 0, 0)) {
+                const uint64_t mine = seen >> (4 * half);
+                float z = 0.0f;                                             // of the scales that the row sees
+                for (int i = 0; i < 16 * KB; ++i)
+                    if (mine >> (8 * (i / 4) + i % 4) & 1) z = fmaxf(z, fabsf(row_scale[st][1][8 * (i / 4) + i % 4 + 4 * half]));
+                held = fmaxf(z, other_half(z)) > MOST_SCALE ? 0.0f : near_of(shift);
+            }
+        }
+        const float less = HALF ? held - zero : -zero;
         float sum = 0.0f;
 #pragma unroll
         for (int b = 0; b < KB; ++b)
@@ -715,7 +735,6 @@ void attention_tile(AttnArgs a, AttnPlan plan) {
                 x[b][i] = __builtin_amdgcn_exp2f(__builtin_fmaf(x[b][i], cs, less));
                 sum += x[b][i];
             }
-        l += sum;
         if constexpr (QUANT) {
 #pragma unroll
             for (int b = 0; b < KB; ++b)
@@ -735,31 +754,37 @@ void attention_tile(AttnArgs a, AttnPlan plan) {
             }
         }
         if constexpr (HALF) {
-            float most = x[0][0];
+            float most = fabsf(x[0][0]);
 #pragma unroll
             for (int b = 0; b < KB; ++b)
 #pragma unroll
                 for (int i = 0; i < 16; ++i) most = fmaxf(most, fabsf(x[b][i]));
-            top_w = fmaxf(top_w, fmaxf(most, other_half(most)));
-            if (__any(top_w >= 32768.0f || (top_w < 16.0f && top_w > 0.0f))) {
+            most = fmaxf(most, other_half(most));
+            const float was = top_w;
+            top_w = fmaxf(was, most);
+            if (__builtin_expect((apart | __ballot((top_w >= 32768.0f) | ((top_w < 16.0f) & (top_w > 0.0f)))) != 0, 0)) {
                 // the row's largest to 2^12 (an infinite scale stays infinite)
-                const int e = (int)(__float_as_uint(top_w) >> 23) - 127;
-                const bool off = top_w > 0.0f && e < 128 && (e >= 15 || e < 4);
-                const float to = off ? fminf(fmaxf(shift + (float)(12 - e), -100.0f), 100.0f) : shift;
-                const float f = __builtin_amdgcn_exp2f(to - shift);
-                shift = to;
-                top_w *= f;
-                l *= f;
+                const int old = (int)shift;
+                const float largest = fmaxf(__builtin_amdgcn_ldexpf(was, -old), __builtin_amdgcn_ldexpf(most, -(int)held));
+                const float there = __builtin_amdgcn_ldexpf(largest, old);
+                const bool off = (largest > 0.0f) & (largest < INFINITY) & ((there >= 32768.0f) | (there < 16.0f));
+                shift = off ? fminf((float)(13 - __builtin_amdgcn_frexp_expf(largest)), MOST) : shift;
+                const int by = (int)shift - old, lacks = (int)(shift - held);
+                top_w = __builtin_amdgcn_ldexpf(largest, (int)shift);
+                l = __builtin_amdgcn_ldexpf(l, (int)(near_of(shift) - near_of((float)old)));
+                sum = __builtin_amdgcn_ldexpf(sum, (int)(near_of(shift) - held));
 #pragma unroll
                 for (int b = 0; b < KB; ++b)
 #pragma unroll
-                    for (int i = 0; i < 16; ++i) x[b][i] *= f;
+                    for (int i = 0; i < 16; ++i) x[b][i] = __builtin_amdgcn_ldexpf(x[b][i], lacks);
 #pragma unroll
-                for (int b = 0; b < NB; ++b)
+                    for (int b = 0; b < NB; ++b)
 #pragma unroll
-                    for (int i = 0; i < 16; ++i) o[b][i] *= f;
+                        for (int i = 0; i < 16; ++i) o[b][i] = __builtin_amdgcn_ldexpf(o[b][i], by);
+                far = __ballot(near_of(shift) != shift);
             }
         }
+        l += sum;
         // values that are not finite, where rows see different keys
         bool dirty = false;
         if (!QUANT && edge && several) {
@@ -891,24 +916,19 @@ void attention_tile(AttnArgs a, AttnPlan plan) {
     // ---- the end of an item's part: rows, or sums for the join
     auto leave = [&]() __attribute__((always_inline)) {
         l += other_half(l);
-        if constexpr (HALF) {
-            const float f = __builtin_amdgcn_exp2f(-shift);
-            l *= f;
-#pragma unroll
-            for (int b = 0; b < NB; ++b)
-#pragma unroll
-                for (int i = 0; i < 16; ++i) o[b][i] *= f;
-        }
+        if constexpr (HALF) l = __builtin_amdgcn_ldexpf(l, -(int)near_of(shift));
         const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+        const float unshift = HALF ? __builtin_amdgcn_ldexpf(1.0f, -(int)shift) : 1.0f;
         if (live) {
 #pragma unroll
             for (int b = 0; b < NB; ++b)
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
                     f32x4 v;
+                    // HALF, of all of a row: the quotient first, which is finite where the sum may not be
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) v[e] = o[b][4 * i + e];
-                    if (whole) write_out<ES, FULL ? ROW_FULL : ST == STAGE_ODD ? ROW_ENDS : ROW_FOURS>(a.O, (int64_t)row * a.ldo + (int64_t)head * D, b * 32 + 8 * i + 4 * half, D, v, l == 0.0f, inv);
+                    for (int e = 0; e < 4; ++e) v[e] = HALF ? o[b][4 * i + e] * (whole ? inv : unshift) : o[b][4 * i + e];
+                    if (whole) write_out<ES, FULL ? ROW_FULL : ST == STAGE_ODD ? ROW_ENDS : ROW_FOURS>(a.O, (int64_t)row * a.ldo + (int64_t)head * D, b * 32 + 8 * i + 4 * half, D, v, l == 0.0f, HALF ? unshift : inv);
                     else plan_sums(a.ws, plan.groups)[(((int64_t)slot * WR + wr) * NB + b) * 256 + i * 64 + lane] = v;
                 }
             if (half == 0 && !whole) {
