@@ -49,6 +49,38 @@ int main() {
     for (const int64_t w : {FAR - held + 1, FAR}) { call(64, 64, 32, 8, 128, 1000, 16, w); CHECK(!tile()); }
     // no table of 2^29 positions, whatever the window
     for (const int64_t w : {(int64_t)5, FAR + 1, ALL}) { call(64, 64, 32, 8, 128, FAR / 16, 16, w); CHECK(!tile()); }
+    // Calls whose items take a workgroup each (tests/test_gpu_attention_items.py).
+    int64_t T = 8;
+    for (int i = 0; i < 2100; ++i) { const int n[10] = {1, 1, 1, 0, 1, 3, 1, 1, 20, 1}; T += n[i % 10]; }
+    const auto own = [&](bool few) {
+        CHECK(tile() && !lp.stream && lp.few == few && tpl::attention_workspace(T, 2100, 2, 1, 32) == 0);
+    };
+    for (const bool int8 : {false, true})
+        for (const int es : {2, 4}) {
+            call(T, 2100, 2, 1, 32, 9, 16, ALL, es, int8); own(true);
+            call(T, 2100, 4, 2, 64, 9, 8, 33, es, int8); own(true);
+            call(T, 2100, 3, 1, 50, 9, 16, ALL, es, int8); own(true);
+            call(T, 2100, 2, 1, 256, 9, 16, 40, es, int8); own(true);
+        }
+    int64_t C = 8;
+    for (int i = 0; i < 540; ++i) { const int n[7] = {1, 0, 37, 9, 60, 5, 0}; C += n[i % 7]; }
+    int64_t H = 1;
+    for (int i = 0; i < 300; ++i) { const int n[5] = {33, 0, 70, 34, 31}; H += n[i % 5]; }
+    for (const bool int8 : {false, true})
+        for (const int es : {2, 4}) {
+            call(C, 540, 8, 1, 64, 10, 16, ALL, es, int8); own(false);
+            call(C, 540, 16, 2, 32, 10, 16, 50, es, int8); own(false);
+            call(C, 540, 8, 1, 36, 30, 5, ALL, es, int8); own(false);
+            CHECK(tpl::attention_workspace(C, 540, 8, 1, 64) == 0);
+            call(H, 300, 8, 8, 32, 7, 16, ALL, es, int8); own(false);
+            CHECK(lp.row_tiles <= 512 && tpl::attention_workspace(H, 300, 8, 8, 32) == 0);
+            // prompts from their first tokens on, and with a wider table
+            for (const int64_t Hq : {8, 4}) {
+                call(440, 4, Hq, Hq / 4, 128, 13, 16, ALL, es, int8); own(false);
+                call(539, 3, Hq, Hq / 4, 128, 13, 16, ALL, es, int8); own(false);
+                call(440, 4, Hq, Hq / 4, 128, 3013, 16, ALL, es, int8); CHECK(tile() && lp.stream && !lp.few);
+            }
+        }
     if (failures) return 1;
     std::printf("attention form driver ok\n");
     return 0;
