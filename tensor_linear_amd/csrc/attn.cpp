@@ -32,7 +32,10 @@ bool dma_ok(const AttnArgs &a, int es) {
 AttnPlan attention_plan(int64_t T, int64_t B, int64_t Hkv, int32_t G, int64_t D, int es, bool quant) {
     AttnPlan p{};
     p.g = divisor(G);
-    // 32 rows a workgroup where the sequences have no more on average
+    // 32 rows a workgroup where the sequences have no more on average.  One form for the whole
+    // call: 64 single tokens behind 8000 at most (214 us) and a chunk of 256 behind 2000 (70),
+    // 8 query heads a key head, are 2560 rows and take 290 us in workgroups of 128; 200 behind
+    // 2000 at most (189) and a chunk of 512 (89) 326 us in ones of 32.
     p.few = T * G <= 32 * B;
     const int64_t rows = p.few ? 32 : 128;
     p.row_tiles = T * G / rows + B;
@@ -70,11 +73,12 @@ hipError_t launch_kv_attention(const AttnArgs &a, int es, hipStream_t s) {
     if (p.stream && p.row_tiles * (p.last_pos / 32 + 8) * a.c.Hkv >= INT32_MAX) p.stream = 0;
     if (!p.stream && p.row_tiles * a.c.Hkv > (1 << 23)) return launch_attention_any(a, es, s);   // more than one launch holds
     // Prompts from their first tokens on: the items' lengths go from one tile of 64 keys to
-    // L, which taking the longest first evens out.  By themselves they then take the time of
-    // 3/4 L tiles or all tiles' share of a workgroup, the runs that share and 6 tiles more,
-    // the sums' way by the workspace (64 query and 8 key heads of 128, one prompt of 512,
-    // 1024 and 2048 tokens: 29, 50 and 115 us for 40, 63 and 136; but with 8 query heads and
-    // one key head 4096 tokens 146 for 78).
+    // L, which taking a prompt's longest first evens out.  By themselves they then take the
+    // time of 3/4 L tiles or all tiles' share of a workgroup, the runs that share and 6 tiles
+    // more, the sums' way by the workspace (64 query and 8 key heads of 128, one prompt of
+    // 512, 1024 and 2048 tokens: 31, 54 and 125 us for 42, 65 and 142; but with 8 query heads
+    // and one key head 4096 tokens 146 for 78).  All that the host knows of the lengths is the
+    // table's width: prompts with a table of more than twice their mean take the runs.
     if (p.stream && !p.few && p.window >= p.last_pos && 2 * a.c.T >= a.c.B * (int64_t)p.last_pos) {
         const int64_t L = p.last_pos / 64, items = p.row_tiles * a.c.Hkv;
         if (L * (3 * p.groups - 2 * items) <= 24 * (int64_t)p.groups) p.stream = 0;

@@ -13,16 +13,22 @@
 // 32 keys, so that a row's maximum and sum need one exchange (with lane l ^ 32), its
 // factors are the lane's own, and the lane's 16 weights are, in order, what the second
 // product takes of it: no weight leaves its lane.  (The order of the keys within an
-// instruction is free as long as the values come in the same one.)
+// instruction is free as long as the values come in the same one.)  That product's weights
+// are of the values' type, since an instruction takes two of one type: bf16 with bf16
+// values, by 2^-8 off at most (a result 1.86e-3 off where its own rounding alone makes it
+// 1.65e-3), fp16 with int8 ones (1.67e-3), exact in fp32.  Their sum is not rounded.
 //
-// K and V tiles lie in LDS as rows of 64, 128 or 256 values, their 16-byte chunks
-// permuted by the row so that reads meet no bank twice: K by chunks of 32 rows, bf16
-// values by the transposing read (4 keys x 16 features a 16-lane group, 8 keys in int8),
-// fp32 values by words.  Two stages: the next tile is fetched while this one is worked on,
-// straight into LDS (16 bytes a lane) where the cache is 16-byte aligned, else by way of
-// registers, of rows that end inside a chunk too.  int8 becomes bf16 or fp32 (exactly; a key's scale multiplies its products, a
-// value's scale its weight) as a wavefront reads it from LDS where it is alone, on the way
-// into LDS where four read the same keys.
+// K and V tiles lie in LDS as rows of 64, 128 or 256 values, their 16-byte chunks permuted
+// by the row so that reads meet no bank twice: K by chunks of 32 rows, bf16 values by the
+// transposing read (4 keys x 16 features a 16-lane group, 8 keys in int8), fp32 values by
+// words.  Two stages: the next tile is fetched while this one is there, straight into LDS
+// (16 bytes a lane) where the cache is 16-byte aligned, else by way of registers, of rows
+// that end inside a chunk too.  (But hipcc waits for every load before a tile's first
+// product, since the query may have been loaded just before: a wavefront's fetch goes on
+// under the work of other wavefronts, not under its own.)  int8 becomes bf16 or fp32
+// (exactly; a key's scale multiplies its products, a value's scale its weight) as a
+// wavefront reads it from LDS where it is alone, on the way into LDS where four read the
+// same keys.
 //
 // What a row does not see must not touch it: keys and values of no position are zeros,
 // products that a row does not see are minus infinity before the maximum, and a tile at
@@ -31,31 +37,36 @@
 // them get the infinity afterwards.
 //
 // Work: `items` are (sequence, rows, key head).  Where there are many, a workgroup takes
-// one, the longest first, neighbours in the grid on other key heads (an XCD, every 8th
-// workgroup, then keeps to few heads, whose keys its L2 holds).  Else the tiles of all
-// items in a row are cut into equal runs, one for each workgroup: a run's whole items are
-// finished, the others' sums go to the workspace and are joined by a second launch in the
-// order of the tiles.  The lengths are on the device: each workgroup adds them up itself.
-// A run's tiles are one stream, across its items: wavefront 0 looks up the rows of the tile
-// after next (and the next item, when one ends), which all need a tile later, so that the
-// fetches never wait for it.  It alone reads the lengths, and the others go by what it
-// leaves in LDS: a workgroup stays together and in bounds whatever is in those arrays, were
-// they to change under it.
+// one, the last rows of the last sequence first (a sequence's longest item; a long first
+// sequence comes last: one of 2048 tokens behind 6000 before 300 of 128 730 us, behind
+// them 712), neighbours in the grid on other key heads (an XCD, every 8th workgroup, then
+// keeps to few heads, whose keys its L2 holds).  Else the tiles of all items in a row are
+// cut into equal runs, one for each workgroup: a run's whole items are finished, the
+// others' sums go to the workspace and are joined by a second launch in the order of the
+// tiles.  The lengths are on the device: each workgroup adds them up itself. A run's tiles
+// are one stream, across its items: wavefront 0 looks up the rows of the tile after next
+// (and the next item, when one ends), which all need a tile later, so that the fetches
+// never wait for it.  It alone reads the lengths, and the others go by what it leaves in
+// LDS: a workgroup stays together and in bounds whatever is in those arrays, were they to
+// change under it.
 //
-// Measured (both launches, a captured graph; inputs that no cache holds).  One token each of
-// 64 sequences of 8000 at most, 64 query and 8 key heads of 128: 214 us, 5.0 TB/s, the rate
-// of a copy; 16000 at most of 32 query heads over int8 213 us, 4.6 TB/s, where a tile's 500
-// vector instructions (its values become bf16 and fp16 in each wavefront) take 52% of the
-// cycles.  A prompt of 4096 tokens, the same heads: 391-425 us by the
-// chip's temperature, 650-700 TFLOP/s: the matrix cores are busy 29% and the vector units 44%
-// of the cycles, four wavefronts that wait for each other every 64 keys the rest (wavefront
-// 0's look-ups 8%).  12 chunks of 600 tokens at most, 24 query and
-// 8 key heads of 96, a window of 1024 over int8: 114 us, 251 TFLOP/s, 630 vector instructions
-// for 24 products a wavefront and tile, and 11 us the join.  4 sequences of 300 keys: 16 us, where the
-// first tile is worked on after 9, lengths, page table, rows and keys read one after another.
-// Split: 64 keys a tile instead of 32 where four wavefronts share them (fewer meetings), two
-// workgroups a CU.  One wavefront a workgroup for 32 rows: four wavefronts that cut the keys
-// of one tile among them and joined their sums in LDS took 257 us for the first case.
+// Measured (both launches, a captured graph; inputs that no cache holds).  One token each
+// of 64 sequences of 8000 at most, 64 query and 8 key heads of 128: 214 us, 5.0 TB/s, the
+// rate of a copy; 16000 at most of 32 query heads over int8 213 us, 4.6 TB/s, where a
+// tile's 500 vector instructions (its values become bf16 and fp16 in each wavefront) take
+// 52% of the cycles.  A prompt of 4096 tokens, the same heads: 385-425 us by the chip's
+// temperature, 650-700 TFLOP/s: the matrix cores are busy 29% and the vector units 44% of
+// the cycles; the rest are the wait for the next tile above and four wavefronts' for each
+// other every 64 keys (wavefront 0's look-ups 8%).  12 chunks of 600 tokens at most, 24
+// query and 8 key heads of 96, a window of 1024 over int8: 114 us, 251 TFLOP/s, 630 vector
+// instructions for 24 products a wavefront and tile, and 11 us the join.  4 sequences of
+// 300 keys: 16 us, where the first tile is worked on after 9, lengths, page table, rows
+// and keys read one after another. Split: 64 keys a tile instead of 32 where four
+// wavefronts share them (fewer meetings), two workgroups a CU.  One wavefront a workgroup
+// for 32 rows: four wavefronts that cut the keys of one tile among them and joined their
+// sums in LDS took 257 us for the first case.  Heads past 128 are 256 features here, whose sums
+// and query do not fit the registers (38 to 702 of them spilled), and take the time of 256: 64
+// sequences of 8000 at most, 32 + 8 heads of 160, 192, 256 534, 551, 562 us.
 #pragma once
 
 #include <hip/hip_runtime.h>
@@ -78,11 +89,9 @@ typedef uint32_t u32_any __attribute__((aligned(1)));
 typedef uint32_t u32x2_any __attribute__((ext_vector_type(2), aligned(1)));
 typedef uint32_t u32x4_any __attribute__((ext_vector_type(4), aligned(1)));
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
-typedef __bf16 bf16x4 __attribute__((ext_vector_type(4)));
 typedef _Float16 f16x2 __attribute__((ext_vector_type(2)));
 typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
 typedef short s16x4 __attribute__((ext_vector_type(4)));
-typedef short s16x8 __attribute__((ext_vector_type(8)));
 
 // Source of the rows of no position (a row is 1 KB at most).
 static __device__ __attribute__((aligned(16))) const uint32_t no_key[256] = {};
@@ -198,12 +207,6 @@ __device__ __forceinline__ u32x4 shift_down(u32x4 x, int n) {
 }
 
 __device__ __forceinline__ float other_half(float v) { return __shfl_xor(v, 32); }
-
-// A value that all lanes have, as a scalar.
-__device__ __forceinline__ int64_t uniform(int64_t v) {
-    const uint32_t lo = __builtin_amdgcn_readfirstlane((uint32_t)v), hi = __builtin_amdgcn_readfirstlane((uint32_t)(v >> 32));
-    return (int64_t)((uint64_t)hi << 32 | lo);
-}
 
 // What lies in LDS: rows of the call's type by way of registers, the same straight from
 // the cache, or int8 straight from the cache.  ODD: as REGS, of rows that end inside a chunk;
@@ -578,7 +581,7 @@ void attention_tile(AttnArgs a, AttnPlan plan) {
             }
         }
     };
-    // Of this tile, while the next one's instructions are under way (66 at most; the counter
+    // Of this tile, while the next one's instructions are under way (64 at most; the counter
     // holds 63).
     auto settle_first = [&]() __attribute__((always_inline)) {
         constexpr int LATER = 2 * LI + (QUANT ? 2 : 0);
@@ -945,7 +948,7 @@ void attention_tile(AttnArgs a, AttnPlan plan) {
 
     // ---- the tiles.  In one loop, so that each step is there once (a launch begins without
     // instructions in the caches): tile n + 2 is looked up, tile n + 1 fetched, tile n worked
-    // on.  A wavefront by itself (ALONE) fetches the next tile before this one is there, as
+    // on.  A wavefront by itself (ALONE) asks for the next tile before this one is there, as
     // soon as its place in LDS is free; four wait for theirs first, and then for each other.
     Tile now{0, 0, -1}, next{0, 0, -1};
     for (int n = -2;; ++n) {
